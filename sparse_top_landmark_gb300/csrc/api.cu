@@ -710,6 +710,341 @@ int backward_impl(const T* q, const T* k, const T* v, const T* dout, int B, int 
   return MITA_OK;
 }
 
+// ---------------------------------------------------------------------------
+// q / k preparation and the paged cache
+// ---------------------------------------------------------------------------
+// The device's state for calls that may be captured: its first use allocates, which would break
+// a capture, so that is refused before anything is touched.
+int device_state_for(cudaStream_t st, DevState** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  bool known = false;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto it = g_dev.find(dev);
+    known = it != g_dev.end() && it->second.status != nullptr;
+  }
+  if (!known) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(st, &cs);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    if (cs != cudaStreamCaptureStatusNone)
+      return fail(MITA_ERR_UNSUPPORTED,
+                  "the library's first call on a device cannot be captured; make one outside "
+                  "capture first");
+  }
+  return device_state(out);
+}
+
+int check_head_dim(int d) {
+  if (d != 16 && d != 32 && d != 64 && d != 128)
+    return fail(MITA_ERR_UNSUPPORTED, "head dim d=%d not in {16, 32, 64, 128}", d);
+  return MITA_OK;
+}
+
+int check_aligned(const void* p, size_t to, const char* name) {
+  if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) % to != 0)
+    return fail(MITA_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, to);
+  return MITA_OK;
+}
+
+int check_rope(int d, int rot, const double* inv_freq, float eps) {
+  if (rot < 0 || rot > d || rot % 8 != 0)
+    return fail(MITA_ERR_INVALID_ARG, "rot=%d must be a multiple of 8 in [0, d=%d]", rot, d);
+  if (rot > 0) MITA_TRY(check_aligned(inv_freq, 8, "inv_freq"));
+  if (!(eps >= 0.f)) return fail(MITA_ERR_INVALID_ARG, "eps must be >= 0");
+  return MITA_OK;
+}
+
+// Element strides of an array of rows: `given`, or those of the dense array when it is NULL.
+// Rows must start on 16-byte boundaries; the stride of a dimension of size 1 is not looked at.
+template <int K>
+int row_strides(const int64_t* given, const int64_t (&dense)[K], const int (&size)[K], size_t esize,
+                const char* name, long long (&out)[K]) {
+  for (int i = 0; i < K; ++i) {
+    out[i] = size[i] == 1 ? 0 : given ? given[i] : dense[i];
+    if (out[i] < 0 || out[i] % (long long)(16 / esize) != 0)
+      return fail(MITA_ERR_INVALID_ARG,
+                  "%s: stride %lld is negative or leaves rows off 16-byte boundaries", name,
+                  out[i]);
+  }
+  return MITA_OK;
+}
+
+int bhn_strides(const int64_t* given, int B, int H, int N, int d, size_t esize, const char* name,
+                long long (&out)[3]) {
+  return row_strides<3>(given, {(int64_t)H * N * d, (int64_t)N * d, (int64_t)d}, {B, H, N}, esize,
+                        name, out);
+}
+
+int check_bhn(int B, int Hq, int Hkv, int N, int d) {
+  if (B < 0 || N < 0 || Hq < 1 || Hkv < 0)
+    return fail(MITA_ERR_INVALID_ARG, "need B, N, Hkv >= 0 and Hq >= 1 (got %d, %d, %d, %d)", B, N,
+                Hkv, Hq);
+  MITA_TRY(check_head_dim(d));
+  if ((long long)B * N >= (1LL << 31) || (long long)B * N * ((long long)Hq + Hkv) >= (1LL << 31))
+    return fail(MITA_ERR_UNSUPPORTED, "B*(Hq+Hkv)*N must be < 2^31");
+  return MITA_OK;
+}
+
+int check_positions(const int32_t* positions, int64_t stride) {
+  if (positions == nullptr) return MITA_OK;
+  if (stride < 0) return fail(MITA_ERR_INVALID_ARG, "positions_stride must be >= 0");
+  return check_aligned(positions, 4, "positions");
+}
+
+template <typename T>
+int norm_rope_impl(const T* q, const T* k, const float* q_weight, const float* k_weight,
+                   const int32_t* positions, int64_t positions_stride, const double* inv_freq,
+                   int B, int Hq, int Hkv, int N, int d, int rot, int interleaved, float eps,
+                   const int64_t* q_strides, const int64_t* k_strides,
+                   const int64_t* q_out_strides, const int64_t* k_out_strides, T* q_out, T* k_out,
+                   cudaStream_t st) {
+  MITA_TRY(check_bhn(B, Hq, Hkv, N, d));
+  MITA_TRY(check_rope(d, rot, inv_freq, eps));
+  if (B == 0 || N == 0) return MITA_OK;
+  NormRopeArgs<T> a{};
+  const T* xs[2] = {q, k};
+  T* ys[2] = {q_out, k_out};
+  const float* ws[2] = {q_weight, k_weight};
+  const int64_t* given[2][2] = {{q_strides, q_out_strides}, {k_strides, k_out_strides}};
+  const int heads[2] = {Hq, Hkv};
+  static const char* const names[2][3] = {{"q", "q_out", "q_weight"}, {"k", "k_out", "k_weight"}};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    MITA_TRY(check_ptrs({{xs[i], names[i][0]}, {ys[i], names[i][1]}}));
+    if (ws[i]) MITA_TRY(check_aligned(ws[i], 16, names[i][2]));
+    long long x[3], y[3];
+    MITA_TRY(bhn_strides(given[i][0], B, heads[i], N, d, sizeof(T), names[i][0], x));
+    MITA_TRY(bhn_strides(given[i][1], B, heads[i], N, d, sizeof(T), names[i][1], y));
+    a.part[i] = {xs[i], ys[i], ws[i], x[0], x[1], x[2], y[0], y[1], y[2], heads[i]};
+  }
+  MITA_TRY(check_positions(positions, positions_stride));
+  a.positions = positions;
+  a.pos_b = positions_stride;
+  a.inv_freq = inv_freq;
+  a.B = B; a.N = N; a.rot = rot; a.interleaved = interleaved != 0; a.eps = eps;
+  DevState* ds = nullptr;
+  MITA_TRY(device_state_for(st, &ds));
+  MITA_CUDA(launch_norm_rope<T>(a, d, ds->num_sms, st), "norm and rotation launch");
+  return MITA_OK;
+}
+
+int current_sms() {
+  int sms = 152, dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetLastError();
+  return sms;
+}
+
+int check_workspace(const void* ws, uint64_t have, uint64_t need) {
+  if (need == 0) return MITA_OK;
+  if (have < need)
+    return fail(MITA_ERR_INVALID_ARG, "workspace of %llu bytes: this call needs %llu",
+                (unsigned long long)have, (unsigned long long)need);
+  return check_aligned(ws, 16, "workspace");
+}
+
+uint64_t norm_rope_backward_ws(int d) {
+  return (uint64_t)norm_rope_backward_blocks(current_sms()) * d * sizeof(float);
+}
+
+template <typename T>
+int norm_rope_backward_impl(const T* q, const T* k, const T* dq_out, const T* dk_out,
+                            const float* q_weight, const float* k_weight, const int32_t* positions,
+                            int64_t positions_stride, const double* inv_freq, int B, int Hq,
+                            int Hkv, int N, int d, int rot, int interleaved, float eps,
+                            const int64_t* q_strides, const int64_t* k_strides,
+                            const int64_t* dq_out_strides, const int64_t* dk_out_strides,
+                            const int64_t* dq_strides, const int64_t* dk_strides, void* workspace,
+                            uint64_t workspace_bytes, T* dq, T* dk, float* dq_weight,
+                            float* dk_weight, cudaStream_t st) {
+  MITA_TRY(check_bhn(B, Hq, Hkv, N, d));
+  MITA_TRY(check_rope(d, rot, inv_freq, eps));
+  const T* xs[2] = {q, k};
+  const T* dys[2] = {dq_out, dk_out};
+  T* dxs[2] = {dq, dk};
+  const float* ws[2] = {q_weight, k_weight};
+  float* dws[2] = {dq_weight, dk_weight};
+  const int64_t* given[2][3] = {{q_strides, dq_out_strides, dq_strides},
+                                {k_strides, dk_out_strides, dk_strides}};
+  const int heads[2] = {Hq, Hkv};
+  static const char* const names[2][5] = {{"q", "dq_out", "dq", "q_weight", "dq_weight"},
+                                          {"k", "dk_out", "dk", "k_weight", "dk_weight"}};
+  const bool empty = B == 0 || N == 0;
+  NormRopeBackwardArgs<T> a{};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) {
+      dws[i] = nullptr;
+      continue;
+    }
+    if (ws[i]) {
+      MITA_TRY(check_aligned(ws[i], 16, names[i][3]));
+      MITA_TRY(check_aligned(dws[i], 4, names[i][4]));
+    } else if (dws[i]) {
+      return fail(MITA_ERR_INVALID_ARG, "%s given without %s", names[i][4], names[i][3]);
+    }
+    if (empty) continue;
+    MITA_TRY(check_ptrs({{dys[i], names[i][1]}, {dxs[i], names[i][2]}}));
+    if (ws[i]) MITA_TRY(check_ptrs({{xs[i], names[i][0]}}));   // else x is not read
+    long long x[3], dy[3], dx[3];
+    MITA_TRY(bhn_strides(given[i][0], B, heads[i], N, d, sizeof(T), names[i][0], x));
+    MITA_TRY(bhn_strides(given[i][1], B, heads[i], N, d, sizeof(T), names[i][1], dy));
+    MITA_TRY(bhn_strides(given[i][2], B, heads[i], N, d, sizeof(T), names[i][2], dx));
+    a.part[i] = {xs[i], dys[i], dxs[i], ws[i], nullptr, x[0], x[1], x[2], dy[0], dy[1], dy[2],
+                 dx[0], dx[1], dx[2], heads[i]};
+  }
+  MITA_TRY(check_positions(positions, positions_stride));
+  if (!empty && (dws[0] || dws[1]))
+    MITA_TRY(check_workspace(workspace, workspace_bytes, norm_rope_backward_ws(d)));
+  if (empty) {
+    for (float* w : dws)
+      if (w) MITA_CUDA(cudaMemsetAsync(w, 0, d * sizeof(float), st), "weight gradient");
+    return MITA_OK;
+  }
+  a.positions = positions;
+  a.pos_b = positions_stride;
+  a.inv_freq = inv_freq;
+  a.B = B; a.N = N; a.rot = rot; a.interleaved = interleaved != 0; a.eps = eps;
+  DevState* ds = nullptr;
+  MITA_TRY(device_state_for(st, &ds));
+  MITA_CUDA(launch_norm_rope_backward<T>(a, d, static_cast<float*>(workspace), ds->num_sms, dws[0],
+                                         dws[1], st),
+            "norm and rotation gradient launch");
+  return MITA_OK;
+}
+
+int check_pages(int S, int Hkv, int num_pages, int page_size, int width) {
+  if (S < 0 || Hkv < 1 || num_pages < 0 || width < 0)
+    return fail(MITA_ERR_INVALID_ARG,
+                "need S, num_pages, table_width >= 0 and Hkv >= 1 (got %d, %d, %d, %d)", S,
+                num_pages, width, Hkv);
+  if (page_size < 1 || page_size > kMaxPageSize || (page_size & (page_size - 1)) != 0)
+    return fail(MITA_ERR_UNSUPPORTED, "page_size=%d is not a power of two in [1, %d]", page_size,
+                kMaxPageSize);
+  if ((long long)width * page_size >= (1LL << 31))
+    return fail(MITA_ERR_UNSUPPORTED, "table_width*page_size must be < 2^31");
+  if ((long long)num_pages * Hkv >= (1LL << 40))
+    return fail(MITA_ERR_UNSUPPORTED, "num_pages*Hkv must be < 2^40");
+  return MITA_OK;
+}
+
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+template <typename T>
+int cache_append_impl(const T* q, const T* k, const T* v, const float* q_weight,
+                      const float* k_weight, const double* inv_freq, const int32_t* page_table,
+                      const int32_t* lengths, const int32_t* seq_start, int tokens, int S, int Hq,
+                      int Hkv, int d, int num_pages, int page_size, int table_width, int rot,
+                      int interleaved, float eps, const int64_t* q_strides,
+                      const int64_t* k_strides, const int64_t* v_strides,
+                      const int64_t* q_out_strides, T* q_out, T* k_cache, T* v_cache,
+                      cudaStream_t st) {
+  if (tokens < 0 || Hq < 0)
+    return fail(MITA_ERR_INVALID_ARG, "need tokens, Hq >= 0 (got %d, %d)", tokens, Hq);
+  MITA_TRY(check_pages(S, Hkv, num_pages, page_size, table_width));
+  MITA_TRY(check_head_dim(d));
+  MITA_TRY(check_rope(d, rot, inv_freq, eps));
+  if ((long long)tokens * ((long long)Hq + 2 * Hkv) >= (1LL << 31))
+    return fail(MITA_ERR_UNSUPPORTED, "tokens*(Hq+2*Hkv) must be < 2^31");
+  if (seq_start == nullptr && tokens != S)
+    return fail(MITA_ERR_INVALID_ARG,
+                "without seq_start every sequence has one new token (tokens=%d, S=%d)", tokens, S);
+  if (tokens == 0 || S == 0) return MITA_OK;
+  CacheAppendArgs<T> a{};
+  if (Hq > 0) {
+    MITA_TRY(check_ptrs({{q, "q"}, {q_out, "q_out"}}));
+    long long x[2], y[2];
+    MITA_TRY(row_strides<2>(q_strides, {(int64_t)Hq * d, d}, {tokens, Hq}, sizeof(T), "q", x));
+    MITA_TRY(row_strides<2>(q_out_strides, {(int64_t)Hq * d, d}, {tokens, Hq}, sizeof(T), "q_out",
+                            y));
+    a.q_t = x[0]; a.q_h = x[1]; a.qo_t = y[0]; a.qo_h = y[1];
+  }
+  MITA_TRY(check_ptrs({{k, "k"}, {v, "v"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}}));
+  if (q_weight) MITA_TRY(check_aligned(q_weight, 16, "q_weight"));
+  if (k_weight) MITA_TRY(check_aligned(k_weight, 16, "k_weight"));
+  MITA_TRY(check_aligned(page_table, 4, "page_table"));
+  MITA_TRY(check_aligned(lengths, 4, "lengths"));
+  if (seq_start) MITA_TRY(check_aligned(seq_start, 4, "seq_start"));
+  long long ks[2], vs[2];
+  MITA_TRY(row_strides<2>(k_strides, {(int64_t)Hkv * d, d}, {tokens, Hkv}, sizeof(T), "k", ks));
+  MITA_TRY(row_strides<2>(v_strides, {(int64_t)Hkv * d, d}, {tokens, Hkv}, sizeof(T), "v", vs));
+  DevState* ds = nullptr;
+  MITA_TRY(device_state_for(st, &ds));
+  a.q = q; a.k = k; a.v = v; a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.q_w = q_weight; a.k_w = k_weight; a.inv_freq = inv_freq; a.seq_start = seq_start;
+  a.k_t = ks[0]; a.k_h = ks[1]; a.v_t = vs[0]; a.v_h = vs[1];
+  a.paged = {page_table, lengths, S, table_width, num_pages, log2_of(page_size)};
+  a.tokens = tokens; a.q_heads = Hq; a.kv_heads = Hkv; a.rot = rot;
+  a.interleaved = interleaved != 0; a.eps = eps; a.status = ds->status;
+  MITA_CUDA(launch_cache_append<T>(a, d, ds->num_sms, st), "cache append launch");
+  return MITA_OK;
+}
+
+int check_paged_attn(int S, int Hq, int Hkv, int d, int num_pages, int page_size, int width) {
+  MITA_TRY(check_pages(S, Hkv, num_pages, page_size, width));
+  MITA_TRY(check_head_dim(d));
+  if (Hq < 1 || Hq % Hkv != 0)
+    return fail(MITA_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d", Hq, Hkv);
+  if ((long long)S * Hq >= (1LL << 31))
+    return fail(MITA_ERR_UNSUPPORTED, "S*Hq must be < 2^31");
+  return MITA_OK;
+}
+
+template <typename T>
+int paged_attn_impl(const T* q, const T* k_cache, const T* v_cache, const int32_t* page_table,
+                    const int32_t* lengths, const float* alibi_slopes, int S, int Hq, int Hkv,
+                    int d, int num_pages, int page_size, int table_width,
+                    const int64_t* q_strides, float scale, float softcap, int window,
+                    void* workspace, uint64_t workspace_bytes, T* out, float* lse,
+                    cudaStream_t st) {
+  MITA_TRY(check_paged_attn(S, Hq, Hkv, d, num_pages, page_size, table_width));
+  if (!std::isfinite(scale)) return fail(MITA_ERR_INVALID_ARG, "scale is not finite");
+  if (!(softcap >= 0.f) || std::isinf(softcap))
+    return fail(MITA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  if (window < 0) return fail(MITA_ERR_INVALID_ARG, "window must be >= 0");
+  if (S == 0) return MITA_OK;
+  MITA_TRY(check_ptrs({{q, "q"}, {out, "out"}}));
+  if (num_pages > 0) MITA_TRY(check_ptrs({{k_cache, "k_cache"}, {v_cache, "v_cache"}}));
+  if (table_width > 0) MITA_TRY(check_aligned(page_table, 4, "page_table"));
+  MITA_TRY(check_aligned(lengths, 4, "lengths"));
+  if (alibi_slopes) MITA_TRY(check_aligned(alibi_slopes, 4, "alibi_slopes"));
+  if (lse) MITA_TRY(check_aligned(lse, 4, "lse"));
+  long long qs[2];
+  MITA_TRY(row_strides<2>(q_strides, {(int64_t)Hq * d, d}, {S, Hq}, sizeof(T), "q", qs));
+  DevState* ds = nullptr;
+  MITA_TRY(device_state_for(st, &ds));
+  const int pl = log2_of(page_size), G = Hq / Hkv;
+  MITA_TRY(check_workspace(workspace, workspace_bytes,
+                           paged_attn_ws_bytes(d, Hkv, G, S, table_width, pl, sizeof(T) == 4,
+                                               ds->num_sms)));
+  PagedAttnArgs<T> a{};
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.out = out; a.lse = lse;
+  a.slopes = alibi_slopes; a.q_s = qs[0]; a.q_h = qs[1];
+  a.paged = {page_table, lengths, S, table_width, num_pages, pl};
+  a.Hkv = Hkv; a.G = G; a.scale = scale; a.softcap = softcap; a.window = window;
+  a.status = ds->status;
+  MITA_CUDA(launch_paged_attn<T>(a, d, workspace, ds->num_sms, st), "paged attention launch");
+  return MITA_OK;
+}
+
+// Nothing thrown may leave a C entry point.
+template <typename F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return MITA_ERR_OOM;      // the host's allocator is all that can throw here
+  }
+}
+
 // The forward on host buffers.  The host link, not the GPU, bounds this call (H2D and D2H
 // each run at about 200 GB/s on this part, whether a copy engine or the SMs drive them), so
 // the heads are split into up to kHostGroups groups that pipeline: a copy stream brings in
@@ -975,6 +1310,144 @@ int mita_forward_host_f32(const float* q, const float* k, const float* v, int B,
                           mita_stream_t stream) {
   return mita::forward_host_impl<float>(q, k, v, B, H, N, d, grid_h, grid_w, m, topk, s, out,
                                         stream);
+}
+
+int mita_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                      const int32_t* positions, int64_t positions_stride, const double* inv_freq,
+                      int B, int Hq, int Hkv, int N, int d, int rot, int interleaved, float eps,
+                      const int64_t* q_strides, const int64_t* k_strides,
+                      const int64_t* q_out_strides, const int64_t* k_out_strides, void* q_out,
+                      void* k_out, mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::norm_rope_impl<bf16>(
+        static_cast<const bf16*>(q), static_cast<const bf16*>(k), q_weight, k_weight, positions,
+        positions_stride, inv_freq, B, Hq, Hkv, N, d, rot, interleaved, eps, q_strides, k_strides,
+        q_out_strides, k_out_strides, static_cast<bf16*>(q_out), static_cast<bf16*>(k_out),
+        stream);
+  });
+}
+int mita_qk_norm_rope_f32(const float* q, const float* k, const float* q_weight,
+                          const float* k_weight, const int32_t* positions,
+                          int64_t positions_stride, const double* inv_freq, int B, int Hq, int Hkv,
+                          int N, int d, int rot, int interleaved, float eps,
+                          const int64_t* q_strides, const int64_t* k_strides,
+                          const int64_t* q_out_strides, const int64_t* k_out_strides, float* q_out,
+                          float* k_out, mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::norm_rope_impl<float>(q, k, q_weight, k_weight, positions, positions_stride,
+                                       inv_freq, B, Hq, Hkv, N, d, rot, interleaved, eps,
+                                       q_strides, k_strides, q_out_strides, k_out_strides, q_out,
+                                       k_out, stream);
+  });
+}
+
+uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d) {
+  return mita::check_head_dim(d) == MITA_OK ? mita::norm_rope_backward_ws(d) : 0;
+}
+
+int mita_qk_norm_rope_backward(const void* q, const void* k, const void* dq_out,
+                               const void* dk_out, const float* q_weight, const float* k_weight,
+                               const int32_t* positions, int64_t positions_stride,
+                               const double* inv_freq, int B, int Hq, int Hkv, int N, int d,
+                               int rot, int interleaved, float eps, const int64_t* q_strides,
+                               const int64_t* k_strides, const int64_t* dq_out_strides,
+                               const int64_t* dk_out_strides, const int64_t* dq_strides,
+                               const int64_t* dk_strides, void* workspace,
+                               uint64_t workspace_bytes, void* dq, void* dk, float* dq_weight,
+                               float* dk_weight, mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::norm_rope_backward_impl<bf16>(
+        static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(dq_out),
+        static_cast<const bf16*>(dk_out), q_weight, k_weight, positions, positions_stride,
+        inv_freq, B, Hq, Hkv, N, d, rot, interleaved, eps, q_strides, k_strides, dq_out_strides,
+        dk_out_strides, dq_strides, dk_strides, workspace, workspace_bytes, static_cast<bf16*>(dq),
+        static_cast<bf16*>(dk), dq_weight, dk_weight, stream);
+  });
+}
+int mita_qk_norm_rope_backward_f32(const float* q, const float* k, const float* dq_out,
+                                   const float* dk_out, const float* q_weight,
+                                   const float* k_weight, const int32_t* positions,
+                                   int64_t positions_stride, const double* inv_freq, int B, int Hq,
+                                   int Hkv, int N, int d, int rot, int interleaved, float eps,
+                                   const int64_t* q_strides, const int64_t* k_strides,
+                                   const int64_t* dq_out_strides, const int64_t* dk_out_strides,
+                                   const int64_t* dq_strides, const int64_t* dk_strides,
+                                   void* workspace, uint64_t workspace_bytes, float* dq, float* dk,
+                                   float* dq_weight, float* dk_weight, mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::norm_rope_backward_impl<float>(
+        q, k, dq_out, dk_out, q_weight, k_weight, positions, positions_stride, inv_freq, B, Hq,
+        Hkv, N, d, rot, interleaved, eps, q_strides, k_strides, dq_out_strides, dk_out_strides,
+        dq_strides, dk_strides, workspace, workspace_bytes, dq, dk, dq_weight, dk_weight, stream);
+  });
+}
+
+int mita_cache_append(const void* q, const void* k, const void* v, const float* q_weight,
+                      const float* k_weight, const double* inv_freq, const int32_t* page_table,
+                      const int32_t* lengths, const int32_t* seq_start, int tokens, int S, int Hq,
+                      int Hkv, int d, int num_pages, int page_size, int table_width, int rot,
+                      int interleaved, float eps, const int64_t* q_strides,
+                      const int64_t* k_strides, const int64_t* v_strides,
+                      const int64_t* q_out_strides, void* q_out, void* k_cache, void* v_cache,
+                      mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::cache_append_impl<bf16>(
+        static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v),
+        q_weight, k_weight, inv_freq, page_table, lengths, seq_start, tokens, S, Hq, Hkv, d,
+        num_pages, page_size, table_width, rot, interleaved, eps, q_strides, k_strides, v_strides,
+        q_out_strides, static_cast<bf16*>(q_out), static_cast<bf16*>(k_cache),
+        static_cast<bf16*>(v_cache), stream);
+  });
+}
+int mita_cache_append_f32(const float* q, const float* k, const float* v, const float* q_weight,
+                          const float* k_weight, const double* inv_freq,
+                          const int32_t* page_table, const int32_t* lengths,
+                          const int32_t* seq_start, int tokens, int S, int Hq, int Hkv, int d,
+                          int num_pages, int page_size, int table_width, int rot, int interleaved,
+                          float eps, const int64_t* q_strides, const int64_t* k_strides,
+                          const int64_t* v_strides, const int64_t* q_out_strides, float* q_out,
+                          float* k_cache, float* v_cache, mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::cache_append_impl<float>(
+        q, k, v, q_weight, k_weight, inv_freq, page_table, lengths, seq_start, tokens, S, Hq, Hkv,
+        d, num_pages, page_size, table_width, rot, interleaved, eps, q_strides, k_strides,
+        v_strides, q_out_strides, q_out, k_cache, v_cache, stream);
+  });
+}
+
+uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page_size,
+                                         int table_width, int is_f32) {
+  if (mita::check_paged_attn(S, Hq, Hkv, d, 0, page_size, table_width) != MITA_OK) return 0;
+  return mita::paged_attn_ws_bytes(d, Hkv, Hq / Hkv, S, table_width, mita::log2_of(page_size),
+                                   is_f32, mita::current_sms());
+}
+
+int mita_paged_attn(const void* q, const void* k_cache, const void* v_cache,
+                    const int32_t* page_table, const int32_t* lengths, const float* alibi_slopes,
+                    int S, int Hq, int Hkv, int d, int num_pages, int page_size, int table_width,
+                    const int64_t* q_strides, float scale, float softcap, int window,
+                    void* workspace, uint64_t workspace_bytes, void* out, float* lse,
+                    mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::paged_attn_impl<bf16>(
+        static_cast<const bf16*>(q), static_cast<const bf16*>(k_cache),
+        static_cast<const bf16*>(v_cache), page_table, lengths, alibi_slopes, S, Hq, Hkv, d,
+        num_pages, page_size, table_width, q_strides, scale, softcap, window, workspace,
+        workspace_bytes, static_cast<bf16*>(out), lse, stream);
+  });
+}
+int mita_paged_attn_f32(const float* q, const float* k_cache, const float* v_cache,
+                        const int32_t* page_table, const int32_t* lengths,
+                        const float* alibi_slopes, int S, int Hq, int Hkv, int d, int num_pages,
+                        int page_size, int table_width, const int64_t* q_strides, float scale,
+                        float softcap, int window, void* workspace, uint64_t workspace_bytes,
+                        float* out, float* lse, mita_stream_t stream) {
+  return mita::guarded([&] {
+    return mita::paged_attn_impl<float>(q, k_cache, v_cache, page_table, lengths, alibi_slopes, S,
+                                        Hq, Hkv, d, num_pages, page_size, table_width, q_strides,
+                                        scale, softcap, window, workspace, workspace_bytes, out,
+                                        lse, stream);
+  });
 }
 
 uint64_t mita_forward_workspace_bytes(int B, int H, int N, int d, int m, int topk, int s,

@@ -259,6 +259,103 @@ struct BwdPass {
 constexpr int kBwdSplitRows = 1024;   // streamed rows per CTA of the tensor-core passes
 cudaError_t launch_bwd_pass_mma(BwdPass p, int kind, cudaStream_t st);
 
+// ---- q and k on the way into attention: per-head RMS norm and position rotation -----------
+// Strides are in elements; rows of d values are contiguous and start 16-byte aligned.
+template <typename T>
+struct NormRopePart {       // q or k
+  const T* x;
+  T* y;
+  const float* w;           // [d] norm weight; null: not normalised
+  long long x_b, x_h, x_n, y_b, y_h, y_n;
+  int heads;                // 0: this part is absent
+};
+template <typename T>
+struct NormRopeArgs {
+  NormRopePart<T> part[2];  // q, k
+  const int32_t* positions; // [B][N], pos_b from batch to batch; null: 0 .. N - 1
+  long long pos_b;
+  const double* inv_freq;   // [rot / 2] radians per position
+  int B, N, rot, interleaved;
+  float eps;
+  int run;                  // set by the launcher
+};
+template <typename T>
+cudaError_t launch_norm_rope(NormRopeArgs<T> a, int d, int sms, cudaStream_t st);
+
+template <typename T>
+struct NormRopeBackwardPart {
+  const T *x, *dy;
+  T* dx;
+  const float* w;
+  float* partial;           // set by the launcher
+  long long x_b, x_h, x_n, dy_b, dy_h, dy_n, dx_b, dx_h, dx_n;
+  int heads;
+};
+template <typename T>
+struct NormRopeBackwardArgs {
+  NormRopeBackwardPart<T> part[2];
+  const int32_t* positions;
+  long long pos_b;
+  const double* inv_freq;
+  int B, N, rot, interleaved;
+  float eps;
+  int run, qblocks;         // set by the launcher
+};
+// Most blocks of the gradient kernel: its weight gradients need that many partial rows of d
+// floats in `partial`.  dwq / dwk [d]: written where not null.
+int norm_rope_backward_blocks(int sms);
+template <typename T>
+cudaError_t launch_norm_rope_backward(NormRopeBackwardArgs<T> a, int d, float* partial, int sms,
+                                      float* dwq, float* dwk, cudaStream_t st);
+
+// ---- paged key-value cache ------------------------------------------------------------------
+// [pages][Hkv][page_size][d]; page_size = 1 << page_log2; sequence s's token p lives in page
+// table[s * width + p / page_size].
+constexpr int kMaxPageSize = 1 << 20;
+struct PagedLayout {
+  const int32_t* table;     // [S][width]
+  const int32_t* lengths;   // [S] tokens of each sequence, the new ones included
+  int S, width, num_pages, page_log2;
+};
+template <typename T>
+struct CacheAppendArgs {
+  const T *q, *k, *v;       // new tokens' rows; q may be null (q_heads = 0)
+  T *q_out, *k_cache, *v_cache;
+  const float *q_w, *k_w;
+  const double* inv_freq;
+  const int32_t* seq_start; // [S + 1], null: token t is sequence t's only new one
+  long long q_t, q_h, k_t, k_h, v_t, v_h, qo_t, qo_h;
+  PagedLayout paged;
+  int tokens, q_heads, kv_heads, rot, interleaved;
+  float eps;
+  int run;                  // set by the launcher
+  int* status;
+};
+template <typename T>
+cudaError_t launch_cache_append(CacheAppendArgs<T> a, int d, int sms, cudaStream_t st);
+
+template <typename T>
+struct PagedAttnArgs {
+  const T *q, *k_cache, *v_cache;
+  T* out;                   // [S][Hq][d]
+  float* lse;               // [S][Hq] or null
+  const float* slopes;      // [Hq] or null
+  long long q_s, q_h;
+  PagedLayout paged;
+  int Hkv, G;               // G = query heads per key head
+  float scale, softcap;
+  int window;               // 0: all keys
+  // set by the launcher
+  int row_blocks;
+  int* meta;
+  float *part_ml, *part_o;
+  int* status;
+};
+size_t paged_attn_ws_bytes(int d, int Hkv, int G, int S, int width, int page_log2, int is_f32,
+                           int sms);
+template <typename T>
+cudaError_t launch_paged_attn(PagedAttnArgs<T> a, int d, void* ws, int sms, cudaStream_t st);
+
 int num_sms_of_current_device();
 
 // Records one kernel launch by this library (process-wide counter behind

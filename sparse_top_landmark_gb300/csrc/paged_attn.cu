@@ -1,0 +1,820 @@
+// Attention of one new token per sequence over a paged key-value cache.
+//
+//   z_j = cap(scale * q . k_j) + slope * (j - (len - 1)),   cap(x) = softcap * tanh(x / softcap)
+//   out = sum_j e^{z_j} v_j / sum_j e^{z_j}   over the keys j < len (the last `window` of them)
+//
+// One pass over keys and values with a running maximum and sum.  The G query heads of a key
+// head read it together: they are the rows of the score tile.  Bound by HBM: 4 G D flops
+// on 4 D bytes (bf16) for each key, far below the tensor cores' rate for any G this takes.
+//
+// Work is dealt out on the device, since lengths live there (a replayed graph sees new ones):
+// every (sequence, key head, block of query rows) is a segment of tiles of kTile keys, the
+// segments stand in one row, and each CTA takes an equal share of that row of tiles, whatever
+// the lengths are.  A CTA finishes the segments that lie wholly in its share; of a
+// segment that is cut it leaves a partial (maximum, sum, weighted values) in its first or
+// its last slot of the workspace, and paged_join_kernel joins those of a segment in
+// their order.  Nothing is added atomically: the result depends on the inputs alone.
+//
+// A warp works on its own 16 keys of each tile through its own ring of shared-memory stages,
+// filled by 16-byte asynchronous copies some stages ahead, across the ends of segments; warps
+// meet only where a segment ends.  Rows that are not to be seen (beyond the length, before the
+// window, on an invalid page) are filled with zeros and never read: what the cache holds there,
+// NaN included, reaches nothing.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace mita {
+namespace {
+
+constexpr int kWarpKeys = 16;          // keys of a warp in a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kNoSegment = -1;
+constexpr int kMaxPagedCtas = 512;     // CTAs of a call: parts of a segment that can be joined
+
+// Shared memory and shape of one instantiation.  RT: query rows of a CTA.
+template <typename T, int D, int RT>
+struct Shape {
+  static constexpr bool kTensor = std::is_same<T, bf16>::value;
+  static constexpr int kWarps = kTensor ? 8 : 4;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kTile = kWarps * kWarpKeys;
+  static constexpr int kRowBytes = D * (int)sizeof(T);
+  static constexpr int kChunks = kRowBytes / 16;               // 16-byte chunks of a row
+  static constexpr int kStageBytes = 2 * kWarpKeys * kRowBytes;  // K then V
+  static constexpr int kStages = kStageBytes * kWarps * 8 <= 196608 ? 8 : 196608 / (kStageBytes * kWarps);
+  static constexpr int kRing = kStages * kStageBytes;          // of one warp
+  static constexpr int kJoinFloats = 5120;                     // outputs being joined over warps
+  // byte offsets
+  static constexpr int kOffJoin = kWarps * kRing;
+  static constexpr int kOffMl = kOffJoin + kJoinFloats * 4;               // [warps][RT][2]
+  static constexpr int kOffTop = kOffMl + kWarps * RT * 8;                // [2][RT]
+  static constexpr int kOffMask = kOffTop + RT * 8;                       // [warps][stages]
+  static constexpr int kOffQ = kOffMask + ((kWarps * kStages * 4 + 15) / 16) * 16;
+  static constexpr int kOffP = kOffQ + (kTensor ? 0 : RT * D * 4);        // fp32: q rows
+  static constexpr int kBytes = kOffP + (kTensor ? 0 : kWarps * RT * kWarpKeys * 4);
+  static_assert(kBytes <= 232448 && kStages >= 3, "shared memory");
+};
+
+// Chunk c of row r lies at chunk c ^ f(r) of it, so that eight rows' equal chunks lie in
+// eight different groups of banks.
+template <int kRowBytes>
+__device__ __forceinline__ int swizzle(int r, int c) {
+  if constexpr (kRowBytes >= 128) return c ^ (r & 7);
+  else if constexpr (kRowBytes == 64) return c ^ ((r >> 1) & 3);
+  else return c ^ ((r >> 2) & 1);
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+// 16 bytes, or zeros where `valid` is not set (src is then not read)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 products summed in fp32
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------------------
+// The row of tiles
+// ---------------------------------------------------------------------------
+// A sequence's seen keys [first, len), in tiles that start at multiples of `tile`.
+struct Span {
+  int first, len, base, tiles;
+};
+__device__ __forceinline__ Span span_of(const PagedLayout& pg, int window, int tile, int s) {
+  Span r;
+  const long long room = (long long)pg.width << pg.page_log2;
+  r.len = (int)min((long long)max(pg.lengths[s], 0), room);
+  r.first = window > 0 ? max(r.len - window, 0) : 0;
+  r.base = r.first / tile * tile;
+  r.tiles = (r.len - r.base + tile - 1) / tile;
+  return r;
+}
+
+// A place in the row of tiles: tile `t` of segment (s, hr), hr = key head * row blocks + block.
+struct Cursor {
+  int s, hr, t;
+  Span span;
+};
+
+__device__ __forceinline__ void advance(Cursor& c, const PagedLayout& pg, int window, int tile,
+                                        int HR) {
+  if (++c.t < c.span.tiles) return;
+  c.t = 0;
+  if (++c.hr < HR) return;
+  c.hr = 0;
+  do {
+    if (++c.s >= pg.S) return;      // behind the last segment: not used any more
+    c.span = span_of(pg, window, tile, c.s);
+  } while (c.span.tiles == 0);
+}
+
+__device__ __forceinline__ long long warp_incl_scan64(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// This CTA's share [u0, u1) of the row of tiles, and where u0 lies.  Each warp finds it for itself.
+__device__ __forceinline__ void my_share(const PagedLayout& pg, int window, int tile, int HR,
+                                         long long* u0, long long* u1, long long* all,
+                                         Cursor* at) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0;
+  for (int s0 = 0; s0 < pg.S; s0 += 32) {
+    const int s = s0 + lane;
+    total += s < pg.S ? span_of(pg, window, tile, s).tiles : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= HR;
+  *all = total;
+  const long long n = gridDim.x, c = blockIdx.x;
+  const long long q = total / n, r = total % n;
+  *u0 = q * c + min(c, r);
+  *u1 = *u0 + q + (c < r ? 1 : 0);
+  if (*u0 >= *u1) return;
+  long long run = 0;
+  for (int s0 = 0; s0 < pg.S; s0 += 32) {
+    const int s = s0 + lane;
+    const long long mine = s < pg.S ? (long long)span_of(pg, window, tile, s).tiles * HR : 0;
+    const long long incl = run + warp_incl_scan64(mine);
+    const unsigned hit = __ballot_sync(0xffffffffu, *u0 < incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const long long before = __shfl_sync(0xffffffffu, incl - mine, src);
+      at->s = s0 + src;
+      at->span = span_of(pg, window, tile, at->s);
+      const long long in = *u0 - before;
+      at->hr = (int)(in / at->span.tiles);
+      at->t = (int)(in % at->span.tiles);
+      return;
+    }
+    run = __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// What a tile's scores need besides q and k.
+struct ScoreRule {
+  float scale2;          // scale * log2(e): the scores of the running softmax are in log2 units
+  float cap, cap2, rcap; // softcap (0: none), softcap * log2(e), scale / softcap
+  int last;              // len - 1
+};
+__device__ __forceinline__ float score_of(const ScoreRule& r, float dot, float slope2, int key) {
+  float z = dot * r.scale2;
+  if (r.cap > 0.f) z = r.cap2 * tanhf(dot * r.rcap);
+  return z + slope2 * (float)(key - r.last);
+}
+
+// ---------------------------------------------------------------------------
+// One warp's running softmax, bf16 on the tensor cores.  A lane has rows lane / 4 and + 8 of
+// the 16 query rows, and columns (lane % 4) * 2, + 1 of every eight keys or values.
+// Rows behind the last query head hold zeros and are computed with the others: the matrix
+// instruction has 16 rows whether they are used or not.
+// ---------------------------------------------------------------------------
+template <int D>
+struct TensorState {
+  using S = Shape<bf16, D, 16>;
+  uint32_t q[D / 16][4];
+  float o[D / 8][4];
+  float m[2], l[2];      // l: of this lane's columns
+  float slope2[2];
+
+  __device__ __forceinline__ void start(const PagedAttnArgs<bf16>& a, int s, int head, int rows,
+                                        uint8_t*) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane / 4 + 8 * i;
+      const bool ok = r < rows;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + s * a.q_s +
+                                                            (long long)(head + r) * a.q_h);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][i] = ok ? p[k * 8 + lane % 4] : 0u;
+        q[k][i + 2] = ok ? p[k * 8 + 4 + lane % 4] : 0u;
+      }
+      slope2[i] = ok && a.slopes ? a.slopes[head + r] * kLog2e : 0.f;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+  }
+
+  // kt, vt: the warp's 16 key and value rows; key0 the first one's position; `mask` the seen ones
+  __device__ __forceinline__ void tile(const ScoreRule& rule, uint32_t kt, uint32_t vt, int key0,
+                                       unsigned mask) {
+    const int lane = threadIdx.x & 31;
+    float z[2][4] = {};
+    {
+      const int row = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldsm4(kt + row * S::kRowBytes + swizzle<S::kRowBytes>(row, 2 * k + c) * 16, b);
+        mma16816(z[0], q[k], b[0], b[1]);
+        mma16816(z[1], q[k], b[2], b[3]);
+      }
+    }
+    float top[2] = {m[0], m[1]};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = 8 * t + (lane % 4) * 2 + (i & 1);
+        z[t][i] = (mask >> j) & 1 ? score_of(rule, z[t][i], slope2[i >> 1], key0 + j) : -INFINITY;
+        top[i >> 1] = fmaxf(top[i >> 1], z[t][i]);
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+    }
+    float base[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) base[i] = top[i] == -INFINITY ? 0.f : top[i];
+    // the running values move to the new maxima; most tiles bring none
+    if (__any_sync(0xffffffffu, top[0] != m[0] || top[1] != m[1])) {
+      float f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[i] = exp2_fast(m[i] - base[i]);
+        l[i] *= f[i];
+        m[i] = top[i];
+      }
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        o[j][0] *= f[0];
+        o[j][1] *= f[0];
+        o[j][2] *= f[1];
+        o[j][3] *= f[1];
+      }
+    }
+    // The weights go to the value product as a sum of two bf16 values, 16 bits in all: one alone
+    // would add an error of the size of the output's own rounding, and the second product
+    // is free where HBM is the bound.
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float p0 = exp2_fast(z[t][2 * i] - base[i]), p1 = exp2_fast(z[t][2 * i + 1] - base[i]);
+        l[i] += p0 + p1;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+        hi[2 * t + i] = *reinterpret_cast<const uint32_t*>(&h);
+        const __nv_bfloat162 e = __floats2bfloat162_rn(
+            p0 - __uint_as_float(hi[2 * t + i] << 16),
+            p1 - __uint_as_float(hi[2 * t + i] & 0xffff0000u));
+        lo[2 * t + i] = *reinterpret_cast<const uint32_t*>(&e);
+      }
+    {
+      const int row = lane & 15, c = lane >> 4;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t b[4];
+        ldsm4_t(vt + row * S::kRowBytes + swizzle<S::kRowBytes>(row, 2 * j + c) * 16, b);
+        mma16816(o[2 * j], hi, b[0], b[1]);
+        mma16816(o[2 * j + 1], hi, b[2], b[3]);
+        mma16816(o[2 * j], lo, b[0], b[1]);
+        mma16816(o[2 * j + 1], lo, b[2], b[3]);
+      }
+    }
+  }
+
+  // this warp's (maximum, sum) of every row
+  __device__ __forceinline__ void put_ml(float2* ml) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (lane % 4 == 0) ml[lane / 4 + 8 * i] = make_float2(m[i], l[i]);
+    }
+  }
+  // columns [c0, c0 + C) of the rows below `rows`, moved to the maxima `top`, to dst[row][..]
+  __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
+                                        const float* top) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane / 4 + 8 * i;
+      if (r >= rows) continue;
+      const float f = exp2_fast(m[i] - top[r]);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+        if (8 * j >= c0 && 8 * j < c0 + C)
+          *reinterpret_cast<float2*>(dst + r * stride + 8 * j - c0 + (lane % 4) * 2) =
+              make_float2(o[j][2 * i] * f, o[j][2 * i + 1] * f);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// One warp's running softmax, fp32 on the FMA units: a tensor-core product of fp32 values would
+// round them.  For the scores a lane has one key and half of the columns; for the
+// values D / 32 columns (one, in the lower half of the warp, for D = 16).
+// ---------------------------------------------------------------------------
+template <int D, int RT>
+struct FmaState {
+  using S = Shape<float, D, RT>;
+  static constexpr int V = D >= 32 ? D / 32 : 1;
+  float o[RT][V];
+  float m[RT], l[RT];    // l: of this lane's key, in the lower half of the warp
+
+  __device__ __forceinline__ void start(const PagedAttnArgs<float>& a, int s, int head, int rows,
+                                        uint8_t* smem) {
+    float* q = reinterpret_cast<float*>(smem + S::kOffQ);
+    for (int e = threadIdx.x; e < rows * D; e += S::kThreads)
+      q[e] = a.q[s * a.q_s + (long long)(head + e / D) * a.q_h + e % D];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[r][v] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void tile(const ScoreRule& rule, const uint8_t* stage, int key0,
+                                       unsigned mask, int rows, uint8_t* smem, const float* slopes,
+                                       int head) {
+    const int lane = threadIdx.x & 31, key = lane & 15, half = lane >> 4;
+    const float* q = reinterpret_cast<const float*>(smem + S::kOffQ);
+    float* p = reinterpret_cast<float*>(smem + S::kOffP) + (threadIdx.x >> 5) * RT * kWarpKeys;
+    float z[RT] = {};
+#pragma unroll 2
+    for (int c = 0; c < D / 8; ++c) {
+      const int ch = half * (D / 8) + c;
+      const float4 k = *reinterpret_cast<const float4*>(
+          stage + key * S::kRowBytes + swizzle<S::kRowBytes>(key, ch) * 16);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        if (r < rows) {
+          const float4 x = *reinterpret_cast<const float4*>(q + r * D + ch * 4);
+          z[r] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, fmaf(x.w, k.w, z[r]))));
+        }
+    }
+    const bool seen = (mask >> key) & 1;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      if (r < rows) {
+        z[r] += __shfl_xor_sync(0xffffffffu, z[r], 16);
+        z[r] = seen ? score_of(rule, z[r], slopes ? slopes[head + r] * kLog2e : 0.f, key0 + key)
+                    : -INFINITY;
+        float top = z[r];
+#pragma unroll
+        for (int i = 8; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        top = fmaxf(top, m[r]);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float f = exp2_fast(m[r] - base);
+        const float w = exp2_fast(z[r] - base);
+        m[r] = top;
+        l[r] = fmaf(l[r], f, half ? 0.f : w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[r][v] *= f;
+        if (half == 0) p[r * kWarpKeys + key] = w;
+      }
+    __syncwarp();
+    if (lane * V < D) {
+      const uint8_t* vs = stage + kWarpKeys * S::kRowBytes;
+      const int ch = lane * V / 4, in = lane * V % 4 * 4;
+#pragma unroll
+      for (int k4 = 0; k4 < kWarpKeys / 4; ++k4) {
+        float x[4][V];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = 4 * k4 + k;
+          const float* src = reinterpret_cast<const float*>(
+              vs + row * S::kRowBytes + swizzle<S::kRowBytes>(row, ch) * 16 + in);
+          if constexpr (V == 4) {
+            const float4 t = *reinterpret_cast<const float4*>(src);
+            x[k][0] = t.x; x[k][1] = t.y; x[k][2] = t.z; x[k][3] = t.w;
+          } else if constexpr (V == 2) {
+            const float2 t = *reinterpret_cast<const float2*>(src);
+            x[k][0] = t.x; x[k][1] = t.y;
+          } else {
+            x[k][0] = *src;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          if (r < rows) {
+            const float4 w = *reinterpret_cast<const float4*>(p + r * kWarpKeys + 4 * k4);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+              o[r][v] = fmaf(w.x, x[0][v], fmaf(w.y, x[1][v], fmaf(w.z, x[2][v],
+                        fmaf(w.w, x[3][v], o[r][v]))));
+          }
+      }
+    }
+    __syncwarp();          // p is written again by the next tile
+  }
+
+  __device__ __forceinline__ void put_ml(float2* ml) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const float sum = warp_sum(l[r]);
+      if ((threadIdx.x & 31) == 0) ml[r] = make_float2(m[r], sum);
+    }
+  }
+  __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
+                                        const float* top) {
+    const int col = (threadIdx.x & 31) * V;
+    if (col >= D || col < c0 || col >= c0 + C) return;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      if (r < rows) {
+        const float f = exp2_fast(m[r] - top[r]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) dst[r * stride + col - c0 + v] = o[r][v] * f;
+      }
+  }
+};
+
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return __float2bfloat16_rn(x); }
+
+// ---------------------------------------------------------------------------
+// The warp's loader: page numbers one tile ahead of the copies, copies kStages - 1 tiles
+// ahead of the arithmetic.
+// ---------------------------------------------------------------------------
+template <typename T, int D, int RT>
+struct Loader {
+  using S = Shape<T, D, RT>;
+  Cursor at;
+  long long left;        // tiles not looked up yet
+  int page, key, head;   // of the tile looked up last: this lane's key
+  bool ok;
+
+  __device__ __forceinline__ void look_up(const PagedAttnArgs<T>& a, int HR) {
+    ok = false;
+    if (left <= 0) return;
+    --left;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    key = at.span.base + at.t * S::kTile + warp * kWarpKeys + (lane & 15);
+    ok = key >= at.span.first && key < at.span.len;
+    head = at.hr / a.row_blocks;
+    if (ok) page = __ldg(a.paged.table + (long long)at.s * a.paged.width +
+                         (key >> a.paged.page_log2));
+    advance(at, a.paged, a.window, S::kTile, HR);
+  }
+
+  // copies the looked-up tile's rows to `stage`, notes which of them are seen, and commits
+  __device__ __forceinline__ void issue(const PagedAttnArgs<T>& a, uint8_t* stage,
+                                        unsigned* mask_out) {
+    const int lane = threadIdx.x & 31;
+    if (ok && (page < 0 || page >= a.paged.num_pages)) {
+      flag_error(a.status, kDevErrBadIndex);
+      ok = false;
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+    if (lane == 0) *mask_out = mask;
+    if (mask) {
+      constexpr int kPerPass = 32 / S::kChunks;      // rows a warp copies at once
+      const int c = lane % S::kChunks;
+      const int in_page = (1 << a.paged.page_log2) - 1;
+#pragma unroll
+      for (int i = 0; i < kWarpKeys / kPerPass; ++i) {
+        const int row = i * kPerPass + lane / S::kChunks;
+        const int pg = __shfl_sync(0xffffffffu, page, row);
+        const int ky = __shfl_sync(0xffffffffu, key, row);
+        const bool live = (mask >> row) & 1;
+        const long long at_row = (((long long)pg * a.Hkv + head) << a.paged.page_log2) +
+                                 (ky & in_page);
+        const long long off = live ? at_row * D + c * (16 / (int)sizeof(T)) : 0;
+        const uint32_t dst = smem_addr(stage) + row * S::kRowBytes +
+                             swizzle<S::kRowBytes>(row, c) * 16;
+        copy16(dst, a.k_cache + off, live);
+        copy16(dst + kWarpKeys * S::kRowBytes, a.v_cache + off, live);
+      }
+    }
+    copy_commit();
+  }
+};
+
+// The index of the CTA whose share holds tile u of `total` dealt to n CTAs.
+__device__ __forceinline__ int owner_of(long long u, long long total, long long n) {
+  const long long q = total / n, r = total % n;
+  return (int)(u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q);
+}
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(Shape<T, D, RT>::kThreads, 1)
+paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
+  using S = Shape<T, D, RT>;
+  using State = typename std::conditional<S::kTensor, TensorState<D>, FmaState<D, RT>>::type;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
+  uint8_t* ring = smem + warp * S::kRing;
+  float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
+  float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
+  unsigned* masks = reinterpret_cast<unsigned*>(smem + S::kOffMask) + warp * S::kStages;
+
+  griddep_wait();
+  // sequences without a key: zeros, and the logarithm of an empty sum
+  for (int s = blockIdx.x; s < a.paged.S; s += gridDim.x) {
+    const int len = a.paged.lengths[s];
+    if (threadIdx.x == 0 && (len < 0 || len > (long long)a.paged.width << a.paged.page_log2))
+      flag_error(a.status, kDevErrBadIndex);
+    if (len > 0 && a.paged.width > 0) continue;
+    for (int e = threadIdx.x; e < Hq * D; e += S::kThreads)
+      a.out[(long long)s * Hq * D + e] = from_f<T>(0.f);
+    if (a.lse)
+      for (int e = threadIdx.x; e < Hq; e += S::kThreads) a.lse[(long long)s * Hq + e] = -INFINITY;
+  }
+
+  long long u0, u1, total;
+  Cursor at;
+  my_share(a.paged, a.window, S::kTile, HR, &u0, &u1, &total, &at);
+  int last_seg = kNoSegment, last_cta = 0;    // the segment this CTA begins and another one ends
+  if (u0 < u1) {
+    Loader<T, D, RT> ld;
+    ld.at = at;
+    ld.left = u1 - u0;
+    ld.page = ld.key = ld.head = 0;
+    ld.look_up(a, HR);
+#pragma unroll 1
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      ld.issue(a, ring + i * S::kStageBytes, masks + i);
+      ld.look_up(a, HR);
+    }
+    State st;
+    ScoreRule rule;
+    rule.scale2 = a.scale * kLog2e;
+    rule.cap = a.softcap;
+    rule.cap2 = a.softcap * kLog2e;
+    rule.rcap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+    int slot = 0, next = S::kStages - 1;     // stages: of this tile, of the next one to issue
+    int from = at.t, head = 0, rows = 0;
+    bool begin = true;
+    for (long long u = u0; u < u1; ++u) {
+      if (begin) {
+        const int rb = at.hr % a.row_blocks;
+        head = at.hr / a.row_blocks * a.G + rb * RT;
+        rows = min(RT, a.G - rb * RT);
+        rule.last = at.span.len - 1;
+        from = at.t;
+        st.start(a, at.s, head, rows, smem);
+        begin = false;
+      }
+      copy_wait<S::kStages - 2>();
+      __syncwarp();
+      ld.issue(a, ring + next * S::kStageBytes, masks + next);
+      ld.look_up(a, HR);
+      const unsigned mask = masks[slot];
+      if (mask) {
+        uint8_t* stage = ring + slot * S::kStageBytes;
+        const int key0 = at.span.base + at.t * S::kTile + warp * kWarpKeys;
+        if constexpr (S::kTensor)
+          st.tile(rule, smem_addr(stage), smem_addr(stage) + kWarpKeys * S::kRowBytes, key0, mask);
+        else
+          st.tile(rule, stage, key0, mask, rows, smem, a.slopes, head);
+      }
+      slot = slot + 1 == S::kStages ? 0 : slot + 1;
+      next = next + 1 == S::kStages ? 0 : next + 1;
+
+      const bool ends = at.t + 1 == at.span.tiles;
+      if (ends || u + 1 == u1) {
+        // join the warps' parts
+        st.put_ml(ml + warp * RT);
+        __syncthreads();
+        float* top = reinterpret_cast<float*>(smem + S::kOffTop);
+        if (threadIdx.x < RT) {
+          float t = -INFINITY, sum = 0.f;
+          for (int w = 0; w < S::kWarps; ++w) t = fmaxf(t, ml[w * RT + threadIdx.x].x);
+          const float base = t == -INFINITY ? 0.f : t;
+          for (int w = 0; w < S::kWarps; ++w) {
+            const float2 x = ml[w * RT + threadIdx.x];
+            sum = fmaf(x.y, exp2_fast(x.x - base), sum);
+          }
+          top[threadIdx.x] = base;
+          top[RT + threadIdx.x] = sum;
+        }
+        __syncthreads();
+        const int seg = at.s * HR + at.hr;
+        const bool whole = ends && from == 0;
+        const int part = blockIdx.x * 2 + (from == 0 ? 1 : 0);
+        if (!whole && from == 0) {
+          last_seg = seg;
+          last_cta = owner_of(u - at.t + at.span.tiles - 1, total, gridDim.x);
+        }
+        if (threadIdx.x < rows) {
+          const float base = top[threadIdx.x], sum = top[RT + threadIdx.x];
+          if (!whole) {
+            a.part_ml[((long long)part * RT + threadIdx.x) * 2] = base;
+            a.part_ml[((long long)part * RT + threadIdx.x) * 2 + 1] = sum;
+          } else if (a.lse) {
+            a.lse[(long long)at.s * Hq + head + threadIdx.x] =
+                sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+          }
+        }
+        // columns at a time: all warps' sums of C columns fit the joining area (rows padded by 8
+        // floats against bank conflicts)
+        const int C = min(D, (S::kJoinFloats / (S::kWarps * rows) - 8) & ~7);
+        const int stride = C + 8;
+        for (int c0 = 0; c0 < D; c0 += C) {
+          st.put_o(join + warp * rows * stride, stride, c0, C, rows, top);
+          __syncthreads();
+          const int cols = min(C, D - c0);
+          for (int e = threadIdx.x; e < rows * cols; e += S::kThreads) {
+            const int r = e / cols, c = e % cols;
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) x += join[(w * rows + r) * stride + c];
+            if (whole) {
+              const float sum = top[RT + r];
+              a.out[((long long)at.s * Hq + head + r) * D + c0 + c] =
+                  from_f<T>(sum == 0.f ? 0.f : x / sum);
+            } else {
+              a.part_o[((long long)part * RT + r) * D + c0 + c] = x;
+            }
+          }
+          __syncthreads();
+        }
+        begin = true;
+      }
+      advance(at, a.paged, a.window, S::kTile, HR);
+    }
+    copy_wait<0>();
+  }
+  if (threadIdx.x == 0) {
+    a.meta[blockIdx.x * 2] = last_seg;
+    a.meta[blockIdx.x * 2 + 1] = last_cta;
+  }
+}
+
+// Joins the partials of a segment that was cut: its beginning is CTA c's last part, its rest
+// the first parts of CTAs c + 1 .. last.  Block (c, row), one column a thread.
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(128)
+paged_join_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
+  __shared__ float weight[kMaxPagedCtas];
+  __shared__ float red[5];
+  griddep_wait();
+  const int c = blockIdx.x, r = blockIdx.y;
+  const int seg = a.meta[c * 2];
+  if (seg == kNoSegment) return;
+  const int n = a.meta[c * 2 + 1] - c + 1;
+  const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
+  const int s = seg / HR, hr = seg % HR, rb = hr % a.row_blocks;
+  if (r >= min(RT, a.G - rb * RT)) return;
+  auto part_of = [&](int i) { return (long long)(i == 0 ? c * 2 + 1 : (c + i) * 2) * RT + r; };
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const float2 x = reinterpret_cast<const float2*>(a.part_ml)[part_of(i)];
+    if (x.y != 0.f) top = fmaxf(top, x.x);      // a part without a key has no maximum
+  }
+  top = block_max(top, red);
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const float2 x = reinterpret_cast<const float2*>(a.part_ml)[part_of(i)];
+    weight[i] = x.y != 0.f ? exp2_fast(x.x - base) : 0.f;
+    sum = fmaf(x.y, weight[i], sum);
+  }
+  sum = block_sum(sum, red);
+  __syncthreads();
+  const int head = hr / a.row_blocks * a.G + rb * RT + r;
+  if (a.lse && threadIdx.x == 0)
+    a.lse[(long long)s * Hq + head] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+  if (threadIdx.x < D) {
+    float x = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) x = fmaf(weight[i], a.part_o[part_of(i) * D + threadIdx.x], x);
+    a.out[((long long)s * Hq + head) * D + threadIdx.x] = from_f<T>(sum == 0.f ? 0.f : x / sum);
+  }
+}
+
+// CTAs for this call: one on each SM, but no more than there can be tiles.
+template <typename T, int D, int RT>
+int grid_of(int S, int width, int page_log2, int HR, int sms) {
+  using Sh = Shape<T, D, RT>;
+  const long long keys = (long long)width << page_log2;
+  const long long tiles = (keys + Sh::kTile - 1) / Sh::kTile * HR * (long long)S;
+  return (int)std::max<long long>(1, std::min<long long>({(long long)sms, tiles, kMaxPagedCtas}));
+}
+
+struct Carve {
+  size_t meta, ml, o, total;
+};
+Carve carve(int ctas, int RT, int D) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  Carve c{};
+  c.meta = 0;
+  c.ml = up((size_t)ctas * 2 * sizeof(int));
+  c.o = c.ml + up((size_t)ctas * 2 * RT * 2 * sizeof(float));
+  c.total = c.o + up((size_t)ctas * 2 * RT * D * sizeof(float));
+  return c;
+}
+
+template <typename T, int D, int RT>
+struct Run {
+  static size_t bytes(int Hkv, int G, int S, int width, int page_log2, int sms) {
+    const int HR = Hkv * ((G + RT - 1) / RT);
+    return carve(grid_of<T, D, RT>(S, width, page_log2, HR, sms), RT, D).total;
+  }
+  static cudaError_t launch(PagedAttnArgs<T> a, void* ws, int sms, cudaStream_t st) {
+    using Sh = Shape<T, D, RT>;
+    a.row_blocks = (a.G + RT - 1) / RT;
+    const int grid = grid_of<T, D, RT>(a.paged.S, a.paged.width, a.paged.page_log2,
+                                       a.Hkv * a.row_blocks, sms);
+    const Carve c = carve(grid, RT, D);
+    a.meta = reinterpret_cast<int*>(static_cast<char*>(ws) + c.meta);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + c.ml);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + c.o);
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, RT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    e = launch_pdl(paged_attn_kernel<T, D, RT>, dim3(grid), dim3(Sh::kThreads), Sh::kBytes, st, a);
+    if (e != cudaSuccess || grid == 1) return e;      // one CTA cuts no segment
+    count_launch();
+    return launch_pdl(paged_join_kernel<T, D, RT>, dim3(grid, std::min(a.G, RT)), dim3(128), 0, st,
+                      a);
+  }
+};
+
+// The instantiation for a head dim, type and group: bf16 takes 16 query rows to a CTA (the
+// matrix instruction's height), fp32 four where the group has no more.
+template <typename T, typename F>
+auto with_shape(int d, int G, F f) {
+  constexpr bool tensor = std::is_same<T, bf16>::value;
+  if constexpr (!tensor) {
+    if (G <= 4) {
+      switch (d) {
+        case 16: return f(Run<T, 16, 4>{});
+        case 32: return f(Run<T, 32, 4>{});
+        case 64: return f(Run<T, 64, 4>{});
+        default: return f(Run<T, 128, 4>{});
+      }
+    }
+  }
+  switch (d) {
+    case 16: return f(Run<T, 16, 16>{});
+    case 32: return f(Run<T, 32, 16>{});
+    case 64: return f(Run<T, 64, 16>{});
+    default: return f(Run<T, 128, 16>{});
+  }
+}
+
+}  // namespace
+
+size_t paged_attn_ws_bytes(int d, int Hkv, int G, int S, int width, int page_log2, int is_f32,
+                           int sms) {
+  auto bytes = [&](auto run) { return run.bytes(Hkv, G, S, width, page_log2, sms); };
+  return is_f32 ? with_shape<float>(d, G, bytes) : with_shape<bf16>(d, G, bytes);
+}
+
+template <typename T>
+cudaError_t launch_paged_attn(PagedAttnArgs<T> a, int d, void* ws, int sms, cudaStream_t st) {
+  return with_shape<T>(d, a.G, [&](auto run) { return run.launch(a, ws, sms, st); });
+}
+
+template cudaError_t launch_paged_attn<float>(PagedAttnArgs<float>, int, void*, int, cudaStream_t);
+template cudaError_t launch_paged_attn<bf16>(PagedAttnArgs<bf16>, int, void*, int, cudaStream_t);
+
+}  // namespace mita
