@@ -319,75 +319,77 @@ int mita_forward_host_f32(const float* q, const float* k, const float* v, int B,
                           mita_stream_t stream);
 
 /*
+ * The entry points below take their arguments in a struct: pointers, then element strides, then
+ * sizes.  The struct and what it says is read before the call returns.  Strided tensors have
+ * contiguous rows of d elements, each starting on a 16-byte boundary; the other dimensions may
+ * have any non-negative strides (that of a dimension of size 1 is not looked at), so q, k and v
+ * may be views of one projection's output.
+ *
  * mita_qk_norm_rope -- queries and keys on their way into attention: RMS norm of every head
  * row, then rotation by position, in one pass.  The pages start from given q and k; this is the
  * step language models put between the projections and attention.
  *   u = w * x / sqrt(mean(x^2) + eps)   (no weight: u = x)
  *   y = u with pair i of its first `rot` values turned by the angle position * inv_freq[i]
- * Sums, norms and angles' products are fp32 or better; the angle keeps its accuracy at any
- * 32-bit position (the product is taken modulo one turn in 64 bits).
- *   q [B,Hq,N,d], k [B,Hkv,N,d]    inputs, strided (below); Hkv = 0: no k.
- *   q_weight, k_weight [d] float    norm weights, 16-byte aligned, or NULL (not normalised).
- *   positions      int32 [B,N], row b at positions + b * positions_stride (0: shared by the
- *                  batch); NULL: 0 .. N-1.
- *   inv_freq       [rot/2] double, radians per position, finite; not read for rot = 0.
- *   rot            a multiple of 8 in [0, d]; values rot .. d-1 are not turned.
- *   interleaved    0: pairs (i, i + rot/2); else pairs (2i, 2i + 1).
- *   q_strides, ..  host arrays of 3: elements between batches, heads and tokens; NULL: dense
- *                  [B,H,N,d].  Rows of d elements are contiguous and start on 16-byte boundaries.
- *                  So q and k may be views of one projection's [B,N,Hq+2Hkv,d] output.
- *   q_out [B,Hq,N,d], k_out [B,Hkv,N,d]  outputs, rounded once.  An output may be its own input
- *                  (same address and strides); other overlaps are undefined.
+ * Sums and norms are fp32; the angle keeps its accuracy at any 32-bit position (the product is
+ * taken modulo one turn in 64 bits).
+ *   q [B,Hq,N,d], k [B,Hkv,N,d]     inputs; Hkv = 0: no k.
+ *   q_weight, k_weight [d] float     norm weights, 16-byte aligned, or NULL (not normalised).
+ *   positions       int32 [B,N], row b at positions + b * positions_stride (0: shared by the
+ *                   batch); NULL: 0 .. N-1.
+ *   inv_freq        [rot/2] double, radians per position, finite; not read for rot = 0.
+ *   q_out [B,Hq,N,d], k_out [B,Hkv,N,d]   outputs, rounded once.  An output may be its own input
+ *                   (same address and strides); other overlaps are undefined.
+ *   *_strides       elements between batches, heads and tokens.
+ *   rot             a multiple of 8 in [0, d]; values rot .. d-1 are not turned.
+ *   interleaved     0: pairs (i, i + rot/2); else pairs (2i, 2i + 1).
  * B or N = 0 does nothing.  Needs no workspace.
  */
-int mita_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
-                      const int32_t* positions, int64_t positions_stride, const double* inv_freq,
-                      int B, int Hq, int Hkv, int N, int d, int rot, int interleaved, float eps,
-                      const int64_t* q_strides, const int64_t* k_strides,
-                      const int64_t* q_out_strides, const int64_t* k_out_strides, void* q_out,
-                      void* k_out, mita_stream_t stream);
-int mita_qk_norm_rope_f32(const float* q, const float* k, const float* q_weight,
-                          const float* k_weight, const int32_t* positions,
-                          int64_t positions_stride, const double* inv_freq, int B, int Hq, int Hkv,
-                          int N, int d, int rot, int interleaved, float eps,
-                          const int64_t* q_strides, const int64_t* k_strides,
-                          const int64_t* q_out_strides, const int64_t* k_out_strides, float* q_out,
-                          float* k_out, mita_stream_t stream);
+typedef struct mita_qk_norm_rope_params {
+  const void *q, *k;
+  const float *q_weight, *k_weight;
+  const int32_t* positions;
+  const double* inv_freq;
+  void *q_out, *k_out;
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3], positions_stride;
+  int32_t B, Hq, Hkv, N, d, rot, interleaved;
+  float eps;
+} mita_qk_norm_rope_params;
+int mita_qk_norm_rope(const mita_qk_norm_rope_params* params, mita_stream_t stream);
+int mita_qk_norm_rope_f32(const mita_qk_norm_rope_params* params, mita_stream_t stream);
 
 /*
  * mita_qk_norm_rope_backward -- gradients of mita_qk_norm_rope.
- *   q, k           the forward's inputs (not read, and may be NULL, where there is no weight).
- *   dq_out, dk_out [B,H,N,d], strided: the gradients of q_out and k_out.
- *   dq, dk         outputs like q and k, in the element type, strided; may be dq_out, dk_out.
+ *   q, k            the forward's inputs (not read, and may be NULL, where there is no weight).
+ *   dq_out, dk_out  [B,H,N,d]: the gradients of q_out and k_out.
+ *   dq, dk          outputs like q and k, in the element type; may be dq_out, dk_out.
  *   dq_weight, dk_weight [d] float  outputs, required with the weight and refused without it:
- *                  sums over every row, the query heads' of q_weight, the key heads' of k_weight.
- *   workspace      device, 16-byte aligned, of mita_qk_norm_rope_backward_workspace_bytes(d);
- *                  not used without weights.  It is the caller's, not the library's cache, so
- *                  that calls captured into different graphs can have their own.
+ *                   sums over every row, the query heads' of q_weight, the key heads' of k_weight.
+ *   workspace       device, 16-byte aligned, of mita_qk_norm_rope_backward_workspace_bytes(d);
+ *                   not used without weights.  It is the caller's, not the library's cache, so
+ *                   that calls captured into different graphs can have their own.
  * The weight gradients are added in a fixed order: the same inputs give the same bits.
  * B or N = 0 clears the weight gradients.  Other parameters as for mita_qk_norm_rope.
  */
-int mita_qk_norm_rope_backward(const void* q, const void* k, const void* dq_out,
-                               const void* dk_out, const float* q_weight, const float* k_weight,
-                               const int32_t* positions, int64_t positions_stride,
-                               const double* inv_freq, int B, int Hq, int Hkv, int N, int d,
-                               int rot, int interleaved, float eps, const int64_t* q_strides,
-                               const int64_t* k_strides, const int64_t* dq_out_strides,
-                               const int64_t* dk_out_strides, const int64_t* dq_strides,
-                               const int64_t* dk_strides, void* workspace,
-                               uint64_t workspace_bytes, void* dq, void* dk, float* dq_weight,
-                               float* dk_weight, mita_stream_t stream);
-int mita_qk_norm_rope_backward_f32(const float* q, const float* k, const float* dq_out,
-                                   const float* dk_out, const float* q_weight,
-                                   const float* k_weight, const int32_t* positions,
-                                   int64_t positions_stride, const double* inv_freq, int B, int Hq,
-                                   int Hkv, int N, int d, int rot, int interleaved, float eps,
-                                   const int64_t* q_strides, const int64_t* k_strides,
-                                   const int64_t* dq_out_strides, const int64_t* dk_out_strides,
-                                   const int64_t* dq_strides, const int64_t* dk_strides,
-                                   void* workspace, uint64_t workspace_bytes, float* dq, float* dk,
-                                   float* dq_weight, float* dk_weight, mita_stream_t stream);
-/* Bytes of workspace mita_qk_norm_rope_backward needs (0 if d is not supported). */
+typedef struct mita_qk_norm_rope_backward_params {
+  const void *q, *k, *dq_out, *dk_out;
+  const float *q_weight, *k_weight;
+  const int32_t* positions;
+  const double* inv_freq;
+  void *dq, *dk;
+  float *dq_weight, *dk_weight;
+  void* workspace;
+  uint64_t workspace_bytes;
+  int64_t q_strides[3], k_strides[3], dq_out_strides[3], dk_out_strides[3], dq_strides[3],
+      dk_strides[3], positions_stride;
+  int32_t B, Hq, Hkv, N, d, rot, interleaved;
+  float eps;
+} mita_qk_norm_rope_backward_params;
+int mita_qk_norm_rope_backward(const mita_qk_norm_rope_backward_params* params,
+                               mita_stream_t stream);
+int mita_qk_norm_rope_backward_f32(const mita_qk_norm_rope_backward_params* params,
+                                   mita_stream_t stream);
+/* Bytes of workspace mita_qk_norm_rope_backward needs on the current device (0 if d is not
+ * supported). */
 uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
 
 /*
@@ -396,7 +398,8 @@ uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
  *   page_table [S,table_width] int32: token p of sequence s lives in row p % page_size of page
  *   page_table[s][p / page_size].  Entries behind a sequence's last page are not read.
  *   lengths [S] int32: tokens of each sequence, the new ones included; 0 is an idle slot.
- * All of it is read on the device, so a captured call replays with new lengths and pages.
+ * All of it is read on the device, so a captured call replays with new lengths and pages; it
+ * must not change while the call runs.
  * An entry outside [0, num_pages) that is needed, or a length outside [0, table_width*page_size]
  * flags MITA_ERR_DEVICE_CHECK; such tokens are left out and never dereferenced (a length that is
  * too large is cut to the table by mita_paged_attn, and nothing of its sequence is
@@ -404,32 +407,28 @@ uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
  *
  * mita_cache_append -- the new tokens' keys, normalised and rotated as by mita_qk_norm_rope, and
  * values into the cache; their queries are normalised and rotated by the same launch.
- *   k, v [tokens,Hkv,d], q [tokens,Hq,d]  inputs, strided (host arrays of 2: elements between
- *                  tokens and heads; NULL: dense); Hq = 0: no queries.
- *   seq_start      [S+1] int32, ascending: rows seq_start[s] .. seq_start[s+1]-1 are sequence s's
- *                  new tokens, at its last positions (lengths[s] counts them).  Rows before
- *                  seq_start[0] and from seq_start[S] on belong to nobody: left out.
- *                  NULL: row s is sequence s's only new token (tokens = S).
- *   q_out [tokens,Hq,d]  output, strided; rows left out, and rows of idle slots, stay as they are.
+ *   k, v [tokens,Hkv,d], q [tokens,Hq,d]   inputs; Hq = 0: no queries.
+ *   seq_start       [S+1] int32, ascending: rows seq_start[s] .. seq_start[s+1]-1 are sequence
+ *                   s's new tokens, at its last positions (lengths[s] counts them).  Rows before
+ *                   seq_start[0] and from seq_start[S] on belong to nobody: left out.
+ *                   NULL: row s is sequence s's only new token (tokens = S).
+ *   q_out [tokens,Hq,d]  output; rows left out, and rows of idle slots, stay as they are.
+ *   *_strides       elements between tokens and heads.
  * The angle of a key or query is that of its position in the sequence.  Two tokens that the
  * table sends to one row of the cache leave either one's values there.
  */
-int mita_cache_append(const void* q, const void* k, const void* v, const float* q_weight,
-                      const float* k_weight, const double* inv_freq, const int32_t* page_table,
-                      const int32_t* lengths, const int32_t* seq_start, int tokens, int S, int Hq,
-                      int Hkv, int d, int num_pages, int page_size, int table_width, int rot,
-                      int interleaved, float eps, const int64_t* q_strides,
-                      const int64_t* k_strides, const int64_t* v_strides,
-                      const int64_t* q_out_strides, void* q_out, void* k_cache, void* v_cache,
-                      mita_stream_t stream);
-int mita_cache_append_f32(const float* q, const float* k, const float* v, const float* q_weight,
-                          const float* k_weight, const double* inv_freq,
-                          const int32_t* page_table, const int32_t* lengths,
-                          const int32_t* seq_start, int tokens, int S, int Hq, int Hkv, int d,
-                          int num_pages, int page_size, int table_width, int rot, int interleaved,
-                          float eps, const int64_t* q_strides, const int64_t* k_strides,
-                          const int64_t* v_strides, const int64_t* q_out_strides, float* q_out,
-                          float* k_cache, float* v_cache, mita_stream_t stream);
+typedef struct mita_cache_append_params {
+  const void *q, *k, *v;
+  const float *q_weight, *k_weight;
+  const double* inv_freq;
+  const int32_t *page_table, *lengths, *seq_start;
+  void *q_out, *k_cache, *v_cache;
+  int64_t q_strides[2], k_strides[2], v_strides[2], q_out_strides[2];
+  int32_t tokens, S, Hq, Hkv, d, num_pages, page_size, table_width, rot, interleaved;
+  float eps;
+} mita_cache_append_params;
+int mita_cache_append(const mita_cache_append_params* params, mita_stream_t stream);
+int mita_cache_append_f32(const mita_cache_append_params* params, mita_stream_t stream);
 
 /*
  * mita_paged_attn -- softmax attention of one new token per sequence over its cached keys: what
@@ -438,28 +437,30 @@ int mita_cache_append_f32(const float* q, const float* k, const float* v, const 
  *   alibi_slopes[head] * (j - (length - 1)) where given;  out = softmax(z) v over the keys
  *   j < length, with window > 0 the last `window` of them.  Query head h reads key head
  *   h / (Hq / Hkv).
- *   q [S,Hq,d]     input, strided as in mita_cache_append.
- *   alibi_slopes   [Hq] float or NULL.
- *   out [S,Hq,d]   output, dense, rounded once.  A sequence without a key (length 0, or all
- *                  pages invalid) gets zeros.
- *   lse [S,Hq] float or NULL  output: ln sum_j e^{z_j} (-inf without a key), for joining with
- *                  attention over other keys.
- *   workspace      device, 16-byte aligned, of mita_paged_attn_workspace_bytes; the caller's, so
- *                  that calls captured into different graphs can have their own.
+ *   q [S,Hq,d]      input; q_strides: elements between sequences and heads.
+ *   alibi_slopes    [Hq] float or NULL.
+ *   out [S,Hq,d]    output, dense, rounded once.  A sequence without a key (length 0, or all
+ *                   pages invalid), or whose scores are all -inf, gets zeros.
+ *   lse [S,Hq] float or NULL   output: ln sum_j e^{z_j} (-inf without a key), for joining with
+ *                   attention over other keys.
+ *   workspace       device, 16-byte aligned, of mita_paged_attn_workspace_bytes; the caller's, so
+ *                   that calls captured into different graphs can have their own.
  * The same inputs give the same bits.  Cache rows that no sequence's length covers are never read.
  */
-int mita_paged_attn(const void* q, const void* k_cache, const void* v_cache,
-                    const int32_t* page_table, const int32_t* lengths, const float* alibi_slopes,
-                    int S, int Hq, int Hkv, int d, int num_pages, int page_size, int table_width,
-                    const int64_t* q_strides, float scale, float softcap, int window,
-                    void* workspace, uint64_t workspace_bytes, void* out, float* lse,
-                    mita_stream_t stream);
-int mita_paged_attn_f32(const float* q, const float* k_cache, const float* v_cache,
-                        const int32_t* page_table, const int32_t* lengths,
-                        const float* alibi_slopes, int S, int Hq, int Hkv, int d, int num_pages,
-                        int page_size, int table_width, const int64_t* q_strides, float scale,
-                        float softcap, int window, void* workspace, uint64_t workspace_bytes,
-                        float* out, float* lse, mita_stream_t stream);
+typedef struct mita_paged_attn_params {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *page_table, *lengths;
+  const float* alibi_slopes;
+  void* workspace;
+  void* out;
+  float* lse;
+  uint64_t workspace_bytes;
+  int64_t q_strides[2];
+  int32_t S, Hq, Hkv, d, num_pages, page_size, table_width, window;
+  float scale, softcap;
+} mita_paged_attn_params;
+int mita_paged_attn(const mita_paged_attn_params* params, mita_stream_t stream);
+int mita_paged_attn_f32(const mita_paged_attn_params* params, mita_stream_t stream);
 /* Bytes of workspace mita_paged_attn needs for this shape on the current device (0 if invalid). */
 uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page_size,
                                          int table_width, int is_f32);

@@ -758,13 +758,13 @@ int check_rope(int d, int rot, const double* inv_freq, float eps) {
   return MITA_OK;
 }
 
-// Element strides of an array of rows: `given`, or those of the dense array when it is NULL.
-// Rows must start on 16-byte boundaries; the stride of a dimension of size 1 is not looked at.
+// Element strides of an array of rows.  Rows must start on 16-byte boundaries; the stride of a
+// dimension of size 1 is not looked at.
 template <int K>
-int row_strides(const int64_t* given, const int64_t (&dense)[K], const int (&size)[K], size_t esize,
-                const char* name, long long (&out)[K]) {
+int row_strides(const int64_t (&given)[K], const int (&size)[K], size_t esize, const char* name,
+                long long (&out)[K]) {
   for (int i = 0; i < K; ++i) {
-    out[i] = size[i] == 1 ? 0 : given ? given[i] : dense[i];
+    out[i] = size[i] == 1 ? 0 : given[i];
     if (out[i] < 0 || out[i] % (long long)(16 / esize) != 0)
       return fail(MITA_ERR_INVALID_ARG,
                   "%s: stride %lld is negative or leaves rows off 16-byte boundaries", name,
@@ -773,18 +773,13 @@ int row_strides(const int64_t* given, const int64_t (&dense)[K], const int (&siz
   return MITA_OK;
 }
 
-int bhn_strides(const int64_t* given, int B, int H, int N, int d, size_t esize, const char* name,
-                long long (&out)[3]) {
-  return row_strides<3>(given, {(int64_t)H * N * d, (int64_t)N * d, (int64_t)d}, {B, H, N}, esize,
-                        name, out);
-}
-
 int check_bhn(int B, int Hq, int Hkv, int N, int d) {
   if (B < 0 || N < 0 || Hq < 1 || Hkv < 0)
     return fail(MITA_ERR_INVALID_ARG, "need B, N, Hkv >= 0 and Hq >= 1 (got %d, %d, %d, %d)", B, N,
                 Hkv, Hq);
   MITA_TRY(check_head_dim(d));
-  if ((long long)B * N >= (1LL << 31) || (long long)B * N * ((long long)Hq + Hkv) >= (1LL << 31))
+  const long long most = 1LL << 31;
+  if ((long long)B * N >= most || (long long)B * N * ((long long)Hq + Hkv) >= most)
     return fail(MITA_ERR_UNSUPPORTED, "B*(Hq+Hkv)*N must be < 2^31");
   return MITA_OK;
 }
@@ -796,39 +791,37 @@ int check_positions(const int32_t* positions, int64_t stride) {
 }
 
 template <typename T>
-int norm_rope_impl(const T* q, const T* k, const float* q_weight, const float* k_weight,
-                   const int32_t* positions, int64_t positions_stride, const double* inv_freq,
-                   int B, int Hq, int Hkv, int N, int d, int rot, int interleaved, float eps,
-                   const int64_t* q_strides, const int64_t* k_strides,
-                   const int64_t* q_out_strides, const int64_t* k_out_strides, T* q_out, T* k_out,
-                   cudaStream_t st) {
-  MITA_TRY(check_bhn(B, Hq, Hkv, N, d));
-  MITA_TRY(check_rope(d, rot, inv_freq, eps));
-  if (B == 0 || N == 0) return MITA_OK;
+int norm_rope_impl(const mita_qk_norm_rope_params* p, cudaStream_t st) {
+  if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  MITA_TRY(check_bhn(p->B, p->Hq, p->Hkv, p->N, p->d));
+  MITA_TRY(check_rope(p->d, p->rot, p->inv_freq, p->eps));
+  MITA_TRY(check_positions(p->positions, p->positions_stride));
+  if (p->B == 0 || p->N == 0) return MITA_OK;
   NormRopeArgs<T> a{};
-  const T* xs[2] = {q, k};
-  T* ys[2] = {q_out, k_out};
-  const float* ws[2] = {q_weight, k_weight};
-  const int64_t* given[2][2] = {{q_strides, q_out_strides}, {k_strides, k_out_strides}};
-  const int heads[2] = {Hq, Hkv};
-  static const char* const names[2][3] = {{"q", "q_out", "q_weight"}, {"k", "k_out", "k_weight"}};
-  for (int i = 0; i < 2; ++i) {
-    if (heads[i] == 0) continue;
-    MITA_TRY(check_ptrs({{xs[i], names[i][0]}, {ys[i], names[i][1]}}));
-    if (ws[i]) MITA_TRY(check_aligned(ws[i], 16, names[i][2]));
-    long long x[3], y[3];
-    MITA_TRY(bhn_strides(given[i][0], B, heads[i], N, d, sizeof(T), names[i][0], x));
-    MITA_TRY(bhn_strides(given[i][1], B, heads[i], N, d, sizeof(T), names[i][1], y));
-    a.part[i] = {xs[i], ys[i], ws[i], x[0], x[1], x[2], y[0], y[1], y[2], heads[i]};
-  }
-  MITA_TRY(check_positions(positions, positions_stride));
-  a.positions = positions;
-  a.pos_b = positions_stride;
-  a.inv_freq = inv_freq;
-  a.B = B; a.N = N; a.rot = rot; a.interleaved = interleaved != 0; a.eps = eps;
+  auto part = [&](NormRopePart<T>& o, const void* x, void* y, const float* w, int heads,
+                  const int64_t (&xs)[3], const int64_t (&ys)[3], const char* nx, const char* ny,
+                  const char* nw) {
+    if (heads == 0) return (int)MITA_OK;
+    MITA_TRY(check_ptrs({{x, nx}, {y, ny}}));
+    if (w) MITA_TRY(check_aligned(w, 16, nw));
+    long long sx[3], sy[3];
+    MITA_TRY(row_strides<3>(xs, {p->B, heads, p->N}, sizeof(T), nx, sx));
+    MITA_TRY(row_strides<3>(ys, {p->B, heads, p->N}, sizeof(T), ny, sy));
+    o = {static_cast<const T*>(x), static_cast<T*>(y), w, sx[0], sx[1], sx[2], sy[0], sy[1], sy[2],
+         heads};
+    return (int)MITA_OK;
+  };
+  MITA_TRY(part(a.part[0], p->q, p->q_out, p->q_weight, p->Hq, p->q_strides, p->q_out_strides, "q",
+                "q_out", "q_weight"));
+  MITA_TRY(part(a.part[1], p->k, p->k_out, p->k_weight, p->Hkv, p->k_strides, p->k_out_strides,
+                "k", "k_out", "k_weight"));
+  a.positions = p->positions;
+  a.pos_b = p->positions_stride;
+  a.inv_freq = p->inv_freq;
+  a.B = p->B; a.N = p->N; a.rot = p->rot; a.interleaved = p->interleaved != 0; a.eps = p->eps;
   DevState* ds = nullptr;
   MITA_TRY(device_state_for(st, &ds));
-  MITA_CUDA(launch_norm_rope<T>(a, d, ds->num_sms, st), "norm and rotation launch");
+  MITA_CUDA(launch_norm_rope<T>(a, p->d, ds->num_sms, st), "norm and rotation launch");
   return MITA_OK;
 }
 
@@ -848,71 +841,63 @@ int check_workspace(const void* ws, uint64_t have, uint64_t need) {
   return check_aligned(ws, 16, "workspace");
 }
 
-uint64_t norm_rope_backward_ws(int d) {
-  return (uint64_t)norm_rope_backward_blocks(current_sms()) * d * sizeof(float);
+uint64_t norm_rope_backward_ws(int d, int sms) {
+  return (uint64_t)norm_rope_backward_blocks(sms) * d * sizeof(float);
 }
 
 template <typename T>
-int norm_rope_backward_impl(const T* q, const T* k, const T* dq_out, const T* dk_out,
-                            const float* q_weight, const float* k_weight, const int32_t* positions,
-                            int64_t positions_stride, const double* inv_freq, int B, int Hq,
-                            int Hkv, int N, int d, int rot, int interleaved, float eps,
-                            const int64_t* q_strides, const int64_t* k_strides,
-                            const int64_t* dq_out_strides, const int64_t* dk_out_strides,
-                            const int64_t* dq_strides, const int64_t* dk_strides, void* workspace,
-                            uint64_t workspace_bytes, T* dq, T* dk, float* dq_weight,
-                            float* dk_weight, cudaStream_t st) {
-  MITA_TRY(check_bhn(B, Hq, Hkv, N, d));
-  MITA_TRY(check_rope(d, rot, inv_freq, eps));
-  const T* xs[2] = {q, k};
-  const T* dys[2] = {dq_out, dk_out};
-  T* dxs[2] = {dq, dk};
-  const float* ws[2] = {q_weight, k_weight};
-  float* dws[2] = {dq_weight, dk_weight};
-  const int64_t* given[2][3] = {{q_strides, dq_out_strides, dq_strides},
-                                {k_strides, dk_out_strides, dk_strides}};
-  const int heads[2] = {Hq, Hkv};
-  static const char* const names[2][5] = {{"q", "dq_out", "dq", "q_weight", "dq_weight"},
-                                          {"k", "dk_out", "dk", "k_weight", "dk_weight"}};
-  const bool empty = B == 0 || N == 0;
+int norm_rope_backward_impl(const mita_qk_norm_rope_backward_params* p, cudaStream_t st) {
+  if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  MITA_TRY(check_bhn(p->B, p->Hq, p->Hkv, p->N, p->d));
+  MITA_TRY(check_rope(p->d, p->rot, p->inv_freq, p->eps));
+  MITA_TRY(check_positions(p->positions, p->positions_stride));
+  const bool empty = p->B == 0 || p->N == 0;
   NormRopeBackwardArgs<T> a{};
-  for (int i = 0; i < 2; ++i) {
-    if (heads[i] == 0) {
-      dws[i] = nullptr;
-      continue;
+  float* dws[2] = {nullptr, nullptr};
+  auto part = [&](int i, const void* x, const void* dy, void* dx, const float* w, float* dw,
+                  int heads, const int64_t (&xs)[3], const int64_t (&dys)[3],
+                  const int64_t (&dxs)[3], const char* const (&name)[5]) {
+    if (heads == 0) return (int)MITA_OK;
+    if (w) {
+      MITA_TRY(check_aligned(w, 16, name[3]));
+      MITA_TRY(check_aligned(dw, 4, name[4]));
+      dws[i] = dw;
+    } else if (dw) {
+      return fail(MITA_ERR_INVALID_ARG, "%s given without %s", name[4], name[3]);
     }
-    if (ws[i]) {
-      MITA_TRY(check_aligned(ws[i], 16, names[i][3]));
-      MITA_TRY(check_aligned(dws[i], 4, names[i][4]));
-    } else if (dws[i]) {
-      return fail(MITA_ERR_INVALID_ARG, "%s given without %s", names[i][4], names[i][3]);
-    }
-    if (empty) continue;
-    MITA_TRY(check_ptrs({{dys[i], names[i][1]}, {dxs[i], names[i][2]}}));
-    if (ws[i]) MITA_TRY(check_ptrs({{xs[i], names[i][0]}}));   // else x is not read
-    long long x[3], dy[3], dx[3];
-    MITA_TRY(bhn_strides(given[i][0], B, heads[i], N, d, sizeof(T), names[i][0], x));
-    MITA_TRY(bhn_strides(given[i][1], B, heads[i], N, d, sizeof(T), names[i][1], dy));
-    MITA_TRY(bhn_strides(given[i][2], B, heads[i], N, d, sizeof(T), names[i][2], dx));
-    a.part[i] = {xs[i], dys[i], dxs[i], ws[i], nullptr, x[0], x[1], x[2], dy[0], dy[1], dy[2],
-                 dx[0], dx[1], dx[2], heads[i]};
-  }
-  MITA_TRY(check_positions(positions, positions_stride));
-  if (!empty && (dws[0] || dws[1]))
-    MITA_TRY(check_workspace(workspace, workspace_bytes, norm_rope_backward_ws(d)));
+    if (empty) return (int)MITA_OK;
+    MITA_TRY(check_ptrs({{dy, name[1]}, {dx, name[2]}}));
+    if (w) MITA_TRY(check_ptrs({{x, name[0]}}));   // else x is not read
+    const int size[3] = {p->B, heads, p->N};
+    long long sx[3] = {}, sdy[3], sdx[3];
+    if (w) MITA_TRY(row_strides<3>(xs, size, sizeof(T), name[0], sx));
+    MITA_TRY(row_strides<3>(dys, size, sizeof(T), name[1], sdy));
+    MITA_TRY(row_strides<3>(dxs, size, sizeof(T), name[2], sdx));
+    a.part[i] = {static_cast<const T*>(x), static_cast<const T*>(dy), static_cast<T*>(dx), w,
+                 nullptr, sx[0], sx[1], sx[2], sdy[0], sdy[1], sdy[2], sdx[0], sdx[1], sdx[2],
+                 heads};
+    return (int)MITA_OK;
+  };
+  MITA_TRY(part(0, p->q, p->dq_out, p->dq, p->q_weight, p->dq_weight, p->Hq, p->q_strides,
+                p->dq_out_strides, p->dq_strides, {"q", "dq_out", "dq", "q_weight", "dq_weight"}));
+  MITA_TRY(part(1, p->k, p->dk_out, p->dk, p->k_weight, p->dk_weight, p->Hkv, p->k_strides,
+                p->dk_out_strides, p->dk_strides, {"k", "dk_out", "dk", "k_weight", "dk_weight"}));
   if (empty) {
     for (float* w : dws)
-      if (w) MITA_CUDA(cudaMemsetAsync(w, 0, d * sizeof(float), st), "weight gradient");
+      if (w) MITA_CUDA(cudaMemsetAsync(w, 0, p->d * sizeof(float), st), "weight gradient");
     return MITA_OK;
   }
-  a.positions = positions;
-  a.pos_b = positions_stride;
-  a.inv_freq = inv_freq;
-  a.B = B; a.N = N; a.rot = rot; a.interleaved = interleaved != 0; a.eps = eps;
+  a.positions = p->positions;
+  a.pos_b = p->positions_stride;
+  a.inv_freq = p->inv_freq;
+  a.B = p->B; a.N = p->N; a.rot = p->rot; a.interleaved = p->interleaved != 0; a.eps = p->eps;
+  if (dws[0] || dws[1])
+    MITA_TRY(check_workspace(p->workspace, p->workspace_bytes,
+                             norm_rope_backward_ws(p->d, current_sms())));
   DevState* ds = nullptr;
   MITA_TRY(device_state_for(st, &ds));
-  MITA_CUDA(launch_norm_rope_backward<T>(a, d, static_cast<float*>(workspace), ds->num_sms, dws[0],
-                                         dws[1], st),
+  MITA_CUDA(launch_norm_rope_backward<T>(a, p->d, static_cast<float*>(p->workspace), ds->num_sms,
+                                         dws[0], dws[1], st),
             "norm and rotation gradient launch");
   return MITA_OK;
 }
@@ -927,8 +912,6 @@ int check_pages(int S, int Hkv, int num_pages, int page_size, int width) {
                 kMaxPageSize);
   if ((long long)width * page_size >= (1LL << 31))
     return fail(MITA_ERR_UNSUPPORTED, "table_width*page_size must be < 2^31");
-  if ((long long)num_pages * Hkv >= (1LL << 40))
-    return fail(MITA_ERR_UNSUPPORTED, "num_pages*Hkv must be < 2^40");
   return MITA_OK;
 }
 
@@ -939,52 +922,57 @@ int log2_of(int x) {
 }
 
 template <typename T>
-int cache_append_impl(const T* q, const T* k, const T* v, const float* q_weight,
-                      const float* k_weight, const double* inv_freq, const int32_t* page_table,
-                      const int32_t* lengths, const int32_t* seq_start, int tokens, int S, int Hq,
-                      int Hkv, int d, int num_pages, int page_size, int table_width, int rot,
-                      int interleaved, float eps, const int64_t* q_strides,
-                      const int64_t* k_strides, const int64_t* v_strides,
-                      const int64_t* q_out_strides, T* q_out, T* k_cache, T* v_cache,
-                      cudaStream_t st) {
-  if (tokens < 0 || Hq < 0)
-    return fail(MITA_ERR_INVALID_ARG, "need tokens, Hq >= 0 (got %d, %d)", tokens, Hq);
-  MITA_TRY(check_pages(S, Hkv, num_pages, page_size, table_width));
-  MITA_TRY(check_head_dim(d));
-  MITA_TRY(check_rope(d, rot, inv_freq, eps));
-  if ((long long)tokens * ((long long)Hq + 2 * Hkv) >= (1LL << 31))
+int cache_append_impl(const mita_cache_append_params* p, cudaStream_t st) {
+  if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  if (p->tokens < 0 || p->Hq < 0)
+    return fail(MITA_ERR_INVALID_ARG, "need tokens, Hq >= 0 (got %d, %d)", p->tokens, p->Hq);
+  MITA_TRY(check_pages(p->S, p->Hkv, p->num_pages, p->page_size, p->table_width));
+  MITA_TRY(check_head_dim(p->d));
+  MITA_TRY(check_rope(p->d, p->rot, p->inv_freq, p->eps));
+  if ((long long)p->Hq + 2LL * p->Hkv >= (1LL << 31) ||
+      (long long)p->tokens * ((long long)p->Hq + 2LL * p->Hkv) >= (1LL << 31))
     return fail(MITA_ERR_UNSUPPORTED, "tokens*(Hq+2*Hkv) must be < 2^31");
-  if (seq_start == nullptr && tokens != S)
+  if (p->seq_start == nullptr && p->tokens != p->S)
     return fail(MITA_ERR_INVALID_ARG,
-                "without seq_start every sequence has one new token (tokens=%d, S=%d)", tokens, S);
-  if (tokens == 0 || S == 0) return MITA_OK;
+                "without seq_start every sequence has one new token (tokens=%d, S=%d)", p->tokens,
+                p->S);
+  if (p->tokens == 0 || p->S == 0) return MITA_OK;
   CacheAppendArgs<T> a{};
-  if (Hq > 0) {
-    MITA_TRY(check_ptrs({{q, "q"}, {q_out, "q_out"}}));
-    long long x[2], y[2];
-    MITA_TRY(row_strides<2>(q_strides, {(int64_t)Hq * d, d}, {tokens, Hq}, sizeof(T), "q", x));
-    MITA_TRY(row_strides<2>(q_out_strides, {(int64_t)Hq * d, d}, {tokens, Hq}, sizeof(T), "q_out",
-                            y));
-    a.q_t = x[0]; a.q_h = x[1]; a.qo_t = y[0]; a.qo_h = y[1];
+  auto rows = [&](const void* x, int heads, const int64_t (&given)[2], const char* name,
+                  long long& t, long long& h) {
+    MITA_TRY(check_ptrs({{x, name}}));
+    long long s[2];
+    MITA_TRY(row_strides<2>(given, {p->tokens, heads}, sizeof(T), name, s));
+    t = s[0];
+    h = s[1];
+    return (int)MITA_OK;
+  };
+  if (p->Hq > 0) {
+    MITA_TRY(rows(p->q, p->Hq, p->q_strides, "q", a.q_t, a.q_h));
+    MITA_TRY(rows(p->q_out, p->Hq, p->q_out_strides, "q_out", a.qo_t, a.qo_h));
   }
-  MITA_TRY(check_ptrs({{k, "k"}, {v, "v"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}}));
-  if (q_weight) MITA_TRY(check_aligned(q_weight, 16, "q_weight"));
-  if (k_weight) MITA_TRY(check_aligned(k_weight, 16, "k_weight"));
-  MITA_TRY(check_aligned(page_table, 4, "page_table"));
-  MITA_TRY(check_aligned(lengths, 4, "lengths"));
-  if (seq_start) MITA_TRY(check_aligned(seq_start, 4, "seq_start"));
-  long long ks[2], vs[2];
-  MITA_TRY(row_strides<2>(k_strides, {(int64_t)Hkv * d, d}, {tokens, Hkv}, sizeof(T), "k", ks));
-  MITA_TRY(row_strides<2>(v_strides, {(int64_t)Hkv * d, d}, {tokens, Hkv}, sizeof(T), "v", vs));
+  MITA_TRY(rows(p->k, p->Hkv, p->k_strides, "k", a.k_t, a.k_h));
+  MITA_TRY(rows(p->v, p->Hkv, p->v_strides, "v", a.v_t, a.v_h));
+  if (p->num_pages > 0)
+    MITA_TRY(check_ptrs({{p->k_cache, "k_cache"}, {p->v_cache, "v_cache"}}));
+  if (p->q_weight) MITA_TRY(check_aligned(p->q_weight, 16, "q_weight"));
+  if (p->k_weight) MITA_TRY(check_aligned(p->k_weight, 16, "k_weight"));
+  if (p->table_width > 0) MITA_TRY(check_aligned(p->page_table, 4, "page_table"));
+  MITA_TRY(check_aligned(p->lengths, 4, "lengths"));
+  if (p->seq_start) MITA_TRY(check_aligned(p->seq_start, 4, "seq_start"));
   DevState* ds = nullptr;
   MITA_TRY(device_state_for(st, &ds));
-  a.q = q; a.k = k; a.v = v; a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
-  a.q_w = q_weight; a.k_w = k_weight; a.inv_freq = inv_freq; a.seq_start = seq_start;
-  a.k_t = ks[0]; a.k_h = ks[1]; a.v_t = vs[0]; a.v_h = vs[1];
-  a.paged = {page_table, lengths, S, table_width, num_pages, log2_of(page_size)};
-  a.tokens = tokens; a.q_heads = Hq; a.kv_heads = Hkv; a.rot = rot;
-  a.interleaved = interleaved != 0; a.eps = eps; a.status = ds->status;
-  MITA_CUDA(launch_cache_append<T>(a, d, ds->num_sms, st), "cache append launch");
+  a.q = static_cast<const T*>(p->q);
+  a.k = static_cast<const T*>(p->k);
+  a.v = static_cast<const T*>(p->v);
+  a.q_out = static_cast<T*>(p->q_out);
+  a.k_cache = static_cast<T*>(p->k_cache);
+  a.v_cache = static_cast<T*>(p->v_cache);
+  a.q_w = p->q_weight; a.k_w = p->k_weight; a.inv_freq = p->inv_freq; a.seq_start = p->seq_start;
+  a.paged = {p->page_table, p->lengths, p->S, p->table_width, p->num_pages, log2_of(p->page_size)};
+  a.tokens = p->tokens; a.q_heads = p->Hq; a.kv_heads = p->Hkv; a.rot = p->rot;
+  a.interleaved = p->interleaved != 0; a.eps = p->eps; a.status = ds->status;
+  MITA_CUDA(launch_cache_append<T>(a, p->d, ds->num_sms, st), "cache append launch");
   return MITA_OK;
 }
 
@@ -999,39 +987,42 @@ int check_paged_attn(int S, int Hq, int Hkv, int d, int num_pages, int page_size
 }
 
 template <typename T>
-int paged_attn_impl(const T* q, const T* k_cache, const T* v_cache, const int32_t* page_table,
-                    const int32_t* lengths, const float* alibi_slopes, int S, int Hq, int Hkv,
-                    int d, int num_pages, int page_size, int table_width,
-                    const int64_t* q_strides, float scale, float softcap, int window,
-                    void* workspace, uint64_t workspace_bytes, T* out, float* lse,
-                    cudaStream_t st) {
-  MITA_TRY(check_paged_attn(S, Hq, Hkv, d, num_pages, page_size, table_width));
-  if (!std::isfinite(scale)) return fail(MITA_ERR_INVALID_ARG, "scale is not finite");
-  if (!(softcap >= 0.f) || std::isinf(softcap))
+int paged_attn_impl(const mita_paged_attn_params* p, cudaStream_t st) {
+  if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  MITA_TRY(check_paged_attn(p->S, p->Hq, p->Hkv, p->d, p->num_pages, p->page_size,
+                            p->table_width));
+  if (!std::isfinite(p->scale)) return fail(MITA_ERR_INVALID_ARG, "scale is not finite");
+  if (!(p->softcap >= 0.f) || std::isinf(p->softcap))
     return fail(MITA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
-  if (window < 0) return fail(MITA_ERR_INVALID_ARG, "window must be >= 0");
-  if (S == 0) return MITA_OK;
-  MITA_TRY(check_ptrs({{q, "q"}, {out, "out"}}));
-  if (num_pages > 0) MITA_TRY(check_ptrs({{k_cache, "k_cache"}, {v_cache, "v_cache"}}));
-  if (table_width > 0) MITA_TRY(check_aligned(page_table, 4, "page_table"));
-  MITA_TRY(check_aligned(lengths, 4, "lengths"));
-  if (alibi_slopes) MITA_TRY(check_aligned(alibi_slopes, 4, "alibi_slopes"));
-  if (lse) MITA_TRY(check_aligned(lse, 4, "lse"));
+  if (p->window < 0) return fail(MITA_ERR_INVALID_ARG, "window must be >= 0");
+  if (p->S == 0) return MITA_OK;
+  MITA_TRY(check_ptrs({{p->q, "q"}, {p->out, "out"}}));
+  if (p->num_pages > 0)
+    MITA_TRY(check_ptrs({{p->k_cache, "k_cache"}, {p->v_cache, "v_cache"}}));
+  if (p->table_width > 0) MITA_TRY(check_aligned(p->page_table, 4, "page_table"));
+  MITA_TRY(check_aligned(p->lengths, 4, "lengths"));
+  if (p->alibi_slopes) MITA_TRY(check_aligned(p->alibi_slopes, 4, "alibi_slopes"));
+  if (p->lse) MITA_TRY(check_aligned(p->lse, 4, "lse"));
   long long qs[2];
-  MITA_TRY(row_strides<2>(q_strides, {(int64_t)Hq * d, d}, {S, Hq}, sizeof(T), "q", qs));
+  MITA_TRY(row_strides<2>(p->q_strides, {p->S, p->Hq}, sizeof(T), "q", qs));
+  const int pl = log2_of(p->page_size), G = p->Hq / p->Hkv;
+  MITA_TRY(check_workspace(p->workspace, p->workspace_bytes,
+                           paged_attn_ws_bytes(p->d, p->Hkv, G, p->S, p->table_width, pl,
+                                               sizeof(T) == 4, current_sms())));
   DevState* ds = nullptr;
   MITA_TRY(device_state_for(st, &ds));
-  const int pl = log2_of(page_size), G = Hq / Hkv;
-  MITA_TRY(check_workspace(workspace, workspace_bytes,
-                           paged_attn_ws_bytes(d, Hkv, G, S, table_width, pl, sizeof(T) == 4,
-                                               ds->num_sms)));
   PagedAttnArgs<T> a{};
-  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.out = out; a.lse = lse;
-  a.slopes = alibi_slopes; a.q_s = qs[0]; a.q_h = qs[1];
-  a.paged = {page_table, lengths, S, table_width, num_pages, pl};
-  a.Hkv = Hkv; a.G = G; a.scale = scale; a.softcap = softcap; a.window = window;
+  a.q = static_cast<const T*>(p->q);
+  a.k_cache = static_cast<const T*>(p->k_cache);
+  a.v_cache = static_cast<const T*>(p->v_cache);
+  a.out = static_cast<T*>(p->out);
+  a.lse = p->lse;
+  a.slopes = p->alibi_slopes; a.q_s = qs[0]; a.q_h = qs[1];
+  a.paged = {p->page_table, p->lengths, p->S, p->table_width, p->num_pages, pl};
+  a.Hkv = p->Hkv; a.G = G; a.scale = p->scale; a.softcap = p->softcap; a.window = p->window;
   a.status = ds->status;
-  MITA_CUDA(launch_paged_attn<T>(a, d, workspace, ds->num_sms, st), "paged attention launch");
+  MITA_CUDA(launch_paged_attn<T>(a, p->d, p->workspace, ds->num_sms, st),
+            "paged attention launch");
   return MITA_OK;
 }
 
@@ -1312,142 +1303,47 @@ int mita_forward_host_f32(const float* q, const float* k, const float* v, int B,
                                         stream);
 }
 
-int mita_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
-                      const int32_t* positions, int64_t positions_stride, const double* inv_freq,
-                      int B, int Hq, int Hkv, int N, int d, int rot, int interleaved, float eps,
-                      const int64_t* q_strides, const int64_t* k_strides,
-                      const int64_t* q_out_strides, const int64_t* k_out_strides, void* q_out,
-                      void* k_out, mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::norm_rope_impl<bf16>(
-        static_cast<const bf16*>(q), static_cast<const bf16*>(k), q_weight, k_weight, positions,
-        positions_stride, inv_freq, B, Hq, Hkv, N, d, rot, interleaved, eps, q_strides, k_strides,
-        q_out_strides, k_out_strides, static_cast<bf16*>(q_out), static_cast<bf16*>(k_out),
-        stream);
-  });
+int mita_qk_norm_rope(const mita_qk_norm_rope_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_impl<bf16>(params, stream); });
 }
-int mita_qk_norm_rope_f32(const float* q, const float* k, const float* q_weight,
-                          const float* k_weight, const int32_t* positions,
-                          int64_t positions_stride, const double* inv_freq, int B, int Hq, int Hkv,
-                          int N, int d, int rot, int interleaved, float eps,
-                          const int64_t* q_strides, const int64_t* k_strides,
-                          const int64_t* q_out_strides, const int64_t* k_out_strides, float* q_out,
-                          float* k_out, mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::norm_rope_impl<float>(q, k, q_weight, k_weight, positions, positions_stride,
-                                       inv_freq, B, Hq, Hkv, N, d, rot, interleaved, eps,
-                                       q_strides, k_strides, q_out_strides, k_out_strides, q_out,
-                                       k_out, stream);
-  });
+int mita_qk_norm_rope_f32(const mita_qk_norm_rope_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_impl<float>(params, stream); });
 }
 
+int mita_qk_norm_rope_backward(const mita_qk_norm_rope_backward_params* params,
+                               mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_backward_impl<bf16>(params, stream); });
+}
+int mita_qk_norm_rope_backward_f32(const mita_qk_norm_rope_backward_params* params,
+                                   mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_backward_impl<float>(params, stream); });
+}
 uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d) {
-  return mita::check_head_dim(d) == MITA_OK ? mita::norm_rope_backward_ws(d) : 0;
+  if (d != 16 && d != 32 && d != 64 && d != 128) return 0;
+  return mita::norm_rope_backward_ws(d, mita::current_sms());
 }
 
-int mita_qk_norm_rope_backward(const void* q, const void* k, const void* dq_out,
-                               const void* dk_out, const float* q_weight, const float* k_weight,
-                               const int32_t* positions, int64_t positions_stride,
-                               const double* inv_freq, int B, int Hq, int Hkv, int N, int d,
-                               int rot, int interleaved, float eps, const int64_t* q_strides,
-                               const int64_t* k_strides, const int64_t* dq_out_strides,
-                               const int64_t* dk_out_strides, const int64_t* dq_strides,
-                               const int64_t* dk_strides, void* workspace,
-                               uint64_t workspace_bytes, void* dq, void* dk, float* dq_weight,
-                               float* dk_weight, mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::norm_rope_backward_impl<bf16>(
-        static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(dq_out),
-        static_cast<const bf16*>(dk_out), q_weight, k_weight, positions, positions_stride,
-        inv_freq, B, Hq, Hkv, N, d, rot, interleaved, eps, q_strides, k_strides, dq_out_strides,
-        dk_out_strides, dq_strides, dk_strides, workspace, workspace_bytes, static_cast<bf16*>(dq),
-        static_cast<bf16*>(dk), dq_weight, dk_weight, stream);
-  });
+int mita_cache_append(const mita_cache_append_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::cache_append_impl<bf16>(params, stream); });
 }
-int mita_qk_norm_rope_backward_f32(const float* q, const float* k, const float* dq_out,
-                                   const float* dk_out, const float* q_weight,
-                                   const float* k_weight, const int32_t* positions,
-                                   int64_t positions_stride, const double* inv_freq, int B, int Hq,
-                                   int Hkv, int N, int d, int rot, int interleaved, float eps,
-                                   const int64_t* q_strides, const int64_t* k_strides,
-                                   const int64_t* dq_out_strides, const int64_t* dk_out_strides,
-                                   const int64_t* dq_strides, const int64_t* dk_strides,
-                                   void* workspace, uint64_t workspace_bytes, float* dq, float* dk,
-                                   float* dq_weight, float* dk_weight, mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::norm_rope_backward_impl<float>(
-        q, k, dq_out, dk_out, q_weight, k_weight, positions, positions_stride, inv_freq, B, Hq,
-        Hkv, N, d, rot, interleaved, eps, q_strides, k_strides, dq_out_strides, dk_out_strides,
-        dq_strides, dk_strides, workspace, workspace_bytes, dq, dk, dq_weight, dk_weight, stream);
-  });
+int mita_cache_append_f32(const mita_cache_append_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::cache_append_impl<float>(params, stream); });
 }
 
-int mita_cache_append(const void* q, const void* k, const void* v, const float* q_weight,
-                      const float* k_weight, const double* inv_freq, const int32_t* page_table,
-                      const int32_t* lengths, const int32_t* seq_start, int tokens, int S, int Hq,
-                      int Hkv, int d, int num_pages, int page_size, int table_width, int rot,
-                      int interleaved, float eps, const int64_t* q_strides,
-                      const int64_t* k_strides, const int64_t* v_strides,
-                      const int64_t* q_out_strides, void* q_out, void* k_cache, void* v_cache,
-                      mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::cache_append_impl<bf16>(
-        static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v),
-        q_weight, k_weight, inv_freq, page_table, lengths, seq_start, tokens, S, Hq, Hkv, d,
-        num_pages, page_size, table_width, rot, interleaved, eps, q_strides, k_strides, v_strides,
-        q_out_strides, static_cast<bf16*>(q_out), static_cast<bf16*>(k_cache),
-        static_cast<bf16*>(v_cache), stream);
-  });
+int mita_paged_attn(const mita_paged_attn_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::paged_attn_impl<bf16>(params, stream); });
 }
-int mita_cache_append_f32(const float* q, const float* k, const float* v, const float* q_weight,
-                          const float* k_weight, const double* inv_freq,
-                          const int32_t* page_table, const int32_t* lengths,
-                          const int32_t* seq_start, int tokens, int S, int Hq, int Hkv, int d,
-                          int num_pages, int page_size, int table_width, int rot, int interleaved,
-                          float eps, const int64_t* q_strides, const int64_t* k_strides,
-                          const int64_t* v_strides, const int64_t* q_out_strides, float* q_out,
-                          float* k_cache, float* v_cache, mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::cache_append_impl<float>(
-        q, k, v, q_weight, k_weight, inv_freq, page_table, lengths, seq_start, tokens, S, Hq, Hkv,
-        d, num_pages, page_size, table_width, rot, interleaved, eps, q_strides, k_strides,
-        v_strides, q_out_strides, q_out, k_cache, v_cache, stream);
-  });
+int mita_paged_attn_f32(const mita_paged_attn_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::paged_attn_impl<float>(params, stream); });
 }
-
 uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page_size,
                                          int table_width, int is_f32) {
-  if (mita::check_paged_attn(S, Hq, Hkv, d, 0, page_size, table_width) != MITA_OK) return 0;
+  if (mita::guarded([&] {
+        return mita::check_paged_attn(S, Hq, Hkv, d, 0, page_size, table_width);
+      }) != MITA_OK)
+    return 0;
   return mita::paged_attn_ws_bytes(d, Hkv, Hq / Hkv, S, table_width, mita::log2_of(page_size),
                                    is_f32, mita::current_sms());
-}
-
-int mita_paged_attn(const void* q, const void* k_cache, const void* v_cache,
-                    const int32_t* page_table, const int32_t* lengths, const float* alibi_slopes,
-                    int S, int Hq, int Hkv, int d, int num_pages, int page_size, int table_width,
-                    const int64_t* q_strides, float scale, float softcap, int window,
-                    void* workspace, uint64_t workspace_bytes, void* out, float* lse,
-                    mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::paged_attn_impl<bf16>(
-        static_cast<const bf16*>(q), static_cast<const bf16*>(k_cache),
-        static_cast<const bf16*>(v_cache), page_table, lengths, alibi_slopes, S, Hq, Hkv, d,
-        num_pages, page_size, table_width, q_strides, scale, softcap, window, workspace,
-        workspace_bytes, static_cast<bf16*>(out), lse, stream);
-  });
-}
-int mita_paged_attn_f32(const float* q, const float* k_cache, const float* v_cache,
-                        const int32_t* page_table, const int32_t* lengths,
-                        const float* alibi_slopes, int S, int Hq, int Hkv, int d, int num_pages,
-                        int page_size, int table_width, const int64_t* q_strides, float scale,
-                        float softcap, int window, void* workspace, uint64_t workspace_bytes,
-                        float* out, float* lse, mita_stream_t stream) {
-  return mita::guarded([&] {
-    return mita::paged_attn_impl<float>(q, k_cache, v_cache, page_table, lengths, alibi_slopes, S,
-                                        Hq, Hkv, d, num_pages, page_size, table_width, q_strides,
-                                        scale, softcap, window, workspace, workspace_bytes, out,
-                                        lse, stream);
-  });
 }
 
 uint64_t mita_forward_workspace_bytes(int B, int H, int N, int d, int m, int topk, int s,

@@ -299,7 +299,7 @@ struct NormRopeBackwardArgs {
   const double* inv_freq;
   int B, N, rot, interleaved;
   float eps;
-  int run, qblocks;         // set by the launcher
+  int run, qruns;           // set by the launcher
 };
 // Most blocks of the gradient kernel: its weight gradients need that many partial rows of d
 // floats in `partial`.  dwq / dwk [d]: written where not null.

@@ -10,7 +10,7 @@
 // Bound by HBM: a row is read once and written once (the gradient reads two and writes one),
 // and a value costs some ten instructions.  A slot of D / 8 lanes takes one token's heads
 // one after the other, so that a token's angles are computed once for all of them, and fetches
-// several heads ahead of working on them (kAhead), which keeps enough bytes in flight.
+// several heads ahead of working on them, which keeps enough bytes in flight.
 #include "norm_rope.cuh"
 
 #include <algorithm>
@@ -20,207 +20,140 @@
 namespace mita {
 namespace {
 
-constexpr int kAhead = 4;      // heads whose loads are issued together
 
-// One block of rows: `chunks` runs of up to `run` heads for each token, tokens fastest, so that
-// neighbouring slots work on neighbouring tokens of the same heads.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads)
+// Block (x, y): the y-th run of heads (q's, then k's) of the tokens x, x + gridDim.x, ..., a slot
+// a token; neighbouring slots have neighbouring tokens.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 norm_rope_kernel(const __grid_constant__ NormRopeArgs<T> a) {
-  constexpr int L = D / 8;
+  constexpr int L = D / 8, kSlots = kRopeThreads / L, K = kRopeAhead<T>;
   __shared__ unsigned long long table[D / 2];
   griddep_wait();
   rope_table(a.inv_freq, a.rot / 2, table);
   __syncthreads();
-  const int g = threadIdx.x % L;
-  int oa, ob;
-  rope_groups(g, a.rot, a.interleaved, &oa, &ob);
-  const bool turned = 8 * g < a.rot;
-  unsigned long long turn[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) turn[i] = turned ? table[4 * g + i] : 0;
+  const RopeLane lane(threadIdx.x % L, a.rot, INTER);
+  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
 
-  const long long tokens = (long long)a.B * a.N;
-  const int nq = (a.part[0].heads + a.run - 1) / a.run;
-  const int nk = (a.part[1].heads + a.run - 1) / a.run;
-  const long long items = tokens * (nq + nk);
-  const long long slots = (long long)gridDim.x * (kRopeThreads / L);
-  long long item = (long long)blockIdx.x * (kRopeThreads / L) + threadIdx.x / L;
-  // all lanes of a warp stay in the loop together (row_sum shuffles across the warp)
-  const long long warp_first = item - (threadIdx.x % 32) / L;
-  for (long long w = warp_first; w < items; w += slots, item += slots) {
-    const bool live = item < items;
-    const long long it = live ? item : items - 1;
-    const int chunk = (int)(it / tokens);
-    const long long t = it - chunk * tokens;
-    const int bt = (int)(t / a.N), n = (int)(t - (long long)bt * a.N);
-    const int isk = chunk >= nq;
-    const NormRopePart<T>& p = a.part[isk];
-    const int h0 = (isk ? chunk - nq : chunk) * a.run;
-    const int h1 = live ? min(h0 + a.run, p.heads) : h0;
-    float cs[4], sn[4];
-    if (turned) rope_angles(turn, a.positions ? a.positions[bt * a.pos_b + n] : n, cs, sn);
-    float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-    if (p.w) {
-      Raw4<float>::unpack(*reinterpret_cast<const float4*>(p.w + oa), wa);
-      Raw4<float>::unpack(*reinterpret_cast<const float4*>(p.w + ob), wb);
-    }
-    const T* x = p.x + bt * p.x_b + n * p.x_n;
-    T* y = p.y + bt * p.y_b + n * p.y_n;
-    for (int h = h0; h < h0 + a.run; h += kAhead) {
-      typename Raw4<T>::Bits ra[kAhead] = {}, rb[kAhead] = {};
+  const int hq = a.part[0].heads, h0 = blockIdx.y * a.run;
+  const int h1 = min(h0 + a.run, hq + a.part[1].heads);
+  const unsigned tokens = (unsigned)a.B * a.N, stride = gridDim.x * kSlots;
+  unsigned t = blockIdx.x * kSlots + threadIdx.x / L;
+  // all lanes of a warp stay in the loop together
+  for (unsigned first = t - (threadIdx.x % 32) / L; first < tokens; first += stride, t += stride) {
+    const bool live = t < tokens;
+    const int bt = live && a.B > 1 ? t / a.N : 0;
+    const int n = live ? t - (unsigned)bt * a.N : 0;
+    V2 cs[2], sn[2];
+    if (lane.turned)
+      rope_angles(turn, a.positions ? a.positions[bt * a.pos_b + n] : n, cs, sn);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (h + i < h1) {
-          const T* r = x + (h + i) * p.x_h;
-          ra[i] = *reinterpret_cast<const typename Raw4<T>::Bits*>(r + oa);
-          rb[i] = *reinterpret_cast<const typename Raw4<T>::Bits*>(r + ob);
-        }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (i >= a.run) break;
-        float va[4], vb[4];
-        Raw4<T>::unpack(ra[i], va);
-        Raw4<T>::unpack(rb[i], vb);
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fmaf(va[j], va[j], fmaf(vb[j], vb[j], ss));
-        ss = row_sum<D>(ss);
-        if (p.w) {
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            va[j] *= r * wa[j];
-            vb[j] *= r * wb[j];
-          }
-        }
-        if (turned) rope_turn(va, vb, cs, sn, a.interleaved, 1.f);
-        if (h + i < h1) {
-          T* o = y + (h + i) * p.y_h;
-          *reinterpret_cast<typename Raw4<T>::Bits*>(o + oa) = Raw4<T>::pack(va);
-          *reinterpret_cast<typename Raw4<T>::Bits*>(o + ob) = Raw4<T>::pack(vb);
-        }
-      }
+    for (int isk = 0; isk < 2; ++isk) {
+      const NormRopePart<T>& p = a.part[isk];
+      int h = isk ? max(h0 - hq, 0) : h0;
+      const int end = isk ? h1 - hq : min(h1, hq);
+      if (h >= end) continue;
+      RopeCoef<INTER> coef;
+      coef.set(lane.turned, cs, sn, p.w ? weights8(p.w, lane) : ones8());
+      const T* x = p.x + bt * p.x_b + n * p.x_n + h * p.x_h;
+      T* y = p.y + bt * p.y_b + n * p.y_n + h * p.y_h;
+      for (; h < end; h += K, x += K * p.x_h, y += K * p.y_h)
+        rope_rows<T, D, INTER>(lane, coef, x, p.x_h, y, p.y_h, end - h, p.w != nullptr, live, a.eps);
     }
   }
 }
 
-// The gradient.  A block works on q rows alone (the first a.qblocks blocks) or on k rows alone;
-// each lane sums its eight columns of dw over its rows, the block joins them in a fixed order
-// and writes one partial row of D; norm_rope_dw_kernel adds the partial rows, again in a fixed
+// The gradient.  A block works on q rows alone (blockIdx.y < a.qruns) or on k rows alone; each
+// lane sums its eight columns of dw over its rows, the block joins them in a fixed order and
+// writes one partial row of D; norm_rope_dw_kernel adds the partial rows, again in a fixed
 // order: no atomics, so the same inputs give the same bits.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads)
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBackwardBlocks)
 norm_rope_backward_kernel(const __grid_constant__ NormRopeBackwardArgs<T> a) {
-  constexpr int L = D / 8;
-  constexpr int kSlots = kRopeThreads / L;
+  constexpr int L = D / 8, kSlots = kRopeThreads / L;
+  constexpr int K = kRopeAhead<T> / 2;      // rows loaded together, each from x and dy
   __shared__ unsigned long long table[D / 2];
-  __shared__ float red[kRopeThreads * 8];
+  __shared__ __align__(16) float red[kRopeThreads * 8];
   griddep_wait();
   rope_table(a.inv_freq, a.rot / 2, table);
   __syncthreads();
-  const int g = threadIdx.x % L;
-  int oa, ob;
-  rope_groups(g, a.rot, a.interleaved, &oa, &ob);
-  const bool turned = 8 * g < a.rot;
-  unsigned long long turn[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) turn[i] = turned ? table[4 * g + i] : 0;
+  const RopeLane lane(threadIdx.x % L, a.rot, INTER);
+  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
 
-  const int isk = (int)blockIdx.x >= a.qblocks;
+  const int isk = (int)blockIdx.y >= a.qruns;
   const NormRopeBackwardPart<T>& p = a.part[isk];
-  const int blk = isk ? blockIdx.x - a.qblocks : blockIdx.x;
-  const int blocks = isk ? gridDim.x - a.qblocks : a.qblocks;
-  const long long tokens = (long long)a.B * a.N;
-  const long long items = tokens * ((p.heads + a.run - 1) / a.run);
-  float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-  if (p.w) {
-    Raw4<float>::unpack(*reinterpret_cast<const float4*>(p.w + oa), wa);
-    Raw4<float>::unpack(*reinterpret_cast<const float4*>(p.w + ob), wb);
-  }
-  float dwa[4] = {}, dwb[4] = {};
-  long long item = (long long)blk * kSlots + threadIdx.x / L;
-  const long long warp_first = item - (threadIdx.x % 32) / L;
-  for (long long w = warp_first; w < items; w += (long long)blocks * kSlots,
-                 item += (long long)blocks * kSlots) {
-    const bool live = item < items;
-    const long long it = live ? item : items - 1;
-    const int chunk = (int)(it / tokens);
-    const long long t = it - chunk * tokens;
-    const int bt = (int)(t / a.N), n = (int)(t - (long long)bt * a.N);
-    const int h0 = chunk * a.run;
-    const int h1 = live ? min(h0 + a.run, p.heads) : h0;
-    float cs[4], sn[4];
-    if (turned) rope_angles(turn, a.positions ? a.positions[bt * a.pos_b + n] : n, cs, sn);
-    const T* x = p.x + bt * p.x_b + n * p.x_n;
-    const T* dy = p.dy + bt * p.dy_b + n * p.dy_n;
-    T* dx = p.dx + bt * p.dx_b + n * p.dx_n;
-    constexpr int kPair = 2;
-    for (int h = h0; h < h0 + a.run; h += kPair) {
-      typename Raw4<T>::Bits xa[kPair] = {}, xb[kPair] = {}, ya[kPair] = {}, yb[kPair] = {};
+  const int run = isk ? blockIdx.y - a.qruns : blockIdx.y;
+  const int h0 = run * a.run, h1 = min(h0 + a.run, p.heads);
+  const bool normed = p.w != nullptr;
+  const V8 w = normed ? weights8(p.w, lane) : ones8();
+  V8 dw = {};
+  const unsigned tokens = (unsigned)a.B * a.N, stride = gridDim.x * kSlots;
+  unsigned t = blockIdx.x * kSlots + threadIdx.x / L;
+  for (unsigned first = t - (threadIdx.x % 32) / L; first < tokens; first += stride, t += stride) {
+    const bool live = t < tokens;
+    const int bt = live && a.B > 1 ? t / a.N : 0;
+    const int n = live ? t - (unsigned)bt * a.N : 0;
+    V2 cs[2], sn[2];
+    if (lane.turned)
+      rope_angles(turn, a.positions ? a.positions[bt * a.pos_b + n] : n, cs, sn);
+    RopeCoef<INTER> back;
+    back.set(lane.turned, cs, sn, ones8(), true);
+    const T* x = p.x + bt * p.x_b + n * p.x_n + h0 * p.x_h;
+    const T* dy = p.dy + bt * p.dy_b + n * p.dy_n + h0 * p.dy_h;
+    T* dx = p.dx + bt * p.dx_b + n * p.dx_n + h0 * p.dx_h;
+    for (int h = h0; h < h1; h += K, x += K * p.x_h, dy += K * p.dy_h, dx += K * p.dx_h) {
+      Raw8<T> rx[K] = {}, rg[K] = {};
 #pragma unroll
-      for (int i = 0; i < kPair; ++i)
-        if (h + i < h1) {
-          const T* r = dy + (h + i) * p.dy_h;
-          ya[i] = *reinterpret_cast<const typename Raw4<T>::Bits*>(r + oa);
-          yb[i] = *reinterpret_cast<const typename Raw4<T>::Bits*>(r + ob);
-          if (p.w) {
-            const T* s = x + (h + i) * p.x_h;
-            xa[i] = *reinterpret_cast<const typename Raw4<T>::Bits*>(s + oa);
-            xb[i] = *reinterpret_cast<const typename Raw4<T>::Bits*>(s + ob);
-          }
+      for (int i = 0; i < K; ++i)
+        if (live && h + i < h1) {
+          rg[i].load(dy + i * p.dy_h, lane.a, lane.b);
+          if (normed) rx[i].load(x + i * p.x_h, lane.a, lane.b);
         }
 #pragma unroll
-      for (int i = 0; i < kPair; ++i) {
-        if (i >= a.run) break;
-        float ga[4], gb[4], va[4], vb[4];
-        Raw4<T>::unpack(ya[i], ga);
-        Raw4<T>::unpack(yb[i], gb);
-        Raw4<T>::unpack(xa[i], va);
-        Raw4<T>::unpack(xb[i], vb);
-        if (turned) rope_turn(ga, gb, cs, sn, a.interleaved, -1.f);
-        float ss = 0.f, dot = 0.f;
+      for (int i = 0; i < K; ++i) {
+        if (h + i >= h1) break;
+        if (normed || back.turned) {
+          V8 g = back.of(rg[i].unpack());
+          if (normed) {
+            // with u = x r: dw += g u, dx = r (w g - u mean(w g u))
+            V8 u = rx[i].unpack(), wg;
+            V2 s2 = mul2(u.v[0], u.v[0]);
+            wg.v[0] = mul2(w.v[0], g.v[0]);
+            V2 d2 = mul2(wg.v[0], u.v[0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ss = fmaf(va[j], va[j], fmaf(vb[j], vb[j], ss));
-          dot = fmaf(wa[j] * ga[j], va[j], fmaf(wb[j] * gb[j], vb[j], dot));
-        }
-        ss = row_sum<D>(ss);
-        dot = row_sum<D>(dot);
-        if (p.w) {
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-          const float c = r * r * r * dot * (1.f / D);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (h + i < h1) {
-              dwa[j] = fmaf(ga[j], va[j] * r, dwa[j]);
-              dwb[j] = fmaf(gb[j], vb[j] * r, dwb[j]);
+            for (int j = 1; j < 4; ++j) {
+              s2 = fma2(u.v[j], u.v[j], s2);
+              wg.v[j] = mul2(w.v[j], g.v[j]);
+              d2 = fma2(wg.v[j], u.v[j], d2);
             }
-            ga[j] = r * (wa[j] * ga[j]) - va[j] * c;
-            gb[j] = r * (wb[j] * gb[j]) - vb[j] * c;
+            float ss = sum2(s2), dot = sum2(d2);
+            slot_sum2<D>(ss, dot, [](float s) { return s; });
+            const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+            const float m = -r * dot * (1.f / D);
+            const V2 rr = f2pack(r, r), mm = f2pack(m, m);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              u.v[j] = mul2(u.v[j], rr);
+              // a lane without a row has g = u = 0
+              dw.v[j] = fma2(g.v[j], u.v[j], dw.v[j]);
+              g.v[j] = mul2(fma2(u.v[j], mm, wg.v[j]), rr);
+            }
           }
+          rg[i].pack(g);
         }
-        if (h + i < h1) {
-          T* o = dx + (h + i) * p.dx_h;
-          *reinterpret_cast<typename Raw4<T>::Bits*>(o + oa) = Raw4<T>::pack(ga);
-          *reinterpret_cast<typename Raw4<T>::Bits*>(o + ob) = Raw4<T>::pack(gb);
-        }
+        if (live) rg[i].store(dx + i * p.dx_h, lane.a, lane.b);
       }
     }
   }
   if (p.partial == nullptr) return;
-  // [slot][column]: slot s of the block wrote columns oa .. oa + 3 and ob .. ob + 3
+  // [slot][column]: a slot has every column once
   float* mine = red + (threadIdx.x / L) * D;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    mine[oa + j] = dwa[j];
-    mine[ob + j] = dwb[j];
-  }
+  *reinterpret_cast<float4*>(mine + lane.a) = Raw4<float>::pack(dw.v);
+  *reinterpret_cast<float4*>(mine + lane.b) = Raw4<float>::pack(dw.v + 2);
   __syncthreads();
   if (threadIdx.x < D) {
     float s = 0.f;
     for (int i = 0; i < kSlots; ++i) s += red[i * D + threadIdx.x];
-    p.partial[(long long)blk * D + threadIdx.x] = s;
+    p.partial[((long long)run * gridDim.x + blockIdx.x) * D + threadIdx.x] = s;
   }
 }
 
@@ -247,54 +180,43 @@ norm_rope_dw_kernel(const float* pq, const float* pk, int qblocks, int kblocks, 
   }
 }
 
-// Heads a slot takes one after the other: as many as still leave every SM its threads twice
-// over (a token's angles are then computed once for them), at least one.
-int heads_per_run(long long tokens, int heads, int lanes, int sms) {
-  int run = 1;
-  while (run < heads && tokens * ((heads + 2 * run - 1) / (2 * run)) * lanes >= 4096LL * sms)
-    run *= 2;
-  return run;
-}
-
 template <typename T, int D>
 cudaError_t forward_d(NormRopeArgs<T>& a, int sms, cudaStream_t st) {
-  constexpr int kSlots = kRopeThreads / (D / 8);
-  const long long tokens = (long long)a.B * a.N;
-  a.run = heads_per_run(tokens, a.part[0].heads + a.part[1].heads, D / 8, sms);
-  const long long items = tokens * ((a.part[0].heads + a.run - 1) / a.run +
-                                    (a.part[1].heads + a.run - 1) / a.run);
-  const int grid = (int)std::min<long long>((items + kSlots - 1) / kSlots, 8LL * sms);
+  const RopeGrid g = rope_grid((long long)a.B * a.N, a.part[0].heads + a.part[1].heads,
+                               kRopeThreads / (D / 8), kRopeBlocks, sms);
+  a.run = g.run;
   count_launch();
-  return launch_pdl(norm_rope_kernel<T, D>, dim3(grid), dim3(kRopeThreads), 0, st, a);
+  return launch_pdl(a.interleaved ? norm_rope_kernel<T, D, true> : norm_rope_kernel<T, D, false>,
+                    dim3(g.x, g.y), dim3(kRopeThreads), 0, st, a);
 }
 
 template <typename T, int D>
 cudaError_t backward_d(NormRopeBackwardArgs<T>& a, float* partial, int sms, float* dwq, float* dwk,
                        cudaStream_t st) {
-  constexpr int kSlots = kRopeThreads / (D / 8);
-  const long long tokens = (long long)a.B * a.N;
-  a.run = heads_per_run(tokens, a.part[0].heads + a.part[1].heads, D / 8, sms);
-  const long long iq = tokens * ((a.part[0].heads + a.run - 1) / a.run);
-  const long long ik = tokens * ((a.part[1].heads + a.run - 1) / a.run);
-  const long long bq = (iq + kSlots - 1) / kSlots, bk = (ik + kSlots - 1) / kSlots;
-  const int cap = norm_rope_backward_blocks(sms);
-  int qb = (int)bq, kb = (int)bk;
-  if (bq + bk > cap) {
-    // the blocks in proportion to the two parts' rows, one at least for each part that has any
-    kb = ik == 0 ? 0 : (int)std::max<long long>(1, cap * ik / (iq + ik));
-    qb = cap - kb;
-  }
-  a.qblocks = qb;
+  const int hq = a.part[0].heads, hk = a.part[1].heads;
+  RopeGrid g = rope_grid((long long)a.B * a.N, hq + hk, kRopeThreads / (D / 8),
+                         kRopeBackwardBlocks, sms);
+  // runs do not cross from q to k, so there can be one more of them than the rule counts; the
+  // blocks stay within the workspace's rows
+  a.run = g.run;
+  auto runs = [&](int heads) { return (heads + a.run - 1) / a.run; };
+  const int most = norm_rope_backward_blocks(sms);
+  while (runs(hq) + runs(hk) > most) a.run *= 2;
+  a.qruns = runs(hq);
+  const int y = a.qruns + runs(hk);
+  const int x = std::min(g.x, most / y);
   a.part[0].partial = dwq ? partial : nullptr;
-  a.part[1].partial = dwk ? partial + (size_t)qb * D : nullptr;
+  a.part[1].partial = dwk ? partial + (size_t)x * a.qruns * D : nullptr;
   count_launch();
-  cudaError_t e = launch_pdl(norm_rope_backward_kernel<T, D>, dim3(qb + kb), dim3(kRopeThreads), 0,
-                             st, a);
+  cudaError_t e =
+      launch_pdl(a.interleaved ? norm_rope_backward_kernel<T, D, true>
+                               : norm_rope_backward_kernel<T, D, false>,
+                 dim3(x, y), dim3(kRopeThreads), 0, st, a);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
   count_launch();
   return launch_pdl(norm_rope_dw_kernel, dim3(2, D / 16), dim3(256), 0, st,
-                    (const float*)a.part[0].partial, (const float*)a.part[1].partial, qb, kb, D,
-                    dwq, dwk);
+                    (const float*)a.part[0].partial, (const float*)a.part[1].partial, x * a.qruns,
+                    x * (y - a.qruns), D, dwq, dwk);
 }
 
 }  // namespace

@@ -10,8 +10,11 @@ current torch CUDA stream unless `stream` is given.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -57,14 +60,11 @@ def load() -> ctypes.CDLL:
                 "mita_dense_attn": [P, P, P, I, I, I, I, P, P],
                 "mita_backward": [P, P, P, P, I, I, I, I, I, I, I, I, I, P, P, P, P, P],
             }
-            I64, U64, F = ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
-            sigs.update({
-                "mita_qk_norm_rope": [P] * 5 + [I64, P] + [I] * 7 + [F] + [P] * 7,
-                "mita_qk_norm_rope_backward": [P] * 7 + [I64, P] + [I] * 7 + [F] + [P] * 7 + [U64]
-                                              + [P] * 5,
-                "mita_cache_append": [P] * 9 + [I] * 10 + [F] + [P] * 8,
-                "mita_paged_attn": [P] * 6 + [I] * 7 + [P, F, F, I, P, U64] + [P] * 3,
-            })
+            # arguments in a struct, packed by the caller
+            U64 = ctypes.c_uint64
+            for name in ("mita_qk_norm_rope", "mita_qk_norm_rope_backward", "mita_cache_append",
+                         "mita_paged_attn"):
+                sigs[name] = [ctypes.c_char_p, P]
             for name, at in sigs.items():
                 for suffix in ("", "_f32"):
                     f = getattr(lib, name + suffix)
@@ -240,99 +240,116 @@ class MiTAFunction(torch.autograd.Function):
 # These calls run on the tensors' device, whatever the current one is, and on `stream` (the
 # device's current stream by default).  What they allocate (outputs, workspaces) belongs to that
 # stream; the caller orders the stream with the ones its inputs come from.
+#
+# A step of a decoder makes a few of these calls for microseconds of GPU work, so the binding's
+# own time counts: arguments go to C as one packed struct (the layouts below are the
+# header's *_params), and tensors are checked with as few attribute reads as it takes.
 # ---------------------------------------------------------------------------
-class _Launch:
-    """The device and stream of one call, as the current ones while it allocates and launches."""
+_NORM_ROPE = struct.Struct("8P13q7if")
+_NORM_ROPE_BACKWARD = struct.Struct("13PQ19q7if")
+_CACHE_APPEND = struct.Struct("12P8q10if4x")
+_PAGED_ATTN = struct.Struct("9PQ2q8i2f")
+_NO_STRIDES = (0, 0, 0)
 
-    __slots__ = ("_outer", "handle")
+_typed = {}
 
-    def __init__(self, stream, device: torch.device):
-        self._outer = []
-        if device.index != torch.cuda.current_device():
-            self._outer.append(torch.cuda.device(device))
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.handle = stream.cuda_stream
-            self._outer.append(torch.cuda.stream(stream))
+
+def _typed_fn(name: str, dtype: torch.dtype):
+    fn = _typed.get((name, dtype))
+    if fn is None:
+        fn = _typed[name, dtype] = _fn(name, dtype)
+    return fn
+
+
+class _on:
+    """`device` and `stream` (or its current stream) as the current ones."""
+
+    def __init__(self, stream, device: int):
+        if stream is not None and stream.device_index != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{device}")
+        self._stack = contextlib.ExitStack()
+        self._enter = (torch.cuda.device(device), torch.cuda.stream(stream))
 
     def __enter__(self):
-        for c in self._outer:
-            c.__enter__()
-        return self.handle
+        for c in self._enter:
+            self._stack.enter_context(c)
 
     def __exit__(self, *exc):
-        for c in reversed(self._outer):
-            c.__exit__(*exc)
+        return self._stack.__exit__(*exc)
 
 
-def _need_rows(t: torch.Tensor, name: str, dim: int, dtype=None, device=None, out: bool = False):
-    """A CUDA tensor of contiguous rows (its other dimensions may have any strides)."""
+def _device_of(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    return t.get_device()
+
+
+def _place(t: torch.Tensor, name: str, shape, dtype, device: int):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if out and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-        raise ValueError(f"{name}: an output cannot be a broadcast view")
-    return t
-
-
-def _need_shape(t: torch.Tensor, name: str, shape):
-    if t.shape != tuple(shape):
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return t
 
 
-def _strides(t: torch.Tensor):
+def _rows(t: torch.Tensor, name: str, shape, dtype, device: int):
+    """Checks a strided input of contiguous rows; returns the strides of its other dimensions."""
+    _place(t, name, shape, dtype, device)
     s = t.stride()
-    return (ctypes.c_int64 * (len(s) - 1))(*s[:-1])
+    if s[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return s[:-1]
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _out_rows(t: torch.Tensor, name: str, shape, dtype, device: int):
+    """_rows of an output that the caller gave."""
+    s = _rows(t, name, shape, dtype, device)
+    if any(n > 1 and step == 0 for n, step in zip(shape, s)):
+        raise ValueError(f"{name}: an output cannot be a broadcast view")
+    return s
 
 
-def _need_rope(inv_freq, weights, d: int, device):
-    """Checks the frequencies and norm weights; returns the rotated width."""
-    for w, name in weights:
-        if w is not None:
-            _need_shape(_need(w, name, torch.float32, device), name, (d,))
+def _dense_strides(H: int, N: int, d: int):
+    return (H * N * d, N * d, d)
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype, device: int):
+    """Checks a contiguous tensor; returns its address."""
+    _place(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rope_of(inv_freq, device: int):
+    """(address, rotated width) of the frequencies."""
     if inv_freq is None:
-        return 0
-    _need(inv_freq, "inv_freq", torch.float64, device)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must have one dimension")
-    return 2 * inv_freq.shape[0]
+        return 0, 0
+    n = inv_freq.numel()
+    return _dense(inv_freq, "inv_freq", (n,), torch.float64, device), 2 * n
 
 
-def _need_positions(positions, B: int, N: int, device):
+def _weight(w, name: str, d: int, device: int):
+    return 0 if w is None else _dense(w, name, (d,), torch.float32, device)
+
+
+def _positions_of(positions, B: int, N: int, device: int):
     """(address, elements between batches) of positions [N] or [B, N]."""
     if positions is None:
-        return None, 0
-    if not positions.is_cuda or positions.dtype != torch.int32 or positions.device != device:
-        raise TypeError(f"positions must be an int32 tensor on {device}")
-    if positions.shape not in ((N,), (B, N)):
-        raise ValueError(f"positions must be {(N,)} or {(B, N)}, got {tuple(positions.shape)}")
-    if N > 1 and positions.stride(-1) != 1:
-        raise ValueError("positions: the last dimension must be contiguous")
-    return positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+        return 0, 0
+    if positions.dim() == 2:
+        step, = _rows(positions, "positions", (B, N), torch.int32, device)
+        return positions.data_ptr(), step if B > 1 else 0
+    return _dense(positions, "positions", (N,), torch.int32, device), 0
 
 
-def _like_rows(x: torch.Tensor) -> torch.Tensor:
-    """An empty gradient for x [B, H, N, d]: dense like a dense x, else token-major (the heads of
-    a token side by side, as in the projection's output that x is a view of)."""
-    if x.is_contiguous():
-        return torch.empty_like(x)
-    B, H, N, d = x.shape
-    return torch.empty((B, N, H, d), dtype=x.dtype, device=x.device).transpose(1, 2)
+def _like_rows(x: torch.Tensor, shape):
+    """An empty gradient for x [B, H, N, d] and its strides: dense like a dense x, else token-major
+    (the heads of a token side by side, as in the projection's output that x is a view of)."""
+    B, H, N, d = shape
+    s = _dense_strides(H, N, d) if x.is_contiguous() else (N * H * d, d, H * d)
+    return torch.empty_strided(shape, s + (1,), dtype=x.dtype, device=x.device), s
 
 
 def mita_qk_norm_rope(q, k=None, inv_freq=None, q_weight=None, k_weight=None, positions=None,
@@ -346,31 +363,42 @@ def mita_qk_norm_rope(q, k=None, inv_freq=None, q_weight=None, k_weight=None, po
     most d).  q_weight, k_weight: float32 [d] (None: not normalised).  positions: int32 [N] or
     [B,N] (None: 0..N-1).  interleaved: pairs (2i, 2i+1) instead of (i, i + rot/2).
     q_out may be q and k_out may be k."""
-    _need_rows(q, "q", 4)
-    dev, dt = q.device, q.dtype
-    fn = _fn("mita_qk_norm_rope", dt)
-    B, Hq, N, d = q.shape
-    Hkv = 0
-    if k is not None:
-        Hkv = _need_rows(k, "k", 4, dt, dev).shape[1]
-        _need_shape(k, "k", (B, Hkv, N, d))
-    rot = _need_rope(inv_freq, ((q_weight, "q_weight"), (k_weight, "k_weight")), d, dev)
-    pos, pos_b = _need_positions(positions, B, N, dev)
-    with _Launch(stream, dev) as st:
-        if q_out is None:
-            q_out = torch.empty((B, Hq, N, d), dtype=dt, device=dev)
+    dev = _device_of(q, "q")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(stream, dev):
+            return mita_qk_norm_rope(q, k, inv_freq, q_weight, k_weight, positions, eps,
+                                     interleaved, q_out, k_out)
+    dt = q.dtype
+    fn = _typed_fn("mita_qk_norm_rope", dt)
+    shape = B, Hq, N, d = q.shape
+    qs = _rows(q, "q", shape, dt, dev)
+    freq, rot = _rope_of(inv_freq, dev)
+    pos, pos_b = _positions_of(positions, B, N, dev)
+    qw, kw = _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=dt, device=q.device)
+        qos = _dense_strides(Hq, N, d)
+    else:
+        qos = _out_rows(q_out, "q_out", shape, dt, dev)
+    Hkv = kp = kop = 0
+    ks = kos = _NO_STRIDES
+    if k is None:
+        k_out = None
+    else:
+        Hkv = k.shape[1]
+        kshape = (B, Hkv, N, d)
+        ks = _rows(k, "k", kshape, dt, dev)
+        if k_out is None:
+            k_out = torch.empty(kshape, dtype=dt, device=q.device)
+            kos = _dense_strides(Hkv, N, d)
         else:
-            _need_shape(_need_rows(q_out, "q_out", 4, dt, dev, out=True), "q_out", q.shape)
-        if k is None:
-            k_out = None
-        elif k_out is None:
-            k_out = torch.empty((B, Hkv, N, d), dtype=dt, device=dev)
-        else:
-            _need_shape(_need_rows(k_out, "k_out", 4, dt, dev, out=True), "k_out", k.shape)
-        _check(fn(_addr(q), _addr(k), _addr(q_weight), _addr(k_weight), pos, pos_b,
-                  _addr(inv_freq), B, Hq, Hkv, N, d, rot, int(interleaved), eps, _strides(q),
-                  None if k is None else _strides(k), _strides(q_out),
-                  None if k is None else _strides(k_out), _addr(q_out), _addr(k_out), st))
+            kos = _out_rows(k_out, "k_out", kshape, dt, dev)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    rc = fn(_NORM_ROPE.pack(q.data_ptr(), kp, qw, kw, pos, freq, q_out.data_ptr(), kop, *qs, *ks,
+                            *qos, *kos, pos_b, B, Hq, Hkv, N, d, rot, interleaved, eps),
+            _raw_stream(dev))
+    if rc:
+        _check(rc)
     return q_out, k_out
 
 
@@ -381,46 +409,59 @@ def mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq=None, q_weight=Non
     outputs.  dq and dk have the inputs' type, and unless given are dense where q is and token-major
     ([B,N,H,d] in memory) where it is a view; the weights' gradients are float32 (None
     without the weight).  k and dk_out may both be None.  dq may be dq_out, dk may be dk_out."""
-    _need_rows(q, "q", 4)
-    dev, dt = q.device, q.dtype
-    fn = _fn("mita_qk_norm_rope_backward", dt)
-    B, Hq, N, d = q.shape
-    _need_shape(_need_rows(dq_out, "dq_out", 4, dt, dev), "dq_out", q.shape)
+    dev = _device_of(q, "q")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(stream, dev):
+            return mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq, q_weight, k_weight,
+                                              positions, eps, interleaved, dq, dk)
+    dt = q.dtype
+    fn = _typed_fn("mita_qk_norm_rope_backward", dt)
+    shape = B, Hq, N, d = q.shape
+    qs = _rows(q, "q", shape, dt, dev)
+    dqos = _rows(dq_out, "dq_out", shape, dt, dev)
+    freq, rot = _rope_of(inv_freq, dev)
+    pos, pos_b = _positions_of(positions, B, N, dev)
+    if dq is None:
+        dq, dqs = _like_rows(q, shape)
+    else:
+        dqs = _out_rows(dq, "dq", shape, dt, dev)
+    Hkv = kp = dkop = dkp = 0
+    ks = dkos = dks = _NO_STRIDES
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out: both or neither")
-    Hkv = 0
-    if k is not None:
-        Hkv = _need_rows(k, "k", 4, dt, dev).shape[1]
-        _need_shape(k, "k", (B, Hkv, N, d))
-        _need_shape(_need_rows(dk_out, "dk_out", 4, dt, dev), "dk_out", k.shape)
+    if k is None:
+        dk = k_weight = None
     else:
-        k_weight = None
-    rot = _need_rope(inv_freq, ((q_weight, "q_weight"), (k_weight, "k_weight")), d, dev)
-    pos, pos_b = _need_positions(positions, B, N, dev)
-    with _Launch(stream, dev) as st:
-        if dq is None:
-            dq = _like_rows(q)
+        Hkv = k.shape[1]
+        kshape = (B, Hkv, N, d)
+        ks = _rows(k, "k", kshape, dt, dev)
+        dkos = _rows(dk_out, "dk_out", kshape, dt, dev)
+        if dk is None:
+            dk, dks = _like_rows(k, kshape)
         else:
-            _need_shape(_need_rows(dq, "dq", 4, dt, dev, out=True), "dq", q.shape)
-        if k is None:
-            dk = None
-        elif dk is None:
-            dk = _like_rows(k)
-        else:
-            _need_shape(_need_rows(dk, "dk", 4, dt, dev, out=True), "dk", k.shape)
-        dwq, dwk = (None if w is None else torch.empty(d, dtype=torch.float32, device=dev)
-                    for w in (q_weight, k_weight))
-        ws, nbytes = None, 0
-        if dwq is not None or dwk is not None:
-            nbytes = load().mita_qk_norm_rope_backward_workspace_bytes(d)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(fn(_addr(q), _addr(k), _addr(dq_out), _addr(dk_out), _addr(q_weight),
-                  _addr(k_weight), pos, pos_b, _addr(inv_freq), B, Hq, Hkv, N, d, rot,
-                  int(interleaved), eps, _strides(q), None if k is None else _strides(k),
-                  _strides(dq_out), None if k is None else _strides(dk_out), _strides(dq),
-                  None if k is None else _strides(dk), _addr(ws), nbytes, _addr(dq), _addr(dk),
-                  _addr(dwq), _addr(dwk), st))
+            dks = _out_rows(dk, "dk", kshape, dt, dev)
+        kp, dkop, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
+    qw, kw = _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev)
+    dwq = dwk = ws = None
+    nbytes = 0
+    if qw or kw:
+        nbytes = _norm_rope_backward_bytes(d, dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        dwq = torch.empty(d, dtype=torch.float32, device=q.device) if qw else None
+        dwk = torch.empty(d, dtype=torch.float32, device=q.device) if kw else None
+    rc = fn(_NORM_ROPE_BACKWARD.pack(
+        q.data_ptr(), kp, dq_out.data_ptr(), dkop, qw, kw, pos, freq, dq.data_ptr(), dkp,
+        dwq.data_ptr() if qw else 0, dwk.data_ptr() if kw else 0, ws.data_ptr() if nbytes else 0,
+        nbytes, *qs, *ks, *dqos, *dkos, *dqs, *dks, pos_b, B, Hq, Hkv, N, d, rot, interleaved,
+        eps), _raw_stream(dev))
+    if rc:
+        _check(rc)
     return dq, dk, dwq, dwk
+
+
+@functools.lru_cache(maxsize=None)
+def _norm_rope_backward_bytes(d: int, device: int) -> int:
+    return load().mita_qk_norm_rope_backward_workspace_bytes(d)
 
 
 class QKNormRopeFunction(torch.autograd.Function):
@@ -442,31 +483,29 @@ class QKNormRopeFunction(torch.autograd.Function):
         q, k, inv_freq, q_weight, k_weight, positions = ctx.saved_tensors
         eps, interleaved = ctx.cfg
         dq, dk, dwq, dwk = mita_qk_norm_rope_backward(
-            q, k, _rows_of(dq_out), None if k is None else _rows_of(dk_out), inv_freq, q_weight,
-            k_weight, positions, eps, interleaved)
+            q, k, _aligned_rows(dq_out), None if k is None else _aligned_rows(dk_out), inv_freq,
+            q_weight, k_weight, positions, eps, interleaved)
         return dq, dk, None, dwq, dwk, None, None, None
 
 
-def _rows_of(t: torch.Tensor) -> torch.Tensor:
-    """t itself where its rows can be read as they lie, else a dense copy (broadcast gradients)."""
+def _aligned_rows(t: torch.Tensor) -> torch.Tensor:
+    """t itself where its rows can be read as they lie, else a dense copy."""
     step = 16 // t.element_size()
     ok = t.stride(-1) == 1 and all(n == 1 or s % step == 0
                                    for n, s in zip(t.shape[:-1], t.stride()[:-1]))
     return t if ok and t.data_ptr() % 16 == 0 else t.contiguous()
 
 
-def _need_cache(k_cache, v_cache, page_table, lengths, dtype, device):
-    """(S, num_pages, Hkv, page_size, d, table width) of a paged cache."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, name, dtype, device)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d]")
-    _need(page_table, "page_table", torch.int32, device)
-    _need(lengths, "lengths", torch.int32, device)
-    if page_table.dim() != 2 or lengths.shape != (page_table.shape[0],):
-        raise ValueError("page_table must be [S, width] and lengths [S]")
-    pages, Hkv, page, d = k_cache.shape
-    return page_table.shape[0], pages, Hkv, page, d, page_table.shape[1]
+def _cache_of(k_cache, v_cache, page_table, lengths, dtype, device: int):
+    """(addresses), (S, num_pages, Hkv, page_size, d, table width) of a paged cache."""
+    shape = k_cache.shape
+    if len(shape) != 4 or page_table.dim() != 2:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] and page_table [S, width]")
+    S, width = tshape = page_table.shape
+    return ((_dense(k_cache, "k_cache", shape, dtype, device),
+             _dense(v_cache, "v_cache", shape, dtype, device),
+             _dense(page_table, "page_table", tshape, torch.int32, device),
+             _dense(lengths, "lengths", (S,), torch.int32, device)), (S, *shape, width))
 
 
 def mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start=None, q=None,
@@ -481,32 +520,38 @@ def mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start=Non
     ones (0: an idle slot, nothing is written for it); seq_start: int32 [S+1], the rows of each
     sequence's new tokens (None: row s is sequence s's only one).  Rows that belong to no sequence
     or to an idle slot leave q_out as it is."""
-    _need_rows(k, "k", 3)
-    dev, dt = k.device, k.dtype
-    fn = _fn("mita_cache_append", dt)
-    S, pages, Hkv, page, d, width = _need_cache(k_cache, v_cache, page_table, lengths, dt, dev)
+    dev = _device_of(k, "k")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(stream, dev):
+            return mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start, q,
+                                     inv_freq, q_weight, k_weight, eps, interleaved, q_out)
+    dt = k.dtype
+    fn = _typed_fn("mita_cache_append", dt)
+    (kc, vc, table, n), (S, pages, Hkv, page, d, width) = _cache_of(k_cache, v_cache, page_table,
+                                                                    lengths, dt, dev)
     T = k.shape[0]
-    _need_shape(k, "k", (T, Hkv, d))
-    _need_shape(_need_rows(v, "v", 3, dt, dev), "v", (T, Hkv, d))
-    if seq_start is not None:
-        _need_shape(_need(seq_start, "seq_start", torch.int32, dev), "seq_start", (S + 1,))
-    Hq = 0
-    if q is not None:
-        Hq = _need_rows(q, "q", 3, dt, dev).shape[1]
-        _need_shape(q, "q", (T, Hq, d))
-    rot = _need_rope(inv_freq, ((q_weight, "q_weight"), (k_weight, "k_weight")), d, dev)
-    with _Launch(stream, dev) as st:
-        if q is None:
-            q_out = None
-        elif q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+    ks, vs = _rows(k, "k", (T, Hkv, d), dt, dev), _rows(v, "v", (T, Hkv, d), dt, dev)
+    start = 0 if seq_start is None else _dense(seq_start, "seq_start", (S + 1,), torch.int32, dev)
+    freq, rot = _rope_of(inv_freq, dev)
+    qw, kw = _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev)
+    Hq = qp = qop = 0
+    qs = qos = (0, 0)
+    if q is None:
+        q_out = None
+    else:
+        Hq = q.shape[1]
+        qs = _rows(q, "q", (T, Hq, d), dt, dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            qos = (Hq * d, d)
         else:
-            _need_shape(_need_rows(q_out, "q_out", 3, dt, dev, out=True), "q_out", q.shape)
-        _check(fn(_addr(q), _addr(k), _addr(v), _addr(q_weight), _addr(k_weight), _addr(inv_freq),
-                  _addr(page_table), _addr(lengths), _addr(seq_start), T, S, Hq, Hkv, d, pages,
-                  page, width, rot, int(interleaved), eps, None if q is None else _strides(q),
-                  _strides(k), _strides(v), None if q is None else _strides(q_out), _addr(q_out),
-                  _addr(k_cache), _addr(v_cache), st))
+            qos = _out_rows(q_out, "q_out", (T, Hq, d), dt, dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    rc = fn(_CACHE_APPEND.pack(qp, k.data_ptr(), v.data_ptr(), qw, kw, freq, table, n, start, qop,
+                               kc, vc, *qs, *ks, *vs, *qos, T, S, Hq, Hkv, d, pages, page, width,
+                               rot, interleaved, eps), _raw_stream(dev))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -520,28 +565,45 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     scale: of the scores (None: d^-1/2).  softcap > 0: scores capped to softcap*tanh(z/softcap).
     alibi_slopes: float32 [Hq], adds slope*(key position - own position).  window > 0: only the
     last `window` keys.  Idle slots (length 0) get zeros and lse -inf."""
-    _need_rows(q, "q", 3)
-    dev, dt = q.device, q.dtype
-    fn = _fn("mita_paged_attn", dt)
-    S, pages, Hkv, page, d, width = _need_cache(k_cache, v_cache, page_table, lengths, dt, dev)
+    dev = _device_of(q, "q")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(stream, dev):
+            return mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale, softcap,
+                                   window, alibi_slopes, return_lse, out)
+    dt = q.dtype
+    fn = _typed_fn("mita_paged_attn", dt)
+    (kc, vc, table, n), (S, pages, Hkv, page, d, width) = _cache_of(k_cache, v_cache, page_table,
+                                                                    lengths, dt, dev)
     Hq = q.shape[1]
-    _need_shape(q, "q", (S, Hq, d))
+    shape = (S, Hq, d)
+    qs = _rows(q, "q", shape, dt, dev)
+    slopes = 0
     if alibi_slopes is not None:
-        _need_shape(_need(alibi_slopes, "alibi_slopes", torch.float32, dev), "alibi_slopes", (Hq,))
-    with _Launch(stream, dev) as st:
-        if out is None:
-            out = torch.empty((S, Hq, d), dtype=dt, device=dev)
-        else:
-            _need_shape(_need(out, "out", dt, dev), "out", q.shape)
-        lse = torch.empty((S, Hq), dtype=torch.float32, device=dev) if return_lse else None
-        nbytes = load().mita_paged_attn_workspace_bytes(S, Hq, Hkv, d, page, width,
-                                                        int(dt == torch.float32))
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(fn(_addr(q), _addr(k_cache), _addr(v_cache), _addr(page_table), _addr(lengths),
-                  _addr(alibi_slopes), S, Hq, Hkv, d, pages, page, width, _strides(q),
-                  d ** -0.5 if scale is None else scale, softcap, window, _addr(ws), nbytes,
-                  _addr(out), _addr(lse), st))
+        slopes = _dense(alibi_slopes, "alibi_slopes", (Hq,), torch.float32, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", shape, dt, dev)
+    lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    nbytes = _paged_attn_bytes(S, Hq, Hkv, d, page, width, dt is torch.float32, dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    rc = fn(_PAGED_ATTN.pack(q.data_ptr(), kc, vc, table, n, slopes, ws.data_ptr(), op,
+                             lse.data_ptr() if return_lse else 0, nbytes, *qs, S, Hq, Hkv, d,
+                             pages, page, width, window, d ** -0.5 if scale is None else scale,
+                             softcap), _raw_stream(dev))
+    if rc:
+        _check(rc)
     return (out, lse) if return_lse else out
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_attn_bytes(S, Hq, Hkv, d, page, width, f32, device: int) -> int:
+    return load().mita_paged_attn_workspace_bytes(S, Hq, Hkv, d, page, width, f32)
+
+
+# the handle of torch.cuda.current_stream(device), without making a Stream object of it (1.1 us)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def mita_dense_attn(q, k, v, out=None, stream=None):
