@@ -15,7 +15,7 @@
 // its last slot of the workspace, and paged_join_kernel joins those of a segment in
 // their order.  Nothing is added atomically: the result depends on the inputs alone.
 //
-// A warp works on its own 16 keys of each tile through its own ring of shared-memory stages,
+// A warp works on its own keys of each tile (kKeys) through its own ring of shared-memory stages,
 // filled by 16-byte asynchronous copies some stages ahead, across the ends of segments; warps
 // meet only where a segment ends.  Rows that are not to be seen (beyond the length, before the
 // window, on an invalid page) are filled with zeros and never read: what the cache holds there,
@@ -29,23 +29,25 @@
 namespace mita {
 namespace {
 
-constexpr int kWarpKeys = 16;          // keys of a warp in a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kNoSegment = -1;
 constexpr int kMaxPagedCtas = 512;     // CTAs of a call: parts of a segment that can be joined
 
-// Shared memory and shape of one instantiation.  RT: query rows of a CTA.
+// Shared memory and shape of one instantiation.  RT: query rows of a CTA.  A warp's stage is 8 KB
+// (less for small heads, whose tiles would get too long): enough work behind each wait, and
+// stages for 128 KB on the way to each SM.
 template <typename T, int D, int RT>
 struct Shape {
   static constexpr bool kTensor = std::is_same<T, bf16>::value;
-  static constexpr int kWarps = kTensor ? 8 : 4;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kTile = kWarps * kWarpKeys;
   static constexpr int kRowBytes = D * (int)sizeof(T);
+  static constexpr int kKeys = (kTensor ? 32 : 16) / (D == 128 ? 2 : 1);   // of a warp in a tile
+  static constexpr int kTile = kWarps * kKeys;
   static constexpr int kChunks = kRowBytes / 16;               // 16-byte chunks of a row
-  static constexpr int kStageBytes = 2 * kWarpKeys * kRowBytes;  // K then V
-  static constexpr int kStages = kStageBytes * kWarps * 8 <= 196608 ? 8 : 196608 / (kStageBytes * kWarps);
+  static constexpr int kStageBytes = 2 * kKeys * kRowBytes;    // K then V
+  static constexpr int kStages = kStageBytes == 8192 ? 3 : kStageBytes == 4096 ? 6 : 8;
   static constexpr int kRing = kStages * kStageBytes;          // of one warp
   static constexpr int kJoinFloats = 5120;                     // outputs being joined over warps
   // byte offsets
@@ -55,7 +57,7 @@ struct Shape {
   static constexpr int kOffMask = kOffTop + RT * 8;                       // [warps][stages]
   static constexpr int kOffQ = kOffMask + ((kWarps * kStages * 4 + 15) / 16) * 16;
   static constexpr int kOffP = kOffQ + (kTensor ? 0 : RT * D * 4);        // fp32: q rows
-  static constexpr int kBytes = kOffP + (kTensor ? 0 : kWarps * RT * kWarpKeys * 4);
+  static constexpr int kBytes = kOffP + (kTensor ? 0 : kWarps * RT * kKeys * 4);
   static_assert(kBytes <= 232448 && kStages >= 3, "shared memory");
 };
 
@@ -197,6 +199,7 @@ struct ScoreRule {
   float scale2;          // scale * log2(e): the scores of the running softmax are in log2 units
   float cap, cap2, rcap; // softcap (0: none), softcap * log2(e), scale / softcap
   int last;              // len - 1
+  bool plain;            // scores are just scale2 * dot, with scale2 >= 0
 };
 __device__ __forceinline__ float score_of(const ScoreRule& r, float dot, float slope2, int key) {
   float z = dot * r.scale2;
@@ -205,18 +208,19 @@ __device__ __forceinline__ float score_of(const ScoreRule& r, float dot, float s
 }
 
 // ---------------------------------------------------------------------------
-// One warp's running softmax, bf16 on the tensor cores.  A lane has rows lane / 4 and + 8 of
-// the 16 query rows, and columns (lane % 4) * 2, + 1 of every eight keys or values.
-// Rows behind the last query head hold zeros and are computed with the others: the matrix
-// instruction has 16 rows whether they are used or not.
+// One warp's running softmax, bf16 on the tensor cores.  A lane has row lane / 4 of the query
+// rows, for RT = 16 also row lane / 4 + 8, and columns (lane % 4) * 2, + 1 of every eight keys or
+// values.  The matrix instruction has 16 rows whether they are used or not; those behind
+// the last query head, and the upper eight of RT = 8, are zeros.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, int RT>
 struct TensorState {
-  using S = Shape<bf16, D, 16>;
+  using S = Shape<bf16, D, RT>;
+  static constexpr int kHalves = RT / 8;
   uint32_t q[D / 16][4];
   float o[D / 8][4];
-  float m[2], l[2];      // l: of this lane's columns
-  float slope2[2];
+  float m[kHalves], l[kHalves];      // l: of this lane's columns
+  float slope2[kHalves];
 
   __device__ __forceinline__ void start(const PagedAttnArgs<bf16>& a, int s, int head, int rows,
                                         uint8_t*) {
@@ -224,7 +228,7 @@ struct TensorState {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = lane / 4 + 8 * i;
-      const bool ok = r < rows;
+      const bool ok = i < kHalves && r < rows;
       const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + s * a.q_s +
                                                             (long long)(head + r) * a.q_h);
 #pragma unroll
@@ -232,9 +236,11 @@ struct TensorState {
         q[k][i] = ok ? p[k * 8 + lane % 4] : 0u;
         q[k][i + 2] = ok ? p[k * 8 + 4 + lane % 4] : 0u;
       }
-      slope2[i] = ok && a.slopes ? a.slopes[head + r] * kLog2e : 0.f;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
+      if (i < kHalves) {
+        slope2[i] = ok && a.slopes ? a.slopes[head + r] * kLog2e : 0.f;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
     }
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
@@ -242,83 +248,102 @@ struct TensorState {
       for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
   }
 
-  // kt, vt: the warp's 16 key and value rows; key0 the first one's position; `mask` the seen ones
+  // kt, vt: the warp's key and value rows; key0 the first one's position; `mask` the seen ones
   __device__ __forceinline__ void tile(const ScoreRule& rule, uint32_t kt, uint32_t vt, int key0,
                                        unsigned mask) {
+    constexpr int kT = S::kKeys / 8;
     const int lane = threadIdx.x & 31;
-    float z[2][4] = {};
+    float z[kT][4] = {};
     {
       const int row = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t b[4];
-        ldsm4(kt + row * S::kRowBytes + swizzle<S::kRowBytes>(row, 2 * k + c) * 16, b);
-        mma16816(z[0], q[k], b[0], b[1]);
-        mma16816(z[1], q[k], b[2], b[3]);
-      }
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int t = 0; t < kT; t += 2) {
+          uint32_t b[4];
+          ldsm4(kt + (row + 8 * t) * S::kRowBytes +
+                    swizzle<S::kRowBytes>(row + 8 * t, 2 * k + c) * 16, b);
+          mma16816(z[t], q[k], b[0], b[1]);
+          mma16816(z[t + 1], q[k], b[2], b[3]);
+        }
     }
-    float top[2] = {m[0], m[1]};
+    // z becomes the scores, or stays the dot products where a factor is all that is missing
+    float factor = rule.scale2;
+    if (!rule.plain || mask != (unsigned)((1ull << S::kKeys) - 1)) {
+      factor = 1.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = 8 * t + (lane % 4) * 2 + (i & 1);
-        z[t][i] = (mask >> j) & 1 ? score_of(rule, z[t][i], slope2[i >> 1], key0 + j) : -INFINITY;
-        top[i >> 1] = fmaxf(top[i >> 1], z[t][i]);
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        for (int i = 0; i < 2 * kHalves; ++i) {
+          const int j = 8 * t + (lane % 4) * 2 + (i & 1);
+          z[t][i] = (mask >> j) & 1 ? score_of(rule, z[t][i], slope2[i >> 1], key0 + j)
+                                    : -INFINITY;
+        }
     }
-    float base[2];
+    float base[kHalves];
+    bool moved = false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) base[i] = top[i] == -INFINITY ? 0.f : top[i];
+    for (int i = 0; i < kHalves; ++i) {
+      float top = fmaxf(z[0][2 * i], z[0][2 * i + 1]);
+#pragma unroll
+      for (int t = 1; t < kT; ++t) top = fmaxf(top, fmaxf(z[t][2 * i], z[t][2 * i + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      base[i] = fmaxf(m[i], top * factor);
+      moved |= base[i] != m[i];
+    }
     // the running values move to the new maxima; most tiles bring none
-    if (__any_sync(0xffffffffu, top[0] != m[0] || top[1] != m[1])) {
-      float f[2];
+    if (__any_sync(0xffffffffu, moved)) {
+      float f[2] = {1.f, 1.f};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        f[i] = exp2_fast(m[i] - base[i]);
+      for (int i = 0; i < kHalves; ++i) {
+        f[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - base[i]);
         l[i] *= f[i];
-        m[i] = top[i];
+        m[i] = base[i];
       }
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        o[j][0] *= f[0];
-        o[j][1] *= f[0];
-        o[j][2] *= f[1];
-        o[j][3] *= f[1];
-      }
+      for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * kHalves; ++i) o[j][i] *= f[i >> 1];
     }
+#pragma unroll
+    for (int i = 0; i < kHalves; ++i) base[i] = base[i] == -INFINITY ? 0.f : base[i];
     // The weights go to the value product as a sum of two bf16 values, 16 bits in all: one alone
     // would add an error of the size of the output's own rounding, and the second product
     // is free where HBM is the bound.
-    uint32_t hi[4], lo[4];
+    uint32_t hi[kT / 2][4], lo[kT / 2][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float p0 = exp2_fast(z[t][2 * i] - base[i]), p1 = exp2_fast(z[t][2 * i + 1] - base[i]);
-        l[i] += p0 + p1;
-        const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-        hi[2 * t + i] = *reinterpret_cast<const uint32_t*>(&h);
-        const __nv_bfloat162 e = __floats2bfloat162_rn(
-            p0 - __uint_as_float(hi[2 * t + i] << 16),
-            p1 - __uint_as_float(hi[2 * t + i] & 0xffff0000u));
-        lo[2 * t + i] = *reinterpret_cast<const uint32_t*>(&e);
+        uint32_t& h = hi[t / 2][2 * (t & 1) + i];
+        uint32_t& e = lo[t / 2][2 * (t & 1) + i];
+        h = e = 0;
+        if (i < kHalves) {
+          const float p0 = exp2_fast(fmaf(z[t][2 * i], factor, -base[i]));
+          const float p1 = exp2_fast(fmaf(z[t][2 * i + 1], factor, -base[i]));
+          l[i] += p0 + p1;
+          const __nv_bfloat162 hh = __floats2bfloat162_rn(p0, p1);
+          h = *reinterpret_cast<const uint32_t*>(&hh);
+          const __nv_bfloat162 ee = __floats2bfloat162_rn(p0 - __uint_as_float(h << 16),
+                                                          p1 - __uint_as_float(h & 0xffff0000u));
+          e = *reinterpret_cast<const uint32_t*>(&ee);
+        }
       }
     {
       const int row = lane & 15, c = lane >> 4;
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t b[4];
-        ldsm4_t(vt + row * S::kRowBytes + swizzle<S::kRowBytes>(row, 2 * j + c) * 16, b);
-        mma16816(o[2 * j], hi, b[0], b[1]);
-        mma16816(o[2 * j + 1], hi, b[2], b[3]);
-        mma16816(o[2 * j], lo, b[0], b[1]);
-        mma16816(o[2 * j + 1], lo, b[2], b[3]);
-      }
+      for (int t = 0; t < kT / 2; ++t)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t b[4];
+          ldsm4_t(vt + (row + 16 * t) * S::kRowBytes +
+                      swizzle<S::kRowBytes>(row + 16 * t, 2 * j + c) * 16, b);
+          mma16816(o[2 * j], hi[t], b[0], b[1]);
+          mma16816(o[2 * j + 1], hi[t], b[2], b[3]);
+          mma16816(o[2 * j], lo[t], b[0], b[1]);
+          mma16816(o[2 * j + 1], lo[t], b[2], b[3]);
+        }
     }
   }
 
@@ -326,7 +351,7 @@ struct TensorState {
   __device__ __forceinline__ void put_ml(float2* ml) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kHalves; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (lane % 4 == 0) ml[lane / 4 + 8 * i] = make_float2(m[i], l[i]);
@@ -337,7 +362,7 @@ struct TensorState {
                                         const float* top) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kHalves; ++i) {
       const int r = lane / 4 + 8 * i;
       if (r >= rows) continue;
       const float f = exp2_fast(m[i] - top[r]);
@@ -352,15 +377,16 @@ struct TensorState {
 
 // ---------------------------------------------------------------------------
 // One warp's running softmax, fp32 on the FMA units: a tensor-core product of fp32 values would
-// round them.  For the scores a lane has one key and half of the columns; for the
+// round them.  For the scores a lane has one key and a share of the columns; for the
 // values D / 32 columns (one, in the lower half of the warp, for D = 16).
 // ---------------------------------------------------------------------------
 template <int D, int RT>
 struct FmaState {
   using S = Shape<float, D, RT>;
   static constexpr int V = D >= 32 ? D / 32 : 1;
+  static constexpr int kParts = 32 / S::kKeys;     // lanes that share a key
   float o[RT][V];
-  float m[RT], l[RT];    // l: of this lane's key, in the lower half of the warp
+  float m[RT], l[RT];    // l: of this lane's key, in the first of its lanes
 
   __device__ __forceinline__ void start(const PagedAttnArgs<float>& a, int s, int head, int rows,
                                         uint8_t* smem) {
@@ -380,13 +406,13 @@ struct FmaState {
   __device__ __forceinline__ void tile(const ScoreRule& rule, const uint8_t* stage, int key0,
                                        unsigned mask, int rows, uint8_t* smem, const float* slopes,
                                        int head) {
-    const int lane = threadIdx.x & 31, key = lane & 15, half = lane >> 4;
+    const int lane = threadIdx.x & 31, key = lane % S::kKeys, part = lane / S::kKeys;
     const float* q = reinterpret_cast<const float*>(smem + S::kOffQ);
-    float* p = reinterpret_cast<float*>(smem + S::kOffP) + (threadIdx.x >> 5) * RT * kWarpKeys;
+    float* p = reinterpret_cast<float*>(smem + S::kOffP) + (threadIdx.x >> 5) * RT * S::kKeys;
     float z[RT] = {};
 #pragma unroll 2
-    for (int c = 0; c < D / 8; ++c) {
-      const int ch = half * (D / 8) + c;
+    for (int c = 0; c < D / 4 / kParts; ++c) {
+      const int ch = part * (D / 4 / kParts) + c;
       const float4 k = *reinterpret_cast<const float4*>(
           stage + key * S::kRowBytes + swizzle<S::kRowBytes>(key, ch) * 16);
 #pragma unroll
@@ -400,28 +426,30 @@ struct FmaState {
 #pragma unroll
     for (int r = 0; r < RT; ++r)
       if (r < rows) {
-        z[r] += __shfl_xor_sync(0xffffffffu, z[r], 16);
+#pragma unroll
+        for (int i = 16; i >= S::kKeys; i >>= 1) z[r] += __shfl_xor_sync(0xffffffffu, z[r], i);
         z[r] = seen ? score_of(rule, z[r], slopes ? slopes[head + r] * kLog2e : 0.f, key0 + key)
                     : -INFINITY;
         float top = z[r];
 #pragma unroll
-        for (int i = 8; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        for (int i = S::kKeys / 2; i > 0; i >>= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
         top = fmaxf(top, m[r]);
         const float base = top == -INFINITY ? 0.f : top;
         const float f = exp2_fast(m[r] - base);
         const float w = exp2_fast(z[r] - base);
         m[r] = top;
-        l[r] = fmaf(l[r], f, half ? 0.f : w);
+        l[r] = fmaf(l[r], f, part ? 0.f : w);
 #pragma unroll
         for (int v = 0; v < V; ++v) o[r][v] *= f;
-        if (half == 0) p[r * kWarpKeys + key] = w;
+        if (part == 0) p[r * S::kKeys + key] = w;
       }
     __syncwarp();
     if (lane * V < D) {
-      const uint8_t* vs = stage + kWarpKeys * S::kRowBytes;
+      const uint8_t* vs = stage + S::kKeys * S::kRowBytes;
       const int ch = lane * V / 4, in = lane * V % 4 * 4;
 #pragma unroll
-      for (int k4 = 0; k4 < kWarpKeys / 4; ++k4) {
+      for (int k4 = 0; k4 < S::kKeys / 4; ++k4) {
         float x[4][V];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -441,7 +469,7 @@ struct FmaState {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
           if (r < rows) {
-            const float4 w = *reinterpret_cast<const float4*>(p + r * kWarpKeys + 4 * k4);
+            const float4 w = *reinterpret_cast<const float4*>(p + r * S::kKeys + 4 * k4);
 #pragma unroll
             for (int v = 0; v < V; ++v)
               o[r][v] = fmaf(w.x, x[0][v], fmaf(w.y, x[1][v], fmaf(w.z, x[2][v],
@@ -479,56 +507,79 @@ template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return __flo
 
 // ---------------------------------------------------------------------------
 // The warp's loader: page numbers one tile ahead of the copies, copies kStages - 1 tiles
-// ahead of the arithmetic.
+// ahead of the arithmetic.  Where a page holds all of a warp's keys of a tile (they then lie one
+// behind the other) one page number does for all; smaller pages are looked up row by row.
 // ---------------------------------------------------------------------------
 template <typename T, int D, int RT>
 struct Loader {
   using S = Shape<T, D, RT>;
   Cursor at;
   long long left;        // tiles not looked up yet
-  int page, key, head;   // of the tile looked up last: this lane's key
-  bool ok;
+  int page, key0, head;  // of the tile looked up last; page: of this lane's key
+  unsigned mask;         // its keys to be seen
 
   __device__ __forceinline__ void look_up(const PagedAttnArgs<T>& a, int HR) {
-    ok = false;
+    mask = 0;
     if (left <= 0) return;
     --left;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    key = at.span.base + at.t * S::kTile + warp * kWarpKeys + (lane & 15);
-    ok = key >= at.span.first && key < at.span.len;
-    head = at.hr / a.row_blocks;
-    if (ok) page = __ldg(a.paged.table + (long long)at.s * a.paged.width +
-                         (key >> a.paged.page_log2));
+    const int warp = threadIdx.x >> 5;
+    key0 = at.span.base + at.t * S::kTile + warp * S::kKeys;
+    const int lo = max(at.span.first - key0, 0), hi = min(at.span.len - key0, S::kKeys);
+    if (lo < hi) {
+      constexpr unsigned kAll = (unsigned)((1ull << S::kKeys) - 1);
+      mask = (kAll << lo) & (kAll >> (S::kKeys - hi));
+      head = at.hr / a.row_blocks;
+      // lanes whose key is not to be seen read the first one's page
+      const int mine = (threadIdx.x & 31) % S::kKeys;
+      const int key = key0 + ((mask >> mine) & 1 ? mine : lo);
+      page = __ldg(a.paged.table + (long long)at.s * a.paged.width + (key >> a.paged.page_log2));
+    }
     advance(at, a.paged, a.window, S::kTile, HR);
   }
 
   // copies the looked-up tile's rows to `stage`, notes which of them are seen, and commits
-  __device__ __forceinline__ void issue(const PagedAttnArgs<T>& a, uint8_t* stage,
+  __device__ __forceinline__ void issue(const PagedAttnArgs<T>& a, uint32_t stage,
                                         unsigned* mask_out) {
     const int lane = threadIdx.x & 31;
-    if (ok && (page < 0 || page >= a.paged.num_pages)) {
-      flag_error(a.status, kDevErrBadIndex);
-      ok = false;
+    if (mask) {
+      const bool bad = page < 0 || page >= a.paged.num_pages;
+      const unsigned wrong = __ballot_sync(0xffffffffu, bad);
+      if (wrong) {
+        if (lane == 0) flag_error(a.status, kDevErrBadIndex);
+        mask &= ~wrong;
+      }
     }
-    const unsigned mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
     if (lane == 0) *mask_out = mask;
     if (mask) {
       constexpr int kPerPass = 32 / S::kChunks;      // rows a warp copies at once
-      const int c = lane % S::kChunks;
-      const int in_page = (1 << a.paged.page_log2) - 1;
+      constexpr int kPasses = S::kKeys / kPerPass;
+      const int c = lane % S::kChunks, r0 = lane / S::kChunks;
+      const int log2 = a.paged.page_log2, in_page = (1 << log2) - 1;
+      if ((1 << log2) >= S::kKeys) {
+        const long long first = ((((long long)page * a.Hkv + head) << log2) + (key0 & in_page)) * D;
+        const long long off = first + r0 * D + c * (16 / (int)sizeof(T));
+        const T *k = a.k_cache + off, *v = a.v_cache + off;
 #pragma unroll
-      for (int i = 0; i < kWarpKeys / kPerPass; ++i) {
-        const int row = i * kPerPass + lane / S::kChunks;
-        const int pg = __shfl_sync(0xffffffffu, page, row);
-        const int ky = __shfl_sync(0xffffffffu, key, row);
-        const bool live = (mask >> row) & 1;
-        const long long at_row = (((long long)pg * a.Hkv + head) << a.paged.page_log2) +
-                                 (ky & in_page);
-        const long long off = live ? at_row * D + c * (16 / (int)sizeof(T)) : 0;
-        const uint32_t dst = smem_addr(stage) + row * S::kRowBytes +
-                             swizzle<S::kRowBytes>(row, c) * 16;
-        copy16(dst, a.k_cache + off, live);
-        copy16(dst + kWarpKeys * S::kRowBytes, a.v_cache + off, live);
+        for (int i = 0; i < kPasses; ++i) {
+          const int row = i * kPerPass + r0;
+          const uint32_t dst = stage + row * S::kRowBytes + swizzle<S::kRowBytes>(row, c) * 16;
+          const bool live = (mask >> row) & 1;
+          copy16(dst, k + i * kPerPass * D, live);
+          copy16(dst + S::kKeys * S::kRowBytes, v + i * kPerPass * D, live);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int row = i * kPerPass + r0;
+          const int pg = __shfl_sync(0xffffffffu, page, row);
+          const bool live = (mask >> row) & 1;
+          const long long at_row = (((long long)pg * a.Hkv + head) << log2) +
+                                   ((key0 + row) & in_page);
+          const long long off = live ? at_row * D + c * (16 / (int)sizeof(T)) : 0;
+          const uint32_t dst = stage + row * S::kRowBytes + swizzle<S::kRowBytes>(row, c) * 16;
+          copy16(dst, a.k_cache + off, live);
+          copy16(dst + S::kKeys * S::kRowBytes, a.v_cache + off, live);
+        }
       }
     }
     copy_commit();
@@ -545,7 +596,7 @@ template <typename T, int D, int RT>
 __global__ void __launch_bounds__(Shape<T, D, RT>::kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   using S = Shape<T, D, RT>;
-  using State = typename std::conditional<S::kTensor, TensorState<D>, FmaState<D, RT>>::type;
+  using State = typename std::conditional<S::kTensor, TensorState<D, RT>, FmaState<D, RT>>::type;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
@@ -575,11 +626,11 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
     Loader<T, D, RT> ld;
     ld.at = at;
     ld.left = u1 - u0;
-    ld.page = ld.key = ld.head = 0;
+    ld.page = ld.key0 = ld.head = 0;
     ld.look_up(a, HR);
 #pragma unroll 1
     for (int i = 0; i < S::kStages - 1; ++i) {
-      ld.issue(a, ring + i * S::kStageBytes, masks + i);
+      ld.issue(a, smem_addr(ring) + i * S::kStageBytes, masks + i);
       ld.look_up(a, HR);
     }
     State st;
@@ -588,6 +639,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
     rule.cap = a.softcap;
     rule.cap2 = a.softcap * kLog2e;
     rule.rcap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+    rule.plain = a.softcap == 0.f && a.slopes == nullptr && a.scale >= 0.f;
     int slot = 0, next = S::kStages - 1;     // stages: of this tile, of the next one to issue
     int from = at.t, head = 0, rows = 0;
     bool begin = true;
@@ -603,14 +655,14 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       }
       copy_wait<S::kStages - 2>();
       __syncwarp();
-      ld.issue(a, ring + next * S::kStageBytes, masks + next);
+      ld.issue(a, smem_addr(ring) + next * S::kStageBytes, masks + next);
       ld.look_up(a, HR);
       const unsigned mask = masks[slot];
       if (mask) {
         uint8_t* stage = ring + slot * S::kStageBytes;
-        const int key0 = at.span.base + at.t * S::kTile + warp * kWarpKeys;
+        const int key0 = at.span.base + at.t * S::kTile + warp * S::kKeys;
         if constexpr (S::kTensor)
-          st.tile(rule, smem_addr(stage), smem_addr(stage) + kWarpKeys * S::kRowBytes, key0, mask);
+          st.tile(rule, smem_addr(stage), smem_addr(stage) + S::kKeys * S::kRowBytes, key0, mask);
         else
           st.tile(rule, stage, key0, mask, rows, smem, a.slopes, head);
       }
@@ -778,27 +830,21 @@ struct Run {
   }
 };
 
-// The instantiation for a head dim, type and group: bf16 takes 16 query rows to a CTA (the
-// matrix instruction's height), fp32 four where the group has no more.
+// The instantiation for a head dim, type and group: a CTA takes 8 query rows where the group has no
+// more (fp32: 4), else 16, the matrix instruction's height.
+template <typename T, int RT, typename F>
+auto with_dim(int d, F f) {
+  switch (d) {
+    case 16: return f(Run<T, 16, RT>{});
+    case 32: return f(Run<T, 32, RT>{});
+    case 64: return f(Run<T, 64, RT>{});
+    default: return f(Run<T, 128, RT>{});
+  }
+}
 template <typename T, typename F>
 auto with_shape(int d, int G, F f) {
-  constexpr bool tensor = std::is_same<T, bf16>::value;
-  if constexpr (!tensor) {
-    if (G <= 4) {
-      switch (d) {
-        case 16: return f(Run<T, 16, 4>{});
-        case 32: return f(Run<T, 32, 4>{});
-        case 64: return f(Run<T, 64, 4>{});
-        default: return f(Run<T, 128, 4>{});
-      }
-    }
-  }
-  switch (d) {
-    case 16: return f(Run<T, 16, 16>{});
-    case 32: return f(Run<T, 32, 16>{});
-    case 64: return f(Run<T, 64, 16>{});
-    default: return f(Run<T, 128, 16>{});
-  }
+  constexpr int kSmall = std::is_same<T, bf16>::value ? 8 : 4;
+  return G <= kSmall ? with_dim<T, kSmall>(d, f) : with_dim<T, 16>(d, f);
 }
 
 }  // namespace
