@@ -719,21 +719,21 @@ int device_state_for(cudaStream_t st, DevState** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  bool known = false;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_dev.find(dev);
-    known = it != g_dev.end() && it->second.status != nullptr;
+    if (it != g_dev.end() && it->second.status != nullptr) {
+      *out = &it->second;
+      return MITA_OK;
+    }
   }
-  if (!known) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    e = cudaStreamIsCapturing(st, &cs);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-    if (cs != cudaStreamCaptureStatusNone)
-      return fail(MITA_ERR_UNSUPPORTED,
-                  "the library's first call on a device cannot be captured; make one outside "
-                  "capture first");
-  }
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  e = cudaStreamIsCapturing(st, &cs);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  if (cs != cudaStreamCaptureStatusNone)
+    return fail(MITA_ERR_UNSUPPORTED,
+                "the library's first call on a device cannot be captured; make one outside "
+                "capture first");
   return device_state(out);
 }
 

@@ -37,6 +37,7 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
   constexpr int L = D / 8, kSlots = kRopeThreads / L, K = kRopeAhead<T>;
   __shared__ unsigned long long table[D / 2];
   griddep_wait();
+  griddep_launch();
   rope_table(a.inv_freq, a.rot / 2, table);
   __syncthreads();
   const RopeLane lane(threadIdx.x % L, a.rot, INTER);

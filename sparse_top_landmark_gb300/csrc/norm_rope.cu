@@ -29,6 +29,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs<T> a) {
   constexpr int L = D / 8, kSlots = kRopeThreads / L, K = kRopeAhead<T>;
   __shared__ unsigned long long table[D / 2];
   griddep_wait();
+  griddep_launch();
   rope_table(a.inv_freq, a.rot / 2, table);
   __syncthreads();
   const RopeLane lane(threadIdx.x % L, a.rot, INTER);
@@ -74,6 +75,7 @@ norm_rope_backward_kernel(const __grid_constant__ NormRopeBackwardArgs<T> a) {
   __shared__ unsigned long long table[D / 2];
   __shared__ __align__(16) float red[kRopeThreads * 8];
   griddep_wait();
+  griddep_launch();
   rope_table(a.inv_freq, a.rot / 2, table);
   __syncthreads();
   const RopeLane lane(threadIdx.x % L, a.rot, INTER);

@@ -21,6 +21,7 @@
 // window, on an invalid page) are filled with zeros and never read: what the cache holds there,
 // NaN included, reaches nothing.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -31,7 +32,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum before the first key: below every finite score, and finite, so that
+// differences with it need no special case (a score of -inf weighs nothing against it).
+constexpr float kLowest = -FLT_MAX;
 constexpr int kNoSegment = -1;
+constexpr int kJoinThreads = 256;
 constexpr int kMaxPagedCtas = 512;     // CTAs of a call: parts of a segment that can be joined
 
 // Shared memory and shape of one instantiation.  RT: query rows of a CTA.  A warp's stage is 8 KB
@@ -100,6 +105,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// An 8 x 8 matrix of 16-bit values, two of a row in a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 // c[16 x 8] += a[16 x 16] b[16 x 8], bf16 products summed in fp32
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -208,63 +219,66 @@ __device__ __forceinline__ float score_of(const ScoreRule& r, float dot, float s
 }
 
 // ---------------------------------------------------------------------------
-// One warp's running softmax, bf16 on the tensor cores.  A lane has row lane / 4 of the query
-// rows, for RT = 16 also row lane / 4 + 8, and columns (lane % 4) * 2, + 1 of every eight keys or
-// values.  The matrix instruction has 16 rows whether they are used or not; those behind
-// the last query head, and the upper eight of RT = 8, are zeros.
+// One warp's running softmax, bf16 on the tensor cores.  Both products are taken transposed, keys
+// and value columns on the matrix instruction's 16 rows and the query heads on its 8 columns: the
+// group of a key head seldom has more than 8, and half of a 16-row tile would be padding.  (The
+// queries on the 16 rows measured 334.9 us where this takes 330.9, 128 sequences of up to 8192 keys.)
+// A lane has columns (lane % 4) * 2, + 1 of each eight query heads (those behind the last are
+// zeros), and rows lane / 4, + 8 of every 16 keys or value columns.
 // ---------------------------------------------------------------------------
 template <int D, int RT>
 struct TensorState {
   using S = Shape<bf16, D, RT>;
-  static constexpr int kHalves = RT / 8;
-  uint32_t q[D / 16][4];
-  float o[D / 8][4];
-  float m[kHalves], l[kHalves];      // l: of this lane's columns
-  float slope2[kHalves];
+  static constexpr int kN = RT / 8;  // tiles of eight query heads
+  uint32_t q[D / 16][kN][2];
+  float o[D / 16][kN][4];
+  float m[kN][2], l[kN][2];          // l: of this lane's keys
+  float slope2[kN][2];
 
   __device__ __forceinline__ void start(const PagedAttnArgs<bf16>& a, int s, int head, int rows,
                                         uint8_t*) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = lane / 4 + 8 * i;
-      const bool ok = i < kHalves && r < rows;
+    for (int n = 0; n < kN; ++n) {
+      const int r = 8 * n + lane / 4;
       const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + s * a.q_s +
                                                             (long long)(head + r) * a.q_h);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        q[k][i] = ok ? p[k * 8 + lane % 4] : 0u;
-        q[k][i + 2] = ok ? p[k * 8 + 4 + lane % 4] : 0u;
+        q[k][n][0] = r < rows ? p[k * 8 + lane % 4] : 0u;
+        q[k][n][1] = r < rows ? p[k * 8 + 4 + lane % 4] : 0u;
       }
-      if (i < kHalves) {
-        slope2[i] = ok && a.slopes ? a.slopes[head + r] * kLog2e : 0.f;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = 8 * n + lane % 4 * 2 + i;
+        slope2[n][i] = a.slopes && c < rows ? a.slopes[head + c] * kLog2e : 0.f;
+        m[n][i] = kLowest;
+        l[n][i] = 0.f;
       }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][n][i] = 0.f;
     }
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
   }
 
   // kt, vt: the warp's key and value rows; key0 the first one's position; `mask` the seen ones
   __device__ __forceinline__ void tile(const ScoreRule& rule, uint32_t kt, uint32_t vt, int key0,
                                        unsigned mask) {
-    constexpr int kT = S::kKeys / 8;
+    constexpr int kT = S::kKeys / 16;
     const int lane = threadIdx.x & 31;
-    float z[kT][4] = {};
+    float z[kT][kN][4] = {};
     {
-      const int row = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
+      const int row = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-        for (int t = 0; t < kT; t += 2) {
-          uint32_t b[4];
-          ldsm4(kt + (row + 8 * t) * S::kRowBytes +
-                    swizzle<S::kRowBytes>(row + 8 * t, 2 * k + c) * 16, b);
-          mma16816(z[t], q[k], b[0], b[1]);
-          mma16816(z[t + 1], q[k], b[2], b[3]);
+        for (int t = 0; t < kT; ++t) {
+          uint32_t x[4];
+          ldsm4(kt + (row + 16 * t) * S::kRowBytes +
+                    swizzle<S::kRowBytes>(row + 16 * t, 2 * k + c) * 16, x);
+#pragma unroll
+          for (int n = 0; n < kN; ++n) mma16816(z[t][n], x, q[k][n][0], q[k][n][1]);
         }
     }
     // z becomes the scores, or stays the dot products where a factor is all that is missing
@@ -274,75 +288,80 @@ struct TensorState {
 #pragma unroll
       for (int t = 0; t < kT; ++t)
 #pragma unroll
-        for (int i = 0; i < 2 * kHalves; ++i) {
-          const int j = 8 * t + (lane % 4) * 2 + (i & 1);
-          z[t][i] = (mask >> j) & 1 ? score_of(rule, z[t][i], slope2[i >> 1], key0 + j)
-                                    : -INFINITY;
-        }
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = 16 * t + lane / 4 + 8 * (i >> 1);
+            z[t][n][i] = (mask >> j) & 1 ? score_of(rule, z[t][n][i], slope2[n][i & 1], key0 + j)
+                                         : -INFINITY;
+          }
     }
-    float base[kHalves];
-    bool moved = false;
-#pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      float top = fmaxf(z[0][2 * i], z[0][2 * i + 1]);
-#pragma unroll
-      for (int t = 1; t < kT; ++t) top = fmaxf(top, fmaxf(z[t][2 * i], z[t][2 * i + 1]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      base[i] = fmaxf(m[i], top * factor);
-      moved |= base[i] != m[i];
-    }
-    // the running values move to the new maxima; most tiles bring none
-    if (__any_sync(0xffffffffu, moved)) {
-      float f[2] = {1.f, 1.f};
-#pragma unroll
-      for (int i = 0; i < kHalves; ++i) {
-        f[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - base[i]);
-        l[i] *= f[i];
-        m[i] = base[i];
-      }
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 2 * kHalves; ++i) o[j][i] *= f[i >> 1];
-    }
-#pragma unroll
-    for (int i = 0; i < kHalves; ++i) base[i] = base[i] == -INFINITY ? 0.f : base[i];
-    // The weights go to the value product as a sum of two bf16 values, 16 bits in all: one alone
-    // would add an error of the size of the output's own rounding, and the second product
-    // is free where HBM is the bound.
-    uint32_t hi[kT / 2][4], lo[kT / 2][4];
+    // The running maxima are looked for again only where a score is above them: most tiles
+    // bring none, and need no exchange between lanes.
+    bool above = false;
 #pragma unroll
     for (int t = 0; t < kT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t& h = hi[t / 2][2 * (t & 1) + i];
-        uint32_t& e = lo[t / 2][2 * (t & 1) + i];
-        h = e = 0;
-        if (i < kHalves) {
-          const float p0 = exp2_fast(fmaf(z[t][2 * i], factor, -base[i]));
-          const float p1 = exp2_fast(fmaf(z[t][2 * i + 1], factor, -base[i]));
-          l[i] += p0 + p1;
-          const __nv_bfloat162 hh = __floats2bfloat162_rn(p0, p1);
-          h = *reinterpret_cast<const uint32_t*>(&hh);
-          const __nv_bfloat162 ee = __floats2bfloat162_rn(p0 - __uint_as_float(h << 16),
-                                                          p1 - __uint_as_float(h & 0xffff0000u));
-          e = *reinterpret_cast<const uint32_t*>(&ee);
-        }
-      }
-    {
-      const int row = lane & 15, c = lane >> 4;
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int t = 0; t < kT / 2; ++t)
+        for (int i = 0; i < 4; ++i) above |= fmaf(z[t][n][i], factor, -m[n][i & 1]) > 0.f;
+    if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = fmaxf(z[0][n][i], z[0][n][i + 2]);
+#pragma unroll
+          for (int t = 1; t < kT; ++t) top = fmaxf(top, fmaxf(z[t][n][i], z[t][n][i + 2]));
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          top = fmaxf(m[n][i], top * factor);
+          f[i] = exp2_fast(m[n][i] - top);
+          l[n][i] *= f[i];
+          m[n][i] = top;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][n][i] *= f[i & 1];
+      }
+    }
+    // The weights go to the value product as a sum of two bf16 values, 16 bits in all: one alone
+    // would add an error of the size of the output's own rounding, and the second product
+    // is free where HBM is the bound.
+    uint32_t hi[kT][kN][2], lo[kT][kN][2];
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p0 = exp2_fast(fmaf(z[t][n][2 * i], factor, -m[n][0]));
+          const float p1 = exp2_fast(fmaf(z[t][n][2 * i + 1], factor, -m[n][1]));
+          l[n][0] += p0;
+          l[n][1] += p1;
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+          const uint32_t h = *reinterpret_cast<const uint32_t*>(&h2);
+          const __nv_bfloat162 e2 = __floats2bfloat162_rn(p0 - __uint_as_float(h << 16),
+                                                          p1 - __uint_as_float(h & 0xffff0000u));
+          hi[t][n][i] = transpose8(h);
+          lo[t][n][i] = transpose8(*reinterpret_cast<const uint32_t*>(&e2));
+        }
+    {
+      const int row = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-          uint32_t b[4];
+          uint32_t x[4];
           ldsm4_t(vt + (row + 16 * t) * S::kRowBytes +
-                      swizzle<S::kRowBytes>(row + 16 * t, 2 * j + c) * 16, b);
-          mma16816(o[2 * j], hi[t], b[0], b[1]);
-          mma16816(o[2 * j + 1], hi[t], b[2], b[3]);
-          mma16816(o[2 * j], lo[t], b[0], b[1]);
-          mma16816(o[2 * j + 1], lo[t], b[2], b[3]);
+                      swizzle<S::kRowBytes>(row + 16 * t, 2 * j + c) * 16, x);
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            mma16816(o[j][n], x, hi[t][n][0], hi[t][n][1]);
+            mma16816(o[j][n], x, lo[t][n][0], lo[t][n][1]);
+          }
         }
     }
   }
@@ -351,27 +370,30 @@ struct TensorState {
   __device__ __forceinline__ void put_ml(float2* ml) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (lane % 4 == 0) ml[lane / 4 + 8 * i] = make_float2(m[i], l[i]);
-    }
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
+        if (lane < 4) ml[8 * n + lane * 2 + i] = make_float2(m[n][i], l[n][i]);
+      }
   }
   // columns [c0, c0 + C) of the rows below `rows`, moved to the maxima `top`, to dst[row][..]
   __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
                                         const float* top) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      const int r = lane / 4 + 8 * i;
-      if (r >= rows) continue;
-      const float f = exp2_fast(m[i] - top[r]);
+    for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        if (8 * j >= c0 && 8 * j < c0 + C)
-          *reinterpret_cast<float2*>(dst + r * stride + 8 * j - c0 + (lane % 4) * 2) =
-              make_float2(o[j][2 * i] * f, o[j][2 * i + 1] * f);
-    }
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * n + lane % 4 * 2 + i;
+        if (r >= rows) continue;
+        const float f = exp2_fast(m[n][i] - top[r]);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          if (8 * j >= c0 && 8 * j < c0 + C)
+            dst[r * stride + 8 * j - c0 + lane / 4] = o[j / 2][n][(j & 1) * 2 + i] * f;
+      }
   }
 };
 
@@ -396,7 +418,7 @@ struct FmaState {
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      m[r] = -INFINITY;
+      m[r] = kLowest;
       l[r] = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) o[r][v] = 0.f;
@@ -435,9 +457,8 @@ struct FmaState {
         for (int i = S::kKeys / 2; i > 0; i >>= 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
         top = fmaxf(top, m[r]);
-        const float base = top == -INFINITY ? 0.f : top;
-        const float f = exp2_fast(m[r] - base);
-        const float w = exp2_fast(z[r] - base);
+        const float f = exp2_fast(m[r] - top);
+        const float w = exp2_fast(z[r] - top);
         m[r] = top;
         l[r] = fmaf(l[r], f, part ? 0.f : w);
 #pragma unroll
@@ -606,18 +627,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   unsigned* masks = reinterpret_cast<unsigned*>(smem + S::kOffMask) + warp * S::kStages;
 
   griddep_wait();
-  // sequences without a key: zeros, and the logarithm of an empty sum
-  for (int s = blockIdx.x; s < a.paged.S; s += gridDim.x) {
-    const int len = a.paged.lengths[s];
-    if (threadIdx.x == 0 && (len < 0 || len > (long long)a.paged.width << a.paged.page_log2))
-      flag_error(a.status, kDevErrBadIndex);
-    if (len > 0 && a.paged.width > 0) continue;
-    for (int e = threadIdx.x; e < Hq * D; e += S::kThreads)
-      a.out[(long long)s * Hq * D + e] = from_f<T>(0.f);
-    if (a.lse)
-      for (int e = threadIdx.x; e < Hq; e += S::kThreads) a.lse[(long long)s * Hq + e] = -INFINITY;
-  }
-
+  griddep_launch();
   long long u0, u1, total;
   Cursor at;
   my_share(a.paged, a.window, S::kTile, HR, &u0, &u1, &total, &at);
@@ -676,9 +686,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
         __syncthreads();
         float* top = reinterpret_cast<float*>(smem + S::kOffTop);
         if (threadIdx.x < RT) {
-          float t = -INFINITY, sum = 0.f;
-          for (int w = 0; w < S::kWarps; ++w) t = fmaxf(t, ml[w * RT + threadIdx.x].x);
-          const float base = t == -INFINITY ? 0.f : t;
+          float base = kLowest, sum = 0.f;
+          for (int w = 0; w < S::kWarps; ++w) base = fmaxf(base, ml[w * RT + threadIdx.x].x);
           for (int w = 0; w < S::kWarps; ++w) {
             const float2 x = ml[w * RT + threadIdx.x];
             sum = fmaf(x.y, exp2_fast(x.x - base), sum);
@@ -737,46 +746,68 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
     a.meta[blockIdx.x * 2] = last_seg;
     a.meta[blockIdx.x * 2 + 1] = last_cta;
   }
+  // sequences without a key: zeros, and the logarithm of an empty sum
+  for (int s = blockIdx.x; s < a.paged.S; s += gridDim.x) {
+    const int len = a.paged.lengths[s];
+    if (threadIdx.x == 0 && (len < 0 || len > (long long)a.paged.width << a.paged.page_log2))
+      flag_error(a.status, kDevErrBadIndex);
+    if (len > 0 && a.paged.width > 0) continue;
+    for (int e = threadIdx.x; e < Hq * D; e += S::kThreads)
+      a.out[(long long)s * Hq * D + e] = from_f<T>(0.f);
+    if (a.lse)
+      for (int e = threadIdx.x; e < Hq; e += S::kThreads) a.lse[(long long)s * Hq + e] = -INFINITY;
+  }
 }
 
 // Joins the partials of a segment that was cut: its beginning is CTA c's last part, its rest
-// the first parts of CTAs c + 1 .. last.  Block (c, row), one column a thread.
+// the first parts of CTAs c + 1 .. last.  Block (c, row).  A segment may be in as many parts as there
+// are CTAs, so they are dealt to groups of D / 4 threads (four columns each), whose loads are all on
+// their way together, and the groups' sums are added in their order.
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
-  __shared__ float weight[kMaxPagedCtas];
-  __shared__ float red[5];
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  __shared__ __align__(16) float sums[kGroups][D];
   griddep_wait();
   const int c = blockIdx.x, r = blockIdx.y;
-  const int seg = a.meta[c * 2];
-  if (seg == kNoSegment) return;
-  const int n = a.meta[c * 2 + 1] - c + 1;
+  const int2 cut = reinterpret_cast<const int2*>(a.meta)[c];
+  if (cut.x == kNoSegment) return;
+  const int n = cut.y - c + 1;
   const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
-  const int s = seg / HR, hr = seg % HR, rb = hr % a.row_blocks;
+  const int s = cut.x / HR, hr = cut.x % HR, rb = hr % a.row_blocks;
   if (r >= min(RT, a.G - rb * RT)) return;
   auto part_of = [&](int i) { return (long long)(i == 0 ? c * 2 + 1 : (c + i) * 2) * RT + r; };
-  float top = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const float2 x = reinterpret_cast<const float2*>(a.part_ml)[part_of(i)];
-    if (x.y != 0.f) top = fmaxf(top, x.x);      // a part without a key has no maximum
-  }
-  top = block_max(top, red);
-  const float base = top == -INFINITY ? 0.f : top;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  // every warp finds the maximum and the sum for itself
+  float base = kLowest;
+  for (int i = threadIdx.x & 31; i < n; i += 32) base = fmaxf(base, ml[part_of(i)].x);
+  base = warp_max(base);
   float sum = 0.f;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const float2 x = reinterpret_cast<const float2*>(a.part_ml)[part_of(i)];
-    weight[i] = x.y != 0.f ? exp2_fast(x.x - base) : 0.f;
-    sum = fmaf(x.y, weight[i], sum);
+  for (int i = threadIdx.x & 31; i < n; i += 32) {
+    const float2 x = ml[part_of(i)];
+    sum = fmaf(x.y, exp2_fast(x.x - base), sum);
   }
-  sum = block_sum(sum, red);
+  sum = warp_sum(sum);
+  const int col = threadIdx.x % kLanes * 4, group = threadIdx.x / kLanes;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = group; i < n; i += kGroups) {
+    const float w = exp2_fast(ml[part_of(i)].x - base);
+    const float4 x = *reinterpret_cast<const float4*>(a.part_o + part_of(i) * D + col);
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  *reinterpret_cast<float4*>(&sums[group][col]) = acc;
   __syncthreads();
   const int head = hr / a.row_blocks * a.G + rb * RT + r;
   if (a.lse && threadIdx.x == 0)
     a.lse[(long long)s * Hq + head] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
   if (threadIdx.x < D) {
     float x = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) x = fmaf(weight[i], a.part_o[part_of(i) * D + threadIdx.x], x);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) x += sums[g][threadIdx.x];
     a.out[((long long)s * Hq + head) * D + threadIdx.x] = from_f<T>(sum == 0.f ? 0.f : x / sum);
   }
 }
@@ -809,6 +840,20 @@ struct Run {
     const int HR = Hkv * ((G + RT - 1) / RT);
     return carve(grid_of<T, D, RT>(S, width, page_log2, HR, sms), RT, D).total;
   }
+  // the kernel's shared memory, allowed once for each device
+  static cudaError_t allow_shared() {
+    static std::atomic<unsigned long long> allowed{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (allowed.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(paged_attn_kernel<T, D, RT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<T, D, RT>::kBytes);
+    if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
   static cudaError_t launch(PagedAttnArgs<T> a, void* ws, int sms, cudaStream_t st) {
     using Sh = Shape<T, D, RT>;
     a.row_blocks = (a.G + RT - 1) / RT;
@@ -818,14 +863,14 @@ struct Run {
     a.meta = reinterpret_cast<int*>(static_cast<char*>(ws) + c.meta);
     a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + c.ml);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + c.o);
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, RT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+    cudaError_t e = allow_shared();
     if (e != cudaSuccess) return e;
     count_launch();
     e = launch_pdl(paged_attn_kernel<T, D, RT>, dim3(grid), dim3(Sh::kThreads), Sh::kBytes, st, a);
     if (e != cudaSuccess || grid == 1) return e;      // one CTA cuts no segment
     count_launch();
-    return launch_pdl(paged_join_kernel<T, D, RT>, dim3(grid, std::min(a.G, RT)), dim3(128), 0, st,
+    return launch_pdl(paged_join_kernel<T, D, RT>, dim3(grid, std::min(a.G, RT)), dim3(kJoinThreads), 0,
+                      st,
                       a);
   }
 };

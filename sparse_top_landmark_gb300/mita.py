@@ -284,21 +284,22 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     return t.get_device()
 
 
-def _place(t: torch.Tensor, name: str, shape, dtype, device: int):
+def _refuse(t: torch.Tensor, name: str, shape, dtype, device: int, layout: str):
+    """Raises what is wrong with a tensor that _rows or _dense does not take."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: {layout}")
 
 
 def _rows(t: torch.Tensor, name: str, shape, dtype, device: int):
     """Checks a strided input of contiguous rows; returns the strides of its other dimensions."""
-    _place(t, name, shape, dtype, device)
     s = t.stride()
-    if s[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or s[-1] != 1:
+        _refuse(t, name, shape, dtype, device, "the last dimension must be contiguous")
     return s[:-1]
 
 
@@ -316,9 +317,9 @@ def _dense_strides(H: int, N: int, d: int):
 
 def _dense(t: torch.Tensor, name: str, shape, dtype, device: int):
     """Checks a contiguous tensor; returns its address."""
-    _place(t, name, shape, dtype, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if (t.dtype is not dtype or t.get_device() != device or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, name, shape, dtype, device, "must be contiguous")
     return t.data_ptr()
 
 
@@ -581,7 +582,8 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     if alibi_slopes is not None:
         slopes = _dense(alibi_slopes, "alibi_slopes", (Hq,), torch.float32, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=q.device)
+        out = (torch.empty_like(q) if q.is_contiguous()
+               else torch.empty(shape, dtype=dt, device=q.device))
         op = out.data_ptr()
     else:
         op = _dense(out, "out", shape, dt, dev)
