@@ -34,22 +34,66 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq_start, int S, int 
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
-  constexpr int L = D / 8, kSlots = kRopeThreads / L, K = kRopeAhead<T>;
+  constexpr int L = D / 8, kSlots = kRopeThreads / L;
   __shared__ unsigned long long table[D / 2];
+  __shared__ __align__(16) char rows_ahead[RowRing<T>::kBytes];
   griddep_wait();
   griddep_launch();
+  RowRing<T> ring(rows_ahead);
+  const RopeLane lane(threadIdx.x % L, a.rot, INTER);
+
+  // this block's rows of a token: those of q, of k, of v, in pairs
+  const int heads[3] = {a.q_heads, a.kv_heads, a.kv_heads};
+  const int h0 = blockIdx.y * a.run, h1 = min(h0 + a.run, a.q_heads + 2 * a.kv_heads);
+  int first[3], rows[3];
+#pragma unroll
+  for (int k = 0, before = 0; k < 3; before += heads[k++]) {
+    first[k] = max(h0 - before, 0);
+    rows[k] = max(min(h1 - before, heads[k]) - first[k], 0);
+  }
+  const unsigned tokens = a.tokens, stride = gridDim.x * kSlots;
+  const unsigned t0 = blockIdx.x * kSlots + threadIdx.x / L;
+  const unsigned in_warp = (threadIdx.x % 32) / L;
+
+  // The next pair to fetch.  Rows are fetched ahead whether or not their token turns out to have a
+  // place: where it has one is a chain of loads of its own.
+  unsigned ahead = t0;
+  int kind, left;
+  const T* x;
+  long long x_h;
+  auto enter = [&](int k) {        // the first kind from k on that this block has rows of
+    if (k == 0 && rows[0] == 0) k = 1;
+    if (k == 1 && rows[1] == 0) k = 2;
+    kind = k;
+    left = k == 0 ? rows[0] : k == 1 ? rows[1] : rows[2];
+    x_h = k == 0 ? a.q_h : k == 1 ? a.k_h : a.v_h;
+    x = (k == 0 ? a.q + ahead * a.q_t : k == 1 ? a.k + ahead * a.k_t : a.v + ahead * a.v_t) +
+        (k == 0 ? first[0] : k == 1 ? first[1] : first[2]) * x_h;
+  };
+  enter(0);
+  auto fetch = [&] {
+    if (ahead < tokens) {
+      ring.fetch(0, x, lane.a, lane.b);
+      if (left > 1) ring.fetch(1, x + x_h, lane.a, lane.b);
+    }
+    ring.next();
+    x += 2 * x_h;
+    left -= 2;
+    if (left <= 0) {
+      const bool same = (kind == 0 && rows[1] + rows[2] > 0) || (kind == 1 && rows[2] > 0);
+      if (!same) ahead += stride;
+      enter(same ? kind + 1 : 0);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < RowRing<T>::kPairs; ++i) fetch();
   rope_table(a.inv_freq, a.rot / 2, table);
   __syncthreads();
-  const RopeLane lane(threadIdx.x % L, a.rot, INTER);
   const unsigned long long* turn = table + 4 * (threadIdx.x % L);
 
-  const int hq = a.q_heads, hkv = a.kv_heads;
-  const int h0 = blockIdx.y * a.run, h1 = min(h0 + a.run, hq + 2 * hkv);
   const PagedLayout& pg = a.paged;
   const int in_page = (1 << pg.page_log2) - 1;
-  const unsigned tokens = a.tokens, stride = gridDim.x * kSlots;
-  unsigned t = blockIdx.x * kSlots + threadIdx.x / L;
-  for (unsigned first = t - (threadIdx.x % 32) / L; first < tokens; first += stride, t += stride) {
+  for (unsigned t = t0; t - in_warp < tokens; t += stride) {
     // where the token belongs
     bool live = t < tokens;
     const int s = !live ? -1 : a.seq_start ? sequence_of(a.seq_start, pg.S, t) : (int)t;
@@ -63,35 +107,34 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
       pos = len - (end - (int)t);
       live = len != 0;                       // else an idle slot
       if (live) {
-        const int slot = pos >> pg.page_log2;
         int page = -1;
         if (len >= end - begin && (len - 1) >> pg.page_log2 < pg.width)
-          page = pg.table[(long long)s * pg.width + slot];
+          page = pg.table[(long long)s * pg.width + (pos >> pg.page_log2)];
         live = page >= 0 && page < pg.num_pages;
         if (!live && threadIdx.x % L == 0) flag_error(a.status, kDevErrBadIndex);
         row = (((long long)page * a.kv_heads) << pg.page_log2) + (pos & in_page);
       }
     }
     V2 cs[2], sn[2];
-    if (lane.turned && h0 < hq + hkv) rope_angles(turn, pos, cs, sn);
-    for (int kind = 0; kind < 3; ++kind) {     // q, k, v
-      const int before = kind == 0 ? 0 : kind == 1 ? hq : hq + hkv;
-      int h = max(h0 - before, 0);
-      const int end = min(h1 - before, kind == 0 ? hq : hkv);
-      if (h >= end) continue;
-      const long long x_h = kind == 0 ? a.q_h : kind == 1 ? a.k_h : a.v_h;
-      const long long y_h = kind == 0 ? a.qo_h : (long long)D << pg.page_log2;
-      const T* x = kind == 0 ? a.q + t * a.q_t : kind == 1 ? a.k + t * a.k_t : a.v + t * a.v_t;
-      T* y = kind == 0 ? a.q_out + t * a.qo_t : (kind == 1 ? a.k_cache : a.v_cache) + row * D;
-      const float* w = kind == 0 ? a.q_w : kind == 1 ? a.k_w : nullptr;
+    if (lane.turned && rows[0] + rows[1] > 0) rope_angles(turn, pos, cs, sn);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (rows[k] == 0) continue;
+      const long long y_h = k == 0 ? a.qo_h : (long long)D << pg.page_log2;
+      T* y = (k == 0 ? a.q_out + t * a.qo_t : (k == 1 ? a.k_cache : a.v_cache) + row * D) +
+             first[k] * y_h;
+      const float* w = k == 0 ? a.q_w : k == 1 ? a.k_w : nullptr;
       RopeCoef<INTER> coef;
-      coef.set(lane.turned && kind < 2, cs, sn, w ? weights8(w, lane) : ones8());
-      x += h * x_h;
-      y += h * y_h;
-      for (; h < end; h += K, x += K * x_h, y += K * y_h)
-        rope_rows<T, D, INTER>(lane, coef, x, x_h, y, y_h, end - h, w != nullptr, live, a.eps);
+      coef.set(lane.turned && k < 2, cs, sn, w ? weights8(w, lane) : ones8());
+      for (int i = 0; i < rows[k]; i += 2, y += 2 * y_h) {
+        ring.wait();
+        rope_pair<T, D, INTER>(lane, coef, ring.get(0), ring.get(1), y, y_h, rows[k] - i,
+                               w != nullptr, live, a.eps);
+        fetch();
+      }
     }
   }
+  ring.drain();
 }
 
 template <typename T, int D>

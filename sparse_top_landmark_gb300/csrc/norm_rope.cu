@@ -9,8 +9,7 @@
 //
 // Bound by HBM: a row is read once and written once (the gradient reads two and writes one),
 // and a value costs some ten instructions.  A slot of D / 8 lanes takes one token's heads
-// one after the other, so that a token's angles are computed once for all of them, and fetches
-// several heads ahead of working on them, which keeps enough bytes in flight.
+// one after the other, so that a token's angles are computed once for all of them.
 #include "norm_rope.cuh"
 
 #include <algorithm>
@@ -26,41 +25,76 @@ namespace {
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 norm_rope_kernel(const __grid_constant__ NormRopeArgs<T> a) {
-  constexpr int L = D / 8, kSlots = kRopeThreads / L, K = kRopeAhead<T>;
+  constexpr int L = D / 8, kSlots = kRopeThreads / L;
   __shared__ unsigned long long table[D / 2];
+  __shared__ __align__(16) char rows_ahead[RowRing<T>::kBytes];
   griddep_wait();
   griddep_launch();
-  rope_table(a.inv_freq, a.rot / 2, table);
-  __syncthreads();
+  RowRing<T> ring(rows_ahead);
   const RopeLane lane(threadIdx.x % L, a.rot, INTER);
-  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
 
+  // this block's rows of a token: those of q, then those of k, in pairs
   const int hq = a.part[0].heads, h0 = blockIdx.y * a.run;
   const int h1 = min(h0 + a.run, hq + a.part[1].heads);
+  const int first[2] = {h0, max(h0 - hq, 0)};
+  const int rows[2] = {max(min(h1, hq) - h0, 0), max(h1 - hq - first[1], 0)};
   const unsigned tokens = (unsigned)a.B * a.N, stride = gridDim.x * kSlots;
-  unsigned t = blockIdx.x * kSlots + threadIdx.x / L;
-  // all lanes of a warp stay in the loop together
-  for (unsigned first = t - (threadIdx.x % 32) / L; first < tokens; first += stride, t += stride) {
-    const bool live = t < tokens;
-    const int bt = live && a.B > 1 ? t / a.N : 0;
-    const int n = live ? t - (unsigned)bt * a.N : 0;
+  const unsigned t0 = blockIdx.x * kSlots + threadIdx.x / L;
+  // all lanes of a warp stay in the loops together: `warp` is its first lane's token
+  const unsigned in_warp = (threadIdx.x % 32) / L;
+
+  // the next pair to fetch: token, part, place and rows left of the part
+  TokenWalk ahead(t0, a.N);
+  int part, left;
+  const T* x;
+  auto enter = [&](int isk) {
+    const NormRopePart<T>& p = a.part[isk];
+    part = isk;
+    left = rows[isk];
+    x = p.x + ahead.b * p.x_b + ahead.n * p.x_n + first[isk] * p.x_h;
+  };
+  enter(rows[0] == 0);
+  auto fetch = [&] {
+    const long long x_h = a.part[part].x_h;
+    if (ahead.t < tokens) {
+      ring.fetch(0, x, lane.a, lane.b);
+      if (left > 1) ring.fetch(1, x + x_h, lane.a, lane.b);
+    }
+    ring.next();
+    x += 2 * x_h;
+    left -= 2;
+    if (left <= 0) {
+      const bool same = part == 0 && rows[1] > 0;
+      if (!same) ahead.step(stride);
+      enter(same || rows[0] == 0);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < RowRing<T>::kPairs; ++i) fetch();
+  rope_table(a.inv_freq, a.rot / 2, table);
+  __syncthreads();
+  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
+  for (TokenWalk at(t0, a.N); at.t - in_warp < tokens; at.step(stride)) {
+    const bool live = at.t < tokens;
     V2 cs[2], sn[2];
     if (lane.turned)
-      rope_angles(turn, a.positions ? a.positions[bt * a.pos_b + n] : n, cs, sn);
+      rope_angles(turn, a.positions && live ? a.positions[at.b * a.pos_b + at.n] : at.n, cs, sn);
 #pragma unroll
     for (int isk = 0; isk < 2; ++isk) {
       const NormRopePart<T>& p = a.part[isk];
-      int h = isk ? max(h0 - hq, 0) : h0;
-      const int end = isk ? h1 - hq : min(h1, hq);
-      if (h >= end) continue;
+      if (rows[isk] == 0) continue;
       RopeCoef<INTER> coef;
       coef.set(lane.turned, cs, sn, p.w ? weights8(p.w, lane) : ones8());
-      const T* x = p.x + bt * p.x_b + n * p.x_n + h * p.x_h;
-      T* y = p.y + bt * p.y_b + n * p.y_n + h * p.y_h;
-      for (; h < end; h += K, x += K * p.x_h, y += K * p.y_h)
-        rope_rows<T, D, INTER>(lane, coef, x, p.x_h, y, p.y_h, end - h, p.w != nullptr, live, a.eps);
+      T* y = p.y + at.b * p.y_b + at.n * p.y_n + first[isk] * p.y_h;
+      for (int i = 0; i < rows[isk]; i += 2, y += 2 * p.y_h) {
+        ring.wait();
+        rope_pair<T, D, INTER>(lane, coef, ring.get(0), ring.get(1), y, p.y_h, rows[isk] - i,
+                               p.w != nullptr, live, a.eps);
+        fetch();
+      }
     }
   }
+  ring.drain();
 }
 
 // The gradient.  A block works on q rows alone (blockIdx.y < a.qruns) or on k rows alone; each
@@ -71,83 +105,102 @@ template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBackwardBlocks)
 norm_rope_backward_kernel(const __grid_constant__ NormRopeBackwardArgs<T> a) {
   constexpr int L = D / 8, kSlots = kRopeThreads / L;
-  constexpr int K = kRopeAhead<T> / 2;      // rows loaded together, each from x and dy
   __shared__ unsigned long long table[D / 2];
-  __shared__ __align__(16) float red[kRopeThreads * 8];
+  __shared__ __align__(16) union {
+    char rows[RowRing<T>::kBytes];           // a row of dy and its row of x are a pair
+    float red[kRopeThreads * 8];
+  } mem;
   griddep_wait();
   griddep_launch();
-  rope_table(a.inv_freq, a.rot / 2, table);
-  __syncthreads();
+  RowRing<T> ring(mem.rows);
   const RopeLane lane(threadIdx.x % L, a.rot, INTER);
-  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
 
   const int isk = (int)blockIdx.y >= a.qruns;
   const NormRopeBackwardPart<T>& p = a.part[isk];
   const int run = isk ? blockIdx.y - a.qruns : blockIdx.y;
-  const int h0 = run * a.run, h1 = min(h0 + a.run, p.heads);
+  const int h0 = run * a.run, rows = min(a.run, p.heads - h0);
   const bool normed = p.w != nullptr;
+  const unsigned tokens = (unsigned)a.B * a.N, stride = gridDim.x * kSlots;
+  const unsigned t0 = blockIdx.x * kSlots + threadIdx.x / L;
+  const unsigned in_warp = (threadIdx.x % 32) / L;
+
+  TokenWalk ahead(t0, a.N);
+  int left;
+  const T *x, *dy;
+  auto enter = [&] {
+    left = rows;
+    x = p.x + ahead.b * p.x_b + ahead.n * p.x_n + h0 * p.x_h;
+    dy = p.dy + ahead.b * p.dy_b + ahead.n * p.dy_n + h0 * p.dy_h;
+  };
+  enter();
+  auto fetch = [&] {
+    if (ahead.t < tokens) {
+      ring.fetch(0, dy, lane.a, lane.b);
+      if (normed) ring.fetch(1, x, lane.a, lane.b);
+    }
+    ring.next();
+    x += p.x_h;
+    dy += p.dy_h;
+    if (--left == 0) {
+      ahead.step(stride);
+      enter();
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < RowRing<T>::kPairs; ++i) fetch();
+  rope_table(a.inv_freq, a.rot / 2, table);
+  __syncthreads();
+  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
   const V8 w = normed ? weights8(p.w, lane) : ones8();
   V8 dw = {};
-  const unsigned tokens = (unsigned)a.B * a.N, stride = gridDim.x * kSlots;
-  unsigned t = blockIdx.x * kSlots + threadIdx.x / L;
-  for (unsigned first = t - (threadIdx.x % 32) / L; first < tokens; first += stride, t += stride) {
-    const bool live = t < tokens;
-    const int bt = live && a.B > 1 ? t / a.N : 0;
-    const int n = live ? t - (unsigned)bt * a.N : 0;
+  for (TokenWalk at(t0, a.N); at.t - in_warp < tokens; at.step(stride)) {
+    const bool live = at.t < tokens;
     V2 cs[2], sn[2];
     if (lane.turned)
-      rope_angles(turn, a.positions ? a.positions[bt * a.pos_b + n] : n, cs, sn);
+      rope_angles(turn, a.positions && live ? a.positions[at.b * a.pos_b + at.n] : at.n, cs, sn);
     RopeCoef<INTER> back;
     back.set(lane.turned, cs, sn, ones8(), true);
-    const T* x = p.x + bt * p.x_b + n * p.x_n + h0 * p.x_h;
-    const T* dy = p.dy + bt * p.dy_b + n * p.dy_n + h0 * p.dy_h;
-    T* dx = p.dx + bt * p.dx_b + n * p.dx_n + h0 * p.dx_h;
-    for (int h = h0; h < h1; h += K, x += K * p.x_h, dy += K * p.dy_h, dx += K * p.dx_h) {
-      Raw8<T> rx[K] = {}, rg[K] = {};
+    T* dx = p.dx + at.b * p.dx_b + at.n * p.dx_n + h0 * p.dx_h;
+    for (int i = 0; i < rows; ++i, dx += p.dx_h) {
+      ring.wait();
+      Raw8<T> rg = ring.get(0);
+      if (normed || back.turned) {
+        V8 g = back.of(rg.unpack());
+        if (normed) {
+          // with u = x r: dw += g u, dx = r (w g - u mean(w g u))
+          V8 u = ring.get(1).unpack(), wg;
+          V2 s2 = mul2(u.v[0], u.v[0]);
+          wg.v[0] = mul2(w.v[0], g.v[0]);
+          V2 d2 = mul2(wg.v[0], u.v[0]);
 #pragma unroll
-      for (int i = 0; i < K; ++i)
-        if (live && h + i < h1) {
-          rg[i].load(dy + i * p.dy_h, lane.a, lane.b);
-          if (normed) rx[i].load(x + i * p.x_h, lane.a, lane.b);
-        }
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        if (h + i >= h1) break;
-        if (normed || back.turned) {
-          V8 g = back.of(rg[i].unpack());
-          if (normed) {
-            // with u = x r: dw += g u, dx = r (w g - u mean(w g u))
-            V8 u = rx[i].unpack(), wg;
-            V2 s2 = mul2(u.v[0], u.v[0]);
-            wg.v[0] = mul2(w.v[0], g.v[0]);
-            V2 d2 = mul2(wg.v[0], u.v[0]);
-#pragma unroll
-            for (int j = 1; j < 4; ++j) {
-              s2 = fma2(u.v[j], u.v[j], s2);
-              wg.v[j] = mul2(w.v[j], g.v[j]);
-              d2 = fma2(wg.v[j], u.v[j], d2);
-            }
-            float ss = sum2(s2), dot = sum2(d2);
-            slot_sum2<D>(ss, dot, [](float s) { return s; });
-            const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-            const float m = -r * dot * (1.f / D);
-            const V2 rr = f2pack(r, r), mm = f2pack(m, m);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              u.v[j] = mul2(u.v[j], rr);
-              // a lane without a row has g = u = 0
-              dw.v[j] = fma2(g.v[j], u.v[j], dw.v[j]);
-              g.v[j] = mul2(fma2(u.v[j], mm, wg.v[j]), rr);
-            }
+          for (int j = 1; j < 4; ++j) {
+            s2 = fma2(u.v[j], u.v[j], s2);
+            wg.v[j] = mul2(w.v[j], g.v[j]);
+            d2 = fma2(wg.v[j], u.v[j], d2);
           }
-          rg[i].pack(g);
+          float ss = sum2(s2), dot = sum2(d2);
+          slot_sum2<D>(ss, dot, [](float s) { return s; });
+          const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+          const float m = -r * dot * (1.f / D);
+          const V2 rr = f2pack(r, r), mm = f2pack(m, m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            u.v[j] = mul2(u.v[j], rr);
+            if (live) dw.v[j] = fma2(g.v[j], u.v[j], dw.v[j]);
+            g.v[j] = mul2(fma2(u.v[j], mm, wg.v[j]), rr);
+          }
         }
-        if (live) rg[i].store(dx + i * p.dx_h, lane.a, lane.b);
+        rg.pack(g);
       }
+      if (live) rg.store(dx, lane.a, lane.b);
+      fetch();
     }
   }
+  ring.drain();
   if (p.partial == nullptr) return;
   // [slot][column]: a slot has every column once
+  __syncthreads();                // the ring's last rows are read
+  float* red = mem.red;
   float* mine = red + (threadIdx.x / L) * D;
   *reinterpret_cast<float4*>(mine + lane.a) = Raw4<float>::pack(dw.v);
   *reinterpret_cast<float4*>(mine + lane.b) = Raw4<float>::pack(dw.v + 2);

@@ -102,9 +102,68 @@ struct Raw8 {
   }
 };
 
-// Rows whose loads are issued together: 64 bytes a lane.
+// Rows on their way from global memory to a thread, two at a time: a ring in shared memory of which
+// every thread has its own column, filled by asynchronous copies kPairs ahead of use.  Nobody else
+// reads a thread's column, so its own wait is all the synchronisation there is; and rows wait in
+// shared memory, not in registers, so that loads are under way all the time.
 template <typename T>
-constexpr int kRopeAhead = 16 / (int)sizeof(T) / 2;
+struct RowRing {
+  using Bits = typename Raw4<T>::Bits;
+  static constexpr int kPairs = 16 / (int)sizeof(T) / 2;        // 128 bytes a thread
+  static constexpr int kGroup = kRopeThreads * (int)sizeof(Bits);   // [pair][row][group][thread]
+  static constexpr int kBytes = kPairs * 4 * kGroup;
+  char* mine;             // this thread's column
+  int at = 0;             // the pair that is used, then fetched, next
+
+  __device__ __forceinline__ explicit RowRing(char* mem)
+      : mine(mem + threadIdx.x * sizeof(Bits)) {}
+  // row 0 or 1 of the pair from p
+  __device__ __forceinline__ void fetch(int row, const T* p, int oa, int ob) const {
+    copy(mine + at + row * 2 * kGroup, p + oa);
+    copy(mine + at + row * 2 * kGroup + kGroup, p + ob);
+  }
+  __device__ __forceinline__ void next() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    at = (at + 4 * kGroup) & (kBytes - 1);
+  }
+  // returns once the oldest of kPairs committed pairs is there
+  __device__ __forceinline__ static void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPairs - 1) : "memory");
+  }
+  __device__ __forceinline__ static void drain() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __device__ __forceinline__ Raw8<T> get(int row) const {
+    const char* p = mine + at + row * 2 * kGroup;
+    return {*reinterpret_cast<const Bits*>(p), *reinterpret_cast<const Bits*>(p + kGroup)};
+  }
+
+ private:
+  __device__ __forceinline__ static void copy(char* dst, const T* src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (sizeof(Bits) == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+  }
+};
+
+// A slot's way over the tokens of [B, N]: first, first + stride, ..., with the batch and the place
+// in it (a division only where a step leaves the batch).
+struct TokenWalk {
+  unsigned t, N;
+  int b, n;
+  __device__ __forceinline__ TokenWalk(unsigned first, unsigned N_) : t(first), N(N_) { place(); }
+  __device__ __forceinline__ void step(unsigned stride) {
+    t += stride;
+    n += stride;
+    if ((unsigned)n >= N) place();
+  }
+  __device__ __forceinline__ void place() {
+    b = t / N;
+    n = t - (unsigned)b * N;
+  }
+};
 
 // The angle of frequency i at position p is p * inv_freq[i] radians.  In fp32 it would lose
 // its fraction of a turn at far positions (an ulp of 10^6 is 1/16 radian), and fp64 arithmetic
@@ -127,13 +186,15 @@ __device__ __forceinline__ void rope_table(const double* inv_freq, int half,
 __device__ __forceinline__ void rope_angles(const unsigned long long* turn, int p, V2* cs, V2* sn) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t quarter[2];
+    uint32_t quarter[2];     // the nearest quarter turn in the top two bits
     float r[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint32_t u = (uint32_t)(((unsigned long long)(long long)p * turn[2 * i + j]) >> 32);
-      quarter[j] = (u + 0x20000000u) >> 30;
-      r[j] = (float)(int)(u - (quarter[j] << 30));
+      const unsigned long long f = turn[2 * i + j];
+      const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
+      const uint32_t u = __umulhi((uint32_t)p, lo) + (uint32_t)p * hi - (p < 0 ? lo : 0u);
+      quarter[j] = u + 0x20000000u;
+      r[j] = (float)(int)(u - (quarter[j] & 0xc0000000u));
     }
     auto both = [](float x) { return f2pack(x, x); };
     const V2 x = mul2(f2pack(r[0], r[1]), both(1.4629180792671596e-9f));   // 2 pi / 2^32
@@ -152,10 +213,11 @@ __device__ __forceinline__ void rope_angles(const unsigned long long* turn, int 
     f2unpack(c, cc[0], cc[1]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const bool odd = quarter[j] & 1;
-      const float co = odd ? ss[j] : cc[j], si = odd ? cc[j] : ss[j];
-      cc[j] = __uint_as_float(__float_as_uint(co) ^ (((quarter[j] + 1) & 2) << 30));
-      ss[j] = __uint_as_float(__float_as_uint(si) ^ ((quarter[j] & 2) << 30));
+      const bool odd = quarter[j] & 0x40000000u;
+      const uint32_t co = __float_as_uint(odd ? ss[j] : cc[j]);
+      const uint32_t si = __float_as_uint(odd ? cc[j] : ss[j]);
+      cc[j] = __uint_as_float(co ^ ((quarter[j] + 0x40000000u) & 0x80000000u));
+      ss[j] = __uint_as_float(si ^ (quarter[j] & 0x80000000u));
     }
     cs[i] = f2pack(cc[0], cc[1]);
     sn[i] = f2pack(ss[0], ss[1]);
@@ -249,21 +311,14 @@ __device__ __forceinline__ void slot_sum2(float& p, float& q, F f) {
   q = upper ? mine : other;
 }
 
-// Up to kRopeAhead rows of a token, x + i * x_h to y + i * y_h: loaded together, then normalised
-// (where `normed`), rotated and stored.  All lanes of a warp call it; `live`: this lane has rows.
+// Two rows of a token (the second may be absent: `rows` = 1), normalised where `normed`, rotated and
+// stored to y and y + y_h.  All lanes of a warp call it; `live`: this lane has rows.
 template <typename T, int D, bool INTER>
-__device__ __forceinline__ void rope_rows(const RopeLane& lane, const RopeCoef<INTER>& coef,
-                                          const T* x, long long x_h, T* y, long long y_h, int rows,
+__device__ __forceinline__ void rope_pair(const RopeLane& lane, const RopeCoef<INTER>& coef,
+                                          Raw8<T> r0, Raw8<T> r1, T* y, long long y_h, int rows,
                                           bool normed, bool live, float eps) {
-  constexpr int K = kRopeAhead<T>;
-  Raw8<T> raw[K] = {};
-#pragma unroll
-  for (int i = 0; i < K; ++i)
-    if (live && i < rows) raw[i].load(x + i * x_h, lane.a, lane.b);
-#pragma unroll
-  for (int i = 0; i < K; i += 2) {
-    if (i >= rows) break;
-    V8 v[2] = {raw[i].unpack(), raw[i + 1].unpack()};
+  if (normed || coef.turned) {     // else values go through bit for bit
+    V8 v[2] = {r0.unpack(), r1.unpack()};
     if (normed) {
       float r[2];
 #pragma unroll
@@ -281,12 +336,12 @@ __device__ __forceinline__ void rope_rows(const RopeLane& lane, const RopeCoef<I
         for (int j = 0; j < 4; ++j) v[k].v[j] = mul2(v[k].v[j], rr);
       }
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      // a value that is neither normalised nor turned goes through bit for bit
-      if (normed || coef.turned) raw[i + k].pack(coef.of(v[k]));
-      if (live && i + k < rows) raw[i + k].store(y + (i + k) * y_h, lane.a, lane.b);
-    }
+    r0.pack(coef.of(v[0]));
+    r1.pack(coef.of(v[1]));
+  }
+  if (live) {
+    r0.store(y, lane.a, lane.b);
+    if (rows > 1) r1.store(y + y_h, lane.a, lane.b);
   }
 }
 
