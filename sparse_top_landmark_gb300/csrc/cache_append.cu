@@ -40,7 +40,7 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
   griddep_wait();
   griddep_launch();
   RowRing<T> ring(rows_ahead);
-  const RopeLane lane(threadIdx.x % L, a.rot, INTER);
+  const RopeLane lane(threadIdx.x % L, D, a.rot, INTER, table);
 
   // this block's rows of a token: those of q, of k, of v, in pairs
   const int heads[3] = {a.q_heads, a.kv_heads, a.kv_heads};
@@ -72,10 +72,8 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
   };
   enter(0);
   auto fetch = [&] {
-    if (ahead < tokens) {
-      ring.fetch(0, x, lane.a, lane.b);
-      if (left > 1) ring.fetch(1, x + x_h, lane.a, lane.b);
-    }
+    ring.template fetch<0>(x, lane.a, lane.b, ahead < tokens);
+    ring.template fetch<1>(x + x_h, lane.a, lane.b, ahead < tokens && left > 1);
     ring.next();
     x += 2 * x_h;
     left -= 2;
@@ -87,9 +85,8 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
   };
 #pragma unroll
   for (int i = 0; i < RowRing<T>::kPairs; ++i) fetch();
-  rope_table(a.inv_freq, a.rot / 2, table);
+  rope_table<D>(a.inv_freq, a.rot / 2, table);
   __syncthreads();
-  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
 
   const PagedLayout& pg = a.paged;
   const int in_page = (1 << pg.page_log2) - 1;
@@ -116,7 +113,7 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
       }
     }
     V2 cs[2], sn[2];
-    if (lane.turned && rows[0] + rows[1] > 0) rope_angles(turn, pos, cs, sn);
+    if (rows[0] + rows[1] > 0) rope_angles(lane.turn, pos, cs, sn);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       if (rows[k] == 0) continue;
@@ -125,11 +122,11 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
              first[k] * y_h;
       const float* w = k == 0 ? a.q_w : k == 1 ? a.k_w : nullptr;
       RopeCoef<INTER> coef;
-      coef.set(lane.turned && k < 2, cs, sn, w ? weights8(w, lane) : ones8());
+      if (k < 2) coef.set(cs, sn, w ? weights8(w, lane) : ones8());
       for (int i = 0; i < rows[k]; i += 2, y += 2 * y_h) {
         ring.wait();
-        rope_pair<T, D, INTER>(lane, coef, ring.get(0), ring.get(1), y, y_h, rows[k] - i,
-                               w != nullptr, live, a.eps);
+        rope_pair<T, D, INTER>(lane, coef, ring.template get<0>(), ring.template get<1>(), y, y_h,
+                               rows[k] - i, w != nullptr, lane.turned && k < 2, live, a.eps);
         fetch();
       }
     }

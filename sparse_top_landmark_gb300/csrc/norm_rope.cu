@@ -31,7 +31,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs<T> a) {
   griddep_wait();
   griddep_launch();
   RowRing<T> ring(rows_ahead);
-  const RopeLane lane(threadIdx.x % L, a.rot, INTER);
+  const RopeLane lane(threadIdx.x % L, D, a.rot, INTER, table);
 
   // this block's rows of a token: those of q, then those of k, in pairs
   const int hq = a.part[0].heads, h0 = blockIdx.y * a.run;
@@ -43,55 +43,79 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs<T> a) {
   // all lanes of a warp stay in the loops together: `warp` is its first lane's token
   const unsigned in_warp = (threadIdx.x % 32) / L;
 
-  // the next pair to fetch: token, part, place and rows left of the part
+  const NormRopePart<T>&q = a.part[0], &k = a.part[1];
+  const long long fq = first[0], fk = first[1];
+
+  // the next pair to fetch: token (its rows of q and k), part, place and rows left of the part
   TokenWalk ahead(t0, a.N);
+  const T *xq, *xk, *x;
+  long long x_h;
   int part, left;
-  const T* x;
-  auto enter = [&](int isk) {
-    const NormRopePart<T>& p = a.part[isk];
-    part = isk;
-    left = rows[isk];
-    x = p.x + ahead.b * p.x_b + ahead.n * p.x_n + first[isk] * p.x_h;
+  auto arrive = [&] {
+    xq = q.x + ahead.b * q.x_b + ahead.n * q.x_n + fq * q.x_h;
+    xk = k.x + ahead.b * k.x_b + ahead.n * k.x_n + fk * k.x_h;
   };
+  auto enter = [&](bool isk) {
+    part = isk;
+    left = isk ? rows[1] : rows[0];
+    x_h = isk ? k.x_h : q.x_h;
+    x = isk ? xk : xq;
+  };
+  arrive();
   enter(rows[0] == 0);
   auto fetch = [&] {
-    const long long x_h = a.part[part].x_h;
-    if (ahead.t < tokens) {
-      ring.fetch(0, x, lane.a, lane.b);
-      if (left > 1) ring.fetch(1, x + x_h, lane.a, lane.b);
-    }
+    ring.template fetch<0>(x, lane.a, lane.b, ahead.t < tokens);
+    ring.template fetch<1>(x + x_h, lane.a, lane.b, ahead.t < tokens && left > 1);
     ring.next();
     x += 2 * x_h;
     left -= 2;
     if (left <= 0) {
       const bool same = part == 0 && rows[1] > 0;
-      if (!same) ahead.step(stride);
+      if (!same) {
+        if (ahead.step(stride)) {
+          xq += stride * q.x_n;
+          xk += stride * k.x_n;
+        } else {
+          arrive();
+        }
+      }
       enter(same || rows[0] == 0);
     }
   };
 #pragma unroll
   for (int i = 0; i < RowRing<T>::kPairs; ++i) fetch();
-  rope_table(a.inv_freq, a.rot / 2, table);
+  rope_table<D>(a.inv_freq, a.rot / 2, table);
   __syncthreads();
-  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
-  for (TokenWalk at(t0, a.N); at.t - in_warp < tokens; at.step(stride)) {
+  TokenWalk at(t0, a.N);
+  T* y[2];
+  auto leave = [&] {
+    y[0] = q.y + at.b * q.y_b + at.n * q.y_n + fq * q.y_h;
+    y[1] = k.y + at.b * k.y_b + at.n * k.y_n + fk * k.y_h;
+  };
+  leave();
+  while (at.t - in_warp < tokens) {
     const bool live = at.t < tokens;
     V2 cs[2], sn[2];
-    if (lane.turned)
-      rope_angles(turn, a.positions && live ? a.positions[at.b * a.pos_b + at.n] : at.n, cs, sn);
+    rope_angles(lane.turn, a.positions && live ? a.positions[at.b * a.pos_b + at.n] : at.n, cs, sn);
 #pragma unroll
     for (int isk = 0; isk < 2; ++isk) {
       const NormRopePart<T>& p = a.part[isk];
       if (rows[isk] == 0) continue;
       RopeCoef<INTER> coef;
-      coef.set(lane.turned, cs, sn, p.w ? weights8(p.w, lane) : ones8());
-      T* y = p.y + at.b * p.y_b + at.n * p.y_n + first[isk] * p.y_h;
-      for (int i = 0; i < rows[isk]; i += 2, y += 2 * p.y_h) {
+      coef.set(cs, sn, p.w ? weights8(p.w, lane) : ones8());
+      T* to = y[isk];
+      for (int i = rows[isk]; i > 0; i -= 2, to += 2 * p.y_h) {
         ring.wait();
-        rope_pair<T, D, INTER>(lane, coef, ring.get(0), ring.get(1), y, p.y_h, rows[isk] - i,
-                               p.w != nullptr, live, a.eps);
+        rope_pair<T, D, INTER>(lane, coef, ring.template get<0>(), ring.template get<1>(), to,
+                               p.y_h, i, p.w != nullptr, lane.turned, live, a.eps);
         fetch();
       }
+    }
+    if (at.step(stride)) {
+      y[0] += stride * q.y_n;
+      y[1] += stride * k.y_n;
+    } else {
+      leave();
     }
   }
   ring.drain();
@@ -113,7 +137,7 @@ norm_rope_backward_kernel(const __grid_constant__ NormRopeBackwardArgs<T> a) {
   griddep_wait();
   griddep_launch();
   RowRing<T> ring(mem.rows);
-  const RopeLane lane(threadIdx.x % L, a.rot, INTER);
+  const RopeLane lane(threadIdx.x % L, D, a.rot, INTER, table);
 
   const int isk = (int)blockIdx.y >= a.qruns;
   const NormRopeBackwardPart<T>& p = a.part[isk];
@@ -125,72 +149,78 @@ norm_rope_backward_kernel(const __grid_constant__ NormRopeBackwardArgs<T> a) {
   const unsigned in_warp = (threadIdx.x % 32) / L;
 
   TokenWalk ahead(t0, a.N);
-  int left;
-  const T *x, *dy;
-  auto enter = [&] {
-    left = rows;
-    x = p.x + ahead.b * p.x_b + ahead.n * p.x_n + h0 * p.x_h;
-    dy = p.dy + ahead.b * p.dy_b + ahead.n * p.dy_n + h0 * p.dy_h;
+  int left = rows;
+  const T *x0, *dy0, *x, *dy;      // of the token, and of its next row
+  auto arrive = [&] {
+    x0 = p.x + ahead.b * p.x_b + ahead.n * p.x_n + h0 * p.x_h;
+    dy0 = p.dy + ahead.b * p.dy_b + ahead.n * p.dy_n + h0 * p.dy_h;
   };
-  enter();
+  arrive();
+  x = x0;
+  dy = dy0;
   auto fetch = [&] {
-    if (ahead.t < tokens) {
-      ring.fetch(0, dy, lane.a, lane.b);
-      if (normed) ring.fetch(1, x, lane.a, lane.b);
-    }
+    ring.template fetch<0>(dy, lane.a, lane.b, ahead.t < tokens);
+    ring.template fetch<1>(x, lane.a, lane.b, ahead.t < tokens && normed);
     ring.next();
     x += p.x_h;
     dy += p.dy_h;
     if (--left == 0) {
-      ahead.step(stride);
-      enter();
+      if (ahead.step(stride)) {
+        x0 += stride * p.x_n;
+        dy0 += stride * p.dy_n;
+      } else {
+        arrive();
+      }
+      left = rows;
+      x = x0;
+      dy = dy0;
     }
   };
 #pragma unroll
   for (int i = 0; i < RowRing<T>::kPairs; ++i) fetch();
-  rope_table(a.inv_freq, a.rot / 2, table);
+  rope_table<D>(a.inv_freq, a.rot / 2, table);
   __syncthreads();
-  const unsigned long long* turn = table + 4 * (threadIdx.x % L);
   const V8 w = normed ? weights8(p.w, lane) : ones8();
   V8 dw = {};
   for (TokenWalk at(t0, a.N); at.t - in_warp < tokens; at.step(stride)) {
     const bool live = at.t < tokens;
     V2 cs[2], sn[2];
-    if (lane.turned)
-      rope_angles(turn, a.positions && live ? a.positions[at.b * a.pos_b + at.n] : at.n, cs, sn);
+    rope_angles(lane.turn, a.positions && live ? a.positions[at.b * a.pos_b + at.n] : at.n, cs, sn);
     RopeCoef<INTER> back;
-    back.set(lane.turned, cs, sn, ones8(), true);
+    back.set(cs, sn, ones8(), true);
     T* dx = p.dx + at.b * p.dx_b + at.n * p.dx_n + h0 * p.dx_h;
     for (int i = 0; i < rows; ++i, dx += p.dx_h) {
       ring.wait();
-      Raw8<T> rg = ring.get(0);
-      if (normed || back.turned) {
-        V8 g = back.of(rg.unpack());
-        if (normed) {
-          // with u = x r: dw += g u, dx = r (w g - u mean(w g u))
-          V8 u = ring.get(1).unpack(), wg;
-          V2 s2 = mul2(u.v[0], u.v[0]);
-          wg.v[0] = mul2(w.v[0], g.v[0]);
-          V2 d2 = mul2(wg.v[0], u.v[0]);
+      Raw8<T> rg = ring.template get<0>();
+      if (normed) {
+        // with u = x r: dw += g u, dx = r (w g - u mean(w g u)); a slot without a token has zeros
+        const V8 g = back.of(rg.unpack());
+        V8 u = ring.template get<1>().unpack(), wg;
+        V2 s2 = mul2(u.v[0], u.v[0]);
+        wg.v[0] = mul2(w.v[0], g.v[0]);
+        V2 d2 = mul2(wg.v[0], u.v[0]);
 #pragma unroll
-          for (int j = 1; j < 4; ++j) {
-            s2 = fma2(u.v[j], u.v[j], s2);
-            wg.v[j] = mul2(w.v[j], g.v[j]);
-            d2 = fma2(wg.v[j], u.v[j], d2);
-          }
-          float ss = sum2(s2), dot = sum2(d2);
-          slot_sum2<D>(ss, dot, [](float s) { return s; });
-          const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-          const float m = -r * dot * (1.f / D);
-          const V2 rr = f2pack(r, r), mm = f2pack(m, m);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            u.v[j] = mul2(u.v[j], rr);
-            if (live) dw.v[j] = fma2(g.v[j], u.v[j], dw.v[j]);
-            g.v[j] = mul2(fma2(u.v[j], mm, wg.v[j]), rr);
-          }
+        for (int j = 1; j < 4; ++j) {
+          s2 = fma2(u.v[j], u.v[j], s2);
+          wg.v[j] = mul2(w.v[j], g.v[j]);
+          d2 = fma2(wg.v[j], u.v[j], d2);
         }
-        rg.pack(g);
+        float ss = sum2(s2), dot = sum2(d2);
+        slot_sum2<D>(ss, dot, [](float s) { return s; });
+        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        const float m = live ? -r * dot * (1.f / D) : 0.f;
+        const float ru = live ? r : 0.f;
+        const V2 rr = f2pack(ru, ru), mm = f2pack(m, m);
+        V8 d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          u.v[j] = mul2(u.v[j], rr);
+          dw.v[j] = fma2(g.v[j], u.v[j], dw.v[j]);
+          d.v[j] = mul2(fma2(u.v[j], mm, wg.v[j]), rr);
+        }
+        rg.pack(d);
+      } else if (lane.turned) {
+        rg.pack(back.of(rg.unpack()));
       }
       if (live) rg.store(dx, lane.a, lane.b);
       fetch();
@@ -212,26 +242,41 @@ norm_rope_backward_kernel(const __grid_constant__ NormRopeBackwardArgs<T> a) {
   }
 }
 
-// dw[c] = the sum of `blocks` partial rows; blockIdx.x: 0 = q, 1 = k; blockIdx.y: 16 columns.
-__global__ void __launch_bounds__(256)
-norm_rope_dw_kernel(const float* pq, const float* pk, int qblocks, int kblocks, int D, float* dwq,
+// dw[c] = the sum of the partial rows; blockIdx.x: 0 = q, 1 = k; blockIdx.y: 16 columns, four to a
+// thread, the rows dealt to 256 threads each.
+constexpr int kDwThreads = 1024;
+__global__ void __launch_bounds__(kDwThreads)
+norm_rope_dw_kernel(const float* pq, const float* pk, int qrows, int krows, int D, float* dwq,
                     float* dwk) {
-  __shared__ float red[16][17];
+  __shared__ float4 red[kDwThreads / 32][4];
   griddep_wait();
   const float* p = blockIdx.x ? pk : pq;
-  float* dw = blockIdx.x ? dwk : dwq;
-  const int blocks = blockIdx.x ? kblocks : qblocks;
   if (p == nullptr) return;
-  const int c = threadIdx.x % 16, r = threadIdx.x / 16;
-  const int col = blockIdx.y * 16 + c;
-  float s = 0.f;
+  const int rows = blockIdx.x ? krows : qrows;
+  const int c = threadIdx.x % 4, col = blockIdx.y * 16 + c * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = r; i < blocks; i += 16) s += p[(long long)i * D + col];
-  red[r][c] = s;
+  for (int i = threadIdx.x / 4; i < rows; i += kDwThreads / 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p + (long long)i * D + col);
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o *= 2) {
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+    s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+  }
+  if (threadIdx.x % 32 < 4) red[threadIdx.x / 32][c] = s;
   __syncthreads();
-  if (r == 0) {
-    for (int i = 1; i < 16; ++i) s += red[i][c];
-    dw[col] = s;
+  if (threadIdx.x < 16) {
+    float x = 0.f;
+    for (int w = 0; w < kDwThreads / 32; ++w)
+      x += reinterpret_cast<const float*>(red[w])[threadIdx.x];
+    (blockIdx.x ? dwk : dwq)[blockIdx.y * 16 + threadIdx.x] = x;
   }
 }
 
@@ -248,11 +293,11 @@ cudaError_t forward_d(NormRopeArgs<T>& a, int sms, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t backward_d(NormRopeBackwardArgs<T>& a, float* partial, int sms, float* dwq, float* dwk,
                        cudaStream_t st) {
+  // runs do not cross from q to k: one length for both, chosen for the longer part; the blocks'
+  // partial rows have to fit the workspace
   const int hq = a.part[0].heads, hk = a.part[1].heads;
-  RopeGrid g = rope_grid((long long)a.B * a.N, hq + hk, kRopeThreads / (D / 8),
-                         kRopeBackwardBlocks, sms);
-  // runs do not cross from q to k, so there can be one more of them than the rule counts; the
-  // blocks stay within the workspace's rows
+  const RopeGrid g = rope_grid((long long)a.B * a.N, std::max(hq, hk), kRopeThreads / (D / 8),
+                               kRopeBackwardBlocks, sms);
   a.run = g.run;
   auto runs = [&](int heads) { return (heads + a.run - 1) / a.run; };
   const int most = norm_rope_backward_blocks(sms);
@@ -269,14 +314,14 @@ cudaError_t backward_d(NormRopeBackwardArgs<T>& a, float* partial, int sms, floa
                  dim3(x, y), dim3(kRopeThreads), 0, st, a);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
   count_launch();
-  return launch_pdl(norm_rope_dw_kernel, dim3(2, D / 16), dim3(256), 0, st,
+  return launch_pdl(norm_rope_dw_kernel, dim3(2, D / 16), dim3(kDwThreads), 0, st,
                     (const float*)a.part[0].partial, (const float*)a.part[1].partial, x * a.qruns,
                     x * (y - a.qruns), D, dwq, dwk);
 }
 
 }  // namespace
 
-int norm_rope_backward_blocks(int sms) { return 4 * sms; }
+int norm_rope_backward_blocks(int sms) { return 8 * sms; }
 
 template <typename T>
 cudaError_t launch_norm_rope(NormRopeArgs<T> a, int d, int sms, cudaStream_t st) {

@@ -2,10 +2,11 @@
 // sequences and their gradient; cache_append.cu: new tokens on their way into the cache).
 //
 // A head row of D values is worked on by D / 8 lanes, a slot.  Lane g holds eight values as two
-// groups of four, chosen so that the rotation never leaves the lane: with the half-split pairing
-// (i, i + rot/2) the groups start at 4g and rot/2 + 4g, with the neighbouring pairing
-// (2i, 2i + 1) at 8g and 8g + 4; the unrotated tail [rot, D) is taken as 8g, 8g + 4 either way.
-// Hence rot % 8 == 0.  Either way the lane's pairs are the rotation's frequencies 4g .. 4g + 3.
+// groups of four, chosen so that the rotation never leaves the lane and that the lanes' groups lie
+// side by side: at 4g and rot/2 + 4g.  With the half-split pairing (i, i + rot/2) each value of
+// the one group is the partner of one in the other; with the neighbouring pairing (2i, 2i + 1)
+// each group holds two pairs.  The unrotated tail [rot, D) is split into halves likewise.  Hence
+// rot % 8 == 0.
 //
 // A row is a few dozen bytes a lane, so the instructions around them decide whether HBM stays
 // the bound (first measured form: 172 warp instructions a row of 128, 82 us for 336 MB).  So the
@@ -112,15 +113,18 @@ struct RowRing {
   static constexpr int kPairs = 16 / (int)sizeof(T) / 2;        // 128 bytes a thread
   static constexpr int kGroup = kRopeThreads * (int)sizeof(Bits);   // [pair][row][group][thread]
   static constexpr int kBytes = kPairs * 4 * kGroup;
-  char* mine;             // this thread's column
-  int at = 0;             // the pair that is used, then fetched, next
+  uint32_t mine;          // this thread's column
+  uint32_t at = 0;        // the pair that is used, then fetched, next
 
-  __device__ __forceinline__ explicit RowRing(char* mem)
-      : mine(mem + threadIdx.x * sizeof(Bits)) {}
-  // row 0 or 1 of the pair from p
-  __device__ __forceinline__ void fetch(int row, const T* p, int oa, int ob) const {
-    copy(mine + at + row * 2 * kGroup, p + oa);
-    copy(mine + at + row * 2 * kGroup + kGroup, p + ob);
+  __device__ __forceinline__ explicit RowRing(const void* mem)
+      : mine((uint32_t)__cvta_generic_to_shared(mem) + threadIdx.x * sizeof(Bits)) {}
+  // row 0 or 1 of the pair from p; zeros, and nothing read, where there is none
+  template <int row>
+  __device__ __forceinline__ void fetch(const T* p, int oa, int ob, bool there) const {
+    const uint32_t to = mine + at;
+    const int bytes = there ? (int)sizeof(Bits) : 0;
+    copy<row * 2 * kGroup>(to, p + oa, bytes);
+    copy<row * 2 * kGroup + kGroup>(to, p + ob, bytes);
   }
   __device__ __forceinline__ void next() {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -133,31 +137,54 @@ struct RowRing {
   __device__ __forceinline__ static void drain() {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
-  __device__ __forceinline__ Raw8<T> get(int row) const {
-    const char* p = mine + at + row * 2 * kGroup;
-    return {*reinterpret_cast<const Bits*>(p), *reinterpret_cast<const Bits*>(p + kGroup)};
+  template <int row>
+  __device__ __forceinline__ Raw8<T> get() const {
+    const uint32_t from = mine + at;
+    return {load<row * 2 * kGroup>(from), load<row * 2 * kGroup + kGroup>(from)};
   }
 
  private:
-  __device__ __forceinline__ static void copy(char* dst, const T* src) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  template <int off>
+  __device__ __forceinline__ static void copy(uint32_t dst, const T* src, int bytes) {
     if constexpr (sizeof(Bits) == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0 + %1], [%2], 16, %3;" ::"r"(dst), "n"(off),
+                   "l"(src), "r"(bytes)
+                   : "memory");
     else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0 + %1], [%2], 8, %3;" ::"r"(dst), "n"(off),
+                   "l"(src), "r"(bytes)
+                   : "memory");
+  }
+  template <int off>
+  __device__ __forceinline__ static Bits load(uint32_t src) {
+    Bits b;
+    if constexpr (sizeof(Bits) == 16)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4 + %5];"
+                   : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                   : "r"(src), "n"(off)
+                   : "memory");
+    else
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];"
+                   : "=r"(b.x), "=r"(b.y)
+                   : "r"(src), "n"(off)
+                   : "memory");
+    return b;
   }
 };
 
-// A slot's way over the tokens of [B, N]: first, first + stride, ..., with the batch and the place
-// in it (a division only where a step leaves the batch).
+// A slot's way over the tokens of [B, N]: first, first + stride, ..., with the batch and the place in
+// it.  step() says whether that stayed in the batch: rows then lie stride tokens further on, which
+// is an addition, where a new batch takes a division and products.
 struct TokenWalk {
   unsigned t, N;
   int b, n;
   __device__ __forceinline__ TokenWalk(unsigned first, unsigned N_) : t(first), N(N_) { place(); }
-  __device__ __forceinline__ void step(unsigned stride) {
+  __device__ __forceinline__ bool step(unsigned stride) {
     t += stride;
     n += stride;
-    if ((unsigned)n >= N) place();
+    if ((unsigned)n < N) return true;
+    place();
+    return false;
   }
   __device__ __forceinline__ void place() {
     b = t / N;
@@ -170,11 +197,13 @@ struct TokenWalk {
 // per token is slow on this part.  So each block turns the frequencies once into unsigned
 // 64-bit fractions of a turn; p * fraction mod 2^64 is then the exact product modulo one turn
 // (the frequency's own rounding, 2^-53 of it, is all that is lost), for any 32-bit p, negative
-// ones included.
+// ones included.  Frequencies from `half` on are 0: their cosine is 1 and their sine 0, exactly,
+// so lanes whose values are not turned need no branch.
+template <int D>
 __device__ __forceinline__ void rope_table(const double* inv_freq, int half,
                                            unsigned long long* turn) {
-  for (int i = threadIdx.x; i < half; i += blockDim.x) {
-    double f = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+  for (int i = threadIdx.x; i < D / 2; i += blockDim.x) {
+    double f = i < half ? inv_freq[i] * 0.15915494309189533577 : 0.0;   // 1 / (2 pi)
     f -= rint(f);                                      // whole turns do nothing; |f| <= 1/2
     turn[i] = (unsigned long long)__double2ll_rn(f * 18446744073709551616.0);   // saturates
   }
@@ -183,14 +212,15 @@ __device__ __forceinline__ void rope_table(const double* inv_freq, int half,
 // cos and sin of four pairs at position p: the angle's top 32 bits, less the nearest quarter
 // turn, give |x| <= pi / 4 to fp32's 24 bits; the Taylor series of sine to x^9 and of cosine to
 // x^10 end below 2e-9 there; the quarter swaps them and sets the signs.
-__device__ __forceinline__ void rope_angles(const unsigned long long* turn, int p, V2* cs, V2* sn) {
+__device__ __forceinline__ void rope_angles(const unsigned long long* const (&turn)[2], int p,
+                                            V2* cs, V2* sn) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t quarter[2];     // the nearest quarter turn in the top two bits
     float r[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const unsigned long long f = turn[2 * i + j];
+      const unsigned long long f = turn[i][j];
       const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
       const uint32_t u = __umulhi((uint32_t)p, lo) + (uint32_t)p * hi - (p < 0 ? lo : 0u);
       quarter[j] = u + 0x20000000u;
@@ -228,59 +258,51 @@ __device__ __forceinline__ void rope_angles(const unsigned long long* turn, int 
 struct RopeLane {
   int a, b;              // its groups of four values
   bool turned;           // whether they are rotated at all
-  __device__ __forceinline__ RopeLane(int g, int rot, bool inter) {
+  const unsigned long long* turn[2];   // its four frequencies in rope_table's table, two and two
+  __device__ __forceinline__ RopeLane(int g, int D, int rot, bool inter,
+                                      const unsigned long long* table) {
     turned = 8 * g < rot;
-    const bool split = !inter && turned;
-    a = split ? 4 * g : 8 * g;
-    b = split ? rot / 2 + 4 * g : 8 * g + 4;
+    a = turned ? 4 * g : rot + (4 * g - rot / 2);
+    b = a + (turned ? rot : D - rot) / 2;
+    turn[0] = table + (!turned ? rot / 2 : inter ? 2 * g : 4 * g);
+    turn[1] = table + (!turned ? rot / 2 : inter ? rot / 4 + 2 * g : 4 * g + 2);
   }
 };
 
 // A token's rotation with the weights worked in: y = x * c + partner(x) * s, the partner of a value
-// being the other one of its pair.  A lane whose values are not turned has c = w and leaves s out.
+// being the other one of its pair.  (Taken by all lanes: a branch around the second product for
+// those that are not turned cost 27 instructions a row of 98 in register moves.)
 template <bool INTER>
 struct RopeCoef {
   V8 c, s;
-  bool turned;
-  // the weights w, and the rotation by (cs, sn); `back`: the rotation back
-  __device__ __forceinline__ void set(bool turn, const V2* cs, const V2* sn, const V8& w,
-                                      bool back = false) {
-    turned = turn;
-    c = w;
-    s = w;
-    if (!turn) return;
-    const V2 minus = f2pack(-1.f, -1.f);
+  // the rotation by (cs, sn), or back, after the weights w
+  __device__ __forceinline__ void set(const V2* cs, const V2* sn, const V8& w, bool back = false) {
+    const float sign = back ? -1.f : 1.f;
     if constexpr (INTER) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float c0, c1, s0, s1, w0, w1;
+        float c0, c1, s0, s1;
         f2unpack(cs[i / 2], c0, c1);
         f2unpack(sn[i / 2], s0, s1);
-        f2unpack(w.v[i], w0, w1);
-        const float co = i % 2 ? c1 : c0, si = (i % 2 ? s1 : s0) * (back ? -1.f : 1.f);
-        c.v[i] = f2pack(co * w0, co * w1);
-        s.v[i] = f2pack(-si * w1, si * w0);
+        const float co = i % 2 ? c1 : c0, si = i % 2 ? s1 : s0;
+        c.v[i] = mul2(f2pack(co, co), w.v[i]);
+        s.v[i] = mul2(f2pack(-sign * si, sign * si), swap2(w.v[i]));
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const V2 neg = mul2(sn[i], minus);
         c.v[i] = mul2(cs[i], w.v[i]);
         c.v[i + 2] = mul2(cs[i], w.v[i + 2]);
-        s.v[i] = mul2(back ? sn[i] : neg, w.v[i + 2]);
-        s.v[i + 2] = mul2(back ? neg : sn[i], w.v[i]);
+        s.v[i] = mul2(mul2(sn[i], f2pack(-sign, -sign)), w.v[i + 2]);
+        s.v[i + 2] = mul2(mul2(sn[i], f2pack(sign, sign)), w.v[i]);
       }
     }
   }
   __device__ __forceinline__ V8 of(const V8& x) const {
     V8 y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y.v[i] = mul2(x.v[i], c.v[i]);
-    if (turned) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        y.v[i] = fma2(INTER ? swap2(x.v[i]) : x.v[i ^ 2], s.v[i], y.v[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+      y.v[i] = fma2(INTER ? swap2(x.v[i]) : x.v[i ^ 2], s.v[i], mul2(x.v[i], c.v[i]));
     return y;
   }
 };
@@ -312,32 +334,34 @@ __device__ __forceinline__ void slot_sum2(float& p, float& q, F f) {
 }
 
 // Two rows of a token (the second may be absent: `rows` = 1), normalised where `normed`, rotated and
-// stored to y and y + y_h.  All lanes of a warp call it; `live`: this lane has rows.
+// stored to y and y + y_h.  All lanes of a warp call it; `live`: this lane has rows; `turned`: its
+// values are rotated (a value that is neither normalised nor turned goes through bit for bit).
 template <typename T, int D, bool INTER>
 __device__ __forceinline__ void rope_pair(const RopeLane& lane, const RopeCoef<INTER>& coef,
                                           Raw8<T> r0, Raw8<T> r1, T* y, long long y_h, int rows,
-                                          bool normed, bool live, float eps) {
-  if (normed || coef.turned) {     // else values go through bit for bit
+                                          bool normed, bool turned, bool live, float eps) {
+  if (normed) {
     V8 v[2] = {r0.unpack(), r1.unpack()};
-    if (normed) {
-      float r[2];
+    float r[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        V2 ss = mul2(v[k].v[0], v[k].v[0]);
+    for (int k = 0; k < 2; ++k) {
+      V2 ss = mul2(v[k].v[0], v[k].v[0]);
 #pragma unroll
-        for (int j = 1; j < 4; ++j) ss = fma2(v[k].v[j], v[k].v[j], ss);
-        r[k] = sum2(ss);
-      }
-      slot_sum2<D>(r[0], r[1], [&](float s) { return rsqrtf(fmaf(s, 1.f / D, eps)); });
+      for (int j = 1; j < 4; ++j) ss = fma2(v[k].v[j], v[k].v[j], ss);
+      r[k] = sum2(ss);
+    }
+    slot_sum2<D>(r[0], r[1], [&](float s) { return rsqrtf(fmaf(s, 1.f / D, eps)); });
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const V2 rr = f2pack(r[k], r[k]);
+    for (int k = 0; k < 2; ++k) {
+      const V2 rr = f2pack(r[k], r[k]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[k].v[j] = mul2(v[k].v[j], rr);
-      }
+      for (int j = 0; j < 4; ++j) v[k].v[j] = mul2(v[k].v[j], rr);
     }
     r0.pack(coef.of(v[0]));
     r1.pack(coef.of(v[1]));
+  } else if (turned) {
+    r0.pack(coef.of(r0.unpack()));
+    r1.pack(coef.of(r1.unpack()));
   }
   if (live) {
     r0.store(y, lane.a, lane.b);
@@ -346,9 +370,13 @@ __device__ __forceinline__ void rope_pair(const RopeLane& lane, const RopeCoef<I
 }
 
 // The grid of such a kernel: `tokens` tokens of `heads` rows each, `slots` tokens to a block at a
-// time, `blocks` blocks to an SM.  A block goes over its tokens with a run of `run` heads
-// (blockIdx.y).  A short run spreads better; a token's angles and places, worth about four rows of
-// arithmetic, are then computed for fewer rows.  The cost is that of the fullest SM's share.
+// time, `blocks` blocks to an SM.  A block goes over its tokens with a run of `run` heads, the
+// blockIdx.y-th.  A short run spreads few tokens better; a token's angles and places, worth about
+// four rows of arithmetic, are then computed for fewer rows: the least cost is that of the fullest
+// SM's share.  No run is longer than kRopeRun: the blocks of the first runs come first, and
+// fewer heads' rows are then written at a time, each head's to a place of its own (2 x 8191 tokens
+// of 40 heads: runs of 40 65 us, of 20 57 us, of 8 62 us).
+constexpr int kRopeRun = 20;
 struct RopeGrid {
   int run, x, y;
 };
@@ -356,19 +384,21 @@ inline RopeGrid rope_grid(long long tokens, int heads, int slots, int blocks, in
   RopeGrid best{};
   long long least = 0;
   const long long per_run = (tokens + slots - 1) / slots;
-  for (int run = 1;; run = 2 * run < heads ? 2 * run : heads) {
+  for (int run = 1; run == 1 || (run < 2 * heads && run <= kRopeRun); ++run) {
     const int y = (heads + run - 1) / run;
-    if (y <= 65535) {                           // a grid's limit
-      long long share = (per_run * y + sms - 1) / sms;
-      if (share < blocks) share = blocks;       // an SM's blocks run side by side
-      const long long cost = share * (run + 4);
-      if (best.run == 0 || cost < least) {
-        const long long most = ((long long)blocks * sms + y - 1) / y;
-        best = {run, (int)(per_run < most ? per_run : most), y};
-        least = cost;
-      }
+    if (run > 1 && (heads + y - 1) / y != run) continue;    // runs of equal length only
+    long long share = (per_run * y + sms - 1) / sms;
+    if (share < blocks) share = blocks;         // an SM's blocks run side by side
+    const long long cost = share * (run + 4);
+    if (best.run == 0 || cost < least) {
+      const long long most = (long long)blocks * sms;
+      best = {run, (int)(per_run < most ? per_run : most), y};
+      least = cost;
     }
-    if (run >= heads) break;
+  }
+  while (best.y > 65535) {                      // a grid's limit
+    best.run *= 2;
+    best.y = (heads + best.run - 1) / best.run;
   }
   return best;
 }
