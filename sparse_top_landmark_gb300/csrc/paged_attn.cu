@@ -9,8 +9,8 @@
 //
 // Work is dealt out on the device, since lengths live there (a replayed graph sees new ones):
 // every (sequence, key head, block of query rows) is a segment of tiles of kTile keys, the
-// segments stand in one row, and each CTA takes an equal share of that row of tiles, whatever
-// the lengths are.  A CTA finishes the segments that lie wholly in its share; of a
+// segments stand in one row, and each CTA takes an equal share of that row, whatever the lengths
+// are.  Ending a segment costs about a tile's time, so it counts as kSegmentCost tiles more.  A CTA finishes the segments that lie wholly in its share; of a
 // segment that is cut it leaves a partial (maximum, sum, weighted values) in its first or
 // its last slot of the workspace, and paged_join_kernel joins those of a segment in
 // their order.  Nothing is added atomically: the result depends on the inputs alone.
@@ -35,6 +35,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum before the first key: below every finite score, and finite, so that
 // differences with it need no special case (a score of -inf weighs nothing against it).
 constexpr float kLowest = -FLT_MAX;
+constexpr int kSegmentCost = 1;
 constexpr int kNoSegment = -1;
 constexpr int kJoinThreads = 256;
 constexpr int kMaxPagedCtas = 512;     // CTAs of a call: parts of a segment that can be joined
@@ -58,8 +59,7 @@ struct Shape {
   // byte offsets
   static constexpr int kOffJoin = kWarps * kRing;
   static constexpr int kOffMl = kOffJoin + kJoinFloats * 4;               // [warps][RT][2]
-  static constexpr int kOffTop = kOffMl + kWarps * RT * 8;                // [2][RT]
-  static constexpr int kOffMask = kOffTop + RT * 8;                       // [warps][stages]
+  static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
   static constexpr int kOffQ = kOffMask + ((kWarps * kStages * 4 + 15) / 16) * 16;
   static constexpr int kOffP = kOffQ + (kTensor ? 0 : RT * D * 4);        // fp32: q rows
   static constexpr int kBytes = kOffP + (kTensor ? 0 : kWarps * RT * kKeys * 4);
@@ -166,43 +166,88 @@ __device__ __forceinline__ long long warp_incl_scan64(long long v) {
   return v;
 }
 
-// This CTA's share [u0, u1) of the row of tiles, and where u0 lies.  Each warp finds it for itself.
-__device__ __forceinline__ void my_share(const PagedLayout& pg, int window, int tile, int HR,
-                                         long long* u0, long long* u1, long long* all,
-                                         Cursor* at) {
+// a / b, which are not negative: 64-bit division is some hundred instructions, and seldom needed.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+// A CTA's share of the row: its tiles, the first one's place, the position of that segment's start in
+// the row, and the row's length (both with the ends of segments counted).
+struct Share {
+  long long tiles, segment, row;
+  Cursor at;
+};
+__device__ __forceinline__ long long share_begin(long long row, int n, int c) {
+  const long long q = quotient(row, n), r = row - q * n;
+  return q * c + min((long long)c, r);
+}
+// The index of the CTA whose share of a row of that length has position x.
+__device__ __forceinline__ int share_of(long long x, long long row, int n) {
+  const long long q = quotient(row, n), r = row - q * n;
+  const long long large = r * (q + 1);       // the length of the r shares that are one longer
+  return (int)(x < large ? quotient(x, (int)q + 1) : r + quotient(x - large, (int)q));
+}
+
+// Each warp finds the share for itself: a sum over the sequences for the row's length, then a
+// running sum until both ends of the share are behind.
+__device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int tile, int HR) {
   const int lane = threadIdx.x & 31;
-  long long total = 0;
-  for (int s0 = 0; s0 < pg.S; s0 += 32) {
-    const int s = s0 + lane;
-    total += s < pg.S ? span_of(pg, window, tile, s).tiles : 0;
-  }
+  auto tiles_of = [&](int s) { return s < pg.S ? span_of(pg, window, tile, s).tiles : 0; };
+  auto cost_of = [&](int tiles) {
+    return tiles > 0 ? (long long)(tiles + kSegmentCost) * HR : 0;
+  };
+  Share sh;
+  sh.tiles = 0;
+  const int mine = tiles_of(lane);           // of the first 32 sequences: often all there are
+  long long row = cost_of(mine);
+  for (int s = 32 + lane; s < pg.S; s += 32) row += cost_of(tiles_of(s));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= HR;
-  *all = total;
-  const long long n = gridDim.x, c = blockIdx.x;
-  const long long q = total / n, r = total % n;
-  *u0 = q * c + min(c, r);
-  *u1 = *u0 + q + (c < r ? 1 : 0);
-  if (*u0 >= *u1) return;
-  long long run = 0;
+  for (int o = 16; o > 0; o >>= 1) row += __shfl_xor_sync(0xffffffffu, row, o);
+  sh.row = row;
+  const long long x0 = share_begin(row, gridDim.x, blockIdx.x);
+  const long long x1 = share_begin(row, gridDim.x, blockIdx.x + 1);
+  if (x0 >= x1) return sh;
+  long long run = 0, before_x0 = 0;          // the row up to this batch; tiles before x0
+  int filled = 0;                            // sequences with a tile up to this batch
   for (int s0 = 0; s0 < pg.S; s0 += 32) {
-    const int s = s0 + lane;
-    const long long mine = s < pg.S ? (long long)span_of(pg, window, tile, s).tiles * HR : 0;
-    const long long incl = run + warp_incl_scan64(mine);
-    const unsigned hit = __ballot_sync(0xffffffffu, *u0 < incl);
-    if (hit) {
+    const int tiles = s0 == 0 ? mine : tiles_of(s0 + lane);
+    const long long cost = cost_of(tiles);
+    const long long incl = run + warp_incl_scan64(cost);
+    const unsigned any = __ballot_sync(0xffffffffu, tiles > 0);
+#pragma unroll
+    for (int end = 0; end < 2; ++end) {
+      const long long x = end ? x1 - 1 : x0;           // the last position has tiles up to it
+      const unsigned hit = __ballot_sync(0xffffffffu, incl - cost <= x && x < incl);
+      if (hit == 0) continue;
       const int src = __ffs(hit) - 1;
-      const long long before = __shfl_sync(0xffffffffu, incl - mine, src);
-      at->s = s0 + src;
-      at->span = span_of(pg, window, tile, at->s);
-      const long long in = *u0 - before;
-      at->hr = (int)(in / at->span.tiles);
-      at->t = (int)(in % at->span.tiles);
-      return;
+      const int n = __shfl_sync(0xffffffffu, tiles, src);
+      const long long start = __shfl_sync(0xffffffffu, incl - cost, src);
+      const int seg = (int)quotient(x - start, n + kSegmentCost);
+      const int in = (int)(x - start - (long long)seg * (n + kSegmentCost));
+      // tiles before the sequence, of its segments before this one, and of this one
+      const long long before =
+          start - (long long)kSegmentCost * HR * (filled + __popc(any & ((1u << src) - 1))) +
+          (long long)seg * n;
+      if (end == 0) {
+        before_x0 = before + min(in, n);
+        sh.segment = x - in;
+        sh.at.s = s0 + src;
+        sh.at.hr = seg;
+        sh.at.t = min(in, n - 1);
+        sh.at.span = span_of(pg, window, tile, sh.at.s);
+        if (in >= n) {                       // the share begins behind a segment's last tile
+          sh.segment += n + kSegmentCost;
+          advance(sh.at, pg, window, tile, HR);
+        }
+      } else {
+        sh.tiles = before + min(in + 1, n) - before_x0;
+      }
     }
+    if (x1 <= __shfl_sync(0xffffffffu, incl, 31)) break;
     run = __shfl_sync(0xffffffffu, incl, 31);
+    filled += __popc(any);
   }
+  return sh;
 }
 
 // What a tile's scores need besides q and k.
@@ -212,9 +257,18 @@ struct ScoreRule {
   int last;              // len - 1
   bool plain;            // scores are just scale2 * dot, with scale2 >= 0
 };
+// tanh to about 2^-22 absolute, from one exponential and one reciprocal: what bf16 weights (2^-16)
+// can tell, in a quarter of tanhf's instructions (53 sequences of G = 8, d = 32: 54 against 38 us).
+__device__ __forceinline__ float tanh_fast(float x) {
+  const float e = exp2_fast(fabsf(x) * (2.f * kLog2e));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return copysignf(fmaf(-2.f, r, 1.f), x);
+}
+template <bool FAST>
 __device__ __forceinline__ float score_of(const ScoreRule& r, float dot, float slope2, int key) {
   float z = dot * r.scale2;
-  if (r.cap > 0.f) z = r.cap2 * tanhf(dot * r.rcap);
+  if (r.cap > 0.f) z = r.cap2 * (FAST ? tanh_fast(dot * r.rcap) : tanhf(dot * r.rcap));
   return z + slope2 * (float)(key - r.last);
 }
 
@@ -292,8 +346,9 @@ struct TensorState {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = 16 * t + lane / 4 + 8 * (i >> 1);
-            z[t][n][i] = (mask >> j) & 1 ? score_of(rule, z[t][n][i], slope2[n][i & 1], key0 + j)
-                                         : -INFINITY;
+            z[t][n][i] = (mask >> j) & 1
+                             ? score_of<true>(rule, z[t][n][i], slope2[n][i & 1], key0 + j)
+                             : -INFINITY;
           }
     }
     // The running maxima are looked for again only where a score is above them: most tiles
@@ -378,9 +433,10 @@ struct TensorState {
         if (lane < 4) ml[8 * n + lane * 2 + i] = make_float2(m[n][i], l[n][i]);
       }
   }
-  // columns [c0, c0 + C) of the rows below `rows`, moved to the maxima `top`, to dst[row][..]
+  // columns [c0, c0 + C) of the rows below `rows`, moved to the maxima top(row), to dst[row][..]
+  template <typename Top>
   __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
-                                        const float* top) {
+                                        Top top) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 0; n < kN; ++n)
@@ -388,7 +444,7 @@ struct TensorState {
       for (int i = 0; i < 2; ++i) {
         const int r = 8 * n + lane % 4 * 2 + i;
         if (r >= rows) continue;
-        const float f = exp2_fast(m[n][i] - top[r]);
+        const float f = exp2_fast(m[n][i] - top(r));
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
           if (8 * j >= c0 && 8 * j < c0 + C)
@@ -432,7 +488,7 @@ struct FmaState {
     const float* q = reinterpret_cast<const float*>(smem + S::kOffQ);
     float* p = reinterpret_cast<float*>(smem + S::kOffP) + (threadIdx.x >> 5) * RT * S::kKeys;
     float z[RT] = {};
-#pragma unroll 2
+#pragma unroll RT <= 4 ? 8 : 2
     for (int c = 0; c < D / 4 / kParts; ++c) {
       const int ch = part * (D / 4 / kParts) + c;
       const float4 k = *reinterpret_cast<const float4*>(
@@ -445,25 +501,42 @@ struct FmaState {
         }
     }
     const bool seen = (mask >> key) & 1;
+    // as on the tensor cores, the maxima are looked for again only where a score is above them
+    bool above = false;
 #pragma unroll
     for (int r = 0; r < RT; ++r)
       if (r < rows) {
 #pragma unroll
         for (int i = 16; i >= S::kKeys; i >>= 1) z[r] += __shfl_xor_sync(0xffffffffu, z[r], i);
-        z[r] = seen ? score_of(rule, z[r], slopes ? slopes[head + r] * kLog2e : 0.f, key0 + key)
+        z[r] = seen ? score_of<false>(rule, z[r], slopes ? slopes[head + r] * kLog2e : 0.f,
+                                      key0 + key)
                     : -INFINITY;
-        float top = z[r];
+        above |= z[r] > m[r];
+      }
+    if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int i = S::kKeys / 2; i > 0; i >>= 1)
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-        top = fmaxf(top, m[r]);
-        const float f = exp2_fast(m[r] - top);
-        const float w = exp2_fast(z[r] - top);
-        m[r] = top;
-        l[r] = fmaf(l[r], f, part ? 0.f : w);
+      for (int r = 0; r < RT; ++r)
+        if (r < rows) {
+          float top = z[r];
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[r][v] *= f;
-        if (part == 0) p[r * S::kKeys + key] = w;
+          for (int i = S::kKeys / 2; i > 0; i >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+          top = fmaxf(top, m[r]);
+          const float f = exp2_fast(m[r] - top);
+          m[r] = top;
+          l[r] *= f;
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[r][v] *= f;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      if (r < rows) {
+        const float w = exp2_fast(z[r] - m[r]);
+        if (part == 0) {
+          l[r] += w;
+          p[r * S::kKeys + key] = w;
+        }
       }
     __syncwarp();
     if (lane * V < D) {
@@ -508,20 +581,25 @@ struct FmaState {
       if ((threadIdx.x & 31) == 0) ml[r] = make_float2(m[r], sum);
     }
   }
+  template <typename Top>
   __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
-                                        const float* top) {
+                                        Top top) const {
     const int col = (threadIdx.x & 31) * V;
     if (col >= D || col < c0 || col >= c0 + C) return;
 #pragma unroll
     for (int r = 0; r < RT; ++r)
       if (r < rows) {
-        const float f = exp2_fast(m[r] - top[r]);
+        const float f = exp2_fast(m[r] - top(r));
 #pragma unroll
         for (int v = 0; v < V; ++v) dst[r * stride + col - c0 + v] = o[r][v] * f;
       }
   }
 };
 
+// ln of a sum that is kept relative to 2^base; -inf of an empty one
+__device__ __forceinline__ float lse_of(float base, float sum) {
+  return sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+}
 template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return __float2bfloat16_rn(x); }
@@ -535,13 +613,16 @@ template <typename T, int D, int RT>
 struct Loader {
   using S = Shape<T, D, RT>;
   Cursor at;
-  long long left;        // tiles not looked up yet
-  int page, key0, head;  // of the tile looked up last; page: of this lane's key
-  unsigned mask;         // its keys to be seen
+  long long left;          // tiles not looked up yet
+  struct Rows {            // a warp's keys of a tile
+    int page, key0, head;  // page: of this lane's key
+    unsigned mask;         // those to be seen
+  };
 
-  __device__ __forceinline__ void look_up(const PagedAttnArgs<T>& a, int HR) {
-    mask = 0;
-    if (left <= 0) return;
+  __device__ __forceinline__ Rows look_up(const PagedAttnArgs<T>& a, int HR) {
+    int page = 0, key0 = 0, head = 0;
+    unsigned mask = 0;
+    if (left <= 0) return {0, 0, 0, 0};
     --left;
     const int warp = threadIdx.x >> 5;
     key0 = at.span.base + at.t * S::kTile + warp * S::kKeys;
@@ -549,19 +630,22 @@ struct Loader {
     if (lo < hi) {
       constexpr unsigned kAll = (unsigned)((1ull << S::kKeys) - 1);
       mask = (kAll << lo) & (kAll >> (S::kKeys - hi));
-      head = at.hr / a.row_blocks;
+      head = a.row_blocks == 1 ? at.hr : at.hr / a.row_blocks;
       // lanes whose key is not to be seen read the first one's page
       const int mine = (threadIdx.x & 31) % S::kKeys;
       const int key = key0 + ((mask >> mine) & 1 ? mine : lo);
       page = __ldg(a.paged.table + (long long)at.s * a.paged.width + (key >> a.paged.page_log2));
     }
     advance(at, a.paged, a.window, S::kTile, HR);
+    return {page, key0, head, mask};
   }
 
-  // copies the looked-up tile's rows to `stage`, notes which of them are seen, and commits
-  __device__ __forceinline__ void issue(const PagedAttnArgs<T>& a, uint32_t stage,
-                                        unsigned* mask_out) {
+  // copies looked-up rows to `stage`, notes which of them are seen, and commits
+  __device__ __forceinline__ void issue(const PagedAttnArgs<T>& a, const Rows& r, uint32_t stage,
+                                        unsigned* mask_out) const {
     const int lane = threadIdx.x & 31;
+    const int page = r.page, key0 = r.key0, head = r.head;
+    unsigned mask = r.mask;
     if (mask) {
       const bool bad = page < 0 || page >= a.paged.num_pages;
       const unsigned wrong = __ballot_sync(0xffffffffu, bad);
@@ -607,10 +691,18 @@ struct Loader {
   }
 };
 
-// The index of the CTA whose share holds tile u of `total` dealt to n CTAs.
-__device__ __forceinline__ int owner_of(long long u, long long total, long long n) {
-  const long long q = total / n, r = total % n;
-  return (int)(u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q);
+// Brings a segment's query rows near, ahead of State::start.
+template <typename T, int D, int RT>
+__device__ __forceinline__ void prefetch_q(const PagedAttnArgs<T>& a, const Cursor& at) {
+  const int kv = a.row_blocks == 1 ? at.hr : at.hr / a.row_blocks;
+  const int rb = at.hr - kv * a.row_blocks;
+  constexpr int kLines = (D * (int)sizeof(T) + 127) / 128;      // of a row
+  const int r = (int)threadIdx.x / kLines;
+  if (r < min(RT, a.G - rb * RT)) {
+    const char* p = reinterpret_cast<const char*>(
+        a.q + at.s * a.q_s + (long long)(kv * a.G + rb * RT + r) * a.q_h);
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p + threadIdx.x % kLines * 128));
+  }
 }
 
 template <typename T, int D, int RT>
@@ -619,7 +711,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   using S = Shape<T, D, RT>;
   using State = typename std::conditional<S::kTensor, TensorState<D, RT>, FmaState<D, RT>>::type;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
   uint8_t* ring = smem + warp * S::kRing;
   float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
@@ -628,21 +720,23 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
 
   griddep_wait();
   griddep_launch();
-  long long u0, u1, total;
-  Cursor at;
-  my_share(a.paged, a.window, S::kTile, HR, &u0, &u1, &total, &at);
+  const Share share = my_share(a.paged, a.window, S::kTile, HR);
+  Cursor at = share.at;
+  long long segment = share.segment;           // where at's segment starts in the row
   int last_seg = kNoSegment, last_cta = 0;    // the segment this CTA begins and another one ends
-  if (u0 < u1) {
-    Loader<T, D, RT> ld;
+  if (share.tiles > 0) {
+    prefetch_q<T, D, RT>(a, at);
+    using Ld = Loader<T, D, RT>;
+    Ld ld;
     ld.at = at;
-    ld.left = u1 - u0;
-    ld.page = ld.key0 = ld.head = 0;
-    ld.look_up(a, HR);
-#pragma unroll 1
-    for (int i = 0; i < S::kStages - 1; ++i) {
-      ld.issue(a, smem_addr(ring) + i * S::kStageBytes, masks + i);
-      ld.look_up(a, HR);
-    }
+    ld.left = share.tiles;
+    typename Ld::Rows rows_of[S::kStages];
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) rows_of[i] = ld.look_up(a, HR);   // their loads together
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i)
+      ld.issue(a, rows_of[i], smem_addr(ring) + i * S::kStageBytes, masks + i);
+    typename Ld::Rows coming = rows_of[S::kStages - 1];
     State st;
     ScoreRule rule;
     rule.scale2 = a.scale * kLog2e;
@@ -653,10 +747,11 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
     int slot = 0, next = S::kStages - 1;     // stages: of this tile, of the next one to issue
     int from = at.t, head = 0, rows = 0;
     bool begin = true;
-    for (long long u = u0; u < u1; ++u) {
+    for (long long left = share.tiles; left > 0; --left) {
       if (begin) {
-        const int rb = at.hr % a.row_blocks;
-        head = at.hr / a.row_blocks * a.G + rb * RT;
+        const int kv = a.row_blocks == 1 ? at.hr : at.hr / a.row_blocks;
+        const int rb = at.hr - kv * a.row_blocks;
+        head = kv * a.G + rb * RT;
         rows = min(RT, a.G - rb * RT);
         rule.last = at.span.len - 1;
         from = at.t;
@@ -665,8 +760,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       }
       copy_wait<S::kStages - 2>();
       __syncwarp();
-      ld.issue(a, smem_addr(ring) + next * S::kStageBytes, masks + next);
-      ld.look_up(a, HR);
+      ld.issue(a, coming, smem_addr(ring) + next * S::kStageBytes, masks + next);
+      coming = ld.look_up(a, HR);
       const unsigned mask = masks[slot];
       if (mask) {
         uint8_t* stage = ring + slot * S::kStageBytes;
@@ -680,63 +775,66 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       next = next + 1 == S::kStages ? 0 : next + 1;
 
       const bool ends = at.t + 1 == at.span.tiles;
-      if (ends || u + 1 == u1) {
-        // join the warps' parts
+      if (ends || left == 1) {
+        // join the warps' parts: every row's sums are added by one warp
+        if (left > 1) {
+          Cursor then = at;
+          advance(then, a.paged, a.window, S::kTile, HR);
+          prefetch_q<T, D, RT>(a, then);
+        }
         st.put_ml(ml + warp * RT);
         __syncthreads();
-        float* top = reinterpret_cast<float*>(smem + S::kOffTop);
-        if (threadIdx.x < RT) {
-          float base = kLowest, sum = 0.f;
-          for (int w = 0; w < S::kWarps; ++w) base = fmaxf(base, ml[w * RT + threadIdx.x].x);
-          for (int w = 0; w < S::kWarps; ++w) {
-            const float2 x = ml[w * RT + threadIdx.x];
-            sum = fmaf(x.y, exp2_fast(x.x - base), sum);
-          }
-          top[threadIdx.x] = base;
-          top[RT + threadIdx.x] = sum;
-        }
-        __syncthreads();
-        const int seg = at.s * HR + at.hr;
         const bool whole = ends && from == 0;
         const int part = blockIdx.x * 2 + (from == 0 ? 1 : 0);
         if (!whole && from == 0) {
-          last_seg = seg;
-          last_cta = owner_of(u - at.t + at.span.tiles - 1, total, gridDim.x);
+          last_seg = at.s * HR + at.hr;
+          last_cta = share_of(segment + at.span.tiles - 1, share.row, gridDim.x);
         }
-        if (threadIdx.x < rows) {
-          const float base = top[threadIdx.x], sum = top[RT + threadIdx.x];
-          if (!whole) {
-            a.part_ml[((long long)part * RT + threadIdx.x) * 2] = base;
-            a.part_ml[((long long)part * RT + threadIdx.x) * 2 + 1] = sum;
-          } else if (a.lse) {
-            a.lse[(long long)at.s * Hq + head + threadIdx.x] =
-                sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
-          }
-        }
+        auto top = [&](int r) {
+          float t = ml[r].x;
+#pragma unroll
+          for (int w = 1; w < S::kWarps; ++w) t = fmaxf(t, ml[w * RT + r].x);
+          return t;
+        };
         // columns at a time: all warps' sums of C columns fit the joining area (rows padded by 8
         // floats against bank conflicts)
-        const int C = min(D, (S::kJoinFloats / (S::kWarps * rows) - 8) & ~7);
+        const int C = rows * S::kWarps * (D + 8) <= S::kJoinFloats
+                          ? D : (S::kJoinFloats / (S::kWarps * rows) - 8) & ~7;
         const int stride = C + 8;
         for (int c0 = 0; c0 < D; c0 += C) {
           st.put_o(join + warp * rows * stride, stride, c0, C, rows, top);
           __syncthreads();
-          const int cols = min(C, D - c0);
-          for (int e = threadIdx.x; e < rows * cols; e += S::kThreads) {
-            const int r = e / cols, c = e % cols;
-            float x = 0.f;
+          for (int r = warp; r < rows; r += S::kWarps) {
+            const float base = top(r);
+            float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) x += join[(w * rows + r) * stride + c];
-            if (whole) {
-              const float sum = top[RT + r];
-              a.out[((long long)at.s * Hq + head + r) * D + c0 + c] =
-                  from_f<T>(sum == 0.f ? 0.f : x / sum);
-            } else {
-              a.part_o[((long long)part * RT + r) * D + c0 + c] = x;
+            for (int w = 0; w < S::kWarps; ++w) {
+              const float2 x = ml[w * RT + r];
+              sum = fmaf(x.y, exp2_fast(x.x - base), sum);
+            }
+            if (c0 == 0 && lane == 0) {
+              if (!whole)
+                reinterpret_cast<float2*>(a.part_ml)[(long long)part * RT + r] =
+                    make_float2(base, sum);
+              else if (a.lse)
+                a.lse[(long long)at.s * Hq + head + r] = lse_of(base, sum);
+            }
+            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+            T* out = a.out + ((long long)at.s * Hq + head + r) * D + c0;
+            float* part_o = a.part_o + ((long long)part * RT + r) * D + c0;
+            const int cols = min(C, D - c0);
+            for (int c = lane; c < cols; c += 32) {
+              float x = 0.f;
+#pragma unroll
+              for (int w = 0; w < S::kWarps; ++w) x += join[(w * rows + r) * stride + c];
+              if (whole) out[c] = from_f<T>(x * inv);
+              else part_o[c] = x;
             }
           }
           __syncthreads();
         }
         begin = true;
+        segment += at.span.tiles + kSegmentCost;
       }
       advance(at, a.paged, a.window, S::kTile, HR);
     }
@@ -803,7 +901,7 @@ paged_join_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   __syncthreads();
   const int head = hr / a.row_blocks * a.G + rb * RT + r;
   if (a.lse && threadIdx.x == 0)
-    a.lse[(long long)s * Hq + head] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+    a.lse[(long long)s * Hq + head] = lse_of(base, sum);
   if (threadIdx.x < D) {
     float x = 0.f;
 #pragma unroll
