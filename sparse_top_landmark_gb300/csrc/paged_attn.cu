@@ -42,18 +42,20 @@ constexpr int kMaxPagedCtas = 512;     // CTAs of a call: parts of a segment tha
 
 // Shared memory and shape of one instantiation.  RT: query rows of a CTA.  A warp's stage is 8 KB
 // (less for small heads, whose tiles would get too long): enough work behind each wait, and
-// stages for 128 KB on the way to each SM.
+// stages for 128 KB on the way to each SM.  Small heads in bf16 leave registers for 16 warps
+// (67 sequences of up to 30515 keys of 32: 35 us with 8, 32 us with 16).
 template <typename T, int D, int RT>
 struct Shape {
   static constexpr bool kTensor = std::is_same<T, bf16>::value;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = kTensor && RT == 8 && D <= 32 ? 16 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRowBytes = D * (int)sizeof(T);
   static constexpr int kKeys = (kTensor ? 32 : 16) / (D == 128 ? 2 : 1);   // of a warp in a tile
   static constexpr int kTile = kWarps * kKeys;
   static constexpr int kChunks = kRowBytes / 16;               // 16-byte chunks of a row
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;    // K then V
-  static constexpr int kStages = kStageBytes == 8192 ? 3 : kStageBytes == 4096 ? 6 : 8;
+  static constexpr int kStages =
+      196608 / (kStageBytes * kWarps) > 8 ? 8 : 196608 / (kStageBytes * kWarps);
   static constexpr int kRing = kStages * kStageBytes;          // of one warp
   static constexpr int kJoinFloats = 5120;                     // outputs being joined over warps
   // byte offsets
@@ -258,7 +260,7 @@ struct ScoreRule {
   bool plain;            // scores are just scale2 * dot, with scale2 >= 0
 };
 // tanh to about 2^-22 absolute, from one exponential and one reciprocal: what bf16 weights (2^-16)
-// can tell, in a quarter of tanhf's instructions (53 sequences of G = 8, d = 32: 54 against 38 us).
+// can tell, in a quarter of tanhf's instructions.
 __device__ __forceinline__ float tanh_fast(float x) {
   const float e = exp2_fast(fabsf(x) * (2.f * kLog2e));
   float r;
