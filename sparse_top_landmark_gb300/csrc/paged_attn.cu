@@ -62,9 +62,7 @@ struct Shape {
   static constexpr int kOffJoin = kWarps * kRing;
   static constexpr int kOffMl = kOffJoin + kJoinFloats * 4;               // [warps][RT][2]
   static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
-  static constexpr int kOffQ = kOffMask + ((kWarps * kStages * 4 + 15) / 16) * 16;
-  static constexpr int kOffP = kOffQ + (kTensor ? 0 : RT * D * 4);        // fp32: q rows
-  static constexpr int kBytes = kOffP + (kTensor ? 0 : kWarps * RT * kKeys * 4);
+  static constexpr int kBytes = kOffMask + kWarps * kStages * 4;
   static_assert(kBytes <= 232448 && kStages >= 3, "shared memory");
 };
 
@@ -291,8 +289,7 @@ struct TensorState {
   float m[kN][2], l[kN][2];          // l: of this lane's keys
   float slope2[kN][2];
 
-  __device__ __forceinline__ void start(const PagedAttnArgs<bf16>& a, int s, int head, int rows,
-                                        uint8_t*) {
+  __device__ __forceinline__ void start(const PagedAttnArgs<bf16>& a, int s, int head, int rows) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
@@ -456,144 +453,206 @@ struct TensorState {
 };
 
 // ---------------------------------------------------------------------------
-// One warp's running softmax, fp32 on the FMA units: a tensor-core product of fp32 values would
-// round them.  For the scores a lane has one key and a share of the columns; for the
-// values D / 32 columns (one, in the lower half of the warp, for D = 16).
+// One warp's running softmax, fp32 on the tensor cores in tf32 (11 bits of a value).  Every value
+// goes in as a sum of two, hi its upper 11 bits and lo = x - hi, of which the upper 11 of at most
+// 13 bits are used: 3 * 2^-23 of the value is lost at most.  The 16 rows of the instruction hold
+// the hi parts of eight query heads (or their weights) and below them the lo parts, so that two
+// products with the hi and the lo part of the other side give all four terms, and a row and the
+// one eight below it add up to the sum.
+// The tensor cores cut sums instead of rounding them, so that long chains lose a little each time:
+// a score is summed in four chains, and a tile's values are added to the running ones outside.
+// A lane has query head lane / 4, and keys (lane % 4) * 2, + 1 of every eight.
 // ---------------------------------------------------------------------------
-template <int D, int RT>
-struct FmaState {
-  using S = Shape<float, D, RT>;
-  static constexpr int V = D >= 32 ? D / 32 : 1;
-  static constexpr int kParts = 32 / S::kKeys;     // lanes that share a key
-  float o[RT][V];
-  float m[RT], l[RT];    // l: of this lane's key, in the first of its lanes
+template <int D>
+struct SplitState {
+  using S = Shape<float, D, 8>;
+  static constexpr int kV = D >= 32 ? 4 : 2;   // value columns a lane reads at once
+  static constexpr int kChains = D >= 64 ? 4 : 2;
+  uint32_t q[D / 8][4];
+  float o[D / 8][2];
+  float m, l;            // l: of this lane's keys
+  float slope2;
+  const float* q_row;    // null behind the last query head
 
-  __device__ __forceinline__ void start(const PagedAttnArgs<float>& a, int s, int head, int rows,
-                                        uint8_t* smem) {
-    float* q = reinterpret_cast<float*>(smem + S::kOffQ);
-    for (int e = threadIdx.x; e < rows * D; e += S::kThreads)
-      q[e] = a.q[s * a.q_s + (long long)(head + e / D) * a.q_h + e % D];
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      m[r] = kLowest;
-      l[r] = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[r][v] = 0.f;
-    }
+  __device__ __forceinline__ static void split(float x, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+  }
+  // c[16 x 8] += a[16 x 8] b[8 x 8], tf32 products
+  __device__ __forceinline__ static void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 
-  __device__ __forceinline__ void tile(const ScoreRule& rule, const uint8_t* stage, int key0,
-                                       unsigned mask, int rows, uint8_t* smem, const float* slopes,
-                                       int head) {
-    const int lane = threadIdx.x & 31, key = lane % S::kKeys, part = lane / S::kKeys;
-    const float* q = reinterpret_cast<const float*>(smem + S::kOffQ);
-    float* p = reinterpret_cast<float*>(smem + S::kOffP) + (threadIdx.x >> 5) * RT * S::kKeys;
-    float z[RT] = {};
-#pragma unroll RT <= 4 ? 8 : 2
-    for (int c = 0; c < D / 4 / kParts; ++c) {
-      const int ch = part * (D / 4 / kParts) + c;
-      const float4 k = *reinterpret_cast<const float4*>(
-          stage + key * S::kRowBytes + swizzle<S::kRowBytes>(key, ch) * 16);
+  __device__ __forceinline__ void start(const PagedAttnArgs<float>& a, int s, int head, int rows) {
+    const int lane = threadIdx.x & 31, r = lane / 4;
+    const float* p = a.q + s * a.q_s + (long long)(head + r) * a.q_h;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        if (r < rows) {
-          const float4 x = *reinterpret_cast<const float4*>(q + r * D + ch * 4);
-          z[r] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, fmaf(x.w, k.w, z[r]))));
-        }
+    for (int k = 0; k < D / 8; ++k) {
+      split(r < rows ? p[k * 8 + lane % 4] : 0.f, q[k][0], q[k][1]);
+      split(r < rows ? p[k * 8 + 4 + lane % 4] : 0.f, q[k][2], q[k][3]);
     }
-    const bool seen = (mask >> key) & 1;
-    // as on the tensor cores, the maxima are looked for again only where a score is above them
+    q_row = r < rows ? p : nullptr;
+    slope2 = a.slopes && r < rows ? a.slopes[head + r] * kLog2e : 0.f;
+    m = kLowest;
+    l = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = 0.f;
+  }
+
+  static __device__ __noinline__ float plain_dot(const float* q_row, uint32_t kt, int row) {
+    float sum = 0.f;
+    if (q_row == nullptr) return sum;
+    for (int c = 0; c < D; ++c) {
+      float k;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(k)
+                   : "r"(kt + row * S::kRowBytes + swizzle<S::kRowBytes>(row, c / 4) * 16 + c % 4 * 4)
+                   : "memory");
+      sum = fmaf(q_row[c], k, sum);
+    }
+    return sum;
+  }
+
+  __device__ __forceinline__ void tile(const ScoreRule& rule, uint32_t kt, uint32_t vt, int key0,
+                                       unsigned mask) {
+    constexpr int kT = S::kKeys / 8;
+    const int lane = threadIdx.x & 31;
+    float z[kT][2];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      float c[kChains][4] = {};
+      const int row = 8 * t + (lane & 7);
+#pragma unroll
+      for (int k = 0; k < D / 8; k += 2) {
+        uint32_t b[4], lo[4];
+        ldsm4(kt + row * S::kRowBytes + swizzle<S::kRowBytes>(row, 2 * k + (lane >> 3)) * 16, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split(__uint_as_float(b[i]), b[i], lo[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma(c[(k + i) % kChains], q[k + i], b[2 * i], b[2 * i + 1]);
+          mma(c[(k + i) % kChains], q[k + i], lo[2 * i], lo[2 * i + 1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        z[t][i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < kChains; ++x) z[t][i] += c[x][i] + c[x][i + 2];
+      }
+    }
+    // An infinite key or query value has no parts: where a sum came out NaN it is done again in
+    // plain fp32.
+    bool odd = false;
+#pragma unroll
+    for (int t = 0; t < kT; ++t) odd |= isnan(z[t][0]) || isnan(z[t][1]);
+    if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (isnan(z[t][i])) z[t][i] = plain_dot(q_row, kt, 8 * t + lane % 4 * 2 + i);
+    }
     bool above = false;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-      if (r < rows) {
+    for (int t = 0; t < kT; ++t)
 #pragma unroll
-        for (int i = 16; i >= S::kKeys; i >>= 1) z[r] += __shfl_xor_sync(0xffffffffu, z[r], i);
-        z[r] = seen ? score_of<false>(rule, z[r], slopes ? slopes[head + r] * kLog2e : 0.f,
-                                      key0 + key)
-                    : -INFINITY;
-        above |= z[r] > m[r];
+      for (int i = 0; i < 2; ++i) {
+        const int j = 8 * t + lane % 4 * 2 + i;
+        z[t][i] = rule.plain ? z[t][i] * rule.scale2
+                             : score_of<false>(rule, z[t][i], slope2, key0 + j);
+        if (!((mask >> j) & 1)) z[t][i] = -INFINITY;
+        above |= z[t][i] > m;
       }
     if (__any_sync(0xffffffffu, above)) {
+      float top = m;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        if (r < rows) {
-          float top = z[r];
+      for (int t = 0; t < kT; ++t) top = fmaxf(top, fmaxf(z[t][0], z[t][1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float f = exp2_fast(m - top);
+      m = top;
+      l *= f;
 #pragma unroll
-          for (int i = S::kKeys / 2; i > 0; i >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-          top = fmaxf(top, m[r]);
-          const float f = exp2_fast(m[r] - top);
-          m[r] = top;
-          l[r] *= f;
-#pragma unroll
-          for (int v = 0; v < V; ++v) o[r][v] *= f;
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-      if (r < rows) {
-        const float w = exp2_fast(z[r] - m[r]);
-        if (part == 0) {
-          l[r] += w;
-          p[r * S::kKeys + key] = w;
-        }
-      }
-    __syncwarp();
-    if (lane * V < D) {
-      const uint8_t* vs = stage + S::kKeys * S::kRowBytes;
-      const int ch = lane * V / 4, in = lane * V % 4 * 4;
-#pragma unroll
-      for (int k4 = 0; k4 < S::kKeys / 4; ++k4) {
-        float x[4][V];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = 4 * k4 + k;
-          const float* src = reinterpret_cast<const float*>(
-              vs + row * S::kRowBytes + swizzle<S::kRowBytes>(row, ch) * 16 + in);
-          if constexpr (V == 4) {
-            const float4 t = *reinterpret_cast<const float4*>(src);
-            x[k][0] = t.x; x[k][1] = t.y; x[k][2] = t.z; x[k][3] = t.w;
-          } else if constexpr (V == 2) {
-            const float2 t = *reinterpret_cast<const float2*>(src);
-            x[k][0] = t.x; x[k][1] = t.y;
-          } else {
-            x[k][0] = *src;
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-          if (r < rows) {
-            const float4 w = *reinterpret_cast<const float4*>(p + r * S::kKeys + 4 * k4);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-              o[r][v] = fmaf(w.x, x[0][v], fmaf(w.y, x[1][v], fmaf(w.z, x[2][v],
-                        fmaf(w.w, x[3][v], o[r][v]))));
-          }
+      for (int j = 0; j < D / 8; ++j) {
+        o[j][0] *= f;
+        o[j][1] *= f;
       }
     }
-    __syncwarp();          // p is written again by the next tile
+    // The weights are the left operand as they lie if its eight keys are taken in the order 0, 2,
+    // 4, 6, 1, 3, 5, 7, and so are the value rows: lane % 4 reads rows 2 (lane % 4) and + 1.
+    uint32_t p[kT][4];
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float w = exp2_fast(z[t][i] - m);
+        l += w;
+        split(w, p[t][2 * i], p[t][2 * i + 1]);
+      }
+    // columns of the values in the order that lets a lane read kV at once: column n of product
+    // kV * g + x is column 8 kV g + kV n + x of the row
+#pragma unroll
+    for (int g = 0; g < D / 8 / kV; ++g) {
+      float c[kV][4] = {};
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        float v[2][kV];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 8 * t + lane % 4 * 2 + i, col = 8 * kV * g + kV * (lane / 4);
+          const uint32_t at = vt + row * S::kRowBytes +
+                              swizzle<S::kRowBytes>(row, col / 4) * 16 + col % 4 * 4;
+          if constexpr (kV == 4)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[i][0]), "=f"(v[i][1]), "=f"(v[i][2]), "=f"(v[i][3])
+                         : "r"(at)
+                         : "memory");
+          else
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(v[i][0]), "=f"(v[i][1])
+                         : "r"(at)
+                         : "memory");
+        }
+#pragma unroll
+        for (int x = 0; x < kV; ++x) {
+          uint32_t h0, h1, l0, l1;
+          split(v[0][x], h0, l0);
+          split(v[1][x], h1, l1);
+          mma(c[x], p[t], h0, h1);
+          mma(c[x], p[t], l0, l1);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kV; ++x) {
+        o[kV * g + x][0] += c[x][0] + c[x][2];
+        o[kV * g + x][1] += c[x][1] + c[x][3];
+      }
+    }
   }
 
   __device__ __forceinline__ void put_ml(float2* ml) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const float sum = warp_sum(l[r]);
-      if ((threadIdx.x & 31) == 0) ml[r] = make_float2(m[r], sum);
-    }
+    const int lane = threadIdx.x & 31;
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (lane % 4 == 0) ml[lane / 4] = make_float2(m, l);
   }
   template <typename Top>
   __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
                                         Top top) const {
-    const int col = (threadIdx.x & 31) * V;
-    if (col >= D || col < c0 || col >= c0 + C) return;
+    const int lane = threadIdx.x & 31, r = lane / 4;
+    if (r >= rows) return;
+    const float f = exp2_fast(m - top(r));
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-      if (r < rows) {
-        const float f = exp2_fast(m[r] - top(r));
+    for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-        for (int v = 0; v < V; ++v) dst[r * stride + col - c0 + v] = o[r][v] * f;
+      for (int i = 0; i < 2; ++i) {
+        const int col = 8 * kV * (j / kV) + kV * (lane % 4 * 2 + i) + j % kV;
+        if (col >= c0 && col < c0 + C) dst[r * stride + col - c0] = o[j][i] * f;
       }
   }
 };
@@ -693,6 +752,10 @@ struct Loader {
   }
 };
 
+template <typename T, int D, int RT> struct StateOf;
+template <int D, int RT> struct StateOf<bf16, D, RT> { using type = TensorState<D, RT>; };
+template <int D> struct StateOf<float, D, 8> { using type = SplitState<D>; };
+
 // Brings a segment's query rows near, ahead of State::start.
 template <typename T, int D, int RT>
 __device__ __forceinline__ void prefetch_q(const PagedAttnArgs<T>& a, const Cursor& at) {
@@ -711,7 +774,7 @@ template <typename T, int D, int RT>
 __global__ void __launch_bounds__(Shape<T, D, RT>::kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   using S = Shape<T, D, RT>;
-  using State = typename std::conditional<S::kTensor, TensorState<D, RT>, FmaState<D, RT>>::type;
+  using State = typename StateOf<T, D, RT>::type;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
@@ -757,7 +820,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
         rows = min(RT, a.G - rb * RT);
         rule.last = at.span.len - 1;
         from = at.t;
-        st.start(a, at.s, head, rows, smem);
+        st.start(a, at.s, head, rows);
         begin = false;
       }
       copy_wait<S::kStages - 2>();
@@ -766,12 +829,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       coming = ld.look_up(a, HR);
       const unsigned mask = masks[slot];
       if (mask) {
-        uint8_t* stage = ring + slot * S::kStageBytes;
-        const int key0 = at.span.base + at.t * S::kTile + warp * S::kKeys;
-        if constexpr (S::kTensor)
-          st.tile(rule, smem_addr(stage), smem_addr(stage) + S::kKeys * S::kRowBytes, key0, mask);
-        else
-          st.tile(rule, stage, key0, mask, rows, smem, a.slopes, head);
+        const uint32_t stage = smem_addr(ring) + slot * S::kStageBytes;
+        st.tile(rule, stage, stage + S::kKeys * S::kRowBytes,
+                at.span.base + at.t * S::kTile + warp * S::kKeys, mask);
       }
       slot = slot + 1 == S::kStages ? 0 : slot + 1;
       next = next + 1 == S::kStages ? 0 : next + 1;
@@ -975,8 +1035,8 @@ struct Run {
   }
 };
 
-// The instantiation for a head dim, type and group: a CTA takes 8 query rows where the group has no
-// more (fp32: 4), else 16, the matrix instruction's height.
+// The instantiation for a head dim, type and group: a CTA takes 8 query rows, in bf16 16 where the
+// group has more; larger groups take several CTAs.
 template <typename T, int RT, typename F>
 auto with_dim(int d, F f) {
   switch (d) {
@@ -988,8 +1048,10 @@ auto with_dim(int d, F f) {
 }
 template <typename T, typename F>
 auto with_shape(int d, int G, F f) {
-  constexpr int kSmall = std::is_same<T, bf16>::value ? 8 : 4;
-  return G <= kSmall ? with_dim<T, kSmall>(d, f) : with_dim<T, 16>(d, f);
+  if constexpr (std::is_same<T, bf16>::value) {
+    if (G > 8) return with_dim<T, 16>(d, f);
+  }
+  return with_dim<T, 8>(d, f);
 }
 
 }  // namespace
