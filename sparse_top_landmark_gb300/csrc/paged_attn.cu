@@ -10,10 +10,11 @@
 // Work is dealt out on the device, since lengths live there (a replayed graph sees new ones):
 // every (sequence, key head, block of query rows) is a segment of tiles of kTile keys, the
 // segments stand in one row, and each CTA takes an equal share of that row, whatever the lengths
-// are.  Ending a segment costs about a tile's time, so it counts as kSegmentCost tiles more.  A CTA finishes the segments that lie wholly in its share; of a
-// segment that is cut it leaves a partial (maximum, sum, weighted values) in its first or
-// its last slot of the workspace, and paged_join_kernel joins those of a segment in
-// their order.  Nothing is added atomically: the result depends on the inputs alone.
+// are.  Ending a segment takes a tile's time or two, so it counts as kSegmentCost tiles more.  A
+// CTA finishes the segments that lie wholly in its share; of a segment that is cut it leaves a
+// partial (maximum, sum, weighted values) in its first or its last slot of the workspace, and
+// paged_join_kernel joins those of a segment in their order.  Nothing is added atomically: the
+// result depends on the inputs alone.
 //
 // A warp works on its own keys of each tile (kKeys) through its own ring of shared-memory stages,
 // filled by 16-byte asynchronous copies some stages ahead, across the ends of segments; warps
@@ -35,7 +36,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum before the first key: below every finite score, and finite, so that
 // differences with it need no special case (a score of -inf weighs nothing against it).
 constexpr float kLowest = -FLT_MAX;
-constexpr int kSegmentCost = 1;
 constexpr int kNoSegment = -1;
 constexpr int kJoinThreads = 256;
 constexpr int kMaxPagedCtas = 512;     // CTAs of a call: parts of a segment that can be joined
@@ -52,6 +52,7 @@ struct Shape {
   static constexpr int kRowBytes = D * (int)sizeof(T);
   static constexpr int kKeys = (kTensor ? 32 : 16) / (D == 128 ? 2 : 1);   // of a warp in a tile
   static constexpr int kTile = kWarps * kKeys;
+  static constexpr int kSegmentCost = kTensor ? 2 : 1;         // tiles that ending a segment is worth
   static constexpr int kChunks = kRowBytes / 16;               // 16-byte chunks of a row
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;    // K then V
   static constexpr int kStages =
@@ -138,21 +139,24 @@ __device__ __forceinline__ Span span_of(const PagedLayout& pg, int window, int t
   return r;
 }
 
-// A place in the row of tiles: tile `t` of segment (s, hr), hr = key head * row blocks + block.
+// A place in the row: tile `t` of segment (s, hr), hr = key head * row blocks + block; the segment
+// begins at position `segment` of the row, and ends kSegmentCost positions after its last tile's.
 struct Cursor {
   int s, hr, t;
+  long long segment;
   Span span;
 };
 
-__device__ __forceinline__ void advance(Cursor& c, const PagedLayout& pg, int window, int tile,
-                                        int HR) {
+template <typename S>
+__device__ __forceinline__ void advance(Cursor& c, const PagedLayout& pg, int window, int HR) {
   if (++c.t < c.span.tiles) return;
   c.t = 0;
+  c.segment += c.span.tiles + S::kSegmentCost;
   if (++c.hr < HR) return;
   c.hr = 0;
   do {
-    if (++c.s >= pg.S) return;      // behind the last segment: not used any more
-    c.span = span_of(pg, window, tile, c.s);
+    if (++c.s >= pg.S) return;      // behind the last segment, and at the end of the row
+    c.span = span_of(pg, window, S::kTile, c.s);
   } while (c.span.tiles == 0);
 }
 
@@ -171,12 +175,6 @@ __device__ __forceinline__ long long quotient(long long a, int b) {
   return a >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// A CTA's share of the row: its tiles, the first one's place, the position of that segment's start in
-// the row, and the row's length (both with the ends of segments counted).
-struct Share {
-  long long tiles, segment, row;
-  Cursor at;
-};
 __device__ __forceinline__ long long share_begin(long long row, int n, int c) {
   const long long q = quotient(row, n), r = row - q * n;
   return q * c + min((long long)c, r);
@@ -188,64 +186,55 @@ __device__ __forceinline__ int share_of(long long x, long long row, int n) {
   return (int)(x < large ? quotient(x, (int)q + 1) : r + quotient(x - large, (int)q));
 }
 
-// Each warp finds the share for itself: a sum over the sequences for the row's length, then a
-// running sum until both ends of the share are behind.
-__device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int tile, int HR) {
+// The length of the row, the place of this CTA's first tile, and the position where its share
+// ends (a share may be empty, or hold ends of segments only: the first tile then lies behind).
+// Each warp finds them for itself: a sum over the sequences, then a running sum until the share's
+// beginning is behind.
+struct Share {
+  long long row, end;
+  Cursor at;
+};
+template <typename S>
+__device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int HR) {
   const int lane = threadIdx.x & 31;
-  auto tiles_of = [&](int s) { return s < pg.S ? span_of(pg, window, tile, s).tiles : 0; };
+  auto tiles_of = [&](int s) { return s < pg.S ? span_of(pg, window, S::kTile, s).tiles : 0; };
   auto cost_of = [&](int tiles) {
-    return tiles > 0 ? (long long)(tiles + kSegmentCost) * HR : 0;
+    return tiles > 0 ? (long long)(tiles + S::kSegmentCost) * HR : 0;
   };
   Share sh;
-  sh.tiles = 0;
   const int mine = tiles_of(lane);           // of the first 32 sequences: often all there are
   long long row = cost_of(mine);
   for (int s = 32 + lane; s < pg.S; s += 32) row += cost_of(tiles_of(s));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) row += __shfl_xor_sync(0xffffffffu, row, o);
   sh.row = row;
-  const long long x0 = share_begin(row, gridDim.x, blockIdx.x);
-  const long long x1 = share_begin(row, gridDim.x, blockIdx.x + 1);
-  if (x0 >= x1) return sh;
-  long long run = 0, before_x0 = 0;          // the row up to this batch; tiles before x0
-  int filled = 0;                            // sequences with a tile up to this batch
+  const long long x = share_begin(row, gridDim.x, blockIdx.x);
+  sh.end = share_begin(row, gridDim.x, blockIdx.x + 1);
+  sh.at.segment = row;
+  sh.at.t = 0;
+  if (x >= sh.end) return sh;
+  long long run = 0;                         // the row up to this batch
   for (int s0 = 0; s0 < pg.S; s0 += 32) {
     const int tiles = s0 == 0 ? mine : tiles_of(s0 + lane);
     const long long cost = cost_of(tiles);
     const long long incl = run + warp_incl_scan64(cost);
-    const unsigned any = __ballot_sync(0xffffffffu, tiles > 0);
-#pragma unroll
-    for (int end = 0; end < 2; ++end) {
-      const long long x = end ? x1 - 1 : x0;           // the last position has tiles up to it
-      const unsigned hit = __ballot_sync(0xffffffffu, incl - cost <= x && x < incl);
-      if (hit == 0) continue;
-      const int src = __ffs(hit) - 1;
-      const int n = __shfl_sync(0xffffffffu, tiles, src);
-      const long long start = __shfl_sync(0xffffffffu, incl - cost, src);
-      const int seg = (int)quotient(x - start, n + kSegmentCost);
-      const int in = (int)(x - start - (long long)seg * (n + kSegmentCost));
-      // tiles before the sequence, of its segments before this one, and of this one
-      const long long before =
-          start - (long long)kSegmentCost * HR * (filled + __popc(any & ((1u << src) - 1))) +
-          (long long)seg * n;
-      if (end == 0) {
-        before_x0 = before + min(in, n);
-        sh.segment = x - in;
-        sh.at.s = s0 + src;
-        sh.at.hr = seg;
-        sh.at.t = min(in, n - 1);
-        sh.at.span = span_of(pg, window, tile, sh.at.s);
-        if (in >= n) {                       // the share begins behind a segment's last tile
-          sh.segment += n + kSegmentCost;
-          advance(sh.at, pg, window, tile, HR);
-        }
-      } else {
-        sh.tiles = before + min(in + 1, n) - before_x0;
-      }
+    const unsigned hit = __ballot_sync(0xffffffffu, x < incl);
+    if (hit == 0) {
+      run = __shfl_sync(0xffffffffu, incl, 31);
+      continue;
     }
-    if (x1 <= __shfl_sync(0xffffffffu, incl, 31)) break;
-    run = __shfl_sync(0xffffffffu, incl, 31);
-    filled += __popc(any);
+    const int src = __ffs(hit) - 1;
+    const int n = __shfl_sync(0xffffffffu, tiles, src);
+    const long long start = __shfl_sync(0xffffffffu, incl - cost, src);
+    const int seg = (int)quotient(x - start, n + S::kSegmentCost);
+    sh.at.segment = start + (long long)seg * (n + S::kSegmentCost);
+    const int in = (int)(x - sh.at.segment);
+    sh.at.s = s0 + src;
+    sh.at.hr = seg;
+    sh.at.t = min(in, n - 1);
+    sh.at.span = span_of(pg, window, S::kTile, sh.at.s);
+    if (in >= n) advance<S>(sh.at, pg, window, HR);   // it begins behind a segment's last tile
+    break;
   }
   return sh;
 }
@@ -674,7 +663,7 @@ template <typename T, int D, int RT>
 struct Loader {
   using S = Shape<T, D, RT>;
   Cursor at;
-  long long left;          // tiles not looked up yet
+  long long end;           // of the share
   struct Rows {            // a warp's keys of a tile
     int page, key0, head;  // page: of this lane's key
     unsigned mask;         // those to be seen
@@ -683,8 +672,7 @@ struct Loader {
   __device__ __forceinline__ Rows look_up(const PagedAttnArgs<T>& a, int HR) {
     int page = 0, key0 = 0, head = 0;
     unsigned mask = 0;
-    if (left <= 0) return {0, 0, 0, 0};
-    --left;
+    if (at.segment + at.t >= end) return {0, 0, 0, 0};
     const int warp = threadIdx.x >> 5;
     key0 = at.span.base + at.t * S::kTile + warp * S::kKeys;
     const int lo = max(at.span.first - key0, 0), hi = min(at.span.len - key0, S::kKeys);
@@ -697,7 +685,7 @@ struct Loader {
       const int key = key0 + ((mask >> mine) & 1 ? mine : lo);
       page = __ldg(a.paged.table + (long long)at.s * a.paged.width + (key >> a.paged.page_log2));
     }
-    advance(at, a.paged, a.window, S::kTile, HR);
+    advance<S>(at, a.paged, a.window, HR);
     return {page, key0, head, mask};
   }
 
@@ -785,16 +773,15 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
 
   griddep_wait();
   griddep_launch();
-  const Share share = my_share(a.paged, a.window, S::kTile, HR);
+  const Share share = my_share<S>(a.paged, a.window, HR);
   Cursor at = share.at;
-  long long segment = share.segment;           // where at's segment starts in the row
   int last_seg = kNoSegment, last_cta = 0;    // the segment this CTA begins and another one ends
-  if (share.tiles > 0) {
+  if (at.segment + at.t < share.end) {
     prefetch_q<T, D, RT>(a, at);
     using Ld = Loader<T, D, RT>;
     Ld ld;
     ld.at = at;
-    ld.left = share.tiles;
+    ld.end = share.end;
     typename Ld::Rows rows_of[S::kStages];
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) rows_of[i] = ld.look_up(a, HR);   // their loads together
@@ -812,7 +799,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
     int slot = 0, next = S::kStages - 1;     // stages: of this tile, of the next one to issue
     int from = at.t, head = 0, rows = 0;
     bool begin = true;
-    for (long long left = share.tiles; left > 0; --left) {
+    do {
       if (begin) {
         const int kv = a.row_blocks == 1 ? at.hr : at.hr / a.row_blocks;
         const int rb = at.hr - kv * a.row_blocks;
@@ -837,20 +824,18 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       next = next + 1 == S::kStages ? 0 : next + 1;
 
       const bool ends = at.t + 1 == at.span.tiles;
-      if (ends || left == 1) {
+      if (ends || at.segment + at.t + 1 == share.end) {
         // join the warps' parts: every row's sums are added by one warp
-        if (left > 1) {
-          Cursor then = at;
-          advance(then, a.paged, a.window, S::kTile, HR);
-          prefetch_q<T, D, RT>(a, then);
-        }
+        Cursor then = at;
+        advance<S>(then, a.paged, a.window, HR);
+        if (ends && then.segment < share.end) prefetch_q<T, D, RT>(a, then);
         st.put_ml(ml + warp * RT);
         __syncthreads();
         const bool whole = ends && from == 0;
         const int part = blockIdx.x * 2 + (from == 0 ? 1 : 0);
         if (!whole && from == 0) {
           last_seg = at.s * HR + at.hr;
-          last_cta = share_of(segment + at.span.tiles - 1, share.row, gridDim.x);
+          last_cta = share_of(at.segment + at.span.tiles - 1, share.row, gridDim.x);
         }
         auto top = [&](int r) {
           float t = ml[r].x;
@@ -896,10 +881,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
           __syncthreads();
         }
         begin = true;
-        segment += at.span.tiles + kSegmentCost;
       }
-      advance(at, a.paged, a.window, S::kTile, HR);
-    }
+      advance<S>(at, a.paged, a.window, HR);
+    } while (at.segment + at.t < share.end);
     copy_wait<0>();
   }
   if (threadIdx.x == 0) {
@@ -1027,7 +1011,9 @@ struct Run {
     if (e != cudaSuccess) return e;
     count_launch();
     e = launch_pdl(paged_attn_kernel<T, D, RT>, dim3(grid), dim3(Sh::kThreads), Sh::kBytes, st, a);
-    if (e != cudaSuccess || grid == 1) return e;      // one CTA cuts no segment
+    // one CTA cuts no segment, nor is a segment of one tile ever cut
+    if (e != cudaSuccess || grid == 1 || (long long)a.paged.width << a.paged.page_log2 <= Sh::kTile)
+      return e;
     count_launch();
     return launch_pdl(paged_join_kernel<T, D, RT>, dim3(grid, std::min(a.G, RT)), dim3(kJoinThreads), 0,
                       st,
