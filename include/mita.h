@@ -342,6 +342,7 @@ int mita_forward_host_f32(const float* q, const float* k, const float* v, int B,
  *   *_strides       elements between batches, heads and tokens.
  *   rot             a multiple of 8 in [0, d]; values rot .. d-1 are not turned.
  *   interleaved     0: pairs (i, i + rot/2); else pairs (2i, 2i + 1).
+ * In a row that holds an infinity or NaN, any value may come out as NaN.
  * B or N = 0 does nothing.  Needs no workspace.
  */
 typedef struct mita_qk_norm_rope_params {
@@ -415,7 +416,7 @@ uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
  *   q_out [tokens,Hq,d]  output; rows left out, and rows of idle slots, stay as they are.
  *   *_strides       elements between tokens and heads.
  * The angle of a key or query is that of its position in the sequence.  Two tokens that the
- * table sends to one row of the cache leave either one's values there.
+ * table sends to one row of the cache leave a mixture of their values there.
  */
 typedef struct mita_cache_append_params {
   const void *q, *k, *v;
@@ -446,6 +447,7 @@ int mita_cache_append_f32(const mita_cache_append_params* params, mita_stream_t 
  *   workspace       device, 16-byte aligned, of mita_paged_attn_workspace_bytes; the caller's, so
  *                   that calls captured into different graphs can have their own.
  * The same inputs give the same bits.  Cache rows that no sequence's length covers are never read.
+ * An infinity among the values that are seen may come out as NaN in its column.
  */
 typedef struct mita_paged_attn_params {
   const void *q, *k_cache, *v_cache;

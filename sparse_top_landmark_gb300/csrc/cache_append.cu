@@ -18,13 +18,14 @@ namespace mita {
 namespace {
 
 // The sequence of token t: the last s with seq_start[s] <= t (empty sequences are passed over);
-// -1 for a token before the first sequence or behind the last one.
+// -1 for a token before the first sequence or behind the last one.  (Whatever the array holds,
+// seq_start[s] <= t < seq_start[s + 1] on return.)
 __device__ __forceinline__ int sequence_of(const int32_t* seq_start, int S, int t) {
-  if (t < __ldg(seq_start) || t >= __ldg(seq_start + S)) return -1;
+  if (t < seq_start[0] || t >= seq_start[S]) return -1;
   int lo = 0, hi = S;       // seq_start[lo] <= t < seq_start[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(seq_start + mid) <= t) lo = mid; else hi = mid;
+    if (seq_start[mid] <= t) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -105,7 +106,7 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
       live = len != 0;                       // else an idle slot
       if (live) {
         int page = -1;
-        if (len >= end - begin && (len - 1) >> pg.page_log2 < pg.width)
+        if (pos >= 0 && len >= end - begin && (len - 1) >> pg.page_log2 < pg.width)
           page = pg.table[(long long)s * pg.width + (pos >> pg.page_log2)];
         live = page >= 0 && page < pg.num_pages;
         if (!live && threadIdx.x % L == 0) flag_error(a.status, kDevErrBadIndex);

@@ -56,7 +56,7 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 
 // Bits of the per-device status word (read by mita_get_last_device_error).
 enum : int {
-  kDevErrBadIndex = 1,    // an expert index outside [0, N)
+  kDevErrBadIndex = 1,    // an expert index outside [0, N); a cache page or length out of range
   kDevErrBadBucket = 2,   // bucket offsets / query ids inconsistent
   kDevErrRoute = 4,       // a routed landmark outside [0, m)
   kDevErrTimeout = 8,     // a bounded wait inside a kernel gave up

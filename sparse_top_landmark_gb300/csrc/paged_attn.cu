@@ -683,7 +683,7 @@ struct Loader {
       // lanes whose key is not to be seen read the first one's page
       const int mine = (threadIdx.x & 31) % S::kKeys;
       const int key = key0 + ((mask >> mine) & 1 ? mine : lo);
-      page = __ldg(a.paged.table + (long long)at.s * a.paged.width + (key >> a.paged.page_log2));
+      page = a.paged.table[(long long)at.s * a.paged.width + (key >> a.paged.page_log2)];
     }
     advance<S>(at, a.paged, a.window, HR);
     return {page, key0, head, mask};
@@ -843,11 +843,11 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
           for (int w = 1; w < S::kWarps; ++w) t = fmaxf(t, ml[w * RT + r].x);
           return t;
         };
-        // columns at a time: all warps' sums of C columns fit the joining area (rows padded by 8
-        // floats against bank conflicts)
-        const int C = rows * S::kWarps * (D + 8) <= S::kJoinFloats
-                          ? D : (S::kJoinFloats / (S::kWarps * rows) - 8) & ~7;
-        const int stride = C + 8;
+        // columns at a time: all warps' sums of C columns fit the joining area (rows padded by 4
+        // floats, which puts put_o's four or eight rows into different banks)
+        const int C = rows * S::kWarps * (D + 4) <= S::kJoinFloats
+                          ? D : (S::kJoinFloats / (S::kWarps * rows) - 4) & ~7;
+        const int stride = C + 4;
         for (int c0 = 0; c0 < D; c0 += C) {
           st.put_o(join + warp * rows * stride, stride, c0, C, rows, top);
           __syncthreads();

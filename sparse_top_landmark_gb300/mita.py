@@ -578,6 +578,7 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     Hq = q.shape[1]
     shape = (S, Hq, d)
     qs = _rows(q, "q", shape, dt, dev)
+    window = min(window, 0x7fffffff)
     slopes = 0
     if alibi_slopes is not None:
         slopes = _dense(alibi_slopes, "alibi_slopes", (Hq,), torch.float32, dev)

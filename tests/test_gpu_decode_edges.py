@@ -1,0 +1,223 @@
+"""Calls of the q / k preparation and the paged cache at the edges of what is allowed: far
+strides, chains of launches on the same memory, empty tables, bad indices, many heads, a first
+call inside a capture."""
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import decode_util as R
+from conftest import ROOT
+
+pytestmark = pytest.mark.gpu
+
+
+def M():
+    from sparse_top_landmark_gb300 import build, mita
+    build.build()
+    return mita
+
+
+def lens(*n):
+    return torch.tensor(n, dtype=torch.int32).cuda()
+
+
+def test_in_place_chain():
+    """Twenty launches back to back, each rotating what the one before left in the same memory (the
+    next kernel's blocks are launched early): the same bits as with a buffer for each."""
+    mita = M()
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(1, 24, 4001, 64, generator=g).bfloat16().cuda()
+    w, freq = (1 + 0.1 * torch.randn(64, generator=g)).cuda(), R.inv_freq(64).cuda()
+    want = [x]
+    for _ in range(20):
+        want.append(mita.mita_qk_norm_rope(want[-1], None, freq, w)[0])
+    got = x.clone()
+    for _ in range(20):
+        mita.mita_qk_norm_rope(got, None, freq, w, q_out=got)
+    assert torch.equal(got, want[-1])
+    for _ in range(20):
+        mita.mita_qk_norm_rope_backward(x, None, got, None, freq, w, dq=got)
+    ref = want[-1]
+    for _ in range(20):
+        ref = mita.mita_qk_norm_rope_backward(x, None, ref, None, freq, w)[0]
+    assert torch.equal(got, ref)
+
+
+def test_append_then_attend_chain():
+    """Steps back to back with nothing waited for, lengths, tables and queries made on the device
+    just before each step: the same bits as with a synchronisation after every call."""
+    mita = M()
+    S, Hq, Hkv, d, page, steps = 5, 8, 2, 64, 16, 60
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(steps, S, Hq + 2 * Hkv, d, generator=g).bfloat16().cuda()
+    freq = R.inv_freq(d).cuda()
+    table0 = torch.randperm(S * 8, generator=g).to(torch.int32).view(S, 8).cuda()
+
+    def decode(wait):
+        kc = torch.zeros(S * 8, Hkv, page, d, dtype=torch.bfloat16, device="cuda")
+        vc, n, outs = torch.zeros_like(kc), torch.zeros(S, dtype=torch.int32, device="cuda"), []
+        table = torch.full_like(table0, -1)
+        for t in range(steps):
+            n += 1
+            if t % page == 0:
+                table[:, t // page] = table0[:, t // page]
+            tok = x[t] * 1.0
+            q = mita.mita_cache_append(tok[:, Hq:Hq + Hkv], tok[:, Hq + Hkv:], kc, vc, table, n,
+                                       q=tok[:, :Hq], inv_freq=freq)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(mita.mita_paged_attn(q, kc, vc, table, n))
+            if wait:
+                torch.cuda.synchronize()
+        return torch.stack(outs), kc, vc
+
+    for a, b in zip(decode(False), decode(True)):
+        assert torch.equal(a, b)
+    assert mita.get_last_device_error() == 0
+
+
+def test_far_strides():
+    """Rows more than 2^31 elements (2^32 bytes) apart, in inputs and outputs."""
+    mita = M()
+    far = 2_300_000_000                                     # a multiple of 8
+    base = torch.zeros(far + 4096, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(base)
+    x = base.as_strided((2, 2, 3, 64), (far, 192, 64, 1))
+    y = out.as_strided((2, 2, 3, 64), (far, 192, 64, 1))
+    g = torch.Generator().manual_seed(0)
+    v = torch.randn(2, 2, 3, 64, generator=g).bfloat16().cuda()
+    x.copy_(v)
+    freq = R.inv_freq(64).cuda()
+    want = mita.mita_qk_norm_rope(v, None, freq)[0]
+    mita.mita_qk_norm_rope(x, None, freq, q_out=y)
+    assert torch.equal(y, want)
+    kc = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    vc, table = torch.zeros_like(kc), lens(1, 0).view(2, 1)
+    tok = x[:, :, 0]
+    mita.mita_cache_append(tok, tok, kc, vc, table, lens(1, 1), q=tok, inv_freq=freq,
+                           q_out=y[:, :, 1])
+    assert torch.equal(vc[[1, 0], :, 0], v[:, :, 0])
+    got = mita.mita_paged_attn(tok, kc, vc, table, lens(1, 1))
+    assert torch.equal(got, v[:, :, 0])                     # one key: its value
+
+
+def test_tables_without_room():
+    mita = M()
+    q = torch.randn(2, 4, 64, device="cuda")
+    kc = torch.zeros(3, 2, 16, 64, device="cuda")
+    none = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    out, lse = mita.mita_paged_attn(q, kc, kc, none, lens(0, 0), return_lse=True)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    assert mita.get_last_device_error() == 0
+    assert bool((mita.mita_paged_attn(q, kc, kc, none, lens(0, 5)) == 0).all())
+    assert mita.get_last_device_error() == 1
+    mita.mita_cache_append(q[:, :2], q[:, :2], kc, kc.clone(), none, lens(1, 0))
+    assert mita.get_last_device_error() == 1 and bool((kc == 0).all())
+    empty = kc[:0]                                          # a cache of no pages
+    out = mita.mita_paged_attn(q, empty, empty, lens(0, 0).view(2, 1), lens(3, 0))
+    assert mita.get_last_device_error() == 1 and bool((out == 0).all())
+
+
+def test_bad_seq_start_writes_nothing_it_should_not():
+    """Descending, negative and far too large row starts: tokens that then have no valid place are
+    flagged or left out; every write lands in the cache rows of the table."""
+    mita = M()
+    big = 2 ** 31 - 1
+    for starts in ((5, 0, 9), (-(2 ** 31), 4, big), (0, big, 3), (9, 9, 9), (-7, -3, -1),
+                   (0, 8, 4)):
+        kc = torch.zeros(6, 1, 4, 32, device="cuda")
+        vc, out = torch.zeros_like(kc), torch.full((8, 2, 32), 9.0, device="cuda")
+        x = torch.randn(8, 4, 32, device="cuda")
+        mita.mita_cache_append(x[:, 2:3], x[:, 3:], kc, vc, lens(0, 1, 2, 3).view(2, 2),
+                               lens(8, 6), seq_start=lens(*starts), q=x[:, :2], q_out=out)
+        assert mita.get_last_device_error() in (0, 1)
+        assert bool((kc[4:] == 0).all()) and bool((vc[4:] == 0).all())
+
+
+def test_many_heads_and_many_sequences():
+    mita = M()
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(1, 301, 70, 16, generator=g).cuda()
+    freq = R.inv_freq(16)
+    q, k = x[:, :, :69].transpose(1, 2), x[:, :, 69:].transpose(1, 2)
+    got = mita.mita_qk_norm_rope(q, k, freq.cuda())
+    for a, b in ((q, got[0]), (k, got[1])):
+        want, bound = R.norm_rope(a.cpu(), None, torch.arange(301).expand(a.shape[:3]), freq, 1e-6,
+                                  False)
+        R.assert_close(b, want, bound, "rows")
+    # 5000 sequences, most of them idle: 40 distinct caches, each shared by many sequences
+    lengths = [(i * 7) % 41 if i % 3 == 0 else 0 for i in range(5000)]
+    cache = R.Cache(range(41), 1, 8, 32, torch.bfloat16)
+    cache.table = cache.table[torch.tensor(lengths)]
+    cache.lengths = lengths
+    q = torch.randn(5000, 2, 32, generator=g).bfloat16()
+    out = mita.mita_paged_attn(q.cuda(), cache.k.cuda(), cache.v.cuda(), cache.table.cuda(),
+                               lens(*lengths))
+    want, bound, _, _ = R.paged_attn(q, cache, lengths)
+    R.assert_close(out, want, bound, "out")
+    assert mita.get_last_device_error() == 0
+
+
+def test_window_of_any_size_and_float_scales():
+    mita = M()
+    cache = R.Cache((70,), 1, 16, 32, torch.float32)
+    q = torch.randn(1, 2, 32, generator=torch.Generator().manual_seed(0))
+    args = (q.cuda(), cache.k.cuda(), cache.v.cuda(), cache.table.cuda(), lens(70))
+    want = mita.mita_paged_attn(*args)
+    for window in (70, 71, 2 ** 31 - 1, 2 ** 40):
+        assert torch.equal(mita.mita_paged_attn(*args, window=window), want)
+
+
+def test_autograd_of_queries_alone_and_of_a_used_half():
+    mita = M()
+    freq = R.inv_freq(32).cuda()
+    q = torch.randn(1, 2, 5, 32, device="cuda", requires_grad=True)
+    w = torch.ones(32, device="cuda", requires_grad=True)
+    out, none = mita.QKNormRopeFunction.apply(q, None, freq, w)
+    assert none is None
+    dy = torch.randn(1, 2, 5, 32, device="cuda")
+    out.backward(dy)
+    want = mita.mita_qk_norm_rope_backward(q.detach(), None, dy, None, freq, w.detach())
+    assert torch.equal(q.grad, want[0]) and torch.equal(w.grad, want[2])
+    # only k is used: q's upstream gradient is made of zeros
+    k = torch.randn(1, 1, 5, 32, device="cuda", requires_grad=True)
+    q.grad = None
+    _, ko = mita.QKNormRopeFunction.apply(q, k, freq, w, w)
+    ko.sum().backward()
+    assert bool((q.grad == 0).all()) and bool((k.grad != 0).any())
+
+
+FIRST_CALL = """
+import torch
+from sparse_top_landmark_gb300 import mita
+q = torch.randn(1, 2, 8, 64, device="cuda")
+torch.cuda.synchronize()
+out = torch.empty_like(q)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    q2 = q + 1
+    try:
+        mita.mita_qk_norm_rope(q, q_out=out)
+        raise SystemExit("not refused")
+    except mita.MitaError as e:
+        assert e.status == 2 and "captured" in str(e), e
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(q2, q + 1)
+want = mita.mita_qk_norm_rope(q)[0]
+with torch.cuda.graph(graph := torch.cuda.CUDAGraph()):
+    mita.mita_qk_norm_rope(q, q_out=out)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, want)
+print("fine")
+"""
+
+
+def test_first_call_inside_a_capture_is_refused_and_leaves_the_capture_whole():
+    M()
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
