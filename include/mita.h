@@ -444,11 +444,15 @@ int mita_cache_append_f32(const mita_cache_append_params* params, mita_stream_t 
  *                   pages invalid), or whose scores are all -inf, gets zeros.
  *   lse [S,Hq] float or NULL   output: ln sum_j e^{z_j} (-inf without a key), for joining with
  *                   attention over other keys.
- *   workspace       device, 16-byte aligned, of mita_paged_attn_workspace_bytes; the caller's, so
- *                   that calls captured into different graphs can have their own.
+ *   workspace       device, 16-byte aligned, of mita_paged_attn_workspace_bytes, its first
+ *                   MITA_PAGED_COUNTERS bytes zero before its first call; every call leaves it fit
+ *                   for the next one, of any shape that it is large enough for.  It is the caller's,
+ *                   so that calls that may overlap (other streams, graphs captured apart) can have
+ *                   their own: each needs one.
  * The same inputs give the same bits.  Cache rows that no sequence's length covers are never read.
  * An infinity among the values that are seen may come out as NaN in its column.
  */
+enum { MITA_PAGED_COUNTERS = 2048 };
 typedef struct mita_paged_attn_params {
   const void *q, *k_cache, *v_cache;
   const int32_t *page_table, *lengths;

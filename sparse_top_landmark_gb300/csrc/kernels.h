@@ -347,7 +347,7 @@ struct PagedAttnArgs {
   int window;               // 0: all keys
   // set by the launcher
   int row_blocks;
-  int* meta;
+  int* counters;            // zero before and after a call
   float *part_ml, *part_o;
   int* status;
 };

@@ -12,9 +12,10 @@
 // segments stand in one row, and each CTA takes an equal share of that row, whatever the lengths
 // are.  Ending a segment takes a tile's time or two, so it counts as kSegmentCost tiles more.  A
 // CTA finishes the segments that lie wholly in its share; of a segment that is cut it leaves a
-// partial (maximum, sum, weighted values) in its first or its last slot of the workspace, and
-// paged_join_kernel joins those of a segment in their order.  Nothing is added atomically: the
-// result depends on the inputs alone.
+// partial (maximum, sum, weighted values) in its first or its last slot of the workspace, and the
+// CTA that is the last one to do so (a counter says which) joins the segment's partials in their
+// order.  No sum is atomic: the result depends on the inputs alone.  (A second kernel for the joins
+// took as long on the GPU and a launch more: 3.5 us of the host's time in each call.)
 //
 // A warp works on its own keys of each tile (kKeys) through its own ring of shared-memory stages,
 // filled by 16-byte asynchronous copies some stages ahead, across the ends of segments; warps
@@ -27,6 +28,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mita.h"
 
 namespace mita {
 namespace {
@@ -36,9 +38,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum before the first key: below every finite score, and finite, so that
 // differences with it need no special case (a score of -inf weighs nothing against it).
 constexpr float kLowest = -FLT_MAX;
-constexpr int kNoSegment = -1;
-constexpr int kJoinThreads = 256;
-constexpr int kMaxPagedCtas = 512;     // CTAs of a call: parts of a segment that can be joined
+constexpr int kMaxPagedCtas = 512;     // CTAs of a call, and counters in its workspace
+
+// A cut segment whose parts are to be joined: the row of its first query, the CTA that begins it,
+// its parts (0: nothing to do) and its query rows.
+struct Join {
+  long long row;
+  int c, n, rows, unused;
+};
 
 // Shared memory and shape of one instantiation.  RT: query rows of a CTA.  A warp's stage is 8 KB
 // (less for small heads, whose tiles would get too long): enough work behind each wait, and
@@ -63,7 +70,8 @@ struct Shape {
   static constexpr int kOffJoin = kWarps * kRing;
   static constexpr int kOffMl = kOffJoin + kJoinFloats * 4;               // [warps][RT][2]
   static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
-  static constexpr int kBytes = kOffMask + kWarps * kStages * 4;
+  static constexpr int kOffJoins = kOffMask + (kWarps * kStages * 4 + 15) / 16 * 16;   // [2]
+  static constexpr int kBytes = kOffJoins + 2 * (int)sizeof(Join);
   static_assert(kBytes <= 232448 && kStages >= 3, "shared memory");
 };
 
@@ -740,6 +748,96 @@ struct Loader {
   }
 };
 
+// Counts one up, after what this CTA's threads wrote before their last barrier, and before what
+// they read after the next one; returns the count before.
+__device__ __forceinline__ int count_up(int* counter) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
+
+// Joins the partials of a cut segment, all of them written: the beginning is CTA c's last part, the
+// rest the first parts of CTAs c + 1 .. c + n - 1; out and lse: the segment's rows.  Called by a
+// whole CTA (out of line: it should not cost the tile loop registers); `mem` is its joining area.
+// D / 4 threads take four columns of a row's parts, kAhead of them on their way at a time, with a
+// running maximum; where there are fewer rows than such groups of threads, a row's parts are dealt
+// to several groups, which are then joined in their order.
+template <typename T, int D, int RT, int kThreads>
+__device__ __noinline__ void join_parts(const float* part_ml, const float* part_o, T* out,
+                                        float* lse, int c, int n, int rows, float* mem) {
+  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kAhead = RT == 16 ? 8 : 4;
+  float4* sums = reinterpret_cast<float4*>(mem);               // [groups][D / 4]
+  float2* totals = reinterpret_cast<float2*>(mem + kThreads * 4);   // [groups] (maximum, sum)
+  static_assert(kThreads * 4 + kGroups * 2 <= 5120, "joining area");
+  const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes;
+  for (int r0 = 0; r0 < rows; r0 += kGroups) {
+    const int now = min(rows - r0, kGroups), share = kGroups / now;
+    const int row = group / share, first = group - row * share;
+    if (row < now) {
+      float base = kLowest, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = first; i0 < n; i0 += share * kAhead) {
+        float2 x[kAhead];
+        float4 v[kAhead];
+        float top = base;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + k * share;
+          // written by other CTAs while this one ran: read past the L1
+          const long long at = (long long)(i == 0 ? c * 2 + 1 : (c + i) * 2) * RT + r0 + row;
+          x[k] = make_float2(kLowest, 0.f);
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n) {
+            x[k] = __ldcg(reinterpret_cast<const float2*>(part_ml) + at);
+            v[k] = __ldcg(reinterpret_cast<const float4*>(part_o) + at * kLanes + col);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, x[k].x);
+        const float f = exp2_fast(base - top);
+        base = top;
+        sum *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float w = exp2_fast(x[k].x - top);
+          sum = fmaf(w, x[k].y, sum);
+          acc.x = fmaf(w, v[k].x, acc.x);
+          acc.y = fmaf(w, v[k].y, acc.y);
+          acc.z = fmaf(w, v[k].z, acc.z);
+          acc.w = fmaf(w, v[k].w, acc.w);
+        }
+      }
+      sums[threadIdx.x] = acc;
+      if (col == 0) totals[group] = make_float2(base, sum);
+    }
+    __syncthreads();
+    if (row < now && first == 0) {
+      float base = kLowest, sum = 0.f;
+      for (int g = 0; g < share; ++g) base = fmaxf(base, totals[group + g].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int g = 0; g < share; ++g) {
+        const float2 x = totals[group + g];
+        const float4 v = sums[threadIdx.x + g * kLanes];
+        const float w = exp2_fast(x.x - base);
+        sum = fmaf(w, x.y, sum);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      T* to = out + (long long)(r0 + row) * D + col * 4;
+      to[0] = from_f<T>(acc.x * inv);
+      to[1] = from_f<T>(acc.y * inv);
+      to[2] = from_f<T>(acc.z * inv);
+      to[3] = from_f<T>(acc.w * inv);
+      if (lse && col == 0) lse[r0 + row] = lse_of(base, sum);
+    }
+    __syncthreads();
+  }
+}
+
 template <typename T, int D, int RT> struct StateOf;
 template <int D, int RT> struct StateOf<bf16, D, RT> { using type = TensorState<D, RT>; };
 template <int D> struct StateOf<float, D, 8> { using type = SplitState<D>; };
@@ -770,13 +868,15 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
   float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
   unsigned* masks = reinterpret_cast<unsigned*>(smem + S::kOffMask) + warp * S::kStages;
+  // of the segment that another CTA begins, and of the one that another CTA ends
+  Join* joins = reinterpret_cast<Join*>(smem + S::kOffJoins);
 
   griddep_wait();
   griddep_launch();
   const Share share = my_share<S>(a.paged, a.window, HR);
   Cursor at = share.at;
-  int last_seg = kNoSegment, last_cta = 0;    // the segment this CTA begins and another one ends
   if (at.segment + at.t < share.end) {
+    if (threadIdx.x < 2) joins[threadIdx.x].n = 0;     // read behind the barriers of the share's end
     prefetch_q<T, D, RT>(a, at);
     using Ld = Loader<T, D, RT>;
     Ld ld;
@@ -833,10 +933,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
         __syncthreads();
         const bool whole = ends && from == 0;
         const int part = blockIdx.x * 2 + (from == 0 ? 1 : 0);
-        if (!whole && from == 0) {
-          last_seg = at.s * HR + at.hr;
-          last_cta = share_of(at.segment + at.span.tiles - 1, share.row, gridDim.x);
-        }
         auto top = [&](int r) {
           float t = ml[r].x;
 #pragma unroll
@@ -880,15 +976,27 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
           }
           __syncthreads();
         }
+        if (!whole && threadIdx.x == 0) {
+          // Whoever leaves a segment's last part joins them all, when its own share is done (the
+          // others go on meanwhile): the count is asked for now, and looked at then.
+          const int c0 = from == 0 ? (int)blockIdx.x : share_of(at.segment, share.row, gridDim.x);
+          const int n = share_of(at.segment + at.span.tiles - 1, share.row, gridDim.x) - c0 + 1;
+          const bool last = count_up(a.counters + c0) == n - 1;
+          joins[from == 0] = {(long long)at.s * Hq + head, c0, last ? n : 0, rows, 0};
+        }
         begin = true;
       }
       advance<S>(at, a.paged, a.window, HR);
     } while (at.segment + at.t < share.end);
     copy_wait<0>();
-  }
-  if (threadIdx.x == 0) {
-    a.meta[blockIdx.x * 2] = last_seg;
-    a.meta[blockIdx.x * 2 + 1] = last_cta;
+    __syncthreads();
+    for (int i = 0; i < 2; ++i) {
+      const Join x = joins[i];
+      if (x.n == 0) continue;
+      join_parts<T, D, RT, S::kThreads>(a.part_ml, a.part_o, a.out + x.row * D,
+                                        a.lse ? a.lse + x.row : nullptr, x.c, x.n, x.rows, join);
+      if (threadIdx.x == 0) a.counters[x.c] = 0;       // as the next call wants it
+    }
   }
   // sequences without a key: zeros, and the logarithm of an empty sum
   for (int s = blockIdx.x; s < a.paged.S; s += gridDim.x) {
@@ -903,59 +1011,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   }
 }
 
-// Joins the partials of a segment that was cut: its beginning is CTA c's last part, its rest
-// the first parts of CTAs c + 1 .. last.  Block (c, row).  A segment may be in as many parts as there
-// are CTAs, so they are dealt to groups of D / 4 threads (four columns each), whose loads are all on
-// their way together, and the groups' sums are added in their order.
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kJoinThreads)
-paged_join_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
-  __shared__ __align__(16) float sums[kGroups][D];
-  griddep_wait();
-  const int c = blockIdx.x, r = blockIdx.y;
-  const int2 cut = reinterpret_cast<const int2*>(a.meta)[c];
-  if (cut.x == kNoSegment) return;
-  const int n = cut.y - c + 1;
-  const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
-  const int s = cut.x / HR, hr = cut.x % HR, rb = hr % a.row_blocks;
-  if (r >= min(RT, a.G - rb * RT)) return;
-  auto part_of = [&](int i) { return (long long)(i == 0 ? c * 2 + 1 : (c + i) * 2) * RT + r; };
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  // every warp finds the maximum and the sum for itself
-  float base = kLowest;
-  for (int i = threadIdx.x & 31; i < n; i += 32) base = fmaxf(base, ml[part_of(i)].x);
-  base = warp_max(base);
-  float sum = 0.f;
-  for (int i = threadIdx.x & 31; i < n; i += 32) {
-    const float2 x = ml[part_of(i)];
-    sum = fmaf(x.y, exp2_fast(x.x - base), sum);
-  }
-  sum = warp_sum(sum);
-  const int col = threadIdx.x % kLanes * 4, group = threadIdx.x / kLanes;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = group; i < n; i += kGroups) {
-    const float w = exp2_fast(ml[part_of(i)].x - base);
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + part_of(i) * D + col);
-    acc.x = fmaf(w, x.x, acc.x);
-    acc.y = fmaf(w, x.y, acc.y);
-    acc.z = fmaf(w, x.z, acc.z);
-    acc.w = fmaf(w, x.w, acc.w);
-  }
-  *reinterpret_cast<float4*>(&sums[group][col]) = acc;
-  __syncthreads();
-  const int head = hr / a.row_blocks * a.G + rb * RT + r;
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(long long)s * Hq + head] = lse_of(base, sum);
-  if (threadIdx.x < D) {
-    float x = 0.f;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) x += sums[g][threadIdx.x];
-    a.out[((long long)s * Hq + head) * D + threadIdx.x] = from_f<T>(sum == 0.f ? 0.f : x / sum);
-  }
-}
-
 // CTAs for this call: one on each SM, but no more than there can be tiles.
 template <typename T, int D, int RT>
 int grid_of(int S, int width, int page_log2, int HR, int sms) {
@@ -965,14 +1020,16 @@ int grid_of(int S, int width, int page_log2, int HR, int sms) {
   return (int)std::max<long long>(1, std::min<long long>({(long long)sms, tiles, kMaxPagedCtas}));
 }
 
+// The counters come first and in the same place for every shape: calls of different shapes can
+// have one workspace.
 struct Carve {
-  size_t meta, ml, o, total;
+  size_t ml, o, total;
 };
 Carve carve(int ctas, int RT, int D) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   Carve c{};
-  c.meta = 0;
-  c.ml = up((size_t)ctas * 2 * sizeof(int));
+  static_assert(kMaxPagedCtas * sizeof(int) == MITA_PAGED_COUNTERS, "counters");
+  c.ml = MITA_PAGED_COUNTERS;
   c.o = c.ml + up((size_t)ctas * 2 * RT * 2 * sizeof(float));
   c.total = c.o + up((size_t)ctas * 2 * RT * D * sizeof(float));
   return c;
@@ -1004,19 +1061,13 @@ struct Run {
     const int grid = grid_of<T, D, RT>(a.paged.S, a.paged.width, a.paged.page_log2,
                                        a.Hkv * a.row_blocks, sms);
     const Carve c = carve(grid, RT, D);
-    a.meta = reinterpret_cast<int*>(static_cast<char*>(ws) + c.meta);
+    a.counters = static_cast<int*>(ws);
     a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + c.ml);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + c.o);
     cudaError_t e = allow_shared();
     if (e != cudaSuccess) return e;
     count_launch();
-    e = launch_pdl(paged_attn_kernel<T, D, RT>, dim3(grid), dim3(Sh::kThreads), Sh::kBytes, st, a);
-    // one CTA cuts no segment, nor is a segment of one tile ever cut
-    if (e != cudaSuccess || grid == 1 || (long long)a.paged.width << a.paged.page_log2 <= Sh::kTile)
-      return e;
-    count_launch();
-    return launch_pdl(paged_join_kernel<T, D, RT>, dim3(grid, std::min(a.G, RT)), dim3(kJoinThreads), 0,
-                      st,
+    return launch_pdl(paged_attn_kernel<T, D, RT>, dim3(grid), dim3(Sh::kThreads), Sh::kBytes, st,
                       a);
   }
 };

@@ -590,14 +590,32 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
         op = _dense(out, "out", shape, dt, dev)
     lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device) if return_lse else None
     nbytes = _paged_attn_bytes(S, Hq, Hkv, d, page, width, dt is torch.float32, dev)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    stream = _raw_stream(dev)
+    ws = _paged_workspace(nbytes, dev, stream)
     rc = fn(_PAGED_ATTN.pack(q.data_ptr(), kc, vc, table, n, slopes, ws.data_ptr(), op,
                              lse.data_ptr() if return_lse else 0, nbytes, *qs, S, Hq, Hkv, d,
                              pages, page, width, window, d ** -0.5 if scale is None else scale,
-                             softcap), _raw_stream(dev))
+                             softcap), stream)
     if rc:
         _check(rc)
     return (out, lse) if return_lse else out
+
+
+_paged_ws = {}      # (device, stream) -> workspace
+_PAGED_COUNTERS = 2048     # bytes of it that have to be zero (the header's MITA_PAGED_COUNTERS)
+
+
+def _paged_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
+    """mita_paged_attn's workspace: one for each stream, whose calls follow one another, its
+    counters zeroed when it is made or grows.  A captured call has one of its graph's own."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    ws = None if capturing else _paged_ws.get((device, stream))
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+        ws[:_PAGED_COUNTERS].zero_()
+        if not capturing:
+            _paged_ws[device, stream] = ws
+    return ws
 
 
 @functools.lru_cache(maxsize=1024)
@@ -776,6 +794,8 @@ def get_last_device_error(stream=None, device=None) -> int:
 
 
 def workspace_release() -> None:
+    """Frees the library's cached workspaces, and mita_paged_attn's."""
+    _paged_ws.clear()
     _check(load().mita_workspace_release())
 
 

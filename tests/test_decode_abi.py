@@ -126,6 +126,12 @@ def test_paged_attn_workspace_query(lib):
     assert f(4, 8, 2, 48, 16, 100, 1) == 0
 
 
+def test_counter_bytes_are_the_headers():
+    with open(mita.HEADER_PATH) as f:
+        want = re.search(r"MITA_PAGED_COUNTERS = (\d+)", f.read()).group(1)
+    assert mita._PAGED_COUNTERS == int(want)
+
+
 def test_null_params(lib):
     for name in ("mita_qk_norm_rope", "mita_qk_norm_rope_backward", "mita_cache_append",
                  "mita_paged_attn"):
