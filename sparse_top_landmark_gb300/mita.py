@@ -306,7 +306,7 @@ def _rows(t: torch.Tensor, name: str, shape, dtype, device: int):
 def _out_rows(t: torch.Tensor, name: str, shape, dtype, device: int):
     """_rows of an output that the caller gave."""
     s = _rows(t, name, shape, dtype, device)
-    if any(n > 1 and step == 0 for n, step in zip(shape, s)):
+    if 0 in s and any(n > 1 and step == 0 for n, step in zip(shape, s)):
         raise ValueError(f"{name}: an output cannot be a broadcast view")
     return s
 
@@ -446,6 +446,8 @@ def mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq=None, q_weight=Non
     dwq = dwk = ws = None
     nbytes = 0
     if qw or kw:
+        # for this call alone: it launches twice, and another thread's call on the same stream may
+        # come in between
         nbytes = _norm_rope_backward_bytes(d, dev)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         dwq = torch.empty(d, dtype=torch.float32, device=q.device) if qw else None
@@ -601,20 +603,21 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     return (out, lse) if return_lse else out
 
 
-_paged_ws = {}      # (device, stream) -> workspace
-_PAGED_COUNTERS = 2048     # bytes of it that have to be zero (the header's MITA_PAGED_COUNTERS)
+_paged_workspaces = {}     # (device, stream) -> uint8 tensor
+_PAGED_COUNTERS = 2048     # its first bytes: zero between calls (the header's MITA_PAGED_COUNTERS)
 
 
 def _paged_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
-    """mita_paged_attn's workspace: one for each stream, whose calls follow one another, its
-    counters zeroed when it is made or grows.  A captured call has one of its graph's own."""
+    """mita_paged_attn's workspace: one for each stream, whose calls (one launch each) follow one
+    another, its counters zeroed when it is made or grows.  A captured call has one of its
+    graph's own."""
     capturing = torch.cuda.is_current_stream_capturing()
-    ws = None if capturing else _paged_ws.get((device, stream))
+    ws = None if capturing else _paged_workspaces.get((device, stream))
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
         ws[:_PAGED_COUNTERS].zero_()
         if not capturing:
-            _paged_ws[device, stream] = ws
+            _paged_workspaces[device, stream] = ws
     return ws
 
 
@@ -794,8 +797,8 @@ def get_last_device_error(stream=None, device=None) -> int:
 
 
 def workspace_release() -> None:
-    """Frees the library's cached workspaces, and mita_paged_attn's."""
-    _paged_ws.clear()
+    """Frees the cached workspaces, the library's and the binding's."""
+    _paged_workspaces.clear()
     _check(load().mita_workspace_release())
 
 

@@ -221,3 +221,58 @@ def test_first_call_inside_a_capture_is_refused_and_leaves_the_capture_whole():
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=ROOT, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+def test_workspaces_are_shared_grown_released_and_left_clean():
+    """Attention and gradients of growing and shrinking shapes in turn on one stream's workspace,
+    and after its release: the same bits as from a workspace that nothing else has used."""
+    mita = M()
+    shapes = [((3000, 40), 4, 1, 128), ((700,), 16, 2, 64), ((9000, 5, 2000), 8, 2, 128), ((50,), 1, 1, 16)]
+    calls = []
+    for lengths, Hq, Hkv, d in shapes:
+        cache = R.Cache(lengths, Hkv, 16, d, torch.bfloat16)
+        q = torch.randn(len(lengths), Hq, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+        x = torch.randn(1, Hq, 300, d, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+        w = torch.ones(d, device="cuda")
+        calls.append((lambda a: mita.mita_paged_attn(*a),
+                      (q.cuda(), cache.k.cuda(), cache.v.cuda(), cache.table.cuda(), lens(*lengths))))
+        calls.append((lambda a: mita.mita_qk_norm_rope_backward(*a)[2], (x, None, x, None, None, w)))
+    want = []
+    for f, a in calls:
+        mita.workspace_release()
+        want.append(f(a))
+    for _ in range(3):
+        for i in (0, 1, 2, 3, 4, 5, 6, 7, 4, 3, 0, 2, 1, 6):
+            assert torch.equal(calls[i][0](calls[i][1]), want[i])
+
+
+def test_two_threads_on_one_stream():
+    """Gradients and attention from two host threads at once, on the same stream."""
+    import threading
+    mita = M()
+    cache = R.Cache((5000, 300), 2, 16, 64, torch.bfloat16)
+    g = torch.Generator().manual_seed(1)
+    work = []
+    for i in range(2):
+        q = torch.randn(2, 8, 64, generator=g).bfloat16().cuda()
+        x = torch.randn(1, 8, 400, 64, generator=g).bfloat16().cuda()
+        a = (q, cache.k.cuda(), cache.v.cuda(), cache.table.cuda(), lens(5000, 300))
+        b = (x, None, x, None, None, torch.ones(64, device="cuda"))
+        work.append((a, b, mita.mita_paged_attn(*a), mita.mita_qk_norm_rope_backward(*b)[2]))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            for _ in range(50):
+                got[i].append((mita.mita_paged_attn(*work[i][0]),
+                               mita.mita_qk_norm_rope_backward(*work[i][1])[2]))
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 50
+        assert all(torch.equal(o, work[i][2]) and torch.equal(w, work[i][3]) for o, w in got[i])
