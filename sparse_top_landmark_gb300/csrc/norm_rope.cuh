@@ -9,10 +9,10 @@
 // rot % 8 == 0.
 //
 // A row is a few dozen bytes a lane, so the instructions around them decide whether HBM stays
-// the bound (first measured form: 172 warp instructions a row of 128, 82 us for 336 MB).  So the
-// arithmetic is on pairs of fp32 values (one instruction for two), a token's cosines and sines are
-// multiplied with the weights once for all of its heads, and rows are normalised two at a time, their
-// sums sharing one tree of shuffles.
+// the bound (first measured form: 172 warp instructions a row of 128, 82 us for 336 MB; now 100
+// and 57 us, of which copying alone takes 56).  So the arithmetic is on pairs of fp32 values (one
+// instruction for two), a token's cosines and sines are multiplied with the weights once for all of
+// its heads, and rows are normalised two at a time, their sums sharing one tree of shuffles.
 #pragma once
 
 #include "common.cuh"
@@ -21,8 +21,9 @@ namespace mita {
 
 // Threads of a block in these kernels.
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBlocks = 3;            // blocks of an SM: forward and append
-constexpr int kRopeBackwardBlocks = 2;    // gradient
+// Blocks of an SM: with three, 80 registers a thread would not hold what the kernels keep (1M
+// tokens of 2 + 2 heads: 199 us, with two 193 us; the gradient 54 and 49 us for 8192 tokens of 40).
+constexpr int kRopeBlocks = 2;
 
 using V2 = unsigned long long;   // two fp32 values
 __device__ __forceinline__ V2 mul2(V2 a, V2 b) {
