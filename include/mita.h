@@ -9,7 +9,8 @@
  *   grouping by expert with online softmax).
  *
  * Conventions (all entry points):
- *   - Tensors are dense, row-major.  Q, K, V and the output are [B, H, N, d]:
+ *   - Tensors are dense, row-major, except where an entry point takes strides
+ *     (mita_qk_norm_rope to mita_paged_attn).  Q, K, V and the output are [B, H, N, d]:
  *     head (b, h) owns N consecutive rows of d elements.  For a 2D token grid
  *     (grid_h > 1) token t sits at row t / grid_w, column t % grid_w.
  *   - Unsuffixed entry points take bfloat16 data (`const void*` holding

@@ -9,7 +9,7 @@
 // rot % 8 == 0.
 //
 // A row is a few dozen bytes a lane, so the instructions around them decide whether HBM stays
-// the bound (first measured form: 172 warp instructions a row of 128, 82 us for 336 MB; now 100
+// the bound (first measured form: 172 warp instructions a row of 128, 82 us for 336 MB; now 90
 // and 57 us, of which copying alone takes 56).  So the arithmetic is on pairs of fp32 values (one
 // instruction for two), a token's cosines and sines are multiplied with the weights once for all of
 // its heads, and rows are normalised two at a time, their sums sharing one tree of shuffles.

@@ -5,8 +5,10 @@ tensors to pointers and picks the bf16 or `_f32` entry point; every step of the
 computation runs in the library's CUDA kernels.  There is no fallback: if
 libmita.so is missing, every call raises.
 
-Tensors must be contiguous; Q/K/V/out are [B, H, N, d].  Calls run on the
-current torch CUDA stream unless `stream` is given.
+Tensors must be contiguous; Q/K/V/out are [B, H, N, d].  (The norm and rotation of
+queries and keys and the paged cache take strided views and packed tokens: their
+docstrings say which.)  Calls run on the current torch CUDA stream unless `stream`
+is given.
 """
 from __future__ import annotations
 
