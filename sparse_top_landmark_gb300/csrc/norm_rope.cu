@@ -44,7 +44,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs<T> a) {
   const int rows[2] = {max(min(h1, hq) - h0, 0), max(h1 - hq - first[1], 0)};
   const unsigned tokens = (unsigned)a.B * a.N, stride = gridDim.x * kSlots;
   const unsigned t0 = blockIdx.x * kSlots + threadIdx.x / L;
-  // all lanes of a warp stay in the loops together: `warp` is its first lane's token
+  // all lanes of a warp stay in the loops together, as long as its first lane has a token
   const unsigned in_warp = (threadIdx.x % 32) / L;
 
   const NormRopePart<T>&q = a.part[0], &k = a.part[1];

@@ -94,10 +94,6 @@ struct Raw8 {
     a = Raw4<T>::pack(x.v);
     b = Raw4<T>::pack(x.v + 2);
   }
-  __device__ __forceinline__ void load(const T* p, int oa, int ob) {
-    a = *reinterpret_cast<const typename Raw4<T>::Bits*>(p + oa);
-    b = *reinterpret_cast<const typename Raw4<T>::Bits*>(p + ob);
-  }
   __device__ __forceinline__ void store(T* p, int oa, int ob) const {
     *reinterpret_cast<typename Raw4<T>::Bits*>(p + oa) = a;
     *reinterpret_cast<typename Raw4<T>::Bits*>(p + ob) = b;

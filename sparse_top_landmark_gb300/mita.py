@@ -241,7 +241,7 @@ class MiTAFunction(torch.autograd.Function):
 #
 # These calls run on the tensors' device, whatever the current one is, and on `stream` (the
 # device's current stream by default).  What they allocate (outputs, workspaces) belongs to that
-# stream; the caller orders the stream with the ones its inputs come from.
+# stream; the caller orders the stream with the ones its inputs come from and its outputs go to.
 #
 # A step of a decoder makes a few of these calls for microseconds of GPU work, so the binding's
 # own time counts: arguments go to C as one packed struct (the layouts below are the
@@ -264,19 +264,25 @@ def _typed_fn(name: str, dtype: torch.dtype):
 
 
 class _on:
-    """`device` and `stream` (or its current stream) as the current ones."""
+    """`device` and `stream` (or its current stream) as the current ones; the tensors that a given
+    stream's call uses stay allocated until that stream is done with them."""
 
-    def __init__(self, stream, device: int):
+    def __init__(self, stream, device: int, *tensors):
         if stream is not None and stream.device_index != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{device}")
         self._stack = contextlib.ExitStack()
         self._enter = (torch.cuda.device(device), torch.cuda.stream(stream))
+        self._stream, self._tensors = stream, tensors
 
     def __enter__(self):
         for c in self._enter:
             self._stack.enter_context(c)
 
     def __exit__(self, *exc):
+        if self._stream is not None and not torch.cuda.is_current_stream_capturing():
+            for t in self._tensors:
+                if t is not None and t.is_cuda:
+                    t.record_stream(self._stream)
         return self._stack.__exit__(*exc)
 
 
@@ -368,7 +374,7 @@ def mita_qk_norm_rope(q, k=None, inv_freq=None, q_weight=None, k_weight=None, po
     q_out may be q and k_out may be k."""
     dev = _device_of(q, "q")
     if stream is not None or dev != torch.cuda.current_device():
-        with _on(stream, dev):
+        with _on(stream, dev, q, k, inv_freq, q_weight, k_weight, positions, q_out, k_out):
             return mita_qk_norm_rope(q, k, inv_freq, q_weight, k_weight, positions, eps,
                                      interleaved, q_out, k_out)
     dt = q.dtype
@@ -414,7 +420,8 @@ def mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq=None, q_weight=Non
     without the weight).  k and dk_out may both be None.  dq may be dq_out, dk may be dk_out."""
     dev = _device_of(q, "q")
     if stream is not None or dev != torch.cuda.current_device():
-        with _on(stream, dev):
+        with _on(stream, dev, q, k, dq_out, dk_out, inv_freq, q_weight, k_weight, positions, dq,
+                 dk):
             return mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq, q_weight, k_weight,
                                               positions, eps, interleaved, dq, dk)
     dt = q.dtype
@@ -527,7 +534,8 @@ def mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start=Non
     or to an idle slot leave q_out as it is."""
     dev = _device_of(k, "k")
     if stream is not None or dev != torch.cuda.current_device():
-        with _on(stream, dev):
+        with _on(stream, dev, k, v, k_cache, v_cache, page_table, lengths, seq_start, q, inv_freq,
+                 q_weight, k_weight, q_out):
             return mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start, q,
                                      inv_freq, q_weight, k_weight, eps, interleaved, q_out)
     dt = k.dtype
@@ -572,7 +580,7 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     last `window` keys.  Idle slots (length 0) get zeros and lse -inf."""
     dev = _device_of(q, "q")
     if stream is not None or dev != torch.cuda.current_device():
-        with _on(stream, dev):
+        with _on(stream, dev, q, k_cache, v_cache, page_table, lengths, alibi_slopes, out):
             return mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale, softcap,
                                    window, alibi_slopes, return_lse, out)
     dt = q.dtype

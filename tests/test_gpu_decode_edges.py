@@ -276,3 +276,27 @@ def test_two_threads_on_one_stream():
     for i in range(2):
         assert len(got[i]) == 50
         assert all(torch.equal(o, work[i][2]) and torch.equal(w, work[i][3]) for o, w in got[i])
+
+
+def test_inputs_dropped_right_after_a_call_on_another_stream():
+    """The caller lets go of the inputs as soon as the call on a busy side stream is made, and
+    allocates and fills as much again on its own: the call still reads what it was given."""
+    mita = M()
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(1, 8, 20000, 64, generator=g).bfloat16()
+    freq = R.inv_freq(64).cuda()
+    want = mita.mita_qk_norm_rope(x.cuda(), None, freq)[0]
+    side, busy = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(4):
+        q = x.cuda()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy @ busy
+        got = mita.mita_qk_norm_rope(q, None, freq, stream=side)[0]
+        del q
+        junk = [torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del junk
