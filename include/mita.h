@@ -396,7 +396,8 @@ uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
 
 /*
  * The paged cache of mita_cache_append and mita_paged_attn:
- *   k_cache, v_cache [num_pages,Hkv,page_size,d], dense; page_size a power of two.
+ *   k_cache, v_cache [num_pages,Hkv,page_size,d], dense; page_size a power of two up to 2^20,
+ *   table_width*page_size at most 2^31 - 2^16.
  *   page_table [S,table_width] int32: token p of sequence s lives in row p % page_size of page
  *   page_table[s][p / page_size].  Entries behind a sequence's last page are not read.
  *   lengths [S] int32: tokens of each sequence, the new ones included; 0 is an idle slot.

@@ -910,8 +910,9 @@ int check_pages(int S, int Hkv, int num_pages, int page_size, int width) {
   if (page_size < 1 || page_size > kMaxPageSize || (page_size & (page_size - 1)) != 0)
     return fail(MITA_ERR_UNSUPPORTED, "page_size=%d is not a power of two in [1, %d]", page_size,
                 kMaxPageSize);
-  if ((long long)width * page_size >= (1LL << 31))
-    return fail(MITA_ERR_UNSUPPORTED, "table_width*page_size must be < 2^31");
+  // positions are 32-bit numbers, those of a tile that begins before the last one included
+  if ((long long)width * page_size > (1LL << 31) - (1 << 16))
+    return fail(MITA_ERR_UNSUPPORTED, "table_width*page_size must be at most 2^31 - 2^16");
   return MITA_OK;
 }
 
@@ -983,6 +984,8 @@ int check_paged_attn(int S, int Hq, int Hkv, int d, int num_pages, int page_size
     return fail(MITA_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d", Hq, Hkv);
   if ((long long)S * Hq >= (1LL << 31))
     return fail(MITA_ERR_UNSUPPORTED, "S*Hq must be < 2^31");
+  if ((long long)Hq * d >= (1LL << 31))
+    return fail(MITA_ERR_UNSUPPORTED, "Hq*d must be < 2^31");
   return MITA_OK;
 }
 

@@ -174,3 +174,20 @@ def test_python_refuses_host_tensors():
         mita.mita_cache_append(t, t, c, c, n[None], n)
     with pytest.raises(ValueError, match="CUDA"):
         mita.mita_paged_attn(t, c, c, n[None], n)
+
+
+@pytest.mark.parametrize("suffix", ["", "_f32"])
+def test_sizes_at_the_ends_of_32_bits(lib, suffix):
+    """A table that a tile behind its last token would lead past 2^31 - 1, and heads whose values
+    have no 32-bit count."""
+    end = dict(width=(1 << 27) - 1)               # 2^31 - 16 tokens
+    attn, append = "mita_paged_attn" + suffix, "mita_cache_append" + suffix
+    assert call(lib, attn, mita._PAGED_ATTN, ATTN, end) == 2, msg(lib)
+    assert "table_width" in msg(lib)
+    assert call(lib, append, mita._CACHE_APPEND, APPEND, end) == 2, msg(lib)
+    assert "table_width" in msg(lib)
+    assert call(lib, attn, mita._PAGED_ATTN, ATTN, dict(S=1, Hq=1 << 25)) == 2, msg(lib)
+    assert "Hq*d" in msg(lib)
+    f = lib.mita_paged_attn_workspace_bytes
+    most = (1 << 27) - (1 << 12)
+    assert f(1, 4, 2, 64, 16, most, suffix != "") > 0 and f(1, 4, 2, 64, 16, most + 1, suffix != "") == 0
