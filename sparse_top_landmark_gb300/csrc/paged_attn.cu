@@ -70,14 +70,13 @@ struct Shape {
   static constexpr int kStages =
       196608 / (kStageBytes * kWarps) > 8 ? 8 : 196608 / (kStageBytes * kWarps);
   static constexpr int kRing = kStages * kStageBytes;          // of one warp
-  static constexpr int kJoinFloats = 5120;                     // outputs being joined over warps
   // byte offsets
-  static constexpr int kOffJoin = kWarps * kRing;
-  static constexpr int kOffMl = kOffJoin + kJoinFloats * 4;               // [warps][RT][2]
+  static constexpr int kOffMl = kWarps * kRing;                           // [warps][RT][2]
   static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
   static constexpr int kOffJoins = kOffMask + (kWarps * kStages * 4 + 15) / 16 * 16;   // [2]
   static constexpr int kBytes = kOffJoins + 2 * (int)sizeof(Join);
   static_assert(kBytes <= 232448 && kStages >= 3, "shared memory");
+  static_assert(RT * D * 4 <= kStageBytes, "a warp's sums in one of its stages");
 };
 
 // Chunk c of row r lies at chunk c ^ f(r) of it, so that eight rows' equal chunks lie in
@@ -434,10 +433,11 @@ struct TensorState {
         if (lane < 4) ml[8 * n + lane * 2 + i] = make_float2(m[n][i], l[n][i]);
       }
   }
-  // columns [c0, c0 + C) of the rows below `rows`, moved to the maxima top(row), to dst[row][..]
+  // column c of a row of sums lies at c ^ spread(row): put_o's four rows lie in different banks
+  __device__ __forceinline__ static int spread(int r) { return ((r >> 1 & 3) * 8) & (D - 1); }
+  // the rows below `rows`, moved to the maxima top(row), to dst[row][..]
   template <typename Top>
-  __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
-                                        Top top) const {
+  __device__ __forceinline__ void put_o(float* dst, int rows, Top top) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 0; n < kN; ++n)
@@ -448,8 +448,7 @@ struct TensorState {
         const float f = exp2_fast(m[n][i] - top(r));
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
-          if (8 * j >= c0 && 8 * j < c0 + C)
-            dst[r * stride + 8 * j - c0 + lane / 4] = o[j / 2][n][(j & 1) * 2 + i] * f;
+          dst[r * D + ((8 * j + lane / 4) ^ spread(r))] = o[j / 2][n][(j & 1) * 2 + i] * f;
       }
   }
 };
@@ -643,9 +642,9 @@ struct SplitState {
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (lane % 4 == 0) ml[lane / 4] = make_float2(m, l);
   }
+  __device__ __forceinline__ static int spread(int r) { return r & 7; }   // eight rows
   template <typename Top>
-  __device__ __forceinline__ void put_o(float* dst, int stride, int c0, int C, int rows,
-                                        Top top) const {
+  __device__ __forceinline__ void put_o(float* dst, int rows, Top top) const {
     const int lane = threadIdx.x & 31, r = lane / 4;
     if (r >= rows) return;
     const float f = exp2_fast(m - top(r));
@@ -654,7 +653,7 @@ struct SplitState {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = 8 * kV * (j / kV) + kV * (lane % 4 * 2 + i) + j % kV;
-        if (col >= c0 && col < c0 + C) dst[r * stride + col - c0] = o[j][i] * f;
+        dst[r * D + (col ^ spread(r))] = o[j][i] * f;
       }
   }
 };
@@ -763,7 +762,8 @@ __device__ __forceinline__ int count_up(int* counter) {
 
 // Joins the partials of a cut segment, all of them written: the beginning is CTA c's last part, the
 // rest the first parts of CTAs c + 1 .. c + n - 1; out and lse: the segment's rows.  Called by a
-// whole CTA (out of line: it should not cost the tile loop registers); `mem` is its joining area.
+// whole CTA (out of line: it should not cost the tile loop registers); `mem`: shared, of
+// kThreads * 4 + kGroups * 2 floats.
 // D / 4 threads take four columns of a row's parts, kAhead of them on their way at a time, with a
 // running maximum; where there are fewer rows than such groups of threads, a row's parts are dealt
 // to several groups, which are then joined in their order.
@@ -773,7 +773,7 @@ __device__ __noinline__ void join_parts(const float* part_ml, const float* part_
   constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kAhead = RT == 16 ? 8 : 4;
   float4* sums = reinterpret_cast<float4*>(mem);               // [groups][D / 4]
   float2* totals = reinterpret_cast<float2*>(mem + kThreads * 4);   // [groups] (maximum, sum)
-  static_assert(kThreads * 4 + kGroups * 2 <= 5120, "joining area");
+  static_assert((kThreads * 4 + kGroups * 2) * 4 <= Shape<T, D, RT>::kOffMl, "shared memory");
   const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes;
   for (int r0 = 0; r0 < rows; r0 += kGroups) {
     const int now = min(rows - r0, kGroups), share = kGroups / now;
@@ -870,7 +870,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
   uint8_t* ring = smem + warp * S::kRing;
-  float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
   float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
   unsigned* masks = reinterpret_cast<unsigned*>(smem + S::kOffMask) + warp * S::kStages;
   // of the segment that another CTA begins, and of the one that another CTA ends
@@ -925,8 +924,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
         st.tile(rule, stage, stage + S::kKeys * S::kRowBytes,
                 at.span.base + at.t * S::kTile + warp * S::kKeys, mask);
       }
-      slot = slot + 1 == S::kStages ? 0 : slot + 1;
-      next = next + 1 == S::kStages ? 0 : next + 1;
 
       const bool ends = at.t + 1 == at.span.tiles;
       if (ends || at.segment + at.t + 1 == share.end) {
@@ -944,43 +941,40 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
           for (int w = 1; w < S::kWarps; ++w) t = fmaxf(t, ml[w * RT + r].x);
           return t;
         };
-        // columns at a time: all warps' sums of C columns fit the joining area (rows padded by 4
-        // floats, which puts put_o's four or eight rows into different banks)
-        const int C = rows * S::kWarps * (D + 4) <= S::kJoinFloats
-                          ? D : (S::kJoinFloats / (S::kWarps * rows) - 4) & ~7;
-        const int stride = C + 4;
-        for (int c0 = 0; c0 < D; c0 += C) {
-          st.put_o(join + warp * rows * stride, stride, c0, C, rows, top);
-          __syncthreads();
-          for (int r = warp; r < rows; r += S::kWarps) {
-            const float base = top(r);
-            float sum = 0.f;
+        // Every warp's sums go to the stage that it has just read: no copy goes there until its
+        // next tile.
+        float* const sums = reinterpret_cast<float*>(smem + slot * S::kStageBytes);
+        st.put_o(sums + warp * (S::kRing / 4), rows, top);
+        __syncthreads();
+        for (int r = warp; r < rows; r += S::kWarps) {
+          const float base = top(r);
+          float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) {
-              const float2 x = ml[w * RT + r];
-              sum = fmaf(x.y, exp2_fast(x.x - base), sum);
-            }
-            if (c0 == 0 && lane == 0) {
-              if (!whole)
-                reinterpret_cast<float2*>(a.part_ml)[(long long)part * RT + r] =
-                    make_float2(base, sum);
-              else if (a.lse)
-                a.lse[(long long)at.s * Hq + head + r] = lse_of(base, sum);
-            }
-            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-            T* out = a.out + ((long long)at.s * Hq + head + r) * D + c0;
-            float* part_o = a.part_o + ((long long)part * RT + r) * D + c0;
-            const int cols = min(C, D - c0);
-            for (int c = lane; c < cols; c += 32) {
-              float x = 0.f;
-#pragma unroll
-              for (int w = 0; w < S::kWarps; ++w) x += join[(w * rows + r) * stride + c];
-              if (whole) out[c] = from_f<T>(x * inv);
-              else part_o[c] = x;
-            }
+          for (int w = 0; w < S::kWarps; ++w) {
+            const float2 x = ml[w * RT + r];
+            sum = fmaf(x.y, exp2_fast(x.x - base), sum);
           }
-          __syncthreads();
+          if (lane == 0) {
+            if (!whole)
+              reinterpret_cast<float2*>(a.part_ml)[(long long)part * RT + r] =
+                  make_float2(base, sum);
+            else if (a.lse)
+              a.lse[(long long)at.s * Hq + head + r] = lse_of(base, sum);
+          }
+          const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+          T* out = a.out + ((long long)at.s * Hq + head + r) * D;
+          float* part_o = a.part_o + ((long long)part * RT + r) * D;
+#pragma unroll
+          for (int c = lane; c < D; c += 32) {
+            const float* from_w = sums + r * D + (c ^ State::spread(r));
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) x += from_w[w * (S::kRing / 4)];
+            if (whole) out[c] = from_f<T>(x * inv);
+            else part_o[c] = x;
+          }
         }
+        __syncthreads();
         if (!whole && threadIdx.x == 0) {
           // Whoever leaves a segment's last part joins them all, when its own share is done (the
           // others go on meanwhile): the count is asked for now, and looked at then.
@@ -991,6 +985,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
         }
         begin = true;
       }
+      slot = slot + 1 == S::kStages ? 0 : slot + 1;
+      next = next + 1 == S::kStages ? 0 : next + 1;
       advance<S>(at, a.paged, a.window, HR);
     } while (at.segment + at.t < share.end);
     copy_wait<0>();
@@ -999,7 +995,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       const Join x = joins[i];
       if (x.n == 0) continue;
       join_parts<T, D, RT, S::kThreads>(a.part_ml, a.part_o, a.out + x.row * D,
-                                        a.lse ? a.lse + x.row : nullptr, x.c, x.n, x.rows, join);
+                                        a.lse ? a.lse + x.row : nullptr, x.c, x.n, x.rows,
+                                        reinterpret_cast<float*>(smem));
       if (threadIdx.x == 0) a.counters[x.c] = 0;       // as the next call wants it
     }
   }
