@@ -209,45 +209,66 @@ struct Share {
 template <typename S>
 __device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int HR) {
   const int lane = threadIdx.x & 31;
-  auto tiles_of = [&](int s) { return s < pg.S ? span_of(pg, window, S::kTile, s).tiles : 0; };
+  constexpr int kEach = 4, kBatch = 32 * kEach;     // sequences of a lane, and of a warp, at a time
   auto cost_of = [&](int tiles) {
     return tiles > 0 ? (long long)(tiles + S::kSegmentCost) * HR : 0;
   };
-  Share sh;
-  const int mine = tiles_of(lane);           // of the first 32 sequences: often all there are
-  long long row = cost_of(mine);
-  for (int s = 32 + lane; s < pg.S; s += 32) row += cost_of(tiles_of(s));
+  const int each = pg.S <= 32 ? 1 : kEach;
+  int tiles[kEach];
+  auto load = [&](int s0) {                         // its lane's tiles, and what they cost
+    int sum = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) row += __shfl_xor_sync(0xffffffffu, row, o);
-  sh.row = row;
-  const long long x = share_begin(row, gridDim.x, blockIdx.x);
-  sh.end = share_begin(row, gridDim.x, blockIdx.x + 1);
-  sh.at.segment = row;
+    for (int i = 0; i < kEach; ++i) {
+      const int s = s0 + lane * each + i;
+      tiles[i] = i < each && s < pg.S ? span_of(pg, window, S::kTile, s).tiles : 0;
+      sum += tiles[i] > 0 ? tiles[i] + S::kSegmentCost : 0;
+    }
+    return (long long)sum * HR;
+  };
+  long long rest = 0;                               // behind the first batch: mostly there is none
+  for (int s0 = kBatch; s0 < pg.S; s0 += kBatch) rest += load(s0);
+  if (pg.S > kBatch) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+  }
+  long long cost = load(0), incl = warp_incl_scan64(cost);
+  Share sh;
+  sh.row = __shfl_sync(0xffffffffu, incl, 31) + rest;
+  const long long x = share_begin(sh.row, gridDim.x, blockIdx.x);
+  sh.end = share_begin(sh.row, gridDim.x, blockIdx.x + 1);
+  sh.at.segment = sh.row;
   sh.at.t = 0;
   if (x >= sh.end) return sh;
-  long long run = 0;                         // the row up to this batch
-  for (int s0 = 0; s0 < pg.S; s0 += 32) {
-    const int tiles = s0 == 0 ? mine : tiles_of(s0 + lane);
-    const long long cost = cost_of(tiles);
-    const long long incl = run + warp_incl_scan64(cost);
-    const unsigned hit = __ballot_sync(0xffffffffu, x < incl);
-    if (hit == 0) {
-      run = __shfl_sync(0xffffffffu, incl, 31);
-      continue;
-    }
-    const int src = __ffs(hit) - 1;
-    const int n = __shfl_sync(0xffffffffu, tiles, src);
-    const long long start = __shfl_sync(0xffffffffu, incl - cost, src);
-    const int seg = (int)quotient(x - start, n + S::kSegmentCost);
-    sh.at.segment = start + (long long)seg * (n + S::kSegmentCost);
-    const int in = (int)(x - sh.at.segment);
-    sh.at.s = s0 + src;
-    sh.at.hr = seg;
-    sh.at.t = min(in, n - 1);
-    sh.at.span = span_of(pg, window, S::kTile, sh.at.s);
-    if (in >= n) advance<S>(sh.at, pg, window, HR);   // it begins behind a segment's last tile
-    break;
+  int s0 = 0;
+  unsigned hit;
+  while ((hit = __ballot_sync(0xffffffffu, x < incl)) == 0) {
+    const long long run = __shfl_sync(0xffffffffu, incl, 31);
+    s0 += kBatch;
+    cost = load(s0);
+    incl = run + warp_incl_scan64(cost);
   }
+  const int src = __ffs(hit) - 1;
+  long long start = __shfl_sync(0xffffffffu, incl - cost, src);
+  int n = __shfl_sync(0xffffffffu, tiles[0], src);
+  sh.at.s = s0 + src * each;
+  if (each > 1) {
+#pragma unroll
+    for (int i = 1; i < kEach; ++i) {
+      const int next = __shfl_sync(0xffffffffu, tiles[i], src);
+      if (sh.at.s == s0 + src * kEach + i - 1 && x - start >= cost_of(n)) {
+        start += cost_of(n);
+        n = next;
+        ++sh.at.s;
+      }
+    }
+  }
+  const int seg = (int)quotient(x - start, n + S::kSegmentCost);
+  sh.at.segment = start + (long long)seg * (n + S::kSegmentCost);
+  const int in = (int)(x - sh.at.segment);
+  sh.at.hr = seg;
+  sh.at.t = min(in, n - 1);
+  sh.at.span = span_of(pg, window, S::kTile, sh.at.s);
+  if (in >= n) advance<S>(sh.at, pg, window, HR);   // it begins behind a segment's last tile
   return sh;
 }
 
