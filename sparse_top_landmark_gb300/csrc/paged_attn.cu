@@ -29,6 +29,7 @@
 // the first keys, 4.5 thousand for a tile and its join.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "common.cuh"
@@ -167,7 +168,10 @@ __device__ __forceinline__ void advance(Cursor& c, const PagedLayout& pg, int wi
   if (++c.hr < HR) return;
   c.hr = 0;
   do {
-    if (++c.s >= pg.S) return;      // behind the last segment, and at the end of the row
+    if (++c.s >= pg.S) {            // behind the last segment: behind every share
+      c.segment = LLONG_MAX / 2;
+      return;
+    }
     c.span = span_of(pg, window, S::kTile, c.s);
   } while (c.span.tiles == 0);
 }
@@ -191,17 +195,20 @@ __device__ __forceinline__ long long share_begin(long long row, int n, int c) {
   const long long q = quotient(row, n), r = row - q * n;
   return q * c + min((long long)c, r);
 }
-// The index of the CTA whose share of a row of that length has position x.
+// The index of the CTA whose share of a row of that length has position x (one of the n, even where
+// a caller changes lengths while they are read, and x lies anywhere).
 __device__ __forceinline__ int share_of(long long x, long long row, int n) {
   const long long q = quotient(row, n), r = row - q * n;
   const long long large = r * (q + 1);       // the length of the r shares that are one longer
-  return (int)(x < large ? quotient(x, (int)q + 1) : r + quotient(x - large, (int)q));
+  if (q == 0) return (int)min(x, (long long)n - 1);
+  return (int)min(x < large ? quotient(x, (int)q + 1) : r + quotient(x - large, (int)q),
+                  (long long)n - 1);
 }
 
 // The length of the row, the place of this CTA's first tile, and the position where its share
 // ends (a share may be empty, or hold ends of segments only: the first tile then lies behind).
-// Each warp finds them for itself: a sum over the sequences, then a running sum until the share's
-// beginning is behind.
+// Each warp finds them for itself: a running sum over the sequences, of which those behind the
+// first batch are summed ahead.
 struct Share {
   long long row, end;
   Cursor at;
@@ -244,6 +251,7 @@ __device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int
   while ((hit = __ballot_sync(0xffffffffu, x < incl)) == 0) {
     const long long run = __shfl_sync(0xffffffffu, incl, 31);
     s0 += kBatch;
+    if (s0 >= pg.S) return sh;
     cost = load(s0);
     incl = run + warp_incl_scan64(cost);
   }
@@ -791,7 +799,7 @@ __device__ __forceinline__ int count_up(int* counter) {
 template <typename T, int D, int RT, int kThreads>
 __device__ __noinline__ void join_parts(const float* part_ml, const float* part_o, T* out,
                                         float* lse, int c, int n, int rows, float* mem) {
-  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kAhead = RT == 16 ? 8 : 4;
+  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kAhead = RT == 16 ? 16 : 6;
   float4* sums = reinterpret_cast<float4*>(mem);               // [groups][D / 4]
   float2* totals = reinterpret_cast<float2*>(mem + kThreads * 4);   // [groups] (maximum, sum)
   static_assert((kThreads * 4 + kGroups * 2) * 4 <= Shape<T, D, RT>::kOffMl, "shared memory");
