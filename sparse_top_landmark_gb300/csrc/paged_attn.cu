@@ -54,16 +54,17 @@ struct Join {
 };
 
 // Shared memory and shape of one instantiation.  RT: query rows of a CTA.  A warp's stage is 8 KB
-// (less for small heads, whose tiles would get too long): enough work behind each wait, and
-// stages for 128 KB on the way to each SM.  Small heads in bf16 leave registers for 16 warps
-// (67 sequences of up to 30515 keys of 32: 35 us with 8, 32 us with 16).
+// (less for small heads: 32 keys are as many as a mask has bits): enough work behind each wait, and
+// stages for 128 KB on the way to each SM (fp32, 64 sequences of up to 20000 keys of 32: 49 us with
+// 16 keys, 38.5 us with 32).  Small heads leave registers for 16 warps (bf16, 67 sequences of up to
+// 30515 keys of 32: 35 us with 8, 32 us with 16; fp32, the 64 with heads of 16: 32.5 and 29.4 us).
 template <typename T, int D, int RT>
 struct Shape {
   static constexpr bool kTensor = std::is_same<T, bf16>::value;
-  static constexpr int kWarps = kTensor && RT == 8 && D <= 32 ? 16 : 8;
+  static constexpr int kWarps = RT == 8 && D <= (kTensor ? 32 : 16) ? 16 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRowBytes = D * (int)sizeof(T);
-  static constexpr int kKeys = (kTensor ? 32 : 16) / (D == 128 ? 2 : 1);   // of a warp in a tile
+  static constexpr int kKeys = (kTensor || D <= 32 ? 32 : 16) / (D == 128 ? 2 : 1);  // of a warp
   static constexpr int kTile = kWarps * kKeys;
   static constexpr int kSegmentCost = kTensor ? 2 : 1;         // tiles that ending a segment is worth
   static constexpr int kChunks = kRowBytes / 16;               // 16-byte chunks of a row
