@@ -349,3 +349,22 @@ def test_shapes_never_run_before_inside_a_capture(dt):
     r = subprocess.run([sys.executable, "-c", NEW_SHAPES_IN_A_CAPTURE, dt], cwd=ROOT,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 127, 128, 129, 257, 513])
+@pytest.mark.parametrize("dt,d", [("bfloat16", 32), ("float32", 16)])
+def test_numbers_of_sequences(n, dt, d):
+    """Batches around the sizes in which sequences are counted, idle slots and long ones among them,
+    a long one first or last, or nothing but idle slots before the last."""
+    mita = M()
+    dt = getattr(torch, dt)
+    for lengths in ([i * 53 % 70 for i in range(n - 1)] + [1500], [1500] + [i % 3 for i in range(n - 1)],
+                    [0] * (n - 1) + [700]):
+        cache = R.Cache(lengths, 2, 16, d, dt)
+        q = torch.randn(n, 4, d, generator=torch.Generator().manual_seed(n)).to(dt)
+        got = mita.mita_paged_attn(q.cuda(), cache.k.cuda(), cache.v.cuda(), cache.table.cuda(),
+                                   lens(*lengths))
+        want, bound = R.paged_attn(q, cache, lengths)[:2]
+        R.assert_close(got, want, bound, "out")
+        assert bool((got.cpu()[torch.tensor(lengths) == 0] == 0).all())
+    assert mita.get_last_device_error() == 0
