@@ -16,6 +16,7 @@
 
 #include "kernels.h"
 #include "norm_rope.cuh"
+#include "token_place.h"
 
 namespace mita {
 namespace {
@@ -105,11 +106,11 @@ cache_append_kernel(const __grid_constant__ CacheAppendArgs<T> a) {
       const int len = pg.lengths[s];
       const int begin = a.seq_start ? a.seq_start[s] : s;
       const int end = a.seq_start ? a.seq_start[s + 1] : s + 1;
-      pos = len - (end - (int)t);
       live = len != 0;                       // else an idle slot
       if (live) {
+        pos = token_position(len, begin, end, (int)t);
         int page = -1;
-        if (pos >= 0 && len >= end - begin && (len - 1) >> pg.page_log2 < pg.width)
+        if (pos >= 0 && fits_table(len, pg.width, pg.page_log2))
           page = pg.table[(long long)s * pg.width + (pos >> pg.page_log2)];
         live = page >= 0 && page < pg.num_pages;
         if (!live && threadIdx.x % L == 0) flag_error(a.status, kDevErrBadIndex);
