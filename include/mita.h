@@ -402,7 +402,8 @@ uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
  *   page_table[s][p / page_size].  Entries behind a sequence's last page are not read.
  *   lengths [S] int32: tokens of each sequence, the new ones included; 0 is an idle slot.
  * All of it is read on the device, so a captured call replays with new lengths and pages; it
- * must not change while the call runs.
+ * must not change while the call runs (the call's own results are then undefined, later calls'
+ * are not).
  * An entry outside [0, num_pages) that is needed, or a length outside [0, table_width*page_size]
  * flags MITA_ERR_DEVICE_CHECK; such tokens are left out and never dereferenced (a length that is
  * too large is cut to the table by mita_paged_attn, and nothing of its sequence is

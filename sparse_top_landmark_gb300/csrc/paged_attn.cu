@@ -45,7 +45,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum before the first key: below every finite score, and finite, so that
 // differences with it need no special case (a score of -inf weighs nothing against it).
 constexpr float kLowest = -FLT_MAX;
-constexpr int kMaxPagedCtas = 512;     // CTAs of a call, and counters in its workspace
+constexpr int kMaxPagedCtas = 511;     // CTAs of a call, and counters in its workspace
+// Behind them one more: the CTAs of a call that will count nothing up any more.
+constexpr int kDoneCounter = kMaxPagedCtas;
 
 // A cut segment whose parts are to be joined: the row of its first query, the CTA that begins it,
 // its parts (0: nothing to do) and its query rows.
@@ -910,8 +912,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   griddep_launch();
   const Share share = my_share<S>(a.paged, a.window, HR);
   Cursor at = share.at;
-  if (at.segment + at.t < share.end) {
-    if (threadIdx.x < 2) joins[threadIdx.x].n = 0;     // read behind the barriers of the share's end
+  const bool any = at.segment + at.t < share.end;
+  if (threadIdx.x < 2) joins[threadIdx.x] = {};        // read behind the barriers of the share's end
+  if (any) {
     prefetch_q<T, D, RT>(a, at);
     using Ld = Loader<T, D, RT>;
     Ld ld;
@@ -1026,6 +1029,15 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       advance<S>(at, a.paged, a.window, HR);
     } while (at.segment + at.t < share.end);
     copy_wait<0>();
+  }
+  // The counters have to be zero again for the next call, whatever this one saw: were a caller to
+  // change lengths while they are read, CTAs would disagree on how many parts a segment has, and a
+  // counter that each segment's join put back would stay where it is.  So every CTA, in any case,
+  // says once that it is done with counting, and the last one to say so clears them all.
+  // (Asked for here, the answer comes while parts are joined.)
+  int done = 0;
+  if (threadIdx.x == 0) done = count_up(a.counters + kDoneCounter);
+  if (any) {
     __syncthreads();
     for (int i = 0; i < 2; ++i) {
       const Join x = joins[i];
@@ -1033,7 +1045,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       join_parts<T, D, RT, S::kThreads>(a.part_ml, a.part_o, a.out + x.row * D,
                                         a.lse ? a.lse + x.row : nullptr, x.c, x.n, x.rows,
                                         reinterpret_cast<float*>(smem));
-      if (threadIdx.x == 0) a.counters[x.c] = 0;       // as the next call wants it
     }
   }
   // sequences without a key: zeros, and the logarithm of an empty sum
@@ -1046,6 +1057,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       a.out[(long long)s * Hq * D + e] = from_f<T>(0.f);
     if (a.lse)
       for (int e = threadIdx.x; e < Hq; e += S::kThreads) a.lse[(long long)s * Hq + e] = -INFINITY;
+  }
+  if (warp == 0 && __shfl_sync(0xffffffffu, done, 0) == (int)gridDim.x - 1) {
+    for (int i = lane; i < (kDoneCounter + 1) / 4; i += 32)
+      reinterpret_cast<int4*>(a.counters)[i] = make_int4(0, 0, 0, 0);
   }
 }
 
@@ -1066,7 +1081,7 @@ struct Carve {
 Carve carve(int ctas, int RT, int D) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   Carve c{};
-  static_assert(kMaxPagedCtas * sizeof(int) == MITA_PAGED_COUNTERS, "counters");
+  static_assert((kDoneCounter + 1) * sizeof(int) == MITA_PAGED_COUNTERS, "counters");
   c.ml = MITA_PAGED_COUNTERS;
   c.o = c.ml + up((size_t)ctas * 2 * RT * 2 * sizeof(float));
   c.total = c.o + up((size_t)ctas * 2 * RT * D * sizeof(float));
