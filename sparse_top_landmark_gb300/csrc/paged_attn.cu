@@ -287,12 +287,24 @@ __device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int
 // What a tile's scores need besides q and k.
 struct ScoreRule {
   float scale2;          // scale * log2(e): the scores of the running softmax are in log2 units
-  float cap, cap2, rcap; // softcap (0: none), softcap * log2(e), scale / softcap
+  float cap, rcap;       // softcap (0: none), scale / softcap
   int last;              // len - 1
   bool plain;            // scores are just scale2 * dot, with scale2 >= 0
 };
-// tanh to about 2^-22 absolute, from one exponential and one reciprocal: what bf16 weights (2^-16)
-// can tell, in a quarter of tanhf's instructions.
+// Below kSeries a capped score is its uncapped one times tanh(x) / x, x = score / softcap, by that
+// function's Taylor series in x^2 (up to x^10: what is left out is below 2^-24 there).  So small scores
+// under a large cap keep fp32's relative accuracy, and caps up to the largest number, where x itself
+// underflows, leave the score as it is.
+constexpr float kSeries = 0.4f;
+__device__ __forceinline__ float tanh_ratio(float xx) {
+  float p = fmaf(xx, -8.8632355e-3f, 2.1869489e-2f);      // -1382/155925, 62/2835
+  p = fmaf(xx, p, -5.3968254e-2f);                        // -17/315
+  p = fmaf(xx, p, 1.3333333e-1f);                         // 2/15
+  p = fmaf(xx, p, -3.3333333e-1f);                        // -1/3
+  return fmaf(xx, p, 1.f);
+}
+// tanh from one exponential and one reciprocal, to 2^-22 absolute: for |x| >= kSeries that is 2^-20 of
+// the value, in a quarter of tanhf's instructions.
 __device__ __forceinline__ float tanh_fast(float x) {
   const float e = exp2_fast(fabsf(x) * (2.f * kLog2e));
   float r;
@@ -302,7 +314,11 @@ __device__ __forceinline__ float tanh_fast(float x) {
 template <bool FAST>
 __device__ __forceinline__ float score_of(const ScoreRule& r, float dot, float slope2, int key) {
   float z = dot * r.scale2;
-  if (r.cap > 0.f) z = r.cap2 * (FAST ? tanh_fast(dot * r.rcap) : tanhf(dot * r.rcap));
+  if (r.cap > 0.f) {
+    const float x = dot * r.rcap;
+    z = fabsf(x) < kSeries ? z * tanh_ratio(x * x)
+                           : r.cap * (FAST ? tanh_fast(x) : tanhf(x)) * kLog2e;
+  }
   return z + slope2 * (float)(key - r.last);
 }
 
@@ -936,8 +952,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
     ScoreRule rule;
     rule.scale2 = a.scale * kLog2e;
     rule.cap = a.softcap;
-    rule.cap2 = a.softcap * kLog2e;
-    rule.rcap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+    // finite, so that a score of zero stays one under the smallest caps too
+    rule.rcap = a.softcap > 0.f ? fminf(fmaxf(a.scale / a.softcap, -FLT_MAX), FLT_MAX) : 0.f;
     rule.plain = a.softcap == 0.f && a.slopes == nullptr && a.scale >= 0.f;
     int slot = 0, next = S::kStages - 1;     // stages: of this tile, of the next one to issue
     int from = at.t, head = 0, rows = 0;
