@@ -505,7 +505,9 @@ def _aligned_rows(t: torch.Tensor) -> torch.Tensor:
     step = 16 // t.element_size()
     ok = t.stride(-1) == 1 and all(n == 1 or s % step == 0
                                    for n, s in zip(t.shape[:-1], t.stride()[:-1]))
-    return t if ok and t.data_ptr() % 16 == 0 else t.contiguous()
+    if ok and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)   # contiguous() may return t itself
 
 
 def _cache_of(k_cache, v_cache, page_table, lengths, dtype, device: int):
