@@ -370,7 +370,8 @@ int mita_qk_norm_rope_f32(const mita_qk_norm_rope_params* params, mita_stream_t 
  *                   not used without weights.  It is the caller's, not the library's cache, so
  *                   that calls captured into different graphs can have their own.
  * The weight gradients are added in a fixed order: the same inputs give the same bits.
- * B or N = 0 clears the weight gradients.  Other parameters as for mita_qk_norm_rope.
+ * A weight gradient over no rows (B, N or, for k, Hkv = 0) is zero.  Other parameters as for
+ * mita_qk_norm_rope.
  */
 typedef struct mita_qk_norm_rope_backward_params {
   const void *q, *k, *dq_out, *dk_out;

@@ -853,19 +853,20 @@ int norm_rope_backward_impl(const mita_qk_norm_rope_backward_params* p, cudaStre
   MITA_TRY(check_positions(p->positions, p->positions_stride));
   const bool empty = p->B == 0 || p->N == 0;
   NormRopeBackwardArgs<T> a{};
-  float* dws[2] = {nullptr, nullptr};
+  float* dws[2] = {nullptr, nullptr};     // of parts with rows
+  float* none[2] = {nullptr, nullptr};    // sums over no rows
   auto part = [&](int i, const void* x, const void* dy, void* dx, const float* w, float* dw,
                   int heads, const int64_t (&xs)[3], const int64_t (&dys)[3],
                   const int64_t (&dxs)[3], const char* const (&name)[5]) {
-    if (heads == 0) return (int)MITA_OK;
+    if (heads == 0 && (!w || !dw)) return (int)MITA_OK;
     if (w) {
       MITA_TRY(check_aligned(w, 16, name[3]));
       MITA_TRY(check_aligned(dw, 4, name[4]));
-      dws[i] = dw;
+      (empty || heads == 0 ? none : dws)[i] = dw;
     } else if (dw) {
       return fail(MITA_ERR_INVALID_ARG, "%s given without %s", name[4], name[3]);
     }
-    if (empty) return (int)MITA_OK;
+    if (empty || heads == 0) return (int)MITA_OK;
     MITA_TRY(check_ptrs({{dy, name[1]}, {dx, name[2]}}));
     if (w) MITA_TRY(check_ptrs({{x, name[0]}}));   // else x is not read
     const int size[3] = {p->B, heads, p->N};
@@ -882,20 +883,20 @@ int norm_rope_backward_impl(const mita_qk_norm_rope_backward_params* p, cudaStre
                 p->dq_out_strides, p->dq_strides, {"q", "dq_out", "dq", "q_weight", "dq_weight"}));
   MITA_TRY(part(1, p->k, p->dk_out, p->dk, p->k_weight, p->dk_weight, p->Hkv, p->k_strides,
                 p->dk_out_strides, p->dk_strides, {"k", "dk_out", "dk", "k_weight", "dk_weight"}));
-  if (empty) {
-    for (float* w : dws)
-      if (w) MITA_CUDA(cudaMemsetAsync(w, 0, p->d * sizeof(float), st), "weight gradient");
-    return MITA_OK;
+  DevState* ds = nullptr;
+  if (!empty) {
+    if (dws[0] || dws[1])
+      MITA_TRY(check_workspace(p->workspace, p->workspace_bytes,
+                               norm_rope_backward_ws(p->d, current_sms())));
+    MITA_TRY(device_state_for(st, &ds));
   }
+  for (float* w : none)
+    if (w) MITA_CUDA(cudaMemsetAsync(w, 0, p->d * sizeof(float), st), "weight gradient");
+  if (empty) return MITA_OK;
   a.positions = p->positions;
   a.pos_b = p->positions_stride;
   a.inv_freq = p->inv_freq;
   a.B = p->B; a.N = p->N; a.rot = p->rot; a.interleaved = p->interleaved != 0; a.eps = p->eps;
-  if (dws[0] || dws[1])
-    MITA_TRY(check_workspace(p->workspace, p->workspace_bytes,
-                             norm_rope_backward_ws(p->d, current_sms())));
-  DevState* ds = nullptr;
-  MITA_TRY(device_state_for(st, &ds));
   MITA_CUDA(launch_norm_rope_backward<T>(a, p->d, static_cast<float*>(p->workspace), ds->num_sms,
                                          dws[0], dws[1], st),
             "norm and rotation gradient launch");
