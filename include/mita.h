@@ -333,7 +333,7 @@ int mita_forward_host_f32(const float* q, const float* k, const float* v, int B,
  *   y = u with pair i of its first `rot` values turned by the angle position * inv_freq[i]
  * Sums and norms are fp32; the angle keeps its accuracy at any 32-bit position (the product is
  * taken modulo one turn in 64 bits).
- *   q [B,Hq,N,d], k [B,Hkv,N,d]     inputs; Hkv = 0: no k.
+ *   q [B,Hq,N,d], k [B,Hkv,N,d]     inputs; Hkv = 0: no k.  Hq+Hkv at most 2^30.
  *   q_weight, k_weight [d] float     norm weights, 16-byte aligned, or NULL (not normalised).
  *   positions       int32 [B,N], row b at positions + b * positions_stride (0: shared by the
  *                   batch); NULL: 0 .. N-1.
@@ -412,7 +412,7 @@ uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
  *
  * mita_cache_append -- the new tokens' keys, normalised and rotated as by mita_qk_norm_rope, and
  * values into the cache; their queries are normalised and rotated by the same launch.
- *   k, v [tokens,Hkv,d], q [tokens,Hq,d]   inputs; Hq = 0: no queries.
+ *   k, v [tokens,Hkv,d], q [tokens,Hq,d]   inputs; Hq = 0: no queries.  Hq+2*Hkv at most 2^30.
  *   seq_start       [S+1] int32, ascending: rows seq_start[s] .. seq_start[s+1]-1 are sequence
  *                   s's new tokens, at its last positions (lengths[s] counts them).  Rows before
  *                   seq_start[0] and from seq_start[S] on belong to nobody: left out.

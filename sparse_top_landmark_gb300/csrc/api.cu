@@ -773,11 +773,19 @@ int row_strides(const int64_t (&given)[K], const int (&size)[K], size_t esize, c
   return MITA_OK;
 }
 
+// Rows of a token: the kernels take runs of them, whose ends (at most 2^16 behind the last) are 32-bit
+// numbers.
+int check_rows(long long rows, const char* name) {
+  if (rows > (1LL << 30)) return fail(MITA_ERR_UNSUPPORTED, "%s must be at most 2^30", name);
+  return MITA_OK;
+}
+
 int check_bhn(int B, int Hq, int Hkv, int N, int d) {
   if (B < 0 || N < 0 || Hq < 1 || Hkv < 0)
     return fail(MITA_ERR_INVALID_ARG, "need B, N, Hkv >= 0 and Hq >= 1 (got %d, %d, %d, %d)", B, N,
                 Hkv, Hq);
   MITA_TRY(check_head_dim(d));
+  MITA_TRY(check_rows((long long)Hq + Hkv, "Hq+Hkv"));
   const long long most = 1LL << 31;
   if ((long long)B * N >= most || (long long)B * N * ((long long)Hq + Hkv) >= most)
     return fail(MITA_ERR_UNSUPPORTED, "B*(Hq+Hkv)*N must be < 2^31");
@@ -934,6 +942,7 @@ int cache_append_impl(const mita_cache_append_params* p, cudaStream_t st) {
   if ((long long)p->Hq + 2LL * p->Hkv >= (1LL << 31) ||
       (long long)p->tokens * ((long long)p->Hq + 2LL * p->Hkv) >= (1LL << 31))
     return fail(MITA_ERR_UNSUPPORTED, "tokens*(Hq+2*Hkv) must be < 2^31");
+  MITA_TRY(check_rows((long long)p->Hq + 2LL * p->Hkv, "Hq+2*Hkv"));
   if (p->seq_start == nullptr && p->tokens != p->S)
     return fail(MITA_ERR_INVALID_ARG,
                 "without seq_start every sequence has one new token (tokens=%d, S=%d)", p->tokens,
