@@ -809,6 +809,15 @@ __device__ __forceinline__ int count_up(int* counter) {
   return old;
 }
 
+// Counts this CTA, which counts nothing up any more, and returns how many had been so before.  Its own
+// counts have been answered (an acquire waits for that), so that whoever is told to be the last
+// comes behind all of them; nothing else is passed on, hence no fence.  The answer is not waited for here.
+__device__ __forceinline__ int count_done(int* counter) {
+  int old;
+  asm volatile("atom.relaxed.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
+
 // Joins the partials of a cut segment, all of them written: the beginning is CTA c's last part, the
 // rest the first parts of CTAs c + 1 .. c + n - 1; out and lse: the segment's rows.  Called by a
 // whole CTA (out of line: it should not cost the tile loop registers); `mem`: shared, of
@@ -1050,9 +1059,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
   // change lengths while they are read, CTAs would disagree on how many parts a segment has, and a
   // counter that each segment's join put back would stay where it is.  So every CTA, in any case,
   // says once that it is done with counting, and the last one to say so clears them all.
-  // (Asked for here, the answer comes while parts are joined.)
+  // (Asked for here, the answer comes while parts are joined: 333 keys 9.2 us, 9.0 without; asked for
+  // with an acquire, the join waits for it: 10.3.)
   int done = 0;
-  if (threadIdx.x == 0) done = count_up(a.counters + kDoneCounter);
+  if (threadIdx.x == 0) done = count_done(a.counters + kDoneCounter);
   if (any) {
     __syncthreads();
     for (int i = 0; i < 2; ++i) {
