@@ -311,6 +311,12 @@ __device__ __forceinline__ float tanh_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return copysignf(fmaf(-2.f, r, 1.f), x);
 }
+// The score where the cap's series does (53 sequences of up to 6276 keys in bf16, cap 30: 37.1 us where
+// every score computes both forms, 34.1 where a warp's tile takes this one if all its scores allow it).
+__device__ __forceinline__ float score_near_zero(const ScoreRule& r, float dot, float slope2, int key) {
+  const float x = dot * r.rcap;
+  return dot * r.scale2 * tanh_ratio(x * x) + slope2 * (float)(key - r.last);
+}
 template <bool FAST>
 __device__ __forceinline__ float score_of(const ScoreRule& r, float dot, float slope2, int key) {
   float z = dot * r.scale2;
@@ -388,17 +394,36 @@ struct TensorState {
     float factor = rule.scale2;
     if (!rule.plain || mask != (unsigned)((1ull << S::kKeys) - 1)) {
       factor = 1.f;
+      bool small = rule.cap > 0.f;
 #pragma unroll
       for (int t = 0; t < kT; ++t)
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = 16 * t + lane / 4 + 8 * (i >> 1);
-            z[t][n][i] = (mask >> j) & 1
-                             ? score_of<true>(rule, z[t][n][i], slope2[n][i & 1], key0 + j)
-                             : -INFINITY;
-          }
+          for (int i = 0; i < 4; ++i) small &= fabsf(z[t][n][i] * rule.rcap) < kSeries;
+      if (__all_sync(0xffffffffu, small)) {
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = 16 * t + lane / 4 + 8 * (i >> 1);
+              z[t][n][i] = (mask >> j) & 1 ? score_near_zero(rule, z[t][n][i], slope2[n][i & 1], key0 + j)
+                                           : -INFINITY;
+            }
+      } else {
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = 16 * t + lane / 4 + 8 * (i >> 1);
+              z[t][n][i] = (mask >> j) & 1 ? score_of<true>(rule, z[t][n][i], slope2[n][i & 1], key0 + j)
+                                           : -INFINITY;
+            }
+      }
     }
     // The running maxima are looked for again only where a score is above them: most tiles
     // bring none, and need no exchange between lanes.
