@@ -455,6 +455,9 @@ int mita_cache_append_f32(const mita_cache_append_params* params, mita_stream_t 
  *                   their own: each needs one.
  * The same inputs give the same bits.  Cache rows that no sequence's length covers are never read.
  * An infinity among the values that are seen may come out as NaN in its column.
+ * The _f32 twin runs on the tensor cores, each factor as a sum of two tf32 values: one in 2^22 of
+ * it is lost at most (a value that close to the largest number may come out infinite), and the result
+ * is as near to the exact one as with fp32 products and sums.
  */
 enum { MITA_PAGED_COUNTERS = 2048 };
 typedef struct mita_paged_attn_params {
