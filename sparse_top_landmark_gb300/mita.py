@@ -638,8 +638,10 @@ def _paged_attn_bytes(S, Hq, Hkv, d, page, width, f32, device: int) -> int:
     return load().mita_paged_attn_workspace_bytes(S, Hq, Hkv, d, page, width, f32)
 
 
-# the handle of torch.cuda.current_stream(device), without making a Stream object of it (1.1 us)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the handle of torch.cuda.current_stream(device), without making a Stream object of it (1.1 us);
+# a torch without CUDA, on which this module can still be imported, has no such function
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def mita_dense_attn(q, k, v, out=None, stream=None):
