@@ -372,7 +372,7 @@ __device__ __forceinline__ void rope_pair(const RopeLane& lane, const RopeCoef<I
 // four rows of arithmetic, are then computed for fewer rows: the least cost is that of the fullest
 // SM's share.  No run is longer than kRopeRun: the blocks of the first runs come first, and
 // fewer heads' rows are then written at a time, each head's to a place of its own (2 x 8191 tokens
-// of 40 heads: runs of 40 65 us, of 20 57 us, of 8 62 us).
+// of 40 heads: runs of 40 65 us, of 20 57 us, of 8 62 us; measured at that shape alone).
 constexpr int kRopeRun = 20;
 struct RopeGrid {
   int run, x, y;

@@ -23,9 +23,9 @@
 // window, on an invalid page) are filled with zeros and never read: what the cache holds there,
 // NaN included, reaches nothing.
 //
-// Measured (bf16): 128 sequences of up to 8192 keys, 32 query and 8 key heads of 128, in 309 us,
-// 6.8 TB/s; one sequence of 1,048,575 keys, 8 and 2 heads of 64, in 88 us, 6.1 TB/s (loading alone
-// takes 85 us); 200 of up to 900 keys, 32 and 8 heads of 128, in 71 us; one of 333 keys in 9.4 us,
+// Measured (bf16): 128 sequences of up to 8192 keys, 32 query and 8 key heads of 128, in 311 us,
+// 6.7 TB/s; one sequence of 1,048,575 keys, 8 and 2 heads of 64, in 88 us, 6.1 TB/s (loading alone
+// takes 85 us); 200 of up to 900 keys, 32 and 8 heads of 128, in 73 us; one of 333 keys in 9.2 to 9.6 us,
 // some 2.5 thousand cycles to find the share, as many to the first keys, 3.5 thousand for a first
 // tile, 1.5 for its end, 2.5 for the count and 3 for a join.
 #include <algorithm>
@@ -61,6 +61,7 @@ struct Join {
 // stages for 128 KB on the way to each SM (fp32, 64 sequences of up to 20000 keys of 32: 49 us with
 // 16 keys, 38.5 us with 32).  Small heads leave registers for 16 warps (bf16, 67 sequences of up to
 // 30515 keys of 32: 35 us with 8, 32 us with 16; fp32, the 64 with heads of 16: 32.5 and 29.4 us).
+// (These choices of shape were measured before fp32 factors were rounded, which takes 5 % more.)
 template <typename T, int D, int RT>
 struct Shape {
   static constexpr bool kTensor = std::is_same<T, bf16>::value;
@@ -311,8 +312,8 @@ __device__ __forceinline__ float tanh_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return copysignf(fmaf(-2.f, r, 1.f), x);
 }
-// The score where the cap's series does (53 sequences of up to 6276 keys in bf16, cap 30: 37.1 us where
-// every score computes both forms, 34.1 where a warp's tile takes this one if all its scores allow it;
+// The score where the cap's series does (the last 2092 keys of 53 sequences in bf16, cap 30: 37.1 us
+// where every score computes both forms, 34.1 where a warp's tile takes this one if all its scores allow it;
 // in fp32, 192 of up to 3783, 85.3 and 82.0).
 __device__ __forceinline__ float score_near_zero(const ScoreRule& r, float dot, float slope2, int key) {
   const float x = dot * r.rcap;
