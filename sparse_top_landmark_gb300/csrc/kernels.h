@@ -347,7 +347,7 @@ struct PagedAttnArgs {
   int window;               // 0: all keys
   // set by the launcher
   int row_blocks;
-  int* counters;            // zero before and after a call
+  unsigned long long* counters;   // zero before the workspace's first call
   float *part_ml, *part_o;
   int* status;
 };

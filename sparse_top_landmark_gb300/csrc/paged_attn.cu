@@ -25,7 +25,7 @@
 //
 // Measured (bf16): 128 sequences of up to 8192 keys, 32 query and 8 key heads of 128, in 311 us,
 // 6.7 TB/s; one sequence of 1,048,575 keys, 8 and 2 heads of 64, in 88 us, 6.1 TB/s (loading alone
-// takes 85 us); 200 of up to 900 keys, 32 and 8 heads of 128, in 73 us; one of 333 keys in 9.2 to 9.6 us,
+// takes 85 us); 200 of up to 900 keys, 32 and 8 heads of 128, in 72 us; one of 333 keys in 9.1 to 9.4 us,
 // some 2.5 thousand cycles to find the share, as many to the first keys, 3.5 thousand for a first
 // tile, 1.5 for its end, 2.5 for the count and 3 for a join.
 #include <algorithm>
@@ -45,9 +45,19 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum before the first key: below every finite score, and finite, so that
 // differences with it need no special case (a score of -inf weighs nothing against it).
 constexpr float kLowest = -FLT_MAX;
-constexpr int kMaxPagedCtas = 511;     // CTAs of a call, and counters in its workspace
-// Behind them one more: the CTAs of a call that will count nothing up any more.
-constexpr int kDoneCounter = kMaxPagedCtas;
+constexpr int kMaxPagedCtas = 255;     // CTAs of a call, and counters in its workspace
+// Counters carry the number of the call that counts, above the count's kCountBits bits: whatever an
+// earlier call left in them is below this one's zero.  (Were a caller to change lengths while they are
+// read, CTAs would disagree on how many parts a segment has, and a counter that a segment's join puts
+// back to zero would stay where it is, for every later call.)  Behind the counters one word gives the
+// calls their numbers: each call adds kCallStep to it, all of its CTAs 1 but the first one, which adds the
+// rest; so whichever comes first, each finds the same multiple of kCallStep there.  Nothing has to
+// be waited for or put back at the end of a call (333 keys 9.4 us; with a word that counts the CTAs that are
+// done, the last of which clears the counters, 10.4 us, and 9.6 where no fence orders the two).
+constexpr int kCallNumber = kMaxPagedCtas;
+constexpr int kCallStep = 256;
+constexpr int kCountBits = 16;
+static_assert(kCallStep > kMaxPagedCtas, "a call's CTAs stay within its step");
 
 // A cut segment whose parts are to be joined: the row of its first query, the CTA that begins it,
 // its parts (0: nothing to do) and its query rows.
@@ -80,7 +90,8 @@ struct Shape {
   static constexpr int kOffMl = kWarps * kRing;                           // [warps][RT][2]
   static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
   static constexpr int kOffJoins = kOffMask + (kWarps * kStages * 4 + 15) / 16 * 16;   // [2]
-  static constexpr int kBytes = kOffJoins + 2 * (int)sizeof(Join);
+  static constexpr int kOffBase = kOffJoins + 2 * (int)sizeof(Join);     // of this call's counts
+  static constexpr int kBytes = kOffBase + 16;
   static_assert(kBytes <= 232448 && kStages >= 3, "shared memory");
   static_assert(RT * D * 4 <= kStageBytes, "a warp's sums in one of its stages");
 };
@@ -862,21 +873,26 @@ struct Loader {
   }
 };
 
-// Counts one up, after what this CTA's threads wrote before their last barrier, and before what
-// they read after the next one; returns the count before.
-__device__ __forceinline__ int count_up(int* counter) {
-  int old;
-  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+// Adds this CTA's part to the word that numbers the calls; returns what it was.
+__device__ __forceinline__ unsigned long long count_call(unsigned long long* number) {
+  const unsigned long long mine = blockIdx.x == 0 ? kCallStep - (gridDim.x - 1) : 1;
+  unsigned long long old;
+  asm volatile("atom.relaxed.gpu.global.add.u64 %0, [%1], %2;"
+               : "=l"(old)
+               : "l"(number), "l"(mine)
+               : "memory");
   return old;
 }
-
-// Counts this CTA, which counts nothing up any more, and returns how many had been so before.  Its own
-// counts have been answered (an acquire waits for that), so that whoever is told to be the last
-// comes behind all of them; nothing else is passed on, hence no fence.  The answer is not waited for here.
-__device__ __forceinline__ int count_done(int* counter) {
-  int old;
-  asm volatile("atom.relaxed.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
-  return old;
+// Counts one up from `base`, this call's zero, after what this CTA's threads wrote before their last
+// barrier, and before what they read after the next one; returns the count before.
+__device__ __forceinline__ int count_up(unsigned long long* counter, unsigned long long base) {
+  unsigned long long old;
+  asm volatile("red.relaxed.gpu.global.max.u64 [%0], %1;" ::"l"(counter), "l"(base) : "memory");
+  asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;"
+               : "=l"(old)
+               : "l"(counter)
+               : "memory");
+  return (int)(old - base);
 }
 
 // Joins the partials of a cut segment, all of them written: the beginning is CTA c's last part, the
@@ -996,11 +1012,12 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
 
   griddep_wait();
   griddep_launch();
+  unsigned long long call = 0;
+  if (threadIdx.x == 0) call = count_call(a.counters + kCallNumber);     // looked at further below
   const Share share = my_share<S>(a.paged, a.window, HR);
   Cursor at = share.at;
-  const bool any = at.segment + at.t < share.end;
   if (threadIdx.x < 2) joins[threadIdx.x] = {};        // read behind the barriers of the share's end
-  if (any) {
+  if (at.segment + at.t < share.end) {
     prefetch_q<T, D, RT>(a, at);
     using Ld = Loader<T, D, RT>;
     Ld ld;
@@ -1018,6 +1035,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       for (int j = 1; j < S::kStages; ++j) rows_of[j - 1] = rows_of[j];
     }
     typename Ld::Rows coming = rows_of[0];
+    // thread 0's alone, kept where it takes no registers
+    auto* const base = reinterpret_cast<unsigned long long*>(smem + S::kOffBase);
+    if (threadIdx.x == 0) *base = call / kCallStep << kCountBits;
     State st;
     ScoreRule rule;
     rule.scale2 = a.scale * kLog2e;
@@ -1105,7 +1125,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
           // others go on meanwhile): the count is asked for now, and looked at then.
           const int c0 = from == 0 ? (int)blockIdx.x : share_of(at.segment, share.row, gridDim.x);
           const int n = share_of(at.segment + at.span.tiles - 1, share.row, gridDim.x) - c0 + 1;
-          const bool last = count_up(a.counters + c0) == n - 1;
+          const bool last = count_up(a.counters + c0, *base) == n - 1;
           joins[from == 0] = {(long long)at.s * Hq + head, c0, last ? n : 0, rows, 0};
         }
         begin = true;
@@ -1115,16 +1135,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
       advance<S>(at, a.paged, a.window, HR);
     } while (at.segment + at.t < share.end);
     copy_wait<0>();
-  }
-  // The counters have to be zero again for the next call, whatever this one saw: were a caller to
-  // change lengths while they are read, CTAs would disagree on how many parts a segment has, and a
-  // counter that each segment's join put back would stay where it is.  So every CTA, in any case,
-  // says once that it is done with counting, and the last one to say so clears them all.
-  // (Asked for here, the answer comes while parts are joined: 333 keys 9.2 us, 9.0 without; asked for
-  // with an acquire, the join waits for it: 10.3.)
-  int done = 0;
-  if (threadIdx.x == 0) done = count_done(a.counters + kDoneCounter);
-  if (any) {
     __syncthreads();
     for (int i = 0; i < 2; ++i) {
       const Join x = joins[i];
@@ -1145,10 +1155,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs<T> a) {
     if (a.lse)
       for (int e = threadIdx.x; e < Hq; e += S::kThreads) a.lse[(long long)s * Hq + e] = -INFINITY;
   }
-  if (warp == 0 && __shfl_sync(0xffffffffu, done, 0) == (int)gridDim.x - 1) {
-    for (int i = lane; i < (kDoneCounter + 1) / 4; i += 32)
-      reinterpret_cast<int4*>(a.counters)[i] = make_int4(0, 0, 0, 0);
-  }
 }
 
 // CTAs for this call: one on each SM, but no more than there can be tiles.
@@ -1168,7 +1174,7 @@ struct Carve {
 Carve carve(int ctas, int RT, int D) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   Carve c{};
-  static_assert((kDoneCounter + 1) * sizeof(int) == MITA_PAGED_COUNTERS, "counters");
+  static_assert((kCallNumber + 1) * sizeof(long long) == MITA_PAGED_COUNTERS, "counters");
   c.ml = MITA_PAGED_COUNTERS;
   c.o = c.ml + up((size_t)ctas * 2 * RT * 2 * sizeof(float));
   c.total = c.o + up((size_t)ctas * 2 * RT * D * sizeof(float));
@@ -1201,7 +1207,7 @@ struct Run {
     const int grid = grid_of<T, D, RT>(a.paged.S, a.paged.width, a.paged.page_log2,
                                        a.Hkv * a.row_blocks, sms);
     const Carve c = carve(grid, RT, D);
-    a.counters = static_cast<int*>(ws);
+    a.counters = static_cast<unsigned long long*>(ws);
     a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + c.ml);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + c.o);
     cudaError_t e = allow_shared();
