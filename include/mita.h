@@ -10,7 +10,7 @@
  *
  * Conventions (all entry points):
  *   - Tensors are dense, row-major, except where an entry point takes strides
- *     (mita_qk_norm_rope to mita_paged_attn).  Q, K, V and the output are [B, H, N, d]:
+ *     (mita_qk_norm_rope to mita_paged_attn_q4).  Q, K, V and the output are [B, H, N, d]:
  *     head (b, h) owns N consecutive rows of d elements.  For a 2D token grid
  *     (grid_h > 1) token t sits at row t / grid_w, column t % grid_w.
  *   - Unsuffixed entry points take bfloat16 data (`const void*` holding
@@ -396,6 +396,51 @@ int mita_qk_norm_rope_backward_f32(const mita_qk_norm_rope_backward_params* para
 uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d);
 
 /*
+ * mita_qk_norm_rope_axes -- mita_qk_norm_rope for tokens that stand somewhere on several axes, such
+ * as rows and columns of an image, or time, rows and columns of a video: frequency i turns pair i by the
+ * angle positions[axis i] * inv_freq[i].
+ *   positions       int32 [axes,B,N]: axis a, batch b, token n at positions +
+ *                   a*positions_axis_stride + b*positions_stride + n (a stride of 0: shared).
+ *   freq_axis       [rot/2] int32: the axis of each frequency, in any order; one outside [0, axes)
+ *                   flags MITA_ERR_DEVICE_CHECK and counts as 0.
+ *   axes            at least 1.
+ * Text among images has the same position on every axis.  Other parameters, and the gradient's, as for
+ * mita_qk_norm_rope and mita_qk_norm_rope_backward (whose workspace size is this one's too).
+ */
+typedef struct mita_qk_norm_rope_axes_params {
+  const void *q, *k;
+  const float *q_weight, *k_weight;
+  const int32_t *positions, *freq_axis;
+  const double* inv_freq;
+  void *q_out, *k_out;
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3], positions_stride,
+      positions_axis_stride;
+  int32_t B, Hq, Hkv, N, d, rot, interleaved, axes;
+  float eps;
+} mita_qk_norm_rope_axes_params;
+int mita_qk_norm_rope_axes(const mita_qk_norm_rope_axes_params* params, mita_stream_t stream);
+int mita_qk_norm_rope_axes_f32(const mita_qk_norm_rope_axes_params* params, mita_stream_t stream);
+
+typedef struct mita_qk_norm_rope_axes_backward_params {
+  const void *q, *k, *dq_out, *dk_out;
+  const float *q_weight, *k_weight;
+  const int32_t *positions, *freq_axis;
+  const double* inv_freq;
+  void *dq, *dk;
+  float *dq_weight, *dk_weight;
+  void* workspace;
+  uint64_t workspace_bytes;
+  int64_t q_strides[3], k_strides[3], dq_out_strides[3], dk_out_strides[3], dq_strides[3],
+      dk_strides[3], positions_stride, positions_axis_stride;
+  int32_t B, Hq, Hkv, N, d, rot, interleaved, axes;
+  float eps;
+} mita_qk_norm_rope_axes_backward_params;
+int mita_qk_norm_rope_axes_backward(const mita_qk_norm_rope_axes_backward_params* params,
+                                    mita_stream_t stream);
+int mita_qk_norm_rope_axes_backward_f32(const mita_qk_norm_rope_axes_backward_params* params,
+                                        mita_stream_t stream);
+
+/*
  * The paged cache of mita_cache_append and mita_paged_attn:
  *   k_cache, v_cache [num_pages,Hkv,page_size,d], dense; page_size a power of two up to 2^20,
  *   table_width*page_size at most 2^31 - 2^16.
@@ -477,6 +522,97 @@ int mita_paged_attn_f32(const mita_paged_attn_params* params, mita_stream_t stre
 /* Bytes of workspace mita_paged_attn needs for this shape on the current device (0 if invalid). */
 uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page_size,
                                          int table_width, int is_f32);
+
+/*
+ * mita_cache_plan -- the pages of a serving step, dealt out on the device: the pages of requests that
+ * are done go back to the pool, new tokens get theirs, and every row of the step's packed tokens gets
+ * its position and its place in the cache.  One launch, for the whole step, in front of
+ * mita_qk_norm_rope (positions), mita_cache_append_q4 (slots) or mita_cache_append (seq_start), and
+ * mita_paged_attn or mita_paged_attn_q4 (page_table, new_lengths).
+ *   new_tokens [S] int32    >= 0: that many rows of the step; -1: the sequence is done.
+ *   lengths [S] int32       tokens of each sequence before the step.
+ *   new_lengths [S] int32   output: after it (0 for a sequence that is done); may be lengths.
+ *   page_table [S,table_width] int32   the rows' next entries are written; held ones stay.
+ *   free_pages [num_pages] int32       a stack of free pages, its first free_count[0] entries.
+ *   free_count, new_free_count [1] int32   before and after; may be the same.
+ *   seq_start [S+1] int32   output: the first row of each sequence, those of new_tokens before it
+ *                   added up (at most `tokens`).
+ *   positions [tokens] int32, slots [tokens] int64   outputs, of every row: its position in its sequence
+ *                   and page*page_size + the row in its page; 0 and -1 for rows behind the last
+ *                   sequence's and of sequences that were not granted.
+ *   granted [S] int32       output: new_tokens, or 0 where the sequence got nothing.
+ *   S               at most 2^14.
+ * Pages of sequences that are done are pushed first, in the order of the sequences and of their
+ * tables, and may be handed out again by the same call.  Then sequence s is granted its tokens if they
+ * fit its row of the table and the step's rows and it needs no page, or the pages that the sequences up to
+ * and with s need (those that fit) are no more than the free ones; the first of its pages is the one
+ * under those that the sequences before it need, counted from the stack's top.  A sequence that is not
+ * granted stays as it is: its rows have no places (mita_cache_append, which goes by lengths, must not be
+ * given its rows).
+ * new_tokens below -1, lengths outside [0, table_width*page_size], a free_count outside [0, num_pages],
+ * pushes beyond num_pages and page numbers outside [0, num_pages) under a row flag
+ * MITA_ERR_DEVICE_CHECK; such sequences get nothing, such rows slot -1.  Every other entry of the
+ * arrays stays as it is.  The arrays must not overlap, except as said.
+ */
+typedef struct mita_cache_plan_params {
+  const int32_t *new_tokens, *lengths;
+  int32_t *new_lengths, *page_table, *free_pages;
+  const int32_t* free_count;
+  int32_t *new_free_count, *seq_start, *positions;
+  int64_t* slots;
+  int32_t* granted;
+  int32_t S, tokens, num_pages, page_size, table_width;
+} mita_cache_plan_params;
+int mita_cache_plan(const mita_cache_plan_params* params, mita_stream_t stream);
+
+/*
+ * The paged cache in 4 bits, of mita_cache_append_q4 and mita_paged_attn_q4: 17/32 byte a value, 3.8
+ * times as many tokens as in bf16.  d in {32, 64, 128}; page_size a power of two from 16 to 2^20.
+ *   k_cache, v_cache [num_pages,Hkv,page_size*17*d/32] bytes, dense.  Of each page and head first the
+ *   codes of its rows, d/2 bytes each, then their scales, d/32 bytes each.
+ *   A value is (code - 8) * scale: codes of 4 bits, value 2b in the lower half of byte b; a scale for
+ *   every 32 values, whose byte is bits 7 to 14 of an fp16 number (5 of exponent, 3 of mantissa).
+ *   The chunks of 32 values (16 bytes) of row r of a page stand in another order: chunk c at
+ *   c ^ (r >> 1 & 3) for d = 128, at c ^ (r >> 2 & 1) for d = 64.
+ * page_table and lengths as for mita_paged_attn.
+ *
+ * mita_cache_append_q4 -- new tokens' keys (normalised and rotated already, mita_qk_norm_rope) and values
+ * into that cache.  Of 32 values of a row the largest size over 7, rounded to the nearest such scale (at
+ * most 61440), is the scale; a value's code is the nearest of -7 to 7 scales, halves towards zero (in fp32:
+ * x * r rounded, r a factor 1 - 2^-20 below 1 / scale).  A block with an infinity or NaN becomes
+ * NaN.
+ *   k, v [tokens,Hkv,d]     inputs.
+ *   slots [tokens] int64    each token's page*page_size + row (mita_cache_plan's); -1: passed over.
+ *                   Others outside [0, num_pages*page_size) flag MITA_ERR_DEVICE_CHECK and are passed
+ *                   over.  Of two tokens with one slot a mixture is left there.
+ *   k_out, v_out [tokens,Hkv,d] or NULL   outputs: the values that the cache now holds for each token, in
+ *                   the element type (exactly, in bf16 too), for attention of a prompt over what later tokens
+ *                   will see.  Rows passed over stay as they are.
+ *   *_strides       elements between tokens and heads.
+ */
+typedef struct mita_cache_append_q4_params {
+  const void *k, *v;
+  const int64_t* slots;
+  void *k_cache, *v_cache, *k_out, *v_out;
+  int64_t k_strides[2], v_strides[2], k_out_strides[2], v_out_strides[2];
+  int32_t tokens, Hkv, d, num_pages, page_size;
+} mita_cache_append_q4_params;
+int mita_cache_append_q4(const mita_cache_append_q4_params* params, mita_stream_t stream);
+int mita_cache_append_q4_f32(const mita_cache_append_q4_params* params, mita_stream_t stream);
+
+/*
+ * mita_paged_attn_q4 -- mita_paged_attn over the cache in 4 bits; the element type is that of q and
+ * out.  Parameters, masks, empty sequences and workspace as there (the workspace's size is
+ * mita_paged_attn_q4_workspace_bytes; one workspace may serve both).  A NaN among the scales of a
+ * row that is seen makes what depends on it NaN.
+ * Runs on the tensor cores in fp16, the codes exact: the bf16 entry point keeps 11 bits of a weight,
+ * the _f32 twin 22 of a query and of a weight.  Query values beyond 2^100 may come out as NaN.
+ */
+int mita_paged_attn_q4(const mita_paged_attn_params* params, mita_stream_t stream);
+int mita_paged_attn_q4_f32(const mita_paged_attn_params* params, mita_stream_t stream);
+/* Bytes of workspace mita_paged_attn_q4 needs for this shape on the current device (0 if invalid). */
+uint64_t mita_paged_attn_q4_workspace_bytes(int S, int Hq, int Hkv, int d, int page_size,
+                                            int table_width, int is_f32);
 
 /* Bytes of workspace mita_forward needs for this shape (0 if invalid). */
 uint64_t mita_forward_workspace_bytes(int B, int H, int N, int d, int m, int topk, int s,

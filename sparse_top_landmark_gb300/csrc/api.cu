@@ -798,13 +798,37 @@ int check_positions(const int32_t* positions, int64_t stride) {
   return check_aligned(positions, 4, "positions");
 }
 
-template <typename T>
-int norm_rope_impl(const mita_qk_norm_rope_params* p, cudaStream_t st) {
+// What the calls with positions of several axes have besides.
+struct Axes {
+  bool several;
+  const int32_t* freq_axis;
+  int64_t stride;
+  int axes;
+};
+template <typename P>
+Axes axes_of(const P* p) {
+  if constexpr (std::is_same<P, mita_qk_norm_rope_axes_params>::value ||
+                std::is_same<P, mita_qk_norm_rope_axes_backward_params>::value)
+    return {true, p->freq_axis, p->positions_axis_stride, p->axes};
+  else
+    return {};
+}
+int check_axes(const Axes& x, const int32_t* positions, int rot) {
+  if (x.axes < 1) return fail(MITA_ERR_INVALID_ARG, "axes=%d must be positive", x.axes);
+  if (x.stride < 0) return fail(MITA_ERR_INVALID_ARG, "positions_axis_stride must be >= 0");
+  MITA_TRY(check_aligned(positions, 4, "positions"));
+  return rot > 0 ? check_aligned(x.freq_axis, 4, "freq_axis") : (int)MITA_OK;
+}
+
+template <typename T, typename P>
+int norm_rope_impl(const P* p, cudaStream_t st) {
   if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  const Axes axes = axes_of(p);
   MITA_TRY(check_bhn(p->B, p->Hq, p->Hkv, p->N, p->d));
   MITA_TRY(check_rope(p->d, p->rot, p->inv_freq, p->eps));
   MITA_TRY(check_positions(p->positions, p->positions_stride));
   if (p->B == 0 || p->N == 0) return MITA_OK;
+  if (axes.several) MITA_TRY(check_axes(axes, p->positions, p->rot));
   NormRopeArgs<T> a{};
   auto part = [&](NormRopePart<T>& o, const void* x, void* y, const float* w, int heads,
                   const int64_t (&xs)[3], const int64_t (&ys)[3], const char* nx, const char* ny,
@@ -829,7 +853,9 @@ int norm_rope_impl(const mita_qk_norm_rope_params* p, cudaStream_t st) {
   a.B = p->B; a.N = p->N; a.rot = p->rot; a.interleaved = p->interleaved != 0; a.eps = p->eps;
   DevState* ds = nullptr;
   MITA_TRY(device_state_for(st, &ds));
-  MITA_CUDA(launch_norm_rope<T>(a, p->d, ds->num_sms, st), "norm and rotation launch");
+  a.freq_axis = axes.freq_axis; a.pos_a = axes.stride; a.axes = axes.axes; a.status = ds->status;
+  MITA_CUDA((axes.several ? launch_norm_rope_axes<T> : launch_norm_rope<T>)(a, p->d, ds->num_sms, st),
+            "norm and rotation launch");
   return MITA_OK;
 }
 
@@ -853,13 +879,15 @@ uint64_t norm_rope_backward_ws(int d, int sms) {
   return (uint64_t)norm_rope_backward_blocks(sms) * d * sizeof(float);
 }
 
-template <typename T>
-int norm_rope_backward_impl(const mita_qk_norm_rope_backward_params* p, cudaStream_t st) {
+template <typename T, typename P>
+int norm_rope_backward_impl(const P* p, cudaStream_t st) {
   if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  const Axes axes = axes_of(p);
   MITA_TRY(check_bhn(p->B, p->Hq, p->Hkv, p->N, p->d));
   MITA_TRY(check_rope(p->d, p->rot, p->inv_freq, p->eps));
   MITA_TRY(check_positions(p->positions, p->positions_stride));
   const bool empty = p->B == 0 || p->N == 0;
+  if (axes.several && !empty) MITA_TRY(check_axes(axes, p->positions, p->rot));
   NormRopeBackwardArgs<T> a{};
   float* dws[2] = {nullptr, nullptr};     // of parts with rows
   float* none[2] = {nullptr, nullptr};    // sums over no rows
@@ -905,8 +933,9 @@ int norm_rope_backward_impl(const mita_qk_norm_rope_backward_params* p, cudaStre
   a.pos_b = p->positions_stride;
   a.inv_freq = p->inv_freq;
   a.B = p->B; a.N = p->N; a.rot = p->rot; a.interleaved = p->interleaved != 0; a.eps = p->eps;
-  MITA_CUDA(launch_norm_rope_backward<T>(a, p->d, static_cast<float*>(p->workspace), ds->num_sms,
-                                         dws[0], dws[1], st),
+  a.freq_axis = axes.freq_axis; a.pos_a = axes.stride; a.axes = axes.axes; a.status = ds->status;
+  MITA_CUDA((axes.several ? launch_norm_rope_axes_backward<T> : launch_norm_rope_backward<T>)(
+                a, p->d, static_cast<float*>(p->workspace), ds->num_sms, dws[0], dws[1], st),
             "norm and rotation gradient launch");
   return MITA_OK;
 }
@@ -999,11 +1028,12 @@ int check_paged_attn(int S, int Hq, int Hkv, int d, int num_pages, int page_size
   return MITA_OK;
 }
 
-template <typename T>
-int paged_attn_impl(const mita_paged_attn_params* p, cudaStream_t st) {
+// C: what the cache is made of; its check of sizes, its workspace and its launch
+template <typename T, typename C, typename Check, typename Bytes, typename Launch>
+int paged_attn_any(const mita_paged_attn_params* p, cudaStream_t st, Check check, Bytes ws_bytes,
+                   Launch launch) {
   if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
-  MITA_TRY(check_paged_attn(p->S, p->Hq, p->Hkv, p->d, p->num_pages, p->page_size,
-                            p->table_width));
+  MITA_TRY(check(p->S, p->Hq, p->Hkv, p->d, p->num_pages, p->page_size, p->table_width));
   if (!std::isfinite(p->scale)) return fail(MITA_ERR_INVALID_ARG, "scale is not finite");
   if (!(p->softcap >= 0.f) || std::isinf(p->softcap))
     return fail(MITA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
@@ -1020,22 +1050,125 @@ int paged_attn_impl(const mita_paged_attn_params* p, cudaStream_t st) {
   MITA_TRY(row_strides<2>(p->q_strides, {p->S, p->Hq}, sizeof(T), "q", qs));
   const int pl = log2_of(p->page_size), G = p->Hq / p->Hkv;
   MITA_TRY(check_workspace(p->workspace, p->workspace_bytes,
-                           paged_attn_ws_bytes(p->d, p->Hkv, G, p->S, p->table_width, pl,
-                                               sizeof(T) == 4, current_sms())));
+                           ws_bytes(p->d, p->Hkv, G, p->S, p->table_width, pl, sizeof(T) == 4,
+                                    current_sms())));
   DevState* ds = nullptr;
   MITA_TRY(device_state_for(st, &ds));
-  PagedAttnArgs<T> a{};
+  PagedAttnArgs<T, C> a{};
   a.q = static_cast<const T*>(p->q);
-  a.k_cache = static_cast<const T*>(p->k_cache);
-  a.v_cache = static_cast<const T*>(p->v_cache);
+  a.k_cache = static_cast<const C*>(p->k_cache);
+  a.v_cache = static_cast<const C*>(p->v_cache);
   a.out = static_cast<T*>(p->out);
   a.lse = p->lse;
   a.slopes = p->alibi_slopes; a.q_s = qs[0]; a.q_h = qs[1];
   a.paged = {p->page_table, p->lengths, p->S, p->table_width, p->num_pages, pl};
   a.Hkv = p->Hkv; a.G = G; a.scale = p->scale; a.softcap = p->softcap; a.window = p->window;
   a.status = ds->status;
-  MITA_CUDA(launch_paged_attn<T>(a, p->d, p->workspace, ds->num_sms, st),
-            "paged attention launch");
+  MITA_CUDA(launch(a, p->d, p->workspace, ds->num_sms, st), "paged attention launch");
+  return MITA_OK;
+}
+
+template <typename T>
+int paged_attn_impl(const mita_paged_attn_params* p, cudaStream_t st) {
+  return paged_attn_any<T, T>(p, st, check_paged_attn, paged_attn_ws_bytes, launch_paged_attn<T>);
+}
+
+// The cache in 4 bits: 32 values a scale, and pages of whole 16-byte pieces of scales.
+int check_q4(int d, int page_size) {
+  if (d < kQ4Block)
+    return fail(MITA_ERR_UNSUPPORTED, "head dim d=%d not in {32, 64, 128} of a 4-bit cache", d);
+  if (page_size < kQ4Page)
+    return fail(MITA_ERR_UNSUPPORTED, "page_size=%d of a 4-bit cache must be at least %d",
+                page_size, kQ4Page);
+  return MITA_OK;
+}
+
+template <typename T>
+int cache_append_q4_impl(const mita_cache_append_q4_params* p, cudaStream_t st) {
+  if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  if (p->tokens < 0) return fail(MITA_ERR_INVALID_ARG, "need tokens >= 0 (got %d)", p->tokens);
+  MITA_TRY(check_pages(0, p->Hkv, p->num_pages, p->page_size, 0));
+  MITA_TRY(check_head_dim(p->d));
+  MITA_TRY(check_q4(p->d, p->page_size));
+  if (p->Hkv >= (1 << 30) || (long long)p->tokens * 2 * p->Hkv >= (1LL << 31))
+    return fail(MITA_ERR_UNSUPPORTED, "tokens*2*Hkv must be < 2^31");
+  if (p->tokens == 0) return MITA_OK;
+  CacheAppendQ4Args<T> a{};
+  auto rows = [&](const void* x, const int64_t (&given)[2], const char* name, long long& t,
+                  long long& h) {
+    MITA_TRY(check_ptrs({{x, name}}));
+    long long s[2];
+    MITA_TRY(row_strides<2>(given, {p->tokens, p->Hkv}, sizeof(T), name, s));
+    t = s[0];
+    h = s[1];
+    return (int)MITA_OK;
+  };
+  MITA_TRY(rows(p->k, p->k_strides, "k", a.k_t, a.k_h));
+  MITA_TRY(rows(p->v, p->v_strides, "v", a.v_t, a.v_h));
+  if (p->k_out) MITA_TRY(rows(p->k_out, p->k_out_strides, "k_out", a.ko_t, a.ko_h));
+  if (p->v_out) MITA_TRY(rows(p->v_out, p->v_out_strides, "v_out", a.vo_t, a.vo_h));
+  if (p->num_pages > 0)
+    MITA_TRY(check_ptrs({{p->k_cache, "k_cache"}, {p->v_cache, "v_cache"}}));
+  MITA_TRY(check_aligned(p->slots, 8, "slots"));
+  DevState* ds = nullptr;
+  MITA_TRY(device_state_for(st, &ds));
+  a.k = static_cast<const T*>(p->k);
+  a.v = static_cast<const T*>(p->v);
+  a.slots = p->slots;
+  a.k_cache = static_cast<uint8_t*>(p->k_cache);
+  a.v_cache = static_cast<uint8_t*>(p->v_cache);
+  a.k_out = static_cast<T*>(p->k_out);
+  a.v_out = static_cast<T*>(p->v_out);
+  a.places = (long long)p->num_pages * p->page_size;
+  a.tokens = p->tokens; a.kv_heads = p->Hkv; a.page_log2 = log2_of(p->page_size);
+  a.status = ds->status;
+  MITA_CUDA(launch_cache_append_q4<T>(a, p->d, ds->num_sms, st), "4-bit cache append launch");
+  return MITA_OK;
+}
+
+int check_paged_attn_q4(int S, int Hq, int Hkv, int d, int num_pages, int page_size, int width) {
+  MITA_TRY(check_paged_attn(S, Hq, Hkv, d, num_pages, page_size, width));
+  return check_q4(d, page_size);
+}
+
+template <typename T>
+int paged_attn_q4_impl(const mita_paged_attn_params* p, cudaStream_t st) {
+  return paged_attn_any<T, uint8_t>(p, st, check_paged_attn_q4, paged_attn_q4_ws_bytes,
+                                    launch_paged_attn_q4<T>);
+}
+
+int cache_plan_impl(const mita_cache_plan_params* p, cudaStream_t st) {
+  if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
+  if (p->tokens < 0) return fail(MITA_ERR_INVALID_ARG, "need tokens >= 0 (got %d)", p->tokens);
+  MITA_TRY(check_pages(p->S, 1, p->num_pages, p->page_size, p->table_width));
+  if (p->S > kMaxPlanSequences)
+    return fail(MITA_ERR_UNSUPPORTED, "S=%d: a plan takes at most %d sequences", p->S,
+                kMaxPlanSequences);
+  if (p->S > 0) {
+    MITA_TRY(check_aligned(p->new_tokens, 4, "new_tokens"));
+    MITA_TRY(check_aligned(p->lengths, 4, "lengths"));
+    MITA_TRY(check_aligned(p->new_lengths, 4, "new_lengths"));
+    MITA_TRY(check_aligned(p->granted, 4, "granted"));
+    if (p->table_width > 0) MITA_TRY(check_aligned(p->page_table, 4, "page_table"));
+  }
+  if (p->num_pages > 0) MITA_TRY(check_aligned(p->free_pages, 4, "free_pages"));
+  MITA_TRY(check_aligned(p->free_count, 4, "free_count"));
+  MITA_TRY(check_aligned(p->new_free_count, 4, "new_free_count"));
+  MITA_TRY(check_aligned(p->seq_start, 4, "seq_start"));
+  if (p->tokens > 0) {
+    MITA_TRY(check_aligned(p->positions, 4, "positions"));
+    MITA_TRY(check_aligned(p->slots, 8, "slots"));
+  }
+  DevState* ds = nullptr;
+  MITA_TRY(device_state_for(st, &ds));
+  CachePlanArgs a{};
+  a.new_tokens = p->new_tokens; a.lengths = p->lengths; a.new_lengths = p->new_lengths;
+  a.page_table = p->page_table; a.free_pages = p->free_pages; a.free_count = p->free_count;
+  a.new_free_count = p->new_free_count; a.seq_start = p->seq_start; a.positions = p->positions;
+  a.granted = p->granted; a.slots = p->slots;
+  a.S = p->S; a.tokens = p->tokens; a.width = p->table_width; a.num_pages = p->num_pages;
+  a.page_log2 = log2_of(p->page_size); a.status = ds->status;
+  MITA_CUDA(launch_cache_plan(a, st), "cache plan launch");
   return MITA_OK;
 }
 
@@ -1336,6 +1469,22 @@ uint64_t mita_qk_norm_rope_backward_workspace_bytes(int d) {
   return mita::norm_rope_backward_ws(d, mita::current_sms());
 }
 
+int mita_qk_norm_rope_axes(const mita_qk_norm_rope_axes_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_impl<bf16>(params, stream); });
+}
+int mita_qk_norm_rope_axes_f32(const mita_qk_norm_rope_axes_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_impl<float>(params, stream); });
+}
+
+int mita_qk_norm_rope_axes_backward(const mita_qk_norm_rope_axes_backward_params* params,
+                                    mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_backward_impl<bf16>(params, stream); });
+}
+int mita_qk_norm_rope_axes_backward_f32(const mita_qk_norm_rope_axes_backward_params* params,
+                                        mita_stream_t stream) {
+  return mita::guarded([&] { return mita::norm_rope_backward_impl<float>(params, stream); });
+}
+
 int mita_cache_append(const mita_cache_append_params* params, mita_stream_t stream) {
   return mita::guarded([&] { return mita::cache_append_impl<bf16>(params, stream); });
 }
@@ -1357,6 +1506,33 @@ uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page
     return 0;
   return mita::paged_attn_ws_bytes(d, Hkv, Hq / Hkv, S, table_width, mita::log2_of(page_size),
                                    is_f32, mita::current_sms());
+}
+
+int mita_paged_attn_q4(const mita_paged_attn_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::paged_attn_q4_impl<bf16>(params, stream); });
+}
+int mita_paged_attn_q4_f32(const mita_paged_attn_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::paged_attn_q4_impl<float>(params, stream); });
+}
+uint64_t mita_paged_attn_q4_workspace_bytes(int S, int Hq, int Hkv, int d, int page_size,
+                                         int table_width, int is_f32) {
+  if (mita::guarded([&] {
+        return mita::check_paged_attn_q4(S, Hq, Hkv, d, 0, page_size, table_width);
+      }) != MITA_OK)
+    return 0;
+  return mita::paged_attn_q4_ws_bytes(d, Hkv, Hq / Hkv, S, table_width, mita::log2_of(page_size),
+                                   is_f32, mita::current_sms());
+}
+
+int mita_cache_append_q4(const mita_cache_append_q4_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::cache_append_q4_impl<bf16>(params, stream); });
+}
+int mita_cache_append_q4_f32(const mita_cache_append_q4_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::cache_append_q4_impl<float>(params, stream); });
+}
+
+int mita_cache_plan(const mita_cache_plan_params* params, mita_stream_t stream) {
+  return mita::guarded([&] { return mita::cache_plan_impl(params, stream); });
 }
 
 uint64_t mita_forward_workspace_bytes(int B, int H, int N, int d, int m, int topk, int s,

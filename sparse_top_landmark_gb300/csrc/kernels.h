@@ -273,7 +273,10 @@ template <typename T>
 struct NormRopeArgs {
   NormRopePart<T> part[2];  // q, k
   const int32_t* positions; // [B][N], pos_b from batch to batch; null: 0 .. N - 1
-  long long pos_b;
+  const int32_t* freq_axis; // [rot / 2] several axes only: of each frequency, positions [axes][B][N]
+  long long pos_b, pos_a;
+  int axes;
+  int* status;
   const double* inv_freq;   // [rot / 2] radians per position
   int B, N, rot, interleaved;
   float eps;
@@ -281,6 +284,8 @@ struct NormRopeArgs {
 };
 template <typename T>
 cudaError_t launch_norm_rope(NormRopeArgs<T> a, int d, int sms, cudaStream_t st);
+template <typename T>
+cudaError_t launch_norm_rope_axes(NormRopeArgs<T> a, int d, int sms, cudaStream_t st);
 
 template <typename T>
 struct NormRopeBackwardPart {
@@ -294,8 +299,10 @@ struct NormRopeBackwardPart {
 template <typename T>
 struct NormRopeBackwardArgs {
   NormRopeBackwardPart<T> part[2];
-  const int32_t* positions;
-  long long pos_b;
+  const int32_t *positions, *freq_axis;
+  long long pos_b, pos_a;
+  int axes;
+  int* status;
   const double* inv_freq;
   int B, N, rot, interleaved;
   float eps;
@@ -307,6 +314,9 @@ int norm_rope_backward_blocks(int sms);
 template <typename T>
 cudaError_t launch_norm_rope_backward(NormRopeBackwardArgs<T> a, int d, float* partial, int sms,
                                       float* dwq, float* dwk, cudaStream_t st);
+template <typename T>
+cudaError_t launch_norm_rope_axes_backward(NormRopeBackwardArgs<T> a, int d, float* partial, int sms,
+                                           float* dwq, float* dwk, cudaStream_t st);
 
 // ---- paged key-value cache ------------------------------------------------------------------
 // [pages][Hkv][page_size][d]; page_size = 1 << page_log2; sequence s's token p lives in page
@@ -334,9 +344,10 @@ struct CacheAppendArgs {
 template <typename T>
 cudaError_t launch_cache_append(CacheAppendArgs<T> a, int d, int sms, cudaStream_t st);
 
-template <typename T>
+template <typename T, typename C = T>      // C: what the cache is made of
 struct PagedAttnArgs {
-  const T *q, *k_cache, *v_cache;
+  const T* q;
+  const C *k_cache, *v_cache;
   T* out;                   // [S][Hq][d]
   float* lse;               // [S][Hq] or null
   const float* slopes;      // [Hq] or null
@@ -355,6 +366,47 @@ size_t paged_attn_ws_bytes(int d, int Hkv, int G, int S, int width, int page_log
                            int sms);
 template <typename T>
 cudaError_t launch_paged_attn(PagedAttnArgs<T> a, int d, void* ws, int sms, cudaStream_t st);
+
+// ---- the paged cache in 4 bits: for each page and head its rows' codes (d / 2 bytes a row), then
+// their scales (d / 32 bytes a row); page_size at least kQ4Page -----------------------------------
+constexpr int kQ4Page = 16, kQ4Block = 32;     // values of a scale
+template <typename T>
+using PagedAttnQ4Args = PagedAttnArgs<T, uint8_t>;
+size_t paged_attn_q4_ws_bytes(int d, int Hkv, int G, int S, int width, int page_log2, int is_f32,
+                              int sms);
+template <typename T>
+cudaError_t launch_paged_attn_q4(PagedAttnQ4Args<T> a, int d, void* ws, int sms, cudaStream_t st);
+
+template <typename T>
+struct CacheAppendQ4Args {
+  const T *k, *v;           // [tokens][Hkv][d]
+  const int64_t* slots;     // [tokens] page * page_size + row; -1: nobody's
+  uint8_t *k_cache, *v_cache;
+  T *k_out, *v_out;         // null: not asked for
+  long long k_t, k_h, v_t, v_h, ko_t, ko_h, vo_t, vo_h;
+  long long places;         // num_pages * page_size
+  int tokens, kv_heads, page_log2;
+  int* status;
+};
+template <typename T>
+cudaError_t launch_cache_append_q4(CacheAppendQ4Args<T> a, int d, int sms, cudaStream_t st);
+
+// ---- pages of a serving step ---------------------------------------------------------------------
+constexpr int kMaxPlanSequences = 1 << 14;
+struct CachePlanArgs {
+  const int32_t* new_tokens;           // [S] >= 0, or -1: the sequence is done
+  const int32_t* lengths;              // [S] before the step
+  int32_t* new_lengths;                // [S] may be lengths
+  int32_t* page_table;                 // [S][width]
+  int32_t* free_pages;                 // [num_pages] a stack
+  const int32_t* free_count;           // [1] may be new_free_count
+  int32_t* new_free_count;
+  int32_t *seq_start, *positions, *granted;
+  int64_t* slots;
+  int S, tokens, width, num_pages, page_log2;
+  int* status;
+};
+cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t st);
 
 int num_sms_of_current_device();
 

@@ -206,11 +206,11 @@ __device__ __forceinline__ void rope_table(const double* inv_freq, int half,
   }
 }
 
-// cos and sin of four pairs at position p: the angle's top 32 bits, less the nearest quarter
+// cos and sin of four pairs, each at its position p: the angle's top 32 bits, less the nearest quarter
 // turn, give |x| <= pi / 4 to fp32's 24 bits; the Taylor series of sine to x^9 and of cosine to
 // x^10 end below 2e-9 there; the quarter swaps them and sets the signs.
-__device__ __forceinline__ void rope_angles(const unsigned long long* const (&turn)[2], int p,
-                                            V2* cs, V2* sn) {
+__device__ __forceinline__ void rope_angles(const unsigned long long* const (&turn)[2],
+                                            const int (&at)[4], V2* cs, V2* sn) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t quarter[2];     // the nearest quarter turn in the top two bits
@@ -218,6 +218,7 @@ __device__ __forceinline__ void rope_angles(const unsigned long long* const (&tu
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const unsigned long long f = turn[i][j];
+      const int p = at[2 * i + j];
       const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
       const uint32_t u = __umulhi((uint32_t)p, lo) + (uint32_t)p * hi - (p < 0 ? lo : 0u);
       quarter[j] = u + 0x20000000u;
@@ -251,6 +252,12 @@ __device__ __forceinline__ void rope_angles(const unsigned long long* const (&tu
   }
 }
 
+__device__ __forceinline__ void rope_angles(const unsigned long long* const (&turn)[2], int p,
+                                            V2* cs, V2* sn) {
+  const int at[4] = {p, p, p, p};
+  rope_angles(turn, at, cs, sn);
+}
+
 // What a lane knows of its place in a row.
 struct RopeLane {
   int a, b;              // its groups of four values
@@ -263,6 +270,60 @@ struct RopeLane {
     b = a + (turned ? rot : D - rot) / 2;
     turn[0] = table + (!turned ? rot / 2 : inter ? 2 * g : 4 * g);
     turn[1] = table + (!turned ? rot / 2 : inter ? rot / 4 + 2 * g : 4 * g + 2);
+  }
+};
+
+// Where a slot's tokens stand, one position for all frequencies (positions [B][N], or 0 .. N - 1).
+struct OnePosition {
+  const int32_t* positions;
+  long long pos_b;
+  template <typename Args>
+  __device__ __forceinline__ OnePosition(const Args& a, const RopeLane&, const unsigned long long*,
+                                         unsigned, unsigned)
+      : positions(a.positions), pos_b(a.pos_b) {}
+  __device__ __forceinline__ void angles(const RopeLane& lane, const TokenWalk& at, bool live, V2* cs,
+                                         V2* sn) {
+    rope_angles(lane.turn, positions && live ? positions[at.b * pos_b + at.n] : at.n, cs, sn);
+  }
+};
+
+// Where they stand on several axes (positions [axes][B][N]), each frequency turning with its axis.  The
+// next token's positions are loaded before this one's rows are worked on: a slot's tokens are far
+// apart, so that each load is a new line.
+struct AxisPositions {
+  const int32_t* from[4];          // of this lane's frequencies
+  int next[4];
+  TokenWalk at;
+  long long pos_b;
+  unsigned tokens, stride;
+  template <typename Args>
+  __device__ __forceinline__ AxisPositions(const Args& a, const RopeLane& lane,
+                                           const unsigned long long* table, unsigned first,
+                                           unsigned stride_)
+      : at(first, a.N), pos_b(a.pos_b), tokens((unsigned)a.B * a.N), stride(stride_) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int f = (int)(lane.turn[i / 2] - table) + i % 2;
+      int axis = f < a.rot / 2 ? a.freq_axis[f] : 0;
+      if (axis < 0 || axis >= a.axes) {
+        flag_error(a.status, kDevErrBadIndex);
+        axis = 0;
+      }
+      from[i] = a.positions + axis * a.pos_a;
+    }
+    load();
+  }
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) next[i] = at.t < tokens ? from[i][at.b * pos_b + at.n] : 0;
+  }
+  __device__ __forceinline__ void angles(const RopeLane& lane, const TokenWalk&, bool, V2* cs, V2* sn) {
+    int p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = next[i];
+    at.step(stride);
+    load();
+    rope_angles(lane.turn, p, cs, sn);
   }
 };
 

@@ -64,8 +64,10 @@ def load() -> ctypes.CDLL:
             }
             # arguments in a struct, packed by the caller
             U64 = ctypes.c_uint64
-            for name in ("mita_qk_norm_rope", "mita_qk_norm_rope_backward", "mita_cache_append",
-                         "mita_paged_attn"):
+            for name in ("mita_qk_norm_rope", "mita_qk_norm_rope_backward",
+                         "mita_qk_norm_rope_axes", "mita_qk_norm_rope_axes_backward",
+                         "mita_cache_append", "mita_paged_attn", "mita_cache_append_q4",
+                         "mita_paged_attn_q4"):
                 sigs[name] = [ctypes.c_char_p, P]
             for name, at in sigs.items():
                 for suffix in ("", "_f32"):
@@ -80,8 +82,11 @@ def load() -> ctypes.CDLL:
             lib.mita_forward_workspace_bytes.restype = ctypes.c_uint64
             lib.mita_qk_norm_rope_backward_workspace_bytes.argtypes = [I]
             lib.mita_qk_norm_rope_backward_workspace_bytes.restype = U64
-            lib.mita_paged_attn_workspace_bytes.argtypes = [I] * 7
-            lib.mita_paged_attn_workspace_bytes.restype = U64
+            for name in ("mita_paged_attn_workspace_bytes", "mita_paged_attn_q4_workspace_bytes"):
+                getattr(lib, name).argtypes = [I] * 7
+                getattr(lib, name).restype = U64
+            lib.mita_cache_plan.argtypes = [ctypes.c_char_p, P]
+            lib.mita_cache_plan.restype = I
             lib.mita_status_string.argtypes = [I]
             lib.mita_status_string.restype = ctypes.c_char_p
             lib.mita_last_error_message.argtypes = []
@@ -251,6 +256,10 @@ _NORM_ROPE = struct.Struct("8P13q7if")
 _NORM_ROPE_BACKWARD = struct.Struct("13PQ19q7if")
 _CACHE_APPEND = struct.Struct("12P8q10if4x")
 _PAGED_ATTN = struct.Struct("9PQ2q8i2f")
+_NORM_ROPE_AXES = struct.Struct("9P14q8if4x")
+_NORM_ROPE_AXES_BACKWARD = struct.Struct("14PQ20q8if4x")
+_CACHE_PLAN = struct.Struct("11P5i4x")
+_CACHE_APPEND_Q4 = struct.Struct("7P8q5i4x")
 _NO_STRIDES = (0, 0, 0)
 
 _typed = {}
@@ -353,6 +362,19 @@ def _positions_of(positions, B: int, N: int, device: int):
     return _dense(positions, "positions", (N,), torch.int32, device), 0
 
 
+def _axes_of(positions, freq_axis, rot: int, B: int, N: int, device: int):
+    """(addresses of positions [axes, N] or [axes, B, N] and of freq_axis, elements between batches
+    and between axes, axes)."""
+    A = positions.shape[0]
+    if positions.dim() == 3:
+        a, b = _rows(positions, "positions", (A, B, N), torch.int32, device)
+    else:
+        a, = _rows(positions, "positions", (A, N), torch.int32, device)
+        b = 0
+    faxis = 0 if rot == 0 else _dense(freq_axis, "freq_axis", (rot // 2,), torch.int32, device)
+    return positions.data_ptr(), faxis, b if B > 1 else 0, a if A > 1 else 0, A
+
+
 def _like_rows(x: torch.Tensor, shape):
     """An empty gradient for x [B, H, N, d] and its strides: dense like a dense x, else token-major
     (the heads of a token side by side, as in the projection's output that x is a view of)."""
@@ -372,17 +394,43 @@ def mita_qk_norm_rope(q, k=None, inv_freq=None, q_weight=None, k_weight=None, po
     most d).  q_weight, k_weight: float32 [d] (None: not normalised).  positions: int32 [N] or
     [B,N] (None: 0..N-1).  interleaved: pairs (2i, 2i+1) instead of (i, i + rot/2).
     q_out may be q and k_out may be k."""
+    return _norm_rope(q, k, inv_freq, None, q_weight, k_weight, positions, eps, interleaved, q_out,
+                      k_out, stream)
+
+
+def mita_qk_norm_rope_axes(q, k, inv_freq, freq_axis, positions, q_weight=None, k_weight=None,
+                           eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None,
+                           stream=None):
+    """mita_qk_norm_rope for tokens that stand somewhere on several axes (rows and columns of an image;
+    time, rows and columns of a video): frequency i turns its pair by the angle
+    positions[freq_axis[i]] * inv_freq[i].
+
+    positions: int32 [axes,N] or [axes,B,N].  freq_axis: int32 [rot/2], the axis of each frequency, in
+    any order (sections, or dealt in turn).  k may be None.  The rest as for mita_qk_norm_rope."""
+    if positions is None or (freq_axis is None and inv_freq is not None):
+        raise ValueError("positions and freq_axis are needed: the axes that the frequencies turn with")
+    return _norm_rope(q, k, inv_freq, (freq_axis,), q_weight, k_weight, positions, eps, interleaved,
+                      q_out, k_out, stream)
+
+
+def _norm_rope(q, k, inv_freq, axes, q_weight, k_weight, positions, eps, interleaved, q_out, k_out,
+               stream):
+    """Both forms; axes: None, or (freq_axis,) for positions of several axes."""
     dev = _device_of(q, "q")
     if stream is not None or dev != torch.cuda.current_device():
-        with _on(stream, dev, q, k, inv_freq, q_weight, k_weight, positions, q_out, k_out):
-            return mita_qk_norm_rope(q, k, inv_freq, q_weight, k_weight, positions, eps,
-                                     interleaved, q_out, k_out)
+        with _on(stream, dev, q, k, inv_freq, q_weight, k_weight, positions, q_out, k_out,
+                 *(axes or ())):
+            return _norm_rope(q, k, inv_freq, axes, q_weight, k_weight, positions, eps, interleaved,
+                              q_out, k_out, None)
     dt = q.dtype
-    fn = _typed_fn("mita_qk_norm_rope", dt)
+    fn = _typed_fn("mita_qk_norm_rope" if axes is None else "mita_qk_norm_rope_axes", dt)
     shape = B, Hq, N, d = q.shape
     qs = _rows(q, "q", shape, dt, dev)
     freq, rot = _rope_of(inv_freq, dev)
-    pos, pos_b = _positions_of(positions, B, N, dev)
+    if axes is None:
+        pos, pos_b = _positions_of(positions, B, N, dev)
+    else:
+        pos, faxis, pos_b, pos_a, A = _axes_of(positions, axes[0], rot, B, N, dev)
     qw, kw = _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev)
     if q_out is None:
         q_out = torch.empty(shape, dtype=dt, device=q.device)
@@ -403,9 +451,14 @@ def mita_qk_norm_rope(q, k=None, inv_freq=None, q_weight=None, k_weight=None, po
         else:
             kos = _out_rows(k_out, "k_out", kshape, dt, dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    rc = fn(_NORM_ROPE.pack(q.data_ptr(), kp, qw, kw, pos, freq, q_out.data_ptr(), kop, *qs, *ks,
-                            *qos, *kos, pos_b, B, Hq, Hkv, N, d, rot, interleaved, eps),
-            _raw_stream(dev))
+    if axes is None:
+        args = _NORM_ROPE.pack(q.data_ptr(), kp, qw, kw, pos, freq, q_out.data_ptr(), kop, *qs, *ks,
+                               *qos, *kos, pos_b, B, Hq, Hkv, N, d, rot, interleaved, eps)
+    else:
+        args = _NORM_ROPE_AXES.pack(q.data_ptr(), kp, qw, kw, pos, faxis, freq, q_out.data_ptr(), kop,
+                                    *qs, *ks, *qos, *kos, pos_b, pos_a, B, Hq, Hkv, N, d, rot,
+                                    interleaved, A, eps)
+    rc = fn(args, _raw_stream(dev))
     if rc:
         _check(rc)
     return q_out, k_out
@@ -418,19 +471,41 @@ def mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq=None, q_weight=Non
     outputs.  dq and dk have the inputs' type, and unless given are dense where q is and token-major
     ([B,N,H,d] in memory) where it is a view; the weights' gradients are float32 (None
     without the weight).  k and dk_out may both be None.  dq may be dq_out, dk may be dk_out."""
+    return _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, None, q_weight, k_weight, positions,
+                               eps, interleaved, dq, dk, stream)
+
+
+def mita_qk_norm_rope_axes_backward(q, k, dq_out, dk_out, inv_freq, freq_axis, positions,
+                                    q_weight=None, k_weight=None, eps: float = 1e-6,
+                                    interleaved: bool = False, dq=None, dk=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of mita_qk_norm_rope_axes, as mita_qk_norm_rope_backward gives
+    them for mita_qk_norm_rope."""
+    if positions is None or (freq_axis is None and inv_freq is not None):
+        raise ValueError("positions and freq_axis are needed: the axes that the frequencies turn with")
+    return _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, (freq_axis,), q_weight, k_weight,
+                               positions, eps, interleaved, dq, dk, stream)
+
+
+def _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, axes, q_weight, k_weight, positions, eps,
+                        interleaved, dq, dk, stream):
+    """Both forms; axes: None, or (freq_axis,) for positions of several axes."""
     dev = _device_of(q, "q")
     if stream is not None or dev != torch.cuda.current_device():
         with _on(stream, dev, q, k, dq_out, dk_out, inv_freq, q_weight, k_weight, positions, dq,
-                 dk):
-            return mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq, q_weight, k_weight,
-                                              positions, eps, interleaved, dq, dk)
+                 dk, *(axes or ())):
+            return _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, axes, q_weight, k_weight,
+                                       positions, eps, interleaved, dq, dk, None)
     dt = q.dtype
-    fn = _typed_fn("mita_qk_norm_rope_backward", dt)
+    fn = _typed_fn("mita_qk_norm_rope_backward" if axes is None
+                   else "mita_qk_norm_rope_axes_backward", dt)
     shape = B, Hq, N, d = q.shape
     qs = _rows(q, "q", shape, dt, dev)
     dqos = _rows(dq_out, "dq_out", shape, dt, dev)
     freq, rot = _rope_of(inv_freq, dev)
-    pos, pos_b = _positions_of(positions, B, N, dev)
+    if axes is None:
+        pos, pos_b = _positions_of(positions, B, N, dev)
+    else:
+        pos, faxis, pos_b, pos_a, A = _axes_of(positions, axes[0], rot, B, N, dev)
     if dq is None:
         dq, dqs = _like_rows(q, shape)
     else:
@@ -461,11 +536,17 @@ def mita_qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq=None, q_weight=Non
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         dwq = torch.empty(d, dtype=torch.float32, device=q.device) if qw else None
         dwk = torch.empty(d, dtype=torch.float32, device=q.device) if kw else None
-    rc = fn(_NORM_ROPE_BACKWARD.pack(
-        q.data_ptr(), kp, dq_out.data_ptr(), dkop, qw, kw, pos, freq, dq.data_ptr(), dkp,
-        dwq.data_ptr() if qw else 0, dwk.data_ptr() if kw else 0, ws.data_ptr() if nbytes else 0,
-        nbytes, *qs, *ks, *dqos, *dkos, *dqs, *dks, pos_b, B, Hq, Hkv, N, d, rot, interleaved,
-        eps), _raw_stream(dev))
+    grads = (dq.data_ptr(), dkp, dwq.data_ptr() if qw else 0, dwk.data_ptr() if kw else 0,
+             ws.data_ptr() if nbytes else 0, nbytes)
+    strides = (*qs, *ks, *dqos, *dkos, *dqs, *dks, pos_b)
+    if axes is None:
+        args = _NORM_ROPE_BACKWARD.pack(q.data_ptr(), kp, dq_out.data_ptr(), dkop, qw, kw, pos, freq,
+                                        *grads, *strides, B, Hq, Hkv, N, d, rot, interleaved, eps)
+    else:
+        args = _NORM_ROPE_AXES_BACKWARD.pack(q.data_ptr(), kp, dq_out.data_ptr(), dkop, qw, kw, pos,
+                                             faxis, freq, *grads, *strides, pos_a, B, Hq, Hkv, N, d,
+                                             rot, interleaved, A, eps)
+    rc = fn(args, _raw_stream(dev))
     if rc:
         _check(rc)
     return dq, dk, dwq, dwk
@@ -498,6 +579,28 @@ class QKNormRopeFunction(torch.autograd.Function):
             q, k, _aligned_rows(dq_out), None if k is None else _aligned_rows(dk_out), inv_freq,
             q_weight, k_weight, positions, eps, interleaved)
         return dq, dk, None, dwq, dwk, None, None, None
+
+
+class QKNormRopeAxesFunction(torch.autograd.Function):
+    """mita_qk_norm_rope_axes as an autograd function: gradients of q, k and the norm weights.  For
+    capture into a CUDA graph as QKNormRopeFunction."""
+
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, freq_axis, positions, q_weight=None, k_weight=None, eps=1e-6,
+                interleaved=False):
+        ctx.save_for_backward(q, k, inv_freq, freq_axis, positions, q_weight, k_weight)
+        ctx.cfg = (eps, interleaved)
+        return mita_qk_norm_rope_axes(q, k, inv_freq, freq_axis, positions, q_weight, k_weight, eps,
+                                      interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, inv_freq, freq_axis, positions, q_weight, k_weight = ctx.saved_tensors
+        dq, dk, dwq, dwk = mita_qk_norm_rope_axes_backward(
+            q, k, _aligned_rows(dq_out), None if k is None else _aligned_rows(dk_out), inv_freq,
+            freq_axis, positions, q_weight, k_weight, *ctx.cfg)
+        return dq, dk, None, None, None, dwq, dwk, None, None
 
 
 def _aligned_rows(t: torch.Tensor) -> torch.Tensor:
@@ -570,6 +673,110 @@ def mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start=Non
     return q_out
 
 
+def mita_cache_plan(new_tokens, lengths, page_table, free_pages, free_count, tokens: int,
+                    page_size: int, new_lengths=None, new_free_count=None, seq_start=None,
+                    positions=None, slots=None, granted=None, stream=None):
+    """A serving step's pages, dealt out on the device; returns (seq_start, positions, slots, granted).
+
+    new_tokens: int32 [S], each sequence's new tokens, -1 for one that is done (its pages go back to
+    the pool).  lengths: int32 [S], tokens before the step; page_table: int32 [S,width]; free_pages:
+    int32 [num_pages], a stack whose first free_count (int32 [1]) entries are the free pages.  These
+    are brought up to date in place (lengths and free_count in new_lengths and new_free_count where
+    given).  tokens: rows of the step's packed (and padded) tokens.
+
+    seq_start: int32 [S+1], the rows of each sequence.  positions: int32 [tokens], in the
+    sequence.  slots: int64 [tokens], page*page_size + row in the page, -1 for rows that belong to nobody
+    or to a sequence that was not granted.  granted: int32 [S], new_tokens, or 0 where its tokens fit
+    neither the pool (first come, first served), the table nor the rows: such a sequence stays
+    as it is."""
+    dev = _device_of(new_tokens, "new_tokens")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(stream, dev, new_tokens, lengths, page_table, free_pages, free_count, new_lengths,
+                 new_free_count, seq_start, positions, slots, granted):
+            return mita_cache_plan(new_tokens, lengths, page_table, free_pages, free_count, tokens,
+                                   page_size, new_lengths, new_free_count, seq_start, positions,
+                                   slots, granted)
+    if page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("page_table must be [S, width] and free_pages [num_pages]")
+    i32 = torch.int32
+    (S, width), pages = page_table.shape, free_pages.shape[0]
+    if new_lengths is None:
+        new_lengths = lengths
+    if new_free_count is None:
+        new_free_count = free_count
+    made = torch.empty(2 * S + 1 + tokens, dtype=i32, device=new_tokens.device)
+    if seq_start is None:
+        seq_start = made[:S + 1]
+    if granted is None:
+        granted = made[S + 1:2 * S + 1]
+    if positions is None:
+        positions = made[2 * S + 1:]
+    if slots is None:
+        slots = torch.empty(tokens, dtype=torch.int64, device=new_tokens.device)
+    rc = load().mita_cache_plan(_CACHE_PLAN.pack(
+        _dense(new_tokens, "new_tokens", (S,), i32, dev), _dense(lengths, "lengths", (S,), i32, dev),
+        _dense(new_lengths, "new_lengths", (S,), i32, dev),
+        _dense(page_table, "page_table", (S, width), i32, dev),
+        _dense(free_pages, "free_pages", (pages,), i32, dev),
+        _dense(free_count, "free_count", (1,), i32, dev),
+        _dense(new_free_count, "new_free_count", (1,), i32, dev),
+        _dense(seq_start, "seq_start", (S + 1,), i32, dev),
+        _dense(positions, "positions", (tokens,), i32, dev),
+        _dense(slots, "slots", (tokens,), torch.int64, dev),
+        _dense(granted, "granted", (S,), i32, dev), S, tokens, pages, page_size, width),
+        _raw_stream(dev))
+    if rc:
+        _check(rc)
+    return seq_start, positions, slots, granted
+
+
+def cache_q4_shape(num_pages: int, Hkv: int, page_size: int, d: int):
+    """The shape of a 4-bit cache's k_cache and v_cache (uint8; zero or empty to begin with)."""
+    return num_pages, Hkv, page_size * (17 * d // 32)
+
+
+def _cache_q4_of(k_cache, v_cache, d: int, device: int):
+    """(addresses), (num_pages, Hkv, page_size) of a 4-bit cache for heads of d."""
+    shape = k_cache.shape
+    if len(shape) != 3 or d < 32 or shape[2] % (17 * d // 32) != 0:
+        raise ValueError(f"k_cache must be uint8 [num_pages, Hkv, page_size * {17 * d // 32}] for heads "
+                         f"of {d}, got {tuple(shape)}")
+    return ((_dense(k_cache, "k_cache", shape, torch.uint8, device),
+             _dense(v_cache, "v_cache", shape, torch.uint8, device)),
+            (shape[0], shape[1], shape[2] // (17 * d // 32)))
+
+
+def mita_cache_append_q4(k, v, k_cache, v_cache, slots, k_out=None, v_out=None, stream=None):
+    """New tokens' keys (normalised and rotated already: mita_qk_norm_rope) and values, k, v [T,Hkv,d],
+    into a paged cache of 4-bit codes with a scale for every 32 values (cache_q4_shape).
+
+    slots: int64 [T], each token's page*page_size + row, as mita_cache_plan gives them; -1: passed over.
+    k_out, v_out [T,Hkv,d]: where given, the values that the cache now holds for each token (a row
+    passed over stays as it is).  All four may be strided views."""
+    dev = _device_of(k, "k")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(stream, dev, k, v, k_cache, v_cache, slots, k_out, v_out):
+            return mita_cache_append_q4(k, v, k_cache, v_cache, slots, k_out, v_out)
+    dt = k.dtype
+    fn = _typed_fn("mita_cache_append_q4", dt)
+    shape = T, Hkv, d = k.shape
+    (kc, vc), (pages, heads, page) = _cache_q4_of(k_cache, v_cache, d, dev)
+    if heads != Hkv:
+        raise ValueError(f"k has {Hkv} heads, k_cache {heads}")
+    ks, vs = _rows(k, "k", shape, dt, dev), _rows(v, "v", shape, dt, dev)
+    kos = vos = (0, 0)
+    if k_out is not None:
+        kos = _out_rows(k_out, "k_out", shape, dt, dev)
+    if v_out is not None:
+        vos = _out_rows(v_out, "v_out", shape, dt, dev)
+    rc = fn(_CACHE_APPEND_Q4.pack(
+        k.data_ptr(), v.data_ptr(), _dense(slots, "slots", (T,), torch.int64, dev), kc, vc,
+        0 if k_out is None else k_out.data_ptr(), 0 if v_out is None else v_out.data_ptr(), *ks, *vs,
+        *kos, *vos, T, Hkv, d, pages, page), _raw_stream(dev))
+    if rc:
+        _check(rc)
+
+
 def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[float] = None,
                     softcap: float = 0.0, window: int = 0, alibi_slopes=None,
                     return_lse: bool = False, out=None, stream=None):
@@ -580,16 +787,38 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     scale: of the scores (None: d^-1/2).  softcap > 0: scores capped to softcap*tanh(z/softcap).
     alibi_slopes: float32 [Hq], adds slope*(key position - own position).  window > 0: only the
     last `window` keys.  Idle slots (length 0) get zeros and lse -inf."""
+    return _paged_attn(False, q, k_cache, v_cache, page_table, lengths, scale, softcap, window,
+                       alibi_slopes, return_lse, out, stream)
+
+
+def mita_paged_attn_q4(q, k_cache, v_cache, page_table, lengths, scale: Optional[float] = None,
+                       softcap: float = 0.0, window: int = 0, alibi_slopes=None,
+                       return_lse: bool = False, out=None, stream=None):
+    """mita_paged_attn over a paged cache of 4-bit codes (mita_cache_append_q4's; uint8
+    [num_pages,Hkv,page_size*17*d/32]); q and out are bf16 or fp32."""
+    return _paged_attn(True, q, k_cache, v_cache, page_table, lengths, scale, softcap, window,
+                       alibi_slopes, return_lse, out, stream)
+
+
+def _paged_attn(q4, q, k_cache, v_cache, page_table, lengths, scale, softcap, window, alibi_slopes,
+                return_lse, out, stream):
     dev = _device_of(q, "q")
     if stream is not None or dev != torch.cuda.current_device():
         with _on(stream, dev, q, k_cache, v_cache, page_table, lengths, alibi_slopes, out):
-            return mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale, softcap,
-                                   window, alibi_slopes, return_lse, out)
+            return _paged_attn(q4, q, k_cache, v_cache, page_table, lengths, scale, softcap, window,
+                               alibi_slopes, return_lse, out, None)
     dt = q.dtype
-    fn = _typed_fn("mita_paged_attn", dt)
-    (kc, vc, table, n), (S, pages, Hkv, page, d, width) = _cache_of(k_cache, v_cache, page_table,
-                                                                    lengths, dt, dev)
-    Hq = q.shape[1]
+    fn = _typed_fn("mita_paged_attn_q4" if q4 else "mita_paged_attn", dt)
+    if q4:
+        Hq, d = q.shape[1:]
+        (kc, vc), (pages, Hkv, page) = _cache_q4_of(k_cache, v_cache, d, dev)
+        S, width = tshape = page_table.shape
+        table = _dense(page_table, "page_table", tshape, torch.int32, dev)
+        n = _dense(lengths, "lengths", (S,), torch.int32, dev)
+    else:
+        (kc, vc, table, n), (S, pages, Hkv, page, d, width) = _cache_of(k_cache, v_cache, page_table,
+                                                                        lengths, dt, dev)
+        Hq = q.shape[1]
     shape = (S, Hq, d)
     qs = _rows(q, "q", shape, dt, dev)
     window = min(window, 0x7fffffff)
@@ -603,7 +832,7 @@ def mita_paged_attn(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     else:
         op = _dense(out, "out", shape, dt, dev)
     lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    nbytes = _paged_attn_bytes(S, Hq, Hkv, d, page, width, dt is torch.float32, dev)
+    nbytes = _paged_attn_bytes(S, Hq, Hkv, d, page, width, dt is torch.float32, dev, q4)
     stream = _raw_stream(dev)
     ws = _paged_workspace(nbytes, dev, stream)
     rc = fn(_PAGED_ATTN.pack(q.data_ptr(), kc, vc, table, n, slopes, ws.data_ptr(), op,
@@ -634,8 +863,10 @@ def _paged_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
 
 
 @functools.lru_cache(maxsize=1024)
-def _paged_attn_bytes(S, Hq, Hkv, d, page, width, f32, device: int) -> int:
-    return load().mita_paged_attn_workspace_bytes(S, Hq, Hkv, d, page, width, f32)
+def _paged_attn_bytes(S, Hq, Hkv, d, page, width, f32, device: int, q4: bool = False) -> int:
+    lib = load()
+    f = lib.mita_paged_attn_q4_workspace_bytes if q4 else lib.mita_paged_attn_workspace_bytes
+    return f(S, Hq, Hkv, d, page, width, f32)
 
 
 # the handle of torch.cuda.current_stream(device), without making a Stream object of it (1.1 us);
