@@ -43,9 +43,10 @@ template <typename T, int D, int RT>
 struct Shape {
   static constexpr bool kTensor = std::is_same<T, bf16>::value;
   static constexpr int kWarps = RT == 8 && D <= (kTensor ? 32 : 16) ? 16 : 8;
-  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kThreads = kWarps * 32, kTeams = 1, kTeamThreads = kThreads;
   static constexpr int kRowBytes = D * (int)sizeof(T);
   static constexpr int kKeys = (kTensor || D <= 32 ? 32 : 16) / (D == 128 ? 2 : 1);  // of a warp
+  using Mask = unsigned;
   static constexpr int kTile = kWarps * kKeys;
   static constexpr int kSegmentCost = kTensor ? 2 : 1;         // tiles that ending a segment is worth
   static constexpr int kChunks = kRowBytes / 16;               // 16-byte chunks of a row
@@ -53,10 +54,11 @@ struct Shape {
   static constexpr int kStages =
       196608 / (kStageBytes * kWarps) > 8 ? 8 : 196608 / (kStageBytes * kWarps);
   static constexpr int kRing = kStages * kStageBytes;          // of one warp
-  static constexpr int kOffSums = -1, kSums = kRing;  // warps' sums at an end: in the stage just read
+  __device__ __forceinline__ static int warp() { return threadIdx.x >> 5; }
   static constexpr int kUnrollStart = kTensor ? 1 : kStages;
   // byte offsets
-  static constexpr int kOffMl = kWarps * kRing;                           // [warps][RT][2]
+  static constexpr int kJoinBytes = kWarps * kRing;
+  static constexpr int kOffMl = kJoinBytes;                               // [warps][RT][2]
   static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
   static constexpr int kOffJoins = kOffMask + (kWarps * kStages * 4 + 15) / 16 * 16;   // [2]
   static constexpr int kOffBase = kOffJoins + 2 * (int)sizeof(Join);     // of this call's counts
@@ -586,7 +588,9 @@ struct Dense {
   using S = Shape<T, D, RT>;
   using State = typename StateOf<T, D, RT>::type;
   using Ld = Loader<T, D, RT>;
+  using Team = WholeCta;
   static constexpr int kD = D, kRT = RT;
+  static auto kernel() { return paged_attn_kernel<Dense>; }
 };
 
 // The instantiation for a head dim, type and group: a CTA takes 8 query rows, in bf16 16 where the

@@ -30,37 +30,80 @@
 
 #include <cuda_fp16.h>
 
+#ifndef Q4_TEAM
+#define Q4_TEAM 6
+#endif
+#ifndef Q4_TSMALL
+#define Q4_TSMALL 8
+#endif
+#ifndef Q4_TEAMS
+#define Q4_TEAMS 2
+#endif
+#ifndef Q4_KEYS
+#define Q4_KEYS 64
+#endif
+#ifndef Q4_COST
+#define Q4_COST 1
+#endif
+
 namespace mita {
 namespace {
 
-constexpr float kBoost = 15.f;       // log2 of the largest weight
+// The running maximum is looked for again only where a lane's weights add up to more than 2^15; the largest
+// weight is then 2^11, so that a tile's eight of a lane stay below that.
+constexpr float kBoost = 11.f, kMostSum = 32768.f;
 
 template <typename T, int D, int RT>
 struct Q4Shape {
-  static constexpr int kWarps = 8;
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kKeys = 32;                        // of a warp: as many as a mask has bits
-  static constexpr int kTile = kWarps * kKeys;
-  static constexpr int kSegmentCost = 2;                  // tiles that ending a segment is worth
-  static constexpr int kUnrollStart = 1;
+  static constexpr bool kSplit = std::is_same<T, float>::value;
+  static constexpr int kTeams = Q4_TEAMS;
+  static constexpr int kTeamWarps = RT > 8 || kSplit ? 4 : D == 128 ? Q4_TEAM : Q4_TSMALL;
+  static constexpr int kWarps = kTeams * kTeamWarps;
+  static constexpr int kThreads = kWarps * 32, kTeamThreads = kTeamWarps * 32;
+  static constexpr int kKeys = Q4_KEYS;                   // of a warp, 32 at a time
+  using Mask = std::conditional_t<kKeys == 64, unsigned long long, unsigned>;
+  static constexpr int kTile = kTeamWarps * kKeys;
+  static constexpr int kSegmentCost = Q4_COST;            // tiles that ending a segment is worth
   static constexpr int kChunks = D / kQ4Block;            // of a row: 16 bytes and one scale each
   static constexpr int kRowBytes = D / 2;
   static constexpr int kCodes = kKeys * kRowBytes, kScales = kKeys * kChunks;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);      // K's codes, V's, K's scales, V's
-  // a warp's sums at an end have a place of their own where a stage does not hold them
-  static constexpr bool kOwnSums = RT * D * 4 > kStageBytes;
-  static constexpr int kSumBytes = kOwnSums ? kWarps * RT * D * 4 : 0;
-  static constexpr int kFit = (196608 - kSumBytes) / (kStageBytes * kWarps);
+  // a warp's decoded scales: K's in fp32, V's in fp16 (of two keys side by side) or fp32
+  static constexpr int kDecodedK = 32 * kChunks * 4, kDecodedV = kSplit ? kDecodedK : kDecodedK / 2;
+  static constexpr int kDecoded = kDecodedK + kDecodedV;
+  // a team's queries as right operands, [part][heads / 8][chunk][lane] of 16 bytes, what a product
+  // starts from, [heads / 8][chunk][lane % 4] of 16 bytes, and [heads] units and slopes; twice
+  static constexpr int kN = RT / 8, kParts = kSplit ? 2 : 1;
+  static constexpr int kOffStart = kParts * kN * kChunks * 512;
+  static constexpr int kOffUnit = kOffStart + (kSplit ? 0 : kN * kChunks * 64);
+  static constexpr int kQueries = kOffUnit + RT * 8;
+  static constexpr int kRest = kWarps * (kDecoded + RT * 8 + 8 * (int)sizeof(Mask)) +
+                               kTeams * (2 * kQueries + 2 * (int)sizeof(Join) + 16);
+  static constexpr int kFit = (232448 - 256 - kRest) / (kStageBytes * kWarps);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kOffSums = kOwnSums ? kWarps * kRing : -1;
-  static constexpr int kSums = kOwnSums ? RT * D * 4 : kRing;
-  static constexpr int kOffMl = kWarps * kRing + kSumBytes;               // [warps][RT][2]
+  static constexpr int kJoinBytes = kTeamWarps * kRing;                   // a team's
+  static constexpr int kOffDecoded = kWarps * kRing;                      // [warps]
+  static constexpr int kOffQueries = kOffDecoded + kWarps * kDecoded;     // [teams][2]
+  static constexpr int kOffMl = kOffQueries + kTeams * 2 * kQueries;      // [teams][team's warps][RT][2]
   static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
-  static constexpr int kOffJoins = kOffMask + (kWarps * kStages * 4 + 15) / 16 * 16;   // [2]
-  static constexpr int kOffBase = kOffJoins + 2 * (int)sizeof(Join);
-  static constexpr int kBytes = kOffBase + 16;
-  static_assert(kBytes <= 232448 && kStages >= 3 && kStageBytes % 16 == 0, "shared memory");
+  static constexpr int kOffJoins = kOffMask + (kWarps * kStages * (int)sizeof(Mask) + 15) / 16 * 16;
+  static constexpr int kOffBase = kOffJoins + kTeams * 2 * (int)sizeof(Join);
+  static constexpr int kBytes = kOffBase + kTeams * 16;
+  static_assert(kBytes <= 232448 && kStages >= 2 && kStageBytes % 16 == 0, "shared memory");
+  static_assert(RT * D * 4 <= kStageBytes, "a warp's sums in one of its stages");
+  static_assert(kTeams <= 2, "two shares to a counter");
+  __device__ __forceinline__ static int warp() { return (threadIdx.x >> 5) % kTeamWarps; }
+};
+
+// The warps that work on one share.
+template <typename S>
+struct Q4Team {
+  __device__ __forceinline__ static int team() { return (threadIdx.x >> 5) / S::kTeamWarps; }
+  __device__ __forceinline__ static int thread() { return threadIdx.x - team() * S::kTeamThreads; }
+  __device__ __forceinline__ static void sync() {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team()), "n"(S::kTeamThreads) : "memory");
+  }
 };
 
 // Chunk c of row r of a page stands at c ^ q4_turn(r).
@@ -69,14 +112,24 @@ __device__ __forceinline__ int q4_turn(int r) {
   return D == 128 ? (r >> 1) & 3 : D == 64 ? (r >> 2) & 1 : 0;
 }
 
-// c[16 x 8] += a[16 x 16] b[16 x 8], fp16 products summed in fp32
+// d[16 x 8] = c + a[16 x 16] b[16 x 8], fp16 products summed in fp32
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        const uint32_t* b, float c0, float c1, float c2, float c3) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         const uint32_t* b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+  mma_f16(c, a0, a1, a2, a3, b, c[0], c[1], c[2], c[3]);
+}
+// An 8 x 8 matrix of 16-bit values, transposed (paged_row.cuh's, free to be moved among the products).
+__device__ __forceinline__ uint32_t turn8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -97,16 +150,16 @@ __device__ __forceinline__ uint32_t mul_half(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 // Codes 0 and 1 of the two 16-bit words of x (of x >> 8: 2 and 3), as fp16 numbers n * 2^-24 and
-// 16 n * 2^-24, or, kSigned, n - 8: with 1024's bits above it a code is 1024 + n or 1024 + 16 n.
+// 16 n * 2^-24, or, kSigned, both as (n - 8) * 2^-9.
 template <bool kSigned>
 __device__ __forceinline__ uint32_t code_lo(uint32_t x) {
-  if constexpr (!kSigned) return x & 0x000f000fu;
-  return fma_half((x & 0x000f000fu) | 0x64006400u, 0x3c003c00u, 0xe408e408u);     // - 1032
+  x &= 0x000f000fu;
+  return kSigned ? fma_half(x, 0x78007800u, 0xa400a400u) : x;       // * 2^15 - 2^-6
 }
 template <bool kSigned>
 __device__ __forceinline__ uint32_t code_hi(uint32_t x) {
-  if constexpr (!kSigned) return x & 0x00f000f0u;
-  return fma_half((x & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);     // / 16 - 72
+  x &= 0x00f000f0u;
+  return kSigned ? fma_half(x, 0x68006800u, 0xa400a400u) : x;       // * 2^11 - 2^-6
 }
 
 // The scale bytes of a row.
@@ -121,13 +174,42 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t base, int key) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w) : "r"(base + key) : "memory");
   return w;
 }
-// Scale c of two rows, as two fp16 values.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t w0, uint32_t w1, int c) {
-  return (__byte_perm(w0, w1, c | c << 4 | (4 + c) << 8 | (4 + c) << 12) & 0x00ff00ffu) << 7;
+// The four (two, one) scales of a word as fp16 values: chunks 0 and 2, chunks 1 and 3.
+__device__ __forceinline__ uint32_t scales_02(uint32_t w) { return (w & 0x00ff00ffu) << 7; }
+__device__ __forceinline__ uint32_t scales_13(uint32_t w) { return w >> 1 & 0x7f807f80u; }
+
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
-__device__ __forceinline__ float scale_of(uint32_t w, int c) {
-  const unsigned short h = (unsigned short)(((w >> (8 * c)) & 0xffu) << 7);
-  return __half2float(__ushort_as_half(h));
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, uint32_t x) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ void store_shared(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void store_shared(uint32_t at, const uint32_t (&x)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3])
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&x)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at) : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[0]) : "r"(at) : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -140,70 +222,79 @@ struct Q4State {
   using S = Q4Shape<T, D, RT>;
   static constexpr bool kSplit = std::is_same<T, float>::value;
   static constexpr int kParts = kSplit ? 2 : 1;      // fp16 values that a factor is given as
-  static constexpr int kN = RT / 8, kC = S::kChunks, kU = S::kKeys / 16;
-  uint32_t q[kParts][2 * kC][kN][2];
-  float off[kC][kN][2];              // -8 times the chunk's sum of the queries
-  float o[kC][2][kN][4];
+  static constexpr int kN = RT / 8, kC = S::kChunks, kU = 2;
+  unsigned long long o[kC][2][kN][2];   // two heads of a value column each
   float m[kN][2], l[kN][2];          // m: the running maximum less kBoost; l: of this lane's keys
-  float unit[kN][2];                 // a dot product's unit
-  float slope2[kN][2];
 
-  __device__ __forceinline__ void start(const PagedAttnQ4Args<T>& a, int s, int head, int rows) {
-    const int lane = threadIdx.x & 31, c2 = lane % 4 * 2;
+  // Puts chunk c of a segment's queries to `to`, as every warp of the team will read them.
+  __device__ __forceinline__ static void put_queries(const PagedAttnQ4Args<T>& a, int s, int head,
+                                                     int rows, int c, uint32_t to) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       const int r = 8 * n + lane / 4;
       const T* p = a.q + s * a.q_s + (long long)(head + r) * a.q_h + lane % 4 * 8;
-      float x[kC][8];
-      float top = 0.f;
+      float x[8], y[8], top = 0.f;
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      if (r < rows) {
 #pragma unroll
-        for (int i = 0; i < 8; i += Vec<T>::N) {
-          if (r < rows) Vec<T>::load(p + c * 32 + i, x[c] + i);
-        }
+        for (int cc = 0; cc < kC; ++cc) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (r >= rows) x[c][i] = 0.f;
-          top = fmaxf(top, fabsf(x[c][i]));
+          for (int i = 0; i < 8; i += Vec<T>::N) Vec<T>::load(p + cc * 32 + i, y + i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            top = fmaxf(top, fabsf(y[i]));
+            if (cc == c) x[i] = y[i];
+          }
         }
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // the power of two at or below the largest, as far as the factors below are numbers
       const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 237);
-      const float to = __uint_as_float((unsigned)(254 + 14 - e) << 23);         // 2^14 / 2^(e - 127)
-      // of a score tile: 1 / to, and 2^24 where codes are subnormals
-      const float one = __uint_as_float((unsigned)(kSplit ? e - 14 : e + 10) << 23);
+      const float up = __uint_as_float((unsigned)(254 + 14 - e) << 23);         // 2^14 / 2^(e - 127)
+      uint32_t q[kParts][4];
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        float sum = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const float f = !kSplit && (i & 1) ? up * 0.0625f : up;
+        float lo = x[i] * f, hi = x[i + 4] * f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = !kSplit && (i & 1) ? 0.0625f : 1.f;
-          float lo = x[c][i] * to * f, hi = x[c][i + 4] * to * f;
-#pragma unroll
-          for (int part = 0; part < kParts; ++part) {
-            const uint32_t h = pack_half(lo, hi);
-            const float2 back = unpack_half(h);
-            q[part][2 * c + i / 2][n][i & 1] = h;
-            sum += (back.x + back.y) * (1.f / f);
-            lo -= back.x;
-            hi -= back.y;
-          }
+        for (int part = 0; part < kParts; ++part) {
+          q[part][i] = pack_half(lo, hi);
+          const float2 back = unpack_half(q[part][i]);
+          lo -= back.x;
+          hi -= back.y;
         }
-        if constexpr (kSplit) continue;
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          off[c][n][i] = __shfl_sync(0xffffffffu, sum, (c2 + i) * 4) * -4.76837158203125e-7f;  // 8 / 2^24
       }
 #pragma unroll
+      for (int part = 0; part < kParts; ++part)
+        store_shared(to + (((part * kN + n) * kC + c) * 32 + lane) * 16, q[part]);
+      if constexpr (!kSplit) {       // -8 times the sum, as products with -8 (and -128) * 2^-24
+        float off[4];
+        mma_f16(off, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, q[0], 0.f, 0.f, 0.f, 0.f);
+        mma_f16(off, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, q[0] + 2);
+        if (lane < 4) {
+          const uint32_t x4[4] = {__float_as_uint(off[0]), __float_as_uint(off[1]),
+                                  __float_as_uint(off[2]), __float_as_uint(off[3])};
+          store_shared(to + S::kOffStart + ((n * kC + c) * 4 + lane) * 16, x4);
+        }
+      }
+      if (c == 0 && lane % 4 == 0) {
+        // a dot product's unit: 1 / up, and what the codes' numbers are smaller than they: 2^24 or 2^9
+        const float one = __uint_as_float((unsigned)(kSplit ? e - 14 + 9 : e - 14 + 24) << 23);
+        const float slope = a.slopes && r < rows ? a.slopes[head + r] * kLog2e : 0.f;
+        store_shared(to + S::kOffUnit + r * 4, __float_as_uint(one));
+        store_shared(to + S::kOffUnit + RT * 4 + r * 4, __float_as_uint(slope));
+      }
+    }
+  }
+
+  __device__ __forceinline__ void start() {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+#pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int c = 8 * n + c2 + i;
-        unit[n][i] = __shfl_sync(0xffffffffu, one, (c2 + i) * 4);
-        slope2[n][i] = a.slopes && c < rows ? a.slopes[head + c] * kLog2e : 0.f;
         m[n][i] = kLowest;
         l[n][i] = 0.f;
       }
@@ -212,8 +303,15 @@ struct Q4State {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[c][t][n][i] = 0.f;
+          for (int i = 0; i < 2; ++i) o[c][t][n][i] = 0;
     }
+  }
+  // a pair of [heads] floats at `at`: those of this lane's columns of tile n
+  __device__ __forceinline__ static void pair_of(uint32_t at, int n, float (&x)[2]) {
+    uint32_t w[2];
+    load_shared(at + (8 * n + (threadIdx.x & 3) * 2) * 4, w);
+    x[0] = __uint_as_float(w[0]);
+    x[1] = __uint_as_float(w[1]);
   }
 
   // Words of two chunks of 16 keys, or (heads of 32) of one chunk of 32 keys: x[0], x[1] the first's
@@ -227,55 +325,141 @@ struct Q4State {
     if constexpr (kTrans) ldsm4_t(at, x); else ldsm4(at, x);
   }
 
-  __device__ __forceinline__ void chunk_scores(const uint32_t* x, int c, float s0, float s1,
-                                               float (&z)[kN][4]) const {
-    const uint32_t y0 = x[0] >> 8, y1 = x[1] >> 8;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      float acc[4] = {};
-      if constexpr (!kSplit)
-        for (int i = 0; i < 4; ++i) acc[i] = off[c][n][i & 1];
-#pragma unroll
-      for (int part = kParts - 1; part >= 0; --part) {
-        mma_f16(acc, code_lo<kSplit>(x[0]), code_lo<kSplit>(x[1]), code_hi<kSplit>(x[0]),
-                code_hi<kSplit>(x[1]), q[part][2 * c][n]);
-        mma_f16(acc, code_lo<kSplit>(y0), code_lo<kSplit>(y1), code_hi<kSplit>(y0),
-                code_hi<kSplit>(y1), q[part][2 * c + 1][n]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[n][i] = fmaf(acc[i], i < 2 ? s0 : s1, z[n][i]);
-    }
-  }
-
-  __device__ __forceinline__ void tile(const ScoreRule& rule, uint32_t stage, int key0,
-                                       unsigned mask) {
+  // Every lane decodes the scales of one key (the lanes that use a key's are many: 4 its K's, 8 its V's).
+  // A value's scale of a key that is not seen is zero, whatever the row holds.  Returns whether a
+  // value's scale is 2 or more.
+  __device__ __forceinline__ static bool decode_scales(uint32_t ks, uint32_t to, unsigned mask) {
     const int lane = threadIdx.x & 31;
-    const uint32_t vt = stage + S::kCodes, ks = vt + S::kCodes, vs = ks + S::kScales;
-    float z[kU][kN][4] = {};
-#pragma unroll
-    for (int u = 0; u < kU; u += kC == 1 ? 2 : 1) {
-#pragma unroll
-      for (int c = 0; c < kC; c += 2) {
-        uint32_t x[4];
-        words<false>(stage, u, c, x);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int uu = kC == 1 ? u + k : u, cc = kC == 1 ? 0 : c + k;
-          const uint32_t w0 = scale_word<kC>(ks, 16 * uu + lane / 4);
-          const uint32_t w1 = scale_word<kC>(ks, 16 * uu + 8 + lane / 4);
-          chunk_scores(x + 2 * k, cc, scale_of(w0, cc), scale_of(w1, cc), z[uu]);
+    const uint32_t wk = scale_word<kC>(ks, lane);
+    uint32_t wv = scale_word<kC>(ks + S::kScales, lane);
+    if (!((mask >> lane) & 1)) wv = 0;
+    auto put = [&](uint32_t at, uint32_t w) {          // as fp32, [key][chunk]
+      const float2 even = unpack_half(scales_02(w)), odd = unpack_half(scales_13(w));
+      if constexpr (kC == 4) {
+        store_shared(at + lane * 16, __float_as_uint(even.x), __float_as_uint(odd.x));
+        store_shared(at + lane * 16 + 8, __float_as_uint(even.y), __float_as_uint(odd.y));
+      } else if constexpr (kC == 2) {
+        store_shared(at + lane * 8, __float_as_uint(even.x), __float_as_uint(odd.x));
+      } else {
+        store_shared(at + lane * 4, __float_as_uint(even.x));
+      }
+    };
+    put(to, wk);
+    to += S::kDecodedK;
+    if constexpr (kSplit) {
+      put(to, wv);
+    } else {                         // as fp16 of two keys, [pair][chunk]: each of the two writes half
+      const uint32_t even = scales_02(wv), odd = scales_13(wv);
+      const uint32_t even2 = __shfl_xor_sync(0xffffffffu, even, 1);
+      const bool second = lane & 1;
+      if constexpr (kC == 1) {
+        if (!second) store_shared(to + lane / 2 * 4, __byte_perm(even, even2, 0x5410));
+      } else {
+        const uint32_t odd2 = __shfl_xor_sync(0xffffffffu, odd, 1);
+        if constexpr (kC == 2) {
+          store_shared(to + lane * 4, second ? __byte_perm(odd2, odd, 0x5410)
+                                             : __byte_perm(even, even2, 0x5410));
+        } else {
+          const uint32_t sel = second ? 0x3276u : 0x5410u;      // upper halves, or lower ones
+          store_shared(to + lane * 8, __byte_perm(even, even2, sel), __byte_perm(odd, odd2, sel));
         }
       }
     }
+    __syncwarp();
+    return __any_sync(0xffffffffu, wv & 0x80808080u);
+  }
+
+  // z += scale * (codes . q) of 16 keys, x their words of a chunk, q the chunk's queries, `from` what
+  // the product starts from
+  __device__ __forceinline__ static void chunk_scores(const uint32_t* x, const uint32_t (&q)[kParts][kN][4],
+                                                      const uint32_t (&from)[kN][4], uint32_t s0,
+                                                      uint32_t s1, float (&z)[kN][4]) {
+    const uint32_t y0 = x[0] >> 8, y1 = x[1] >> 8;
+    const uint32_t a[8] = {code_lo<kSplit>(x[0]), code_lo<kSplit>(x[1]), code_hi<kSplit>(x[0]),
+                           code_hi<kSplit>(x[1]), code_lo<kSplit>(y0), code_lo<kSplit>(y1),
+                           code_hi<kSplit>(y0), code_hi<kSplit>(y1)};
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float acc[4];
+      if constexpr (kSplit) {
+        mma_f16(acc, a[0], a[1], a[2], a[3], q[1][n], 0.f, 0.f, 0.f, 0.f);
+        mma_f16(acc, a[4], a[5], a[6], a[7], q[1][n] + 2);
+        mma_f16(acc, a[0], a[1], a[2], a[3], q[0][n]);
+      } else {
+        mma_f16(acc, a[0], a[1], a[2], a[3], q[0][n], __uint_as_float(from[n][0]),
+                __uint_as_float(from[n][1]), __uint_as_float(from[n][2]), __uint_as_float(from[n][3]));
+      }
+      mma_f16(acc, a[4], a[5], a[6], a[7], q[0][n] + 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[n][i] = fmaf(acc[i], __uint_as_float(i < 2 ? s0 : s1), z[n][i]);
+    }
+  }
+
+  __device__ __forceinline__ void tile(const ScoreRule& rule, uint32_t queries, uint32_t stage, int key0,
+                                       typename S::Mask mask) {
+    if constexpr (S::kKeys == 32) {
+      keys32(rule, queries, stage, stage + 2 * S::kCodes, key0, mask);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < S::kKeys; i += 32)
+        if (const unsigned seen = (unsigned)(mask >> i))
+          keys32(rule, queries, stage + i * S::kRowBytes, stage + 2 * S::kCodes + i * kC, key0 + i, seen);
+    }
+  }
+
+  // kt: the codes of 32 keys (of their values S::kCodes further on); ks: their scales (S::kScales further on)
+  __device__ __forceinline__ void keys32(const ScoreRule& rule, uint32_t queries, uint32_t kt, uint32_t ks,
+                                         int key0, unsigned mask) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t vt = kt + S::kCodes;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sk = smem_addr(smem) + S::kOffDecoded + (threadIdx.x >> 5) * S::kDecoded;
+    const uint32_t sv = sk + S::kDecodedK;
+    constexpr int kX = kU * kC / 2;  // words of two chunks of 16 keys, or of one chunk of 32
+    uint32_t x[kX][4];
+#pragma unroll
+    for (int i = 0; i < kX; ++i) words<false>(kt, i * 2 / kC, i * 2 % kC, x[i]);
+    __syncwarp();                    // the last tile's scales have been read
+    const bool large = decode_scales(ks, sk, mask);
+    float z[kU][kN][4] = {};
+    uint32_t sc[kU][2][kC];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_shared(sk + (16 * u + lane / 4 + 8 * i) * kC * 4, sc[u][i]);
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      uint32_t q[kParts][kN][4], from[kN][4];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int part = 0; part < kParts; ++part)
+          load_shared(queries + (((part * kN + n) * kC + c) * 32 + lane) * 16, q[part][n]);
+        if constexpr (!kSplit)
+          load_shared(queries + S::kOffStart + ((n * kC + c) * 4 + lane % 4) * 16, from[n]);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = u * kC + c;    // of the chunks of 16 keys
+        chunk_scores(x[i / 2] + i % 2 * 2, q, from, sc[u][0][c], sc[u][1][c], z[u]);
+      }
+    }
+    // the values' words, on their way while the weights are computed
+#pragma unroll
+    for (int i = 0; i < kX; ++i) words<true>(vt, i * 2 / kC, i * 2 % kC, x[i]);
     // z becomes the scores, or stays the sums above where a factor is all that is missing
     float factor[kN][2];
-    const bool full = mask == 0xffffffffu;
-    if (rule.plain && full) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) pair_of(queries + S::kOffUnit, n, factor[n]);
+    if (rule.plain && mask == 0xffffffffu) {
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) factor[n][i] = rule.scale2 * unit[n][i];
+        for (int i = 0; i < 2; ++i) factor[n][i] *= rule.scale2;
     } else {
+      float slope2[kN][2];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) pair_of(queries + S::kOffUnit + RT * 4, n, slope2[n]);
       bool small = rule.cap > 0.f;
 #pragma unroll
       for (int u = 0; u < kU; ++u)
@@ -283,7 +467,7 @@ struct Q4State {
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            z[u][n][i] *= unit[n][i & 1];
+            z[u][n][i] *= factor[n][i & 1];
             small &= fabsf(z[u][n][i] * rule.rcap) < kSeries;
           }
       const bool series = __all_sync(0xffffffffu, small);
@@ -296,89 +480,83 @@ struct Q4State {
             const int j = 16 * u + lane / 4 + 8 * (i >> 1);
             float& x = z[u][n][i];
             x = !((mask >> j) & 1) ? -INFINITY
+                : rule.plain       ? x * rule.scale2
                 : series           ? score_near_zero(rule, x, slope2[n][i & 1], key0 + j)
                                    : score_of<!kSplit>(rule, x, slope2[n][i & 1], key0 + j);
           }
 #pragma unroll
       for (int n = 0; n < kN; ++n) factor[n][0] = factor[n][1] = 1.f;
     }
-    // The running maxima are looked for again only where a score is above them.
+    float drop = 0.f, up = 1.f;      // of the weights, so that their products with the scales stay finite
+    if (large) {
+      const uint32_t w = (mask >> lane) & 1 ? scale_word<kC>(ks + S::kScales, lane) : 0u;
+      unsigned most = 0;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) most = max(most, (w >> (8 * c + 3)) & 31u);
+      most = __reduce_max_sync(0xffffffffu, most);
+      drop = (float)((int)most - 15);
+      up = __uint_as_float((most - 15 + 127) << 23);
+    }
+    float p[kU][kN][4], sum_l[kN][2];
+    auto weigh = [&](float up) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const unsigned long long f = f2pack(factor[n][0], factor[n][1]);
+        const unsigned long long less = f2pack(-m[n][0] - drop, -m[n][1] - drop);
+        unsigned long long sum = 0;
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float t0, t1;
+            f2unpack(fma2(f2pack(z[u][n][2 * i], z[u][n][2 * i + 1]), f, less), t0, t1);
+            p[u][n][2 * i] = exp2_fast(t0);
+            p[u][n][2 * i + 1] = exp2_fast(t1);
+            const unsigned long long both = f2pack(p[u][n][2 * i], p[u][n][2 * i + 1]);
+            sum = u + i == 0 ? both : add2(sum, both);
+          }
+        f2unpack(mul2(sum, f2pack(up, up)), sum_l[n][0], sum_l[n][1]);
+      }
+    };
+    weigh(up);
     bool above = false;
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          above |= fmaf(z[u][n][i], factor[n][i & 1], -m[n][i & 1]) > kBoost;
+    for (int n = 0; n < kN; ++n) above |= sum_l[n][0] > kMostSum || sum_l[n][1] > kMostSum;
     if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        float f[2];
+        float top[2] = {-INFINITY, -INFINITY}, f[2];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            top[0] = fmaxf(top[0], z[u][n][2 * i] * factor[n][0]);
+            top[1] = fmaxf(top[1], z[u][n][2 * i + 1] * factor[n][1]);
+          }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float top = fmaxf(z[0][n][i] * factor[n][i], z[0][n][i + 2] * factor[n][i]);
 #pragma unroll
-          for (int u = 1; u < kU; ++u)
-            top = fmaxf(top, fmaxf(z[u][n][i] * factor[n][i], z[u][n][i + 2] * factor[n][i]));
-#pragma unroll
-          for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          top = fmaxf(m[n][i], top - kBoost);
-          f[i] = exp2_fast(m[n][i] - top);
+          for (int x = 4; x < 32; x *= 2)
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], x));
+          top[i] = fmaxf(m[n][i], top[i] - kBoost);
+          f[i] = exp2_fast(m[n][i] - top[i]);
           l[n][i] *= f[i];
-          m[n][i] = top;
+          m[n][i] = top[i];
         }
+        const unsigned long long ff = f2pack(f[0], f[1]), none = 0;
 #pragma unroll
         for (int c = 0; c < kC; ++c)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[c][t][n][i] *= f[i & 1];
+            for (int i = 0; i < 2; ++i) o[c][t][n][i] = fma2(o[c][t][n][i], ff, none);
       }
+      weigh(up);
     }
-    // The values' scales: of keys (lane % 4) * 2, + 1, + 8, + 9 of every 16 (the weights' order as right
-    // operand), or, where weights are split, lane / 4, + 8 (their order as scores).  What a free row
-    // holds is not looked at.
-    constexpr int kW = kSplit ? 2 : 4;
-    uint32_t w[kU][kW];
-    uint32_t large = 0;
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        const int key = 16 * u + (kSplit ? lane / 4 + 8 * k : lane % 4 * 2 + (k & 1) + 8 * (k >> 1));
-        w[u][k] = scale_word<kC>(vs, key);
-        if (!full && !((mask >> key) & 1)) w[u][k] = 0;
-        large |= w[u][k];
-      }
-    float drop = 0.f, up = 1.f;      // of the weights, so that their products with the scales stay finite
-    if (__any_sync(0xffffffffu, large & 0x80808080u)) {
-      unsigned most = 0;
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int k = 0; k < kW; ++k)
-#pragma unroll
-          for (int c = 0; c < kC; ++c) most = max(most, (w[u][k] >> (8 * c + 3)) & 31u);
-      most = __reduce_max_sync(0xffffffffu, most);
-      drop = (float)((int)most - 15);
-      up = __uint_as_float((most - 15 + 127) << 23);
-    }
-    float p[kU][kN][4];
-    float sum_l[kN][2] = {};
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[u][n][i] = exp2_fast(fmaf(z[u][n][i], factor[n][i & 1], -m[n][i & 1] - drop));
-          sum_l[n][i & 1] += p[u][n][i];
-        }
 #pragma unroll
     for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) l[n][i] = fmaf(sum_l[n][i], up, l[n][i]);
+      for (int i = 0; i < 2; ++i) l[n][i] += sum_l[n][i];
     uint32_t pt[kU][kN][2];          // weights as right operand: keys in pairs, a column a head
     if constexpr (!kSplit) {
 #pragma unroll
@@ -387,70 +565,70 @@ struct Q4State {
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            pt[u][n][i] = transpose8(pack_half(p[u][n][2 * i], p[u][n][2 * i + 1]));
+            pt[u][n][i] = turn8(pack_half(p[u][n][2 * i], p[u][n][2 * i + 1]));
     }
-    // chunk c of the values, x its words of every 16 keys
-    auto chunk_values = [&](int c, const uint32_t* const (&x)[kU]) {
+    // the values' scales: fp16 of keys (lane % 4) * 2, + 1 (i = 0), + 8, + 9 (1) of every 16, as the
+    // right operand has them; or, where weights are split, fp32 of keys lane / 4 and + 8
+    uint32_t w[kU][2][kC];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        load_shared(sv + (kSplit ? 16 * u + 8 * i + lane / 4 : 8 * u + 4 * i + lane % 4) * kC * 4, w[u][i]);
+    auto chunk_values = [&](int c) {
       uint32_t ps[kParts][kU][kN][2];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if constexpr (kSplit) {
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-          for (int n = 0; n < kN; ++n)
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float s = scale_of(w[u][i], c);
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (kSplit) {
+              const float s = __uint_as_float(w[u][i][c]);
               const float lo = p[u][n][2 * i] * s, hi = p[u][n][2 * i + 1] * s;
               const uint32_t h = pack_half(lo, hi);
               const float2 back = unpack_half(h);
-              ps[0][u][n][i] = transpose8(h);
-              ps[kParts - 1][u][n][i] = transpose8(pack_half(lo - back.x, hi - back.y));
+              ps[0][u][n][i] = turn8(h);
+              ps[kParts - 1][u][n][i] = turn8(pack_half(lo - back.x, hi - back.y));
+            } else {
+              ps[0][u][n][i] = mul_half(pt[u][n][i], w[u][i][c]);
             }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t s = scale_pair(w[u][(2 * i) % kW], w[u][(2 * i + 1) % kW], c);
-#pragma unroll
-            for (int n = 0; n < kN; ++n) ps[0][u][n][i] = mul_half(pt[u][n][i], s);
           }
-        }
+      uint32_t a[kU][8];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = u * kC + c;
+        const uint32_t x0 = x[i / 2][i % 2 * 2], x1 = x[i / 2][i % 2 * 2 + 1];
+        const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+        a[u][0] = code_lo<true>(x0);
+        a[u][1] = code_hi<true>(x0);
+        a[u][2] = code_lo<true>(x1);
+        a[u][3] = code_hi<true>(x1);
+        a[u][4] = code_lo<true>(y0);
+        a[u][5] = code_hi<true>(y0);
+        a[u][6] = code_lo<true>(y1);
+        a[u][7] = code_hi<true>(y1);
       }
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        float sum[2][4] = {};
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const uint32_t x0 = x[u][0], x1 = x[u][1], y0 = x0 >> 8, y1 = x1 >> 8;
+        for (int t = 0; t < 2; ++t) {
+          float sum[4];
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) {
-            mma_f16(sum[0], code_lo<true>(x0), code_hi<true>(x0), code_lo<true>(x1),
-                    code_hi<true>(x1), ps[part][u][n]);
-            mma_f16(sum[1], code_lo<true>(y0), code_hi<true>(y0), code_lo<true>(y1),
-                    code_hi<true>(y1), ps[part][u][n]);
-          }
+          for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+              const uint32_t* y = a[u] + 4 * t;
+              if (u == 0 && part == 0) mma_f16(sum, y[0], y[1], y[2], y[3], ps[0][0][n], 0.f, 0.f, 0.f, 0.f);
+              else mma_f16(sum, y[0], y[1], y[2], y[3], ps[part][u][n]);
+            }
+          const unsigned long long up2 = f2pack(up, up);
+          o[c][t][n][0] = fma2(f2pack(sum[0], sum[1]), up2, o[c][t][n][0]);
+          o[c][t][n][1] = fma2(f2pack(sum[2], sum[3]), up2, o[c][t][n][1]);
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[c][t][n][i] = fmaf(sum[t][i], up, o[c][t][n][i]);
-      }
     };
-    if constexpr (kC == 1) {
-      static_assert(kU == 2, "both units' words at once");
-      uint32_t x[4];
-      words<true>(vt, 0, 0, x);
-      chunk_values(0, {x, x + 2});
-    } else {
 #pragma unroll
-      for (int c = 0; c < kC; c += 2) {
-        uint32_t x[kU][4];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) words<true>(vt, u, c, x[u]);
-        static_assert(kU == 2, "words of two units");
-        chunk_values(c, {x[0], x[1]});
-        chunk_values(c + 1, {x[0] + 2, x[1] + 2});
-      }
-    }
+    for (int c = 0; c < kC; ++c) chunk_values(c);
   }
 
   // this warp's (maximum, sum) of every row
@@ -476,13 +654,15 @@ struct Q4State {
       for (int i = 0; i < 2; ++i) {
         const int r = 8 * n + lane % 4 * 2 + i;
         if (r >= rows) continue;
-        const float f = exp2_fast(m[n][i] - top(r));
+        const float f = exp2_fast(m[n][i] - top(r)) * 512.f;     // codes are 2^-9 of their numbers
 #pragma unroll
         for (int c = 0; c < kC; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[r * D + ((32 * c + 4 * (lane / 4) + k) ^ spread(r))] =
-                o[c][k / 2][n][(k & 1) * 2 + i] * f;
+          for (int k = 0; k < 4; ++k) {
+            float x[2];
+            f2unpack(o[c][k / 2][n][k & 1], x[0], x[1]);
+            dst[r * D + ((32 * c + 4 * (lane / 4) + k) ^ spread(r))] = x[i] * f;
+          }
       }
   }
 };
@@ -496,43 +676,280 @@ struct Q4Loader : RowLoader<Q4Shape<T, D, RT>, PagedAttnQ4Args<T>> {
   using Rows = typename RowLoader<S, PagedAttnQ4Args<T>>::Rows;
 
   __device__ __forceinline__ void issue(const PagedAttnQ4Args<T>& a, const Rows& r, uint32_t stage,
-                                        unsigned* mask_out) const {
+                                        typename S::Mask* mask_out) const {
     const int lane = threadIdx.x & 31;
-    const unsigned mask = this->valid_keys(a, r);
+    const auto mask = this->valid_keys(a, r);
     if (lane == 0) *mask_out = mask;
     if (mask) {
       const int log2 = a.paged.page_log2, in_page = (1 << log2) - 1;
       // a page's bytes of one head: 16 codes' and one scale byte for every chunk
       const long long head_bytes = (long long)(17 * S::kChunks) << log2;
       const int scales_at = S::kRowBytes << log2;
-      constexpr int kRows = 32 / S::kChunks;          // rows a warp copies at once
-      const int row0 = lane / S::kChunks;
+      constexpr int kPasses = S::kCodes / 512;
+      constexpr int kPieces = S::kScales / 16, kOf = 16 / S::kChunks;      // 16 bytes of scales: kOf rows'
+      if (mask == this->kAll && (1 << log2) >= S::kKeys) {
+        // all rows of one page: they and their scales lie one behind the other
+        const int row = r.key0 & in_page;
+        const long long head0 = ((long long)r.page * a.Hkv + r.head) * head_bytes;
+        const long long off = head0 + row * S::kRowBytes + lane * 16;
+        const uint8_t *k = a.k_cache + off, *v = a.v_cache + off;
+        const uint32_t dst = stage + lane * 16;
 #pragma unroll
-      for (int i = 0; i < S::kChunks; ++i) {
-        const int row = i * kRows + row0;
-        const int page = __shfl_sync(0xffffffffu, r.page, row);
-        const bool live = (mask >> row) & 1;
-        const long long off = ((long long)page * a.Hkv + r.head) * head_bytes +
-                              ((r.key0 + row) & in_page) * S::kRowBytes + lane % S::kChunks * 16;
-        const uint32_t dst = stage + (i * 32 + lane) * 16;
-        copy16(dst, a.k_cache + (live ? off : 0), live);
-        copy16(dst + S::kCodes, a.v_cache + (live ? off : 0), live);
-      }
-      // scales, K's and V's: 16 bytes are those of 16 / kChunks rows
-      constexpr int kPieces = S::kScales / 16, kEach = 16 / S::kChunks;
-      const int piece = lane % kPieces, row = piece * kEach;
-      const int page = __shfl_sync(0xffffffffu, r.page, row);
-      if (lane < 2 * kPieces) {
-        const bool live = (mask >> row) & ((1u << kEach) - 1);
-        const long long off = ((long long)page * a.Hkv + r.head) * head_bytes + scales_at +
-                              ((r.key0 + row) & in_page) * S::kChunks;
-        copy16(stage + 2 * S::kCodes + lane * 16,
-               (lane < kPieces ? a.k_cache : a.v_cache) + (live ? off : 0), live);
+        for (int i = 0; i < kPasses; ++i) {
+          copy16(dst + i * 512, k + i * 512, true);
+          copy16(dst + S::kCodes + i * 512, v + i * 512, true);
+        }
+        if (lane < 2 * kPieces)
+          copy16(stage + 2 * S::kCodes + lane * 16,
+                 (lane < kPieces ? a.k_cache : a.v_cache) + head0 + scales_at + row * S::kChunks +
+                     lane % kPieces * 16,
+                 true);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int row = (i * 32 + lane) / S::kChunks;
+          const int page = __shfl_sync(0xffffffffu, r.page, row / this->kEach);
+          const bool live = (mask >> row) & 1;
+          const long long off = ((long long)page * a.Hkv + r.head) * head_bytes +
+                                ((r.key0 + row) & in_page) * S::kRowBytes + lane % S::kChunks * 16;
+          const uint32_t dst = stage + (i * 32 + lane) * 16;
+          copy16(dst, a.k_cache + (live ? off : 0), live);
+          copy16(dst + S::kCodes, a.v_cache + (live ? off : 0), live);
+        }
+        const int piece = lane % kPieces, row = piece * kOf;
+        const int page = __shfl_sync(0xffffffffu, r.page, row / this->kEach);
+        if (lane < 2 * kPieces) {
+          const bool live = (unsigned)(mask >> row) & ((1u << kOf) - 1);
+          const long long off = ((long long)page * a.Hkv + r.head) * head_bytes + scales_at +
+                                ((r.key0 + row) & in_page) * S::kChunks;
+          copy16(stage + 2 * S::kCodes + lane * 16,
+                 (lane < kPieces ? a.k_cache : a.v_cache) + (live ? off : 0), live);
+        }
       }
     }
     copy_commit();
   }
 };
+
+// Counts a part of the segment that share c0 begins, of n parts in all, as count_up does; returns those
+// counted before.  Two shares have one counter, c0 / 2, which is enough: where the even one's last
+// segment has more than two parts, the odd one begins none.  Two parts of the even one's are counted
+// by 1, all else by 4.
+__device__ __forceinline__ int count_part(unsigned long long* counters, int c0, int n,
+                                          unsigned long long base) {
+  const bool two = c0 % 2 == 0 && n == 2;
+  unsigned long long* const counter = counters + c0 / 2;
+  unsigned long long old;
+  asm volatile("red.relaxed.gpu.global.max.u64 [%0], %1;" ::"l"(counter), "l"(base) : "memory");
+  asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;"
+               : "=l"(old)
+               : "l"(counter), "l"(two ? 1ull : 4ull)
+               : "memory");
+  const int count = (int)(old - base);
+  return two ? count & 3 : count >> 2;
+}
+
+// As paged_attn_kernel (paged_row.cuh), with two shares to a CTA, each a team of warps': ends of segments
+// are some thousand cycles of latency, during which the other team has the SM.  And each team has its
+// queries in shared memory, put there by a warp for each chunk while the segment before ends.
+template <typename K>
+__global__ void __launch_bounds__(K::S::kThreads, 1)
+paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
+  using T = typename K::Type;
+  using S = typename K::S;
+  using State = typename K::State;
+  using Ld = typename K::Ld;
+  using Team = typename K::Team;
+  using Mask = typename S::Mask;
+  constexpr int D = K::kD, RT = K::kRT, kTeamWarps = S::kTeamWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, tw = S::warp(), team = Team::team();
+  const int worker = blockIdx.x * S::kTeams + team, workers = gridDim.x * S::kTeams;
+  const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
+  const uint32_t ring = smem_addr(smem) + warp * S::kRing;
+  const uint32_t queries = smem_addr(smem) + S::kOffQueries + team * 2 * S::kQueries;
+  float2* const ml = reinterpret_cast<float2*>(smem + S::kOffMl) + team * kTeamWarps * RT;
+  Mask* const masks = reinterpret_cast<Mask*>(smem + S::kOffMask) + warp * S::kStages;
+  // of the segment that another share begins, and of the one that another share ends
+  Join* const joins = reinterpret_cast<Join*>(smem + S::kOffJoins) + team * 2;
+  auto* const base = reinterpret_cast<unsigned long long*>(smem + S::kOffBase) + team * 2;
+
+  griddep_wait();
+  griddep_launch();
+  unsigned long long call = 0;
+  if (threadIdx.x == 0) call = count_call(a.counters + kCallNumber);     // looked at further below
+  const Share share = my_share<S>(a.paged, a.window, HR, worker, workers);
+  Cursor at = share.at;
+  if (Team::thread() < 2) joins[Team::thread()] = {};  // read behind the barriers of the share's end
+  const bool busy = at.segment + at.t < share.end;
+  // a segment's first query head and its query rows
+  auto head_of = [&](const Cursor& c, int& head, int& rows) {
+    const int kv = a.row_blocks == 1 ? c.hr : c.hr / a.row_blocks, rb = c.hr - kv * a.row_blocks;
+    head = kv * a.G + rb * RT;
+    rows = min(RT, a.G - rb * RT);
+  };
+  auto put_queries = [&](const Cursor& c, int which) {
+    int head, rows;
+    head_of(c, head, rows);
+    for (int chunk = tw; chunk < S::kChunks; chunk += kTeamWarps)
+      State::put_queries(a, c.s, head, rows, chunk, queries + which * S::kQueries);
+  };
+  Ld ld;
+  ld.at = at;
+  ld.end = share.end;
+  typename Ld::Rows coming{};
+  if (busy) {
+    typename Ld::Rows rows_of[S::kStages];
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) rows_of[i] = ld.look_up(a, HR);   // their loads together
+#pragma unroll 1
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      ld.issue(a, rows_of[0], ring + i * S::kStageBytes, masks + i);
+#pragma unroll
+      for (int j = 1; j < S::kStages; ++j) rows_of[j - 1] = rows_of[j];
+    }
+    coming = rows_of[0];
+    put_queries(at, 0);
+  }
+  // the call's number, from thread 0 to all teams, with the queries
+  if (threadIdx.x == 0)
+    for (int i = 0; i < S::kTeams; ++i)
+      reinterpret_cast<unsigned long long*>(smem + S::kOffBase)[2 * i] = call / kCallStep << kCountBits;
+  __syncthreads();
+  if (busy) {
+    State st;
+    ScoreRule rule;
+    rule.scale2 = a.scale * kLog2e;
+    rule.cap = a.softcap;
+    // finite, so that a score of zero stays one under the smallest caps too
+    rule.rcap = a.softcap > 0.f ? fminf(fmaxf(a.scale / a.softcap, -FLT_MAX), FLT_MAX) : 0.f;
+    rule.plain = a.softcap == 0.f && a.slopes == nullptr && a.scale >= 0.f;
+    int slot = 0, next = S::kStages - 1;     // stages: of this tile, of the next one to issue
+    int from = at.t, which = 0;
+    bool begin = true;
+    do {
+      if (begin) {
+        rule.last = at.span.len - 1;
+        from = at.t;
+        st.start();
+        begin = false;
+        // the next segment's queries are brought near
+        Cursor then = at;
+        then.t = at.span.tiles - 1;
+        advance<S>(then, a.paged, a.window, HR);
+        if (then.segment < share.end) {
+          int head, rows;
+          head_of(then, head, rows);
+          constexpr int kLines = (D * (int)sizeof(T) + 127) / 128;      // of a row
+          const int r = Team::thread() / kLines;
+          if (r < rows)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                reinterpret_cast<const char*>(a.q + then.s * a.q_s + (long long)(head + r) * a.q_h) +
+                Team::thread() % kLines * 128));
+        }
+      }
+      copy_wait<S::kStages - 2>();
+      __syncwarp();
+      ld.issue(a, coming, ring + next * S::kStageBytes, masks + next);
+      coming = ld.look_up(a, HR);
+      const Mask mask = masks[slot];
+      if (mask)
+        st.tile(rule, queries + which * S::kQueries, ring + slot * S::kStageBytes,
+                at.span.base + at.t * S::kTile + tw * S::kKeys, mask);
+
+      const bool ends = at.t + 1 == at.span.tiles;
+      if (ends || at.segment + at.t + 1 == share.end) {
+        // join the warps' parts
+        int head, rows;
+        head_of(at, head, rows);
+        st.put_ml(ml + tw * RT);
+        Cursor then = at;
+        advance<S>(then, a.paged, a.window, HR);
+        if (ends && then.segment < share.end) put_queries(then, which ^ 1);
+        Team::sync();
+        const bool whole = ends && from == 0;
+        const int part = worker * 2 + (from == 0 ? 1 : 0);
+        auto top = [&](int r) {
+          float t = ml[r].x;
+#pragma unroll
+          for (int w = 1; w < kTeamWarps; ++w) t = fmaxf(t, ml[w * RT + r].x);
+          return t;
+        };
+        // Every warp's sums go to the stage that it has just read: no copy goes there until its
+        // next tile.
+        uint8_t* const sums = smem + team * kTeamWarps * S::kRing + slot * S::kStageBytes;
+        st.put_o(reinterpret_cast<float*>(sums + tw * S::kRing), rows, top);
+        Team::sync();
+        for (int e = Team::thread(); e < rows * (D / 4); e += S::kTeamThreads) {
+          const int r = e / (D / 4), c = e % (D / 4) * 4;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float tp = top(r);
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kTeamWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(sums + w * S::kRing + (r * D + c) * 4);
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+            const float2 z = ml[w * RT + r];
+            sum = fmaf(z.y, exp2_fast(z.x - tp), sum);
+          }
+          // columns c + k of a row stand at c + (k ^ spread)
+          const int turn = State::spread(r);
+          if (turn & 1) x = make_float4(x.y, x.x, x.w, x.z);
+          if (turn & 2) x = make_float4(x.z, x.w, x.x, x.y);
+          if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            T* to = a.out + ((long long)at.s * Hq + head + r) * D + c;
+            to[0] = from_f<T>(x.x * inv);
+            to[1] = from_f<T>(x.y * inv);
+            to[2] = from_f<T>(x.z * inv);
+            to[3] = from_f<T>(x.w * inv);
+            if (c == 0 && a.lse) a.lse[(long long)at.s * Hq + head + r] = lse_of(tp, sum);
+          } else {
+            reinterpret_cast<float4*>(a.part_o)[(((long long)part * RT + r) * D + c) / 4] = x;
+            if (c == 0)
+              reinterpret_cast<float2*>(a.part_ml)[(long long)part * RT + r] = make_float2(tp, sum);
+          }
+        }
+        Team::sync();
+        if (!whole && Team::thread() == 0) {
+          // Whoever leaves a segment's last part joins them all, when its own share is done (the
+          // others go on meanwhile): the count is asked for now, and looked at then.
+          const int c0 = from == 0 ? worker : share_of(at.segment, share.row, workers);
+          const int n = share_of(at.segment + at.span.tiles - 1, share.row, workers) - c0 + 1;
+          const bool last = count_part(a.counters, c0, n, *base) == n - 1;
+          joins[from == 0] = {(long long)at.s * Hq + head, c0, last ? n : 0, rows, 0};
+        }
+        begin = true;
+        which ^= 1;
+      }
+      slot = slot + 1 == S::kStages ? 0 : slot + 1;
+      next = next + 1 == S::kStages ? 0 : next + 1;
+      advance<S>(at, a.paged, a.window, HR);
+    } while (at.segment + at.t < share.end);
+    copy_wait<0>();
+    Team::sync();
+    for (int i = 0; i < 2; ++i) {
+      const Join x = joins[i];
+      if (x.n == 0) continue;
+      join_parts<K>(a.part_ml, a.part_o, a.out + x.row * D, a.lse ? a.lse + x.row : nullptr, x.c, x.n,
+                    x.rows, reinterpret_cast<float*>(smem + team * kTeamWarps * S::kRing));
+    }
+  }
+  // sequences without a key: zeros, and the logarithm of an empty sum
+  for (int s = blockIdx.x; s < a.paged.S; s += gridDim.x) {
+    const int len = a.paged.lengths[s];
+    if (threadIdx.x == 0 && (len < 0 || len > (long long)a.paged.width << a.paged.page_log2))
+      flag_error(a.status, kDevErrBadIndex);
+    if (len > 0 && a.paged.width > 0) continue;
+    for (int e = threadIdx.x; e < Hq * D; e += S::kThreads)
+      a.out[(long long)s * Hq * D + e] = from_f<T>(0.f);
+    if (a.lse)
+      for (int e = threadIdx.x; e < Hq; e += S::kThreads) a.lse[(long long)s * Hq + e] = -INFINITY;
+  }
+}
 
 template <typename T, int D, int RT>
 struct Q4 {
@@ -541,7 +958,9 @@ struct Q4 {
   using S = Q4Shape<T, D, RT>;
   using State = Q4State<T, D, RT>;
   using Ld = Q4Loader<T, D, RT>;
+  using Team = Q4Team<S>;
   static constexpr int kD = D, kRT = RT;
+  static auto kernel() { return paged_attn_q4_kernel<Q4>; }
 };
 
 // A CTA takes 8 query rows, in bf16 16 where the group has more; larger groups take several CTAs.

@@ -151,13 +151,14 @@ __device__ __forceinline__ int share_of(long long x, long long row, int n) {
 // The length of the row, the place of this CTA's first tile, and the position where its share
 // ends (a share may be empty, or hold ends of segments only: the first tile then lies behind).
 // Each warp finds them for itself: a running sum over the sequences, of which those behind the
-// first batch are summed ahead.
+// first batch are summed ahead.  (worker, workers: this CTA and the grid, where a CTA is not several.)
 struct Share {
   long long row, end;
   Cursor at;
 };
 template <typename S>
-__device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int HR) {
+__device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int HR, int worker,
+                                          int workers) {
   const int lane = threadIdx.x & 31;
   constexpr int kEach = 4, kBatch = 32 * kEach;     // sequences of a lane, and of a warp, at a time
   auto cost_of = [&](int tiles) {
@@ -184,8 +185,8 @@ __device__ __forceinline__ Share my_share(const PagedLayout& pg, int window, int
   long long cost = load(0), incl = warp_incl_scan64(cost);
   Share sh;
   sh.row = __shfl_sync(0xffffffffu, incl, 31) + rest;
-  const long long x = share_begin(sh.row, gridDim.x, blockIdx.x);
-  sh.end = share_begin(sh.row, gridDim.x, blockIdx.x + 1);
+  const long long x = share_begin(sh.row, workers, worker);
+  sh.end = share_begin(sh.row, workers, worker + 1);
   sh.at.segment = sh.row;
   sh.at.t = 0;
   if (x >= sh.end) return sh;
@@ -282,26 +283,28 @@ template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return __flo
 // ---------------------------------------------------------------------------
 template <typename S, typename Args>
 struct RowLoader {
+  using Mask = typename S::Mask;         // a bit a key
+  static constexpr Mask kAll = (Mask)(~0ull >> (64 - S::kKeys));
+  static constexpr int kEach = S::kKeys > 32 ? S::kKeys / 32 : 1;    // keys whose page a lane looks up
   Cursor at;
   long long end;           // of the share
   struct Rows {            // a warp's keys of a tile
-    int page, key0, head;  // page: of this lane's key
-    unsigned mask;         // those to be seen
+    int page, key0, head;  // page: of this lane's first key
+    Mask mask;             // those to be seen
   };
 
   __device__ __forceinline__ Rows look_up(const Args& a, int HR) {
     int page = 0, key0 = 0, head = 0;
-    unsigned mask = 0;
+    Mask mask = 0;
     if (at.segment + at.t >= end) return {0, 0, 0, 0};
-    const int warp = threadIdx.x >> 5;
+    const int warp = S::warp();
     key0 = at.span.base + at.t * S::kTile + warp * S::kKeys;
     const int lo = max(at.span.first - key0, 0), hi = min(at.span.len - key0, S::kKeys);
     if (lo < hi) {
-      constexpr unsigned kAll = (unsigned)((1ull << S::kKeys) - 1);
       mask = (kAll << lo) & (kAll >> (S::kKeys - hi));
       head = a.row_blocks == 1 ? at.hr : at.hr / a.row_blocks;
       // lanes whose key is not to be seen read the first one's page
-      const int mine = (threadIdx.x & 31) % S::kKeys;
+      const int mine = (threadIdx.x & 31) * kEach % S::kKeys;
       const int key = key0 + ((mask >> mine) & 1 ? mine : lo);
       page = a.paged.table[(long long)at.s * a.paged.width + (key >> a.paged.page_log2)];
     }
@@ -309,16 +312,20 @@ struct RowLoader {
     return {page, key0, head, mask};
   }
 
-
   // the keys of `r` to be seen, without those on invalid pages (which are flagged)
-  __device__ __forceinline__ static unsigned valid_keys(const Args& a, const Rows& r) {
-    unsigned mask = r.mask;
+  __device__ __forceinline__ static Mask valid_keys(const Args& a, const Rows& r) {
+    Mask mask = r.mask;
     if (mask) {
       const bool bad = r.page < 0 || r.page >= a.paged.num_pages;
       const unsigned wrong = __ballot_sync(0xffffffffu, bad);
       if (wrong) {
         if ((threadIdx.x & 31) == 0) flag_error(a.status, kDevErrBadIndex);
-        mask &= ~wrong;
+        if constexpr (kEach == 1) {
+          mask &= ~wrong;
+        } else {
+          for (int i = 0; i < 32; ++i)
+            if ((wrong >> i) & 1) mask &= ~((Mask)((1u << kEach) - 1) << (kEach * i));
+        }
       }
     }
     return mask;
@@ -347,9 +354,15 @@ __device__ __forceinline__ int count_up(unsigned long long* counter, unsigned lo
   return (int)(old - base);
 }
 
+// The threads that work on one share.
+struct WholeCta {
+  __device__ __forceinline__ static int thread() { return threadIdx.x; }
+  __device__ __forceinline__ static void sync() { __syncthreads(); }
+};
+
 // Joins the partials of a cut segment, all of them written: the beginning is CTA c's last part, the
-// rest the first parts of CTAs c + 1 .. c + n - 1; out and lse: the segment's rows.  Called by a
-// whole CTA (out of line: it should not cost the tile loop registers); `mem`: shared, of
+// rest the first parts of CTAs c + 1 .. c + n - 1; out and lse: the segment's rows.  Called by all
+// threads of a share (out of line: it should not cost the tile loop registers); `mem`: shared, of
 // kThreads * 4 + kGroups * 2 floats.
 // D / 4 threads take four columns of a row's parts, kAhead of them on their way at a time, with a
 // running maximum; where there are fewer rows than such groups of threads, a row's parts are dealt
@@ -357,12 +370,13 @@ __device__ __forceinline__ int count_up(unsigned long long* counter, unsigned lo
 template <typename K, typename T>
 __device__ __noinline__ void join_parts(const float* part_ml, const float* part_o, T* out,
                                         float* lse, int c, int n, int rows, float* mem) {
-  constexpr int D = K::kD, RT = K::kRT, kThreads = K::S::kThreads;
+  using Team = typename K::Team;
+  constexpr int D = K::kD, RT = K::kRT, kThreads = K::S::kTeamThreads;
   constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kAhead = RT == 16 ? 16 : 6;
   float4* sums = reinterpret_cast<float4*>(mem);               // [groups][D / 4]
   float2* totals = reinterpret_cast<float2*>(mem + kThreads * 4);   // [groups] (maximum, sum)
-  static_assert((kThreads * 4 + kGroups * 2) * 4 <= K::S::kOffMl, "shared memory");
-  const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes;
+  static_assert((kThreads * 4 + kGroups * 2) * 4 <= K::S::kJoinBytes, "shared memory");
+  const int thread = Team::thread(), group = thread / kLanes, col = thread % kLanes;
   for (int r0 = 0; r0 < rows; r0 += kGroups) {
     const int now = min(rows - r0, kGroups), share = kGroups / now;
     const int row = group / share, first = group - row * share;
@@ -401,17 +415,17 @@ __device__ __noinline__ void join_parts(const float* part_ml, const float* part_
           acc.w = fmaf(w, v[k].w, acc.w);
         }
       }
-      sums[threadIdx.x] = acc;
+      sums[thread] = acc;
       if (col == 0) totals[group] = make_float2(base, sum);
     }
-    __syncthreads();
+    Team::sync();
     if (row < now && first == 0) {
       float base = kLowest, sum = 0.f;
       for (int g = 0; g < share; ++g) base = fmaxf(base, totals[group + g].x);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int g = 0; g < share; ++g) {
         const float2 x = totals[group + g];
-        const float4 v = sums[threadIdx.x + g * kLanes];
+        const float4 v = sums[thread + g * kLanes];
         const float w = exp2_fast(x.x - base);
         sum = fmaf(w, x.y, sum);
         acc.x = fmaf(w, v.x, acc.x);
@@ -427,7 +441,7 @@ __device__ __noinline__ void join_parts(const float* part_ml, const float* part_
       to[3] = from_f<T>(acc.w * inv);
       if (lse && col == 0) lse[r0 + row] = lse_of(base, sum);
     }
-    __syncthreads();
+    Team::sync();
   }
 }
 
@@ -462,7 +476,8 @@ paged_attn_kernel(const __grid_constant__ typename K::Args a) {
   const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
   uint8_t* ring = smem + warp * S::kRing;
   float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
-  unsigned* masks = reinterpret_cast<unsigned*>(smem + S::kOffMask) + warp * S::kStages;
+  using Mask = typename S::Mask;
+  Mask* masks = reinterpret_cast<Mask*>(smem + S::kOffMask) + warp * S::kStages;
   // of the segment that another CTA begins, and of the one that another CTA ends
   Join* joins = reinterpret_cast<Join*>(smem + S::kOffJoins);
 
@@ -470,7 +485,7 @@ paged_attn_kernel(const __grid_constant__ typename K::Args a) {
   griddep_launch();
   unsigned long long call = 0;
   if (threadIdx.x == 0) call = count_call(a.counters + kCallNumber);     // looked at further below
-  const Share share = my_share<S>(a.paged, a.window, HR);
+  const Share share = my_share<S>(a.paged, a.window, HR, blockIdx.x, gridDim.x);
   Cursor at = share.at;
   if (threadIdx.x < 2) joins[threadIdx.x] = {};        // read behind the barriers of the share's end
   if (at.segment + at.t < share.end) {
@@ -518,7 +533,7 @@ paged_attn_kernel(const __grid_constant__ typename K::Args a) {
       __syncwarp();
       ld.issue(a, coming, smem_addr(ring) + next * S::kStageBytes, masks + next);
       coming = ld.look_up(a, HR);
-      const unsigned mask = masks[slot];
+      const Mask mask = masks[slot];
       if (mask) {
         const uint32_t stage = smem_addr(ring) + slot * S::kStageBytes;
         st.tile(rule, stage, at.span.base + at.t * S::kTile + warp * S::kKeys, mask);
@@ -540,11 +555,10 @@ paged_attn_kernel(const __grid_constant__ typename K::Args a) {
           for (int w = 1; w < S::kWarps; ++w) t = fmaxf(t, ml[w * RT + r].x);
           return t;
         };
-        // Every warp's sums go to the stage that it has just read (no copy goes there until its
-        // next tile), where they fit there.
-        float* const sums = reinterpret_cast<float*>(
-            smem + (S::kOffSums < 0 ? slot * S::kStageBytes : S::kOffSums));
-        st.put_o(sums + warp * (S::kSums / 4), rows, top);
+        // Every warp's sums go to the stage that it has just read: no copy goes there until its
+        // next tile.
+        float* const sums = reinterpret_cast<float*>(smem + slot * S::kStageBytes);
+        st.put_o(sums + warp * (S::kRing / 4), rows, top);
         __syncthreads();
         for (int r = warp; r < rows; r += S::kWarps) {
           const float base = top(r);
@@ -569,7 +583,7 @@ paged_attn_kernel(const __grid_constant__ typename K::Args a) {
             const float* from_w = sums + r * D + (c ^ State::spread(r));
             float x = 0.f;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) x += from_w[w * (S::kSums / 4)];
+            for (int w = 0; w < S::kWarps; ++w) x += from_w[w * (S::kRing / 4)];
             if (whole) out[c] = from_f<T>(x * inv);
             else part_o[c] = x;
           }
@@ -612,7 +626,8 @@ paged_attn_kernel(const __grid_constant__ typename K::Args a) {
   }
 }
 
-// CTAs for this call: one on each SM, but no more than there can be tiles.
+// CTAs for this call: one on each SM, but no more than there can be tiles.  (K::S::kTeams: the shares
+// of a CTA; K::kernel: the kernel.)
 template <typename K>
 int grid_of(int S, int width, int page_log2, int HR, int sms) {
   using Sh = typename K::S;
@@ -641,7 +656,7 @@ struct Run {
   static constexpr int D = K::kD, RT = K::kRT;
   static size_t bytes(int Hkv, int G, int S, int width, int page_log2, int sms) {
     const int HR = Hkv * ((G + RT - 1) / RT);
-    return carve(grid_of<K>(S, width, page_log2, HR, sms), RT, D).total;
+    return carve(grid_of<K>(S, width, page_log2, HR, sms) * K::S::kTeams, RT, D).total;
   }
   // the kernel's shared memory, allowed once for each device
   static cudaError_t allow_shared() {
@@ -651,7 +666,7 @@ struct Run {
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
     if (allowed.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(paged_attn_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(K::kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              K::S::kBytes);
     if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
     return e;
@@ -661,14 +676,14 @@ struct Run {
     a.row_blocks = (a.G + RT - 1) / RT;
     const int grid = grid_of<K>(a.paged.S, a.paged.width, a.paged.page_log2,
                                        a.Hkv * a.row_blocks, sms);
-    const Carve c = carve(grid, RT, D);
+    const Carve c = carve(grid * K::S::kTeams, RT, D);
     a.counters = static_cast<unsigned long long*>(ws);
     a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + c.ml);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + c.o);
     cudaError_t e = allow_shared();
     if (e != cudaSuccess) return e;
     count_launch();
-    return launch_pdl(paged_attn_kernel<K>, dim3(grid), dim3(Sh::kThreads), Sh::kBytes, st,
+    return launch_pdl(K::kernel(), dim3(grid), dim3(Sh::kThreads), Sh::kBytes, st,
                       a);
   }
 };
