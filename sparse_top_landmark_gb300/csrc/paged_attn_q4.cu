@@ -39,11 +39,8 @@
 #ifndef Q4_TEAMS
 #define Q4_TEAMS 2
 #endif
-#ifndef Q4_KEYS
-#define Q4_KEYS 64
-#endif
 #ifndef Q4_COST
-#define Q4_COST 1
+#define Q4_COST 2
 #endif
 
 namespace mita {
@@ -60,16 +57,17 @@ struct Q4Shape {
   static constexpr int kTeamWarps = RT > 8 || kSplit ? 4 : D == 128 ? Q4_TEAM : Q4_TSMALL;
   static constexpr int kWarps = kTeams * kTeamWarps;
   static constexpr int kThreads = kWarps * 32, kTeamThreads = kTeamWarps * 32;
-  static constexpr int kKeys = Q4_KEYS;                   // of a warp, 32 at a time
-  using Mask = std::conditional_t<kKeys == 64, unsigned long long, unsigned>;
+  static constexpr int kKeys = 64;                        // of a warp
+  using Mask = unsigned long long;
   static constexpr int kTile = kTeamWarps * kKeys;
   static constexpr int kSegmentCost = Q4_COST;            // tiles that ending a segment is worth
   static constexpr int kChunks = D / kQ4Block;            // of a row: 16 bytes and one scale each
   static constexpr int kRowBytes = D / 2;
   static constexpr int kCodes = kKeys * kRowBytes, kScales = kKeys * kChunks;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);      // K's codes, V's, K's scales, V's
-  // a warp's decoded scales: K's in fp32, V's in fp16 (of two keys side by side) or fp32
-  static constexpr int kDecodedK = 32 * kChunks * 4, kDecodedV = kSplit ? kDecodedK : kDecodedK / 2;
+  // a warp's decoded scales: K's in fp32, V's in fp32 or (where the scales' bytes stood in the stage) in
+  // fp16, of two keys side by side
+  static constexpr int kDecodedK = kKeys * kChunks * 4, kDecodedV = kSplit ? kDecodedK : 0;
   static constexpr int kDecoded = kDecodedK + kDecodedV;
   // a team's queries as right operands, [part][heads / 8][chunk][lane] of 16 bytes, what a product
   // starts from, [heads / 8][chunk][lane % 4] of 16 bytes, and [heads] units and slopes; twice
@@ -77,9 +75,9 @@ struct Q4Shape {
   static constexpr int kOffStart = kParts * kN * kChunks * 512;
   static constexpr int kOffUnit = kOffStart + (kSplit ? 0 : kN * kChunks * 64);
   static constexpr int kQueries = kOffUnit + RT * 8;
-  static constexpr int kRest = kWarps * (kDecoded + RT * 8 + 8 * (int)sizeof(Mask)) +
+  static constexpr int kRest = kWarps * (kDecoded + RT * 8) +
                                kTeams * (2 * kQueries + 2 * (int)sizeof(Join) + 16);
-  static constexpr int kFit = (232448 - 256 - kRest) / (kStageBytes * kWarps);
+  static constexpr int kFit = (232448 - 16 - kRest) / (kWarps * (kStageBytes + (int)sizeof(Mask)));
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kJoinBytes = kTeamWarps * kRing;                   // a team's
@@ -222,7 +220,9 @@ struct Q4State {
   using S = Q4Shape<T, D, RT>;
   static constexpr bool kSplit = std::is_same<T, float>::value;
   static constexpr int kParts = kSplit ? 2 : 1;      // fp16 values that a factor is given as
-  static constexpr int kN = RT / 8, kC = S::kChunks, kU = 2;
+  static constexpr int kN = RT / 8, kC = S::kChunks;
+  // 16 keys are a unit of work, kU of them are worked on together (as many as registers hold), and kP chunks
+  static constexpr int kU = kN == 1 && !kSplit ? 4 : 2, kP = kC == 1 ? 1 : 2;
   unsigned long long o[kC][2][kN][2];   // two heads of a value column each
   float m[kN][2], l[kN][2];          // m: the running maximum less kBoost; l: of this lane's keys
 
@@ -314,59 +314,83 @@ struct Q4State {
     x[1] = __uint_as_float(w[1]);
   }
 
-  // Words of two chunks of 16 keys, or (heads of 32) of one chunk of 32 keys: x[0], x[1] the first's
-  // keys 0-7 and 8-15, x[2], x[3] the second's.  `first`: chunk, or unit of 16 keys.
-  template <bool kTrans>
-  __device__ __forceinline__ static void words(uint32_t codes, int u, int c, uint32_t* x) {
-    const int lane = threadIdx.x & 31, second = lane >> 4, half = lane >> 3 & 1;
-    const int key = 16 * (kC == 1 ? u + second : u) + 8 * half + (lane & 7);
-    const int chunk = kC == 1 ? 0 : c + second;
-    const uint32_t at = codes + key * S::kRowBytes + (chunk ^ q4_turn<D>(key)) * 16;
-    if constexpr (kTrans) ldsm4_t(at, x); else ldsm4(at, x);
+  // Words of chunks c .. c + kP - 1 of kM units from unit u0 on: [unit][chunk] keys 0-7 and 8-15.
+  template <bool kTrans, int kM>
+  __device__ __forceinline__ static void words(uint32_t codes, int u0, int c, uint32_t (&x)[kM][kP][2]) {
+    const int lane = threadIdx.x & 31, second = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < kM * kP / 2; ++i) {      // four matrices: two units', or two chunks'
+      const int key = 16 * (u0 + (kP == 1 ? 2 * i + second : i)) + (lane >> 3 & 1) * 8 + (lane & 7);
+      const int chunk = kP == 1 ? 0 : c + second;
+      const uint32_t at = codes + key * S::kRowBytes + (chunk ^ q4_turn<D>(lane & 7)) * 16;
+      uint32_t y[4];
+      if constexpr (kTrans) ldsm4_t(at, y); else ldsm4(at, y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[kP == 1 ? 2 * i + k / 2 : i][kP == 1 ? 0 : k / 2][k & 1] = y[k];
+    }
   }
 
-  // Every lane decodes the scales of one key (the lanes that use a key's are many: 4 its K's, 8 its V's).
-  // A value's scale of a key that is not seen is zero, whatever the row holds.  Returns whether a
-  // value's scale is 2 or more.
-  __device__ __forceinline__ static bool decode_scales(uint32_t ks, uint32_t to, unsigned mask) {
+  // Every lane decodes the scales of two keys (the lanes that use a key's are many: 4 its K's, 8 its V's):
+  // from `ks`, K's bytes and then V's, to `sk`, K's as fp32, and `sv`.  A value's scale of a key that is not
+  // seen is zero, whatever the row holds.  Returns the largest upper five bits of a value's scale, or
+  // less than 16.
+  __device__ __forceinline__ static unsigned decode_scales(uint32_t ks, uint32_t sk, uint32_t sv,
+                                                           typename S::Mask mask) {
     const int lane = threadIdx.x & 31;
-    const uint32_t wk = scale_word<kC>(ks, lane);
-    uint32_t wv = scale_word<kC>(ks + S::kScales, lane);
-    if (!((mask >> lane) & 1)) wv = 0;
+    uint32_t wk[2], wv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      wk[h] = scale_word<kC>(ks, lane + 32 * h);
+      wv[h] = scale_word<kC>(ks + S::kScales, lane + 32 * h);
+      if (!((unsigned)(mask >> (32 * h)) >> lane & 1)) wv[h] = 0;
+    }
+    __syncwarp();                    // they, and the last tile's scales, have been read
     auto put = [&](uint32_t at, uint32_t w) {          // as fp32, [key][chunk]
       const float2 even = unpack_half(scales_02(w)), odd = unpack_half(scales_13(w));
       if constexpr (kC == 4) {
-        store_shared(at + lane * 16, __float_as_uint(even.x), __float_as_uint(odd.x));
-        store_shared(at + lane * 16 + 8, __float_as_uint(even.y), __float_as_uint(odd.y));
+        const uint32_t x[4] = {__float_as_uint(even.x), __float_as_uint(odd.x), __float_as_uint(even.y),
+                               __float_as_uint(odd.y)};
+        store_shared(at + lane * 16, x);
       } else if constexpr (kC == 2) {
         store_shared(at + lane * 8, __float_as_uint(even.x), __float_as_uint(odd.x));
       } else {
         store_shared(at + lane * 4, __float_as_uint(even.x));
       }
     };
-    put(to, wk);
-    to += S::kDecodedK;
-    if constexpr (kSplit) {
-      put(to, wv);
-    } else {                         // as fp16 of two keys, [pair][chunk]: each of the two writes half
-      const uint32_t even = scales_02(wv), odd = scales_13(wv);
-      const uint32_t even2 = __shfl_xor_sync(0xffffffffu, even, 1);
-      const bool second = lane & 1;
-      if constexpr (kC == 1) {
-        if (!second) store_shared(to + lane / 2 * 4, __byte_perm(even, even2, 0x5410));
-      } else {
-        const uint32_t odd2 = __shfl_xor_sync(0xffffffffu, odd, 1);
-        if constexpr (kC == 2) {
-          store_shared(to + lane * 4, second ? __byte_perm(odd2, odd, 0x5410)
-                                             : __byte_perm(even, even2, 0x5410));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      put(sk + h * 128 * kC, wk[h]);
+      if constexpr (kSplit) {
+        put(sv + h * 128 * kC, wv[h]);
+      } else {                       // as fp16 of two keys, [pair][chunk]: each of the two writes half
+        const uint32_t to = sv + h * 64 * kC;
+        const uint32_t even = scales_02(wv[h]), odd = scales_13(wv[h]);
+        const uint32_t even2 = __shfl_xor_sync(0xffffffffu, even, 1);
+        const bool second = lane & 1;
+        if constexpr (kC == 1) {
+          if (!second) store_shared(to + lane / 2 * 4, __byte_perm(even, even2, 0x5410));
         } else {
-          const uint32_t sel = second ? 0x3276u : 0x5410u;      // upper halves, or lower ones
-          store_shared(to + lane * 8, __byte_perm(even, even2, sel), __byte_perm(odd, odd2, sel));
+          const uint32_t odd2 = __shfl_xor_sync(0xffffffffu, odd, 1);
+          if constexpr (kC == 2) {
+            store_shared(to + lane * 4, second ? __byte_perm(odd2, odd, 0x5410)
+                                               : __byte_perm(even, even2, 0x5410));
+          } else {
+            const uint32_t sel = second ? 0x3276u : 0x5410u;      // upper halves, or lower ones
+            store_shared(to + lane * 8, __byte_perm(even, even2, sel), __byte_perm(odd, odd2, sel));
+          }
         }
       }
     }
     __syncwarp();
-    return __any_sync(0xffffffffu, wv & 0x80808080u);
+    unsigned most = 0;
+    if (__any_sync(0xffffffffu, (wv[0] | wv[1]) & 0x80808080u)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) most = max(most, (wv[h] >> (8 * c + 3)) & 31u);
+      most = __reduce_max_sync(0xffffffffu, most);
+    }
+    return most;
   }
 
   // z += scale * (codes . q) of 16 keys, x their words of a chunk, q the chunk's queries, `from` what
@@ -395,63 +419,61 @@ struct Q4State {
     }
   }
 
+  // stage: the warp's rows and scales; key0 the first one's position; `mask` the seen ones
   __device__ __forceinline__ void tile(const ScoreRule& rule, uint32_t queries, uint32_t stage, int key0,
                                        typename S::Mask mask) {
-    if constexpr (S::kKeys == 32) {
-      keys32(rule, queries, stage, stage + 2 * S::kCodes, key0, mask);
-    } else {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t ks = stage + 2 * S::kCodes;
+    const uint32_t sk = smem_addr(smem) + S::kOffDecoded + (threadIdx.x >> 5) * S::kDecoded;
+    const uint32_t sv = kSplit ? sk + S::kDecodedK : ks;
+    const unsigned most = decode_scales(ks, sk, sv, mask);
 #pragma unroll 1
-      for (int i = 0; i < S::kKeys; i += 32)
-        if (const unsigned seen = (unsigned)(mask >> i))
-          keys32(rule, queries, stage + i * S::kRowBytes, stage + 2 * S::kCodes + i * kC, key0 + i, seen);
-    }
+    for (int u = 0; u < S::kKeys / 16; u += kU)
+      units(rule, queries, stage, sk, sv, u, key0 + 16 * u,
+            mask >> (16 * u) & (~0ull >> (64 - 16 * kU)), most);
   }
 
-  // kt: the codes of 32 keys (of their values S::kCodes further on); ks: their scales (S::kScales further on)
-  __device__ __forceinline__ void keys32(const ScoreRule& rule, uint32_t queries, uint32_t kt, uint32_t ks,
-                                         int key0, unsigned mask) {
+  // units u0 .. u0 + kU - 1; mask: their seen keys; most: decode_scales'
+  __device__ __forceinline__ void units(const ScoreRule& rule, uint32_t queries, uint32_t stage,
+                                        uint32_t sk, uint32_t sv, int u0, int key0,
+                                        typename S::Mask mask, unsigned most) {
+    if (kU < S::kKeys / 16 && mask == 0) return;
     const int lane = threadIdx.x & 31;
-    const uint32_t vt = kt + S::kCodes;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t sk = smem_addr(smem) + S::kOffDecoded + (threadIdx.x >> 5) * S::kDecoded;
-    const uint32_t sv = sk + S::kDecodedK;
-    constexpr int kX = kU * kC / 2;  // words of two chunks of 16 keys, or of one chunk of 32
-    uint32_t x[kX][4];
-#pragma unroll
-    for (int i = 0; i < kX; ++i) words<false>(kt, i * 2 / kC, i * 2 % kC, x[i]);
-    __syncwarp();                    // the last tile's scales have been read
-    const bool large = decode_scales(ks, sk, mask);
+    const uint32_t vt = stage + S::kCodes;
+    const bool full = mask == (~0ull >> (64 - 16 * kU));
     float z[kU][kN][4] = {};
-    uint32_t sc[kU][2][kC];
+#pragma unroll 1
+    for (int c0 = 0; c0 < kC; c0 += kP) {        // (not unrolled: the tile's instructions have to fit their cache)
+      uint32_t x[kU][kP][2];
+      words<false>(stage, u0, c0, x);
+      uint32_t sc[kU][2][kP];
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) load_shared(sk + (16 * u + lane / 4 + 8 * i) * kC * 4, sc[u][i]);
+        for (int i = 0; i < 2; ++i)
+          load_shared(sk + ((16 * (u0 + u) + lane / 4 + 8 * i) * kC + c0) * 4, sc[u][i]);
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      uint32_t q[kParts][kN][4], from[kN][4];
+      for (int k = 0; k < kP; ++k) {
+        const int c = c0 + k;
+        uint32_t q[kParts][kN][4], from[kN][4];
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
+        for (int n = 0; n < kN; ++n) {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part)
-          load_shared(queries + (((part * kN + n) * kC + c) * 32 + lane) * 16, q[part][n]);
-        if constexpr (!kSplit)
-          load_shared(queries + S::kOffStart + ((n * kC + c) * 4 + lane % 4) * 16, from[n]);
-      }
+          for (int part = 0; part < kParts; ++part)
+            load_shared(queries + (((part * kN + n) * kC + c) * 32 + lane) * 16, q[part][n]);
+          if constexpr (!kSplit)
+            load_shared(queries + S::kOffStart + ((n * kC + c) * 4 + lane % 4) * 16, from[n]);
+        }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int i = u * kC + c;    // of the chunks of 16 keys
-        chunk_scores(x[i / 2] + i % 2 * 2, q, from, sc[u][0][c], sc[u][1][c], z[u]);
+        for (int u = 0; u < kU; ++u)
+          chunk_scores(x[u][k], q, from, sc[u][0][k], sc[u][1][k], z[u]);
       }
     }
-    // the values' words, on their way while the weights are computed
-#pragma unroll
-    for (int i = 0; i < kX; ++i) words<true>(vt, i * 2 / kC, i * 2 % kC, x[i]);
     // z becomes the scores, or stays the sums above where a factor is all that is missing
     float factor[kN][2];
 #pragma unroll
     for (int n = 0; n < kN; ++n) pair_of(queries + S::kOffUnit, n, factor[n]);
-    if (rule.plain && mask == 0xffffffffu) {
+    if (rule.plain && full) {
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -488,12 +510,7 @@ struct Q4State {
       for (int n = 0; n < kN; ++n) factor[n][0] = factor[n][1] = 1.f;
     }
     float drop = 0.f, up = 1.f;      // of the weights, so that their products with the scales stay finite
-    if (large) {
-      const uint32_t w = (mask >> lane) & 1 ? scale_word<kC>(ks + S::kScales, lane) : 0u;
-      unsigned most = 0;
-#pragma unroll
-      for (int c = 0; c < kC; ++c) most = max(most, (w >> (8 * c + 3)) & 31u);
-      most = __reduce_max_sync(0xffffffffu, most);
+    if (most >= 16) {
       drop = (float)((int)most - 15);
       up = __uint_as_float((most - 15 + 127) << 23);
     }
@@ -567,68 +584,86 @@ struct Q4State {
           for (int i = 0; i < 2; ++i)
             pt[u][n][i] = turn8(pack_half(p[u][n][2 * i], p[u][n][2 * i + 1]));
     }
-    // the values' scales: fp16 of keys (lane % 4) * 2, + 1 (i = 0), + 8, + 9 (1) of every 16, as the
-    // right operand has them; or, where weights are split, fp32 of keys lane / 4 and + 8
-    uint32_t w[kU][2][kC];
+    // two units' values at a time
+#pragma unroll 1
+    for (int v0 = 0; v0 < kU; v0 += 2) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+      for (int c0 = 0; c0 < kC; c0 += kP) {
+        uint32_t x[2][kP][2];
+        words<true>(vt, u0 + v0, c0, x);
+        // the values' scales: fp16 of keys (lane % 4) * 2, + 1 (i = 0), + 8, + 9 (1) of every 16, as the
+        // right operand has them; or, where weights are split, fp32 of keys lane / 4 and + 8
+        uint32_t w[2][2][kP];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        load_shared(sv + (kSplit ? 16 * u + 8 * i + lane / 4 : 8 * u + 4 * i + lane % 4) * kC * 4, w[u][i]);
-    auto chunk_values = [&](int c) {
-      uint32_t ps[kParts][kU][kN][2];
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if constexpr (kSplit) {
-              const float s = __uint_as_float(w[u][i][c]);
-              const float lo = p[u][n][2 * i] * s, hi = p[u][n][2 * i + 1] * s;
-              const uint32_t h = pack_half(lo, hi);
-              const float2 back = unpack_half(h);
-              ps[0][u][n][i] = turn8(h);
-              ps[kParts - 1][u][n][i] = turn8(pack_half(lo - back.x, hi - back.y));
-            } else {
-              ps[0][u][n][i] = mul_half(pt[u][n][i], w[u][i][c]);
+            const int unit = u0 + v0 + u;
+            load_shared(sv + ((kSplit ? 16 * unit + 8 * i + lane / 4 : 8 * unit + 4 * i + lane % 4) * kC +
+                              c0) * 4, w[u][i]);
+          }
+#pragma unroll
+        for (int k = 0; k < kP; ++k) {
+          uint32_t ps[kParts][2][kN][2], y[2][8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if constexpr (kSplit) {
+                  const float f = __uint_as_float(w[u][i][k]);
+                  const float lo = p[u][n][2 * i] * f, hi = p[u][n][2 * i + 1] * f;
+                  const uint32_t h = pack_half(lo, hi);
+                  const float2 back = unpack_half(h);
+                  ps[0][u][n][i] = turn8(h);
+                  ps[kParts - 1][u][n][i] = turn8(pack_half(lo - back.x, hi - back.y));
+                } else {
+                  ps[0][u][n][i] = mul_half(pt[u][n][i], w[u][i][k]);
+                }
+              }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x0 = x[u][k][i], x1 = x0 >> 8;
+              y[u][2 * i] = code_lo<true>(x0);
+              y[u][2 * i + 1] = code_hi<true>(x0);
+              y[u][4 + 2 * i] = code_lo<true>(x1);
+              y[u][5 + 2 * i] = code_hi<true>(x1);
             }
           }
-      uint32_t a[kU][8];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int i = u * kC + c;
-        const uint32_t x0 = x[i / 2][i % 2 * 2], x1 = x[i / 2][i % 2 * 2 + 1];
-        const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-        a[u][0] = code_lo<true>(x0);
-        a[u][1] = code_hi<true>(x0);
-        a[u][2] = code_lo<true>(x1);
-        a[u][3] = code_hi<true>(x1);
-        a[u][4] = code_lo<true>(y0);
-        a[u][5] = code_hi<true>(y0);
-        a[u][6] = code_lo<true>(y1);
-        a[u][7] = code_hi<true>(y1);
-      }
+          for (int n = 0; n < kN; ++n) {
+            float sum[2][4];
 #pragma unroll
-      for (int n = 0; n < kN; ++n)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float sum[4];
+              for (int part = 0; part < kParts; ++part)
 #pragma unroll
-          for (int u = 0; u < kU; ++u)
+                for (int t = 0; t < 2; ++t) {
+                  const uint32_t* v = y[u] + 4 * t;
+                  if (u == 0 && part == 0)
+                    mma_f16(sum[t], v[0], v[1], v[2], v[3], ps[0][0][n], 0.f, 0.f, 0.f, 0.f);
+                  else
+                    mma_f16(sum[t], v[0], v[1], v[2], v[3], ps[part][u][n]);
+                }
+            const unsigned long long up2 = f2pack(up, up);
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-              const uint32_t* y = a[u] + 4 * t;
-              if (u == 0 && part == 0) mma_f16(sum, y[0], y[1], y[2], y[3], ps[0][0][n], 0.f, 0.f, 0.f, 0.f);
-              else mma_f16(sum, y[0], y[1], y[2], y[3], ps[part][u][n]);
-            }
-          const unsigned long long up2 = f2pack(up, up);
-          o[c][t][n][0] = fma2(f2pack(sum[0], sum[1]), up2, o[c][t][n][0]);
-          o[c][t][n][1] = fma2(f2pack(sum[2], sum[3]), up2, o[c][t][n][1]);
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                o[c0 + k][t][n][i] = fma2(f2pack(sum[t][2 * i], sum[t][2 * i + 1]), up2, o[c0 + k][t][n][i]);
+          }
         }
-    };
+      }
+      if constexpr (kU > 2 && !kSplit) {         // the next two units' weights
 #pragma unroll
-    for (int c = 0; c < kC; ++c) chunk_values(c);
+        for (int u = 0; u + 2 < kU; ++u)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pt[u][n][i] = pt[u + 2][n][i];
+      }
+    }
   }
 
   // this warp's (maximum, sum) of every row
@@ -658,12 +693,43 @@ struct Q4State {
 #pragma unroll
         for (int c = 0; c < kC; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x[2];
-            f2unpack(o[c][k / 2][n][k & 1], x[0], x[1]);
-            dst[r * D + ((32 * c + 4 * (lane / 4) + k) ^ spread(r))] = x[i] * f;
+          for (int k = 0; k < 4; k += 2) {
+            float x[2], y[2];
+            f2unpack(o[c][k / 2][n][0], x[0], x[1]);
+            f2unpack(o[c][k / 2][n][1], y[0], y[1]);
+            float* to = dst + r * D + 32 * c + 4 * (lane / 4);
+            to[k ^ spread(r)] = x[i] * f;
+            to[(k + 1) ^ spread(r)] = y[i] * f;
           }
       }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// A place in a share: the tiles of a segment that lie in it, one after the other, then the next segment's.
+// ---------------------------------------------------------------------------
+template <typename S>
+struct Portion {
+  Cursor at;               // t: the next tile
+  int left;                // tiles of this segment from here on that are the share's; 0: none
+
+  __device__ __forceinline__ void enter(long long end) {
+    left = (int)max(0ll, min((long long)(at.span.tiles - at.t), end - (at.segment + at.t)));
+  }
+  // the segment behind this one, and whether it begins in the share
+  __device__ __forceinline__ bool skip(const PagedLayout& pg, int window, int HR, long long end) {
+    at.t = at.span.tiles - 1;
+    advance<S>(at, pg, window, HR);
+    return at.segment < end;
+  }
+  __device__ __forceinline__ void step(const PagedLayout& pg, int window, int HR, long long end) {
+    ++at.t;
+    if (--left > 0) return;
+    if (at.t < at.span.tiles || !skip(pg, window, HR, end)) {
+      left = 0;
+      return;
+    }
+    enter(end);
   }
 };
 
@@ -671,14 +737,50 @@ struct Q4State {
 // The warp's loader: rows and scales as they lie, 16 keys of a page at a time (a page holds as many).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int RT>
-struct Q4Loader : RowLoader<Q4Shape<T, D, RT>, PagedAttnQ4Args<T>> {
+struct Q4Loader {
   using S = Q4Shape<T, D, RT>;
-  using Rows = typename RowLoader<S, PagedAttnQ4Args<T>>::Rows;
+  using Mask = typename S::Mask;
+  static constexpr Mask kAll = (Mask)(~0ull >> (64 - S::kKeys));
+  static constexpr int kEach = S::kKeys / 32;      // keys whose page a lane looks up
+  Portion<S> p;
+  long long end;           // of the share
+  struct Rows {            // a warp's keys of a tile
+    int page, key0, head;  // page: of this lane's first key
+    Mask mask;             // those to be seen
+  };
 
-  __device__ __forceinline__ void issue(const PagedAttnQ4Args<T>& a, const Rows& r, uint32_t stage,
-                                        typename S::Mask* mask_out) const {
+  __device__ __forceinline__ Rows look_up(const PagedAttnQ4Args<T>& a, int HR) {
+    Rows r{0, 0, 0, 0};
+    if (p.left == 0) return r;
+    r.key0 = p.at.span.base + p.at.t * S::kTile + S::warp() * S::kKeys;
+    const int lo = p.at.span.first - r.key0, hi = p.at.span.len - r.key0;
+    int key = r.key0 + (threadIdx.x & 31) * kEach;
+    if (lo <= 0 && hi >= S::kKeys) {
+      r.mask = kAll;
+    } else if (lo < S::kKeys && hi > 0) {
+      r.mask = (kAll << max(lo, 0)) & (kAll >> max(S::kKeys - hi, 0));
+      // lanes whose key is not to be seen read the first one's page
+      if (!((r.mask >> ((threadIdx.x & 31) * kEach)) & 1)) key = r.key0 + max(lo, 0);
+    }
+    if (r.mask) {
+      r.head = a.row_blocks == 1 ? p.at.hr : p.at.hr / a.row_blocks;
+      r.page = a.paged.table[(long long)p.at.s * a.paged.width + (key >> a.paged.page_log2)];
+    }
+    p.step(a.paged, a.window, HR, end);
+    return r;
+  }
+
+  __device__ __forceinline__ static void issue(const PagedAttnQ4Args<T>& a, const Rows& r, uint32_t stage,
+                                               Mask* mask_out) {
     const int lane = threadIdx.x & 31;
-    const auto mask = this->valid_keys(a, r);
+    Mask mask = r.mask;
+    const unsigned wrong =
+        __ballot_sync(0xffffffffu, mask != 0 && (unsigned)r.page >= (unsigned)a.paged.num_pages);
+    if (wrong) {
+      if (lane == 0) flag_error(a.status, kDevErrBadIndex);
+      for (int i = 0; i < 32; ++i)
+        if ((wrong >> i) & 1) mask &= ~((Mask)((1u << kEach) - 1) << (kEach * i));
+    }
     if (lane == 0) *mask_out = mask;
     if (mask) {
       const int log2 = a.paged.page_log2, in_page = (1 << log2) - 1;
@@ -687,7 +789,7 @@ struct Q4Loader : RowLoader<Q4Shape<T, D, RT>, PagedAttnQ4Args<T>> {
       const int scales_at = S::kRowBytes << log2;
       constexpr int kPasses = S::kCodes / 512;
       constexpr int kPieces = S::kScales / 16, kOf = 16 / S::kChunks;      // 16 bytes of scales: kOf rows'
-      if (mask == this->kAll && (1 << log2) >= S::kKeys) {
+      if (mask == kAll && (1 << log2) >= S::kKeys) {
         // all rows of one page: they and their scales lie one behind the other
         const int row = r.key0 & in_page;
         const long long head0 = ((long long)r.page * a.Hkv + r.head) * head_bytes;
@@ -700,7 +802,7 @@ struct Q4Loader : RowLoader<Q4Shape<T, D, RT>, PagedAttnQ4Args<T>> {
           copy16(dst + S::kCodes + i * 512, v + i * 512, true);
         }
         if (lane < 2 * kPieces)
-          copy16(stage + 2 * S::kCodes + lane * 16,
+          copy16(dst + 2 * S::kCodes,
                  (lane < kPieces ? a.k_cache : a.v_cache) + head0 + scales_at + row * S::kChunks +
                      lane % kPieces * 16,
                  true);
@@ -708,7 +810,7 @@ struct Q4Loader : RowLoader<Q4Shape<T, D, RT>, PagedAttnQ4Args<T>> {
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
           const int row = (i * 32 + lane) / S::kChunks;
-          const int page = __shfl_sync(0xffffffffu, r.page, row / this->kEach);
+          const int page = __shfl_sync(0xffffffffu, r.page, row / kEach);
           const bool live = (mask >> row) & 1;
           const long long off = ((long long)page * a.Hkv + r.head) * head_bytes +
                                 ((r.key0 + row) & in_page) * S::kRowBytes + lane % S::kChunks * 16;
@@ -717,7 +819,7 @@ struct Q4Loader : RowLoader<Q4Shape<T, D, RT>, PagedAttnQ4Args<T>> {
           copy16(dst + S::kCodes, a.v_cache + (live ? off : 0), live);
         }
         const int piece = lane % kPieces, row = piece * kOf;
-        const int page = __shfl_sync(0xffffffffu, r.page, row / this->kEach);
+        const int page = __shfl_sync(0xffffffffu, r.page, row / kEach);
         if (lane < 2 * kPieces) {
           const bool live = (unsigned)(mask >> row) & ((1u << kOf) - 1);
           const long long off = ((long long)page * a.Hkv + r.head) * head_bytes + scales_at +
@@ -779,9 +881,12 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
   unsigned long long call = 0;
   if (threadIdx.x == 0) call = count_call(a.counters + kCallNumber);     // looked at further below
   const Share share = my_share<S>(a.paged, a.window, HR, worker, workers);
-  Cursor at = share.at;
-  if (Team::thread() < 2) joins[Team::thread()] = {};  // read behind the barriers of the share's end
+  Portion<S> p;
+  p.at = share.at;
+  const Cursor& at = p.at;
   const bool busy = at.segment + at.t < share.end;
+  if (Team::thread() < 2) joins[Team::thread()] = {};  // read behind the barriers of the share's end
+  if (busy) p.enter(share.end); else p.left = 0;
   // a segment's first query head and its query rows
   auto head_of = [&](const Cursor& c, int& head, int& rows) {
     const int kv = a.row_blocks == 1 ? c.hr : c.hr / a.row_blocks, rb = c.hr - kv * a.row_blocks;
@@ -795,7 +900,7 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
       State::put_queries(a, c.s, head, rows, chunk, queries + which * S::kQueries);
   };
   Ld ld;
-  ld.at = at;
+  ld.p = p;
   ld.end = share.end;
   typename Ld::Rows coming{};
   if (busy) {
@@ -834,17 +939,15 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
         st.start();
         begin = false;
         // the next segment's queries are brought near
-        Cursor then = at;
-        then.t = at.span.tiles - 1;
-        advance<S>(then, a.paged, a.window, HR);
-        if (then.segment < share.end) {
+        Portion<S> then = p;
+        if (then.skip(a.paged, a.window, HR, share.end)) {
           int head, rows;
-          head_of(then, head, rows);
+          head_of(then.at, head, rows);
           constexpr int kLines = (D * (int)sizeof(T) + 127) / 128;      // of a row
           const int r = Team::thread() / kLines;
           if (r < rows)
             asm volatile("prefetch.global.L1 [%0];" ::"l"(
-                reinterpret_cast<const char*>(a.q + then.s * a.q_s + (long long)(head + r) * a.q_h) +
+                reinterpret_cast<const char*>(a.q + then.at.s * a.q_s + (long long)(head + r) * a.q_h) +
                 Team::thread() % kLines * 128));
         }
       }
@@ -857,15 +960,14 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
         st.tile(rule, queries + which * S::kQueries, ring + slot * S::kStageBytes,
                 at.span.base + at.t * S::kTile + tw * S::kKeys, mask);
 
-      const bool ends = at.t + 1 == at.span.tiles;
-      if (ends || at.segment + at.t + 1 == share.end) {
+      if (p.left == 1) {
         // join the warps' parts
+        const bool ends = at.t + 1 == at.span.tiles;
         int head, rows;
         head_of(at, head, rows);
         st.put_ml(ml + tw * RT);
-        Cursor then = at;
-        advance<S>(then, a.paged, a.window, HR);
-        if (ends && then.segment < share.end) put_queries(then, which ^ 1);
+        Portion<S> then = p;
+        if (ends && then.skip(a.paged, a.window, HR, share.end)) put_queries(then.at, which ^ 1);
         Team::sync();
         const bool whole = ends && from == 0;
         const int part = worker * 2 + (from == 0 ? 1 : 0);
@@ -927,8 +1029,8 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
       }
       slot = slot + 1 == S::kStages ? 0 : slot + 1;
       next = next + 1 == S::kStages ? 0 : next + 1;
-      advance<S>(at, a.paged, a.window, HR);
-    } while (at.segment + at.t < share.end);
+      p.step(a.paged, a.window, HR, share.end);
+    } while (p.left > 0);
     copy_wait<0>();
     Team::sync();
     for (int i = 0; i < 2; ++i) {
