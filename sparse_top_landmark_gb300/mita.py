@@ -530,10 +530,8 @@ def _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, axes, q_weight, k_weight
     dwq = dwk = ws = None
     nbytes = 0
     if qw or kw:
-        # for this call alone: it launches twice, and another thread's call on the same stream may
-        # come in between
         nbytes = _norm_rope_backward_bytes(d, dev)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = _norm_rope_backward_workspace(nbytes, dev)
         dwq = torch.empty(d, dtype=torch.float32, device=q.device) if qw else None
         dwk = torch.empty(d, dtype=torch.float32, device=q.device) if kw else None
     grads = (dq.data_ptr(), dkp, dwq.data_ptr() if qw else 0, dwk.data_ptr() if kw else 0,
@@ -550,6 +548,28 @@ def _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, axes, q_weight, k_weight
     if rc:
         _check(rc)
     return dq, dk, dwq, dwk
+
+
+_backward_workspaces = threading.local()
+
+
+def _norm_rope_backward_workspace(nbytes: int, device: int) -> torch.Tensor:
+    """The gradient's workspace: one for each thread and stream, since a call launches twice, and another
+    thread's call on the same stream may come in between.  A captured call has one of its graph's own."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    held = _backward_workspaces.__dict__
+    key = device, _raw_stream(device), _released
+    ws = held.get(key)
+    if ws is None or ws.numel() < nbytes:
+        if ws is None:                 # those from before the last workspace_release()
+            for old in [k for k in held if k[2] != _released]:
+                del held[old]
+        ws = held[key] = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    return ws
+
+
+_released = 0              # calls of workspace_release()
 
 
 @functools.lru_cache(maxsize=None)
@@ -700,34 +720,47 @@ def mita_cache_plan(new_tokens, lengths, page_table, free_pages, free_count, tok
         raise ValueError("page_table must be [S, width] and free_pages [num_pages]")
     i32 = torch.int32
     (S, width), pages = page_table.shape, free_pages.shape[0]
-    if new_lengths is None:
-        new_lengths = lengths
-    if new_free_count is None:
-        new_free_count = free_count
-    made = torch.empty(2 * S + 1 + tokens, dtype=i32, device=new_tokens.device)
+    # what is not given: one allocation for the int32 arrays, in which nothing needs to be checked
+    at = [0, 0, 0]
+    if seq_start is None or granted is None or positions is None:
+        made = torch.empty(2 * S + 1 + tokens, dtype=i32, device=new_tokens.device)
+        parts = made.split_with_sizes((S + 1, S, tokens))
+        base = made.data_ptr()
+        at = [base, base + 4 * (S + 1), base + 4 * (2 * S + 1)]
     if seq_start is None:
-        seq_start = made[:S + 1]
+        seq_start = parts[0]
+    else:
+        at[0] = _dense(seq_start, "seq_start", (S + 1,), i32, dev)
     if granted is None:
-        granted = made[S + 1:2 * S + 1]
+        granted = parts[1]
+    else:
+        at[1] = _dense(granted, "granted", (S,), i32, dev)
     if positions is None:
-        positions = made[2 * S + 1:]
+        positions = parts[2]
+    else:
+        at[2] = _dense(positions, "positions", (tokens,), i32, dev)
     if slots is None:
         slots = torch.empty(tokens, dtype=torch.int64, device=new_tokens.device)
-    rc = load().mita_cache_plan(_CACHE_PLAN.pack(
-        _dense(new_tokens, "new_tokens", (S,), i32, dev), _dense(lengths, "lengths", (S,), i32, dev),
-        _dense(new_lengths, "new_lengths", (S,), i32, dev),
+        slot_at = slots.data_ptr()
+    else:
+        slot_at = _dense(slots, "slots", (tokens,), torch.int64, dev)
+    n = _dense(lengths, "lengths", (S,), i32, dev)
+    count = _dense(free_count, "free_count", (1,), i32, dev)
+    rc = _plan_fn()(_CACHE_PLAN.pack(
+        _dense(new_tokens, "new_tokens", (S,), i32, dev), n,
+        n if new_lengths is None else _dense(new_lengths, "new_lengths", (S,), i32, dev),
         _dense(page_table, "page_table", (S, width), i32, dev),
-        _dense(free_pages, "free_pages", (pages,), i32, dev),
-        _dense(free_count, "free_count", (1,), i32, dev),
-        _dense(new_free_count, "new_free_count", (1,), i32, dev),
-        _dense(seq_start, "seq_start", (S + 1,), i32, dev),
-        _dense(positions, "positions", (tokens,), i32, dev),
-        _dense(slots, "slots", (tokens,), torch.int64, dev),
-        _dense(granted, "granted", (S,), i32, dev), S, tokens, pages, page_size, width),
-        _raw_stream(dev))
+        _dense(free_pages, "free_pages", (pages,), i32, dev), count,
+        count if new_free_count is None else _dense(new_free_count, "new_free_count", (1,), i32, dev),
+        at[0], at[2], slot_at, at[1], S, tokens, pages, page_size, width), _raw_stream(dev))
     if rc:
         _check(rc)
     return seq_start, positions, slots, granted
+
+
+@functools.lru_cache(maxsize=None)
+def _plan_fn():
+    return load().mita_cache_plan
 
 
 def cache_q4_shape(num_pages: int, Hkv: int, page_size: int, d: int):
@@ -1043,7 +1076,10 @@ def get_last_device_error(stream=None, device=None) -> int:
 
 def workspace_release() -> None:
     """Frees the cached workspaces, the library's and the binding's."""
+    global _released
+    _released += 1
     _paged_workspaces.clear()
+    _backward_workspaces.__dict__.clear()
     _check(load().mita_workspace_release())
 
 
