@@ -14,10 +14,13 @@
 // - keys (bf16): as the bits of an fp16 number a code n is the subnormal n * 2^-24 and n << 4 is 16 n * 2^-24;
 //   the 16 is taken out of the queries (an exact division), and the 8 out of the sum where it begins:
 //   z = sum over chunks c of s_c (-8 sum_i q_i + sum_i n_i q_i).
-// - values, and keys in fp32: 1024's bits above the code, and one fp16 instruction that leaves n - 8.  (The
-//   tensor cores cut sums.  Taken as n p from a sum of -8 p, a long context's values, which nearly
-//   cancel, lean by 2^-23 of eight times the sum of the weights for every product: 4.8e-6 of an fp32 result
-//   at 1000 keys, 1e-3 at a million.)
+// - values, and keys in fp32: one fp16 instruction more makes n - 8 of it.  (The tensor cores cut sums.
+//   Taken as n p from a sum of -8 p, a long context's values, which nearly cancel, lean by 2^-23 of
+//   eight times the sum of the weights for every product: 4.8e-6 of an fp32 result at 1000 keys, 1e-3 at a
+//   million.  With a sum of its own for 8 p they do not lean, for 2 % less time, but where a key of value zero has
+//   nearly all the weight, what is left of the others is off by 2^-21 of that key's scale: not kept.)  Of two
+//   codes of a word the lower one is taken alone and both as a byte, from whose sums the lower one's
+//   are taken at the end: an instruction less for four values.
 //
 // Queries are scaled by a power of two, their row's largest to 2^14, so that fp16 holds what bf16 does,
 // down to 2^-38 of it; weights p are at most 2^15, so that fp16's subnormals begin at 2^-29 of a
@@ -26,22 +29,16 @@
 // added to the running ones (in fp32, outside the tensor cores: paged_attn.cu says why).  The bf16 twin
 // rounds a weight and its product with the scale to fp16's 11 bits; the fp32 twin gives every query and
 // every p s as a sum of two fp16 values, 22 bits.
+//
+// Bound by instructions: a tile of 32 keys of 128 takes a warp some 580 (128 masks and 48 shifts and
+// byte moves for 8192 codes, 64 to make values signed, 48 for the scales, 32 products), of which the four
+// schedulers issue 0.54 a cycle with 12 warps and with 16; with all pages in L2 it is 3 % faster, loads alone take
+// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 118 us, 4.7 TB/s
+// (paged_attn.cu takes 311 us for the same in bf16); one sequence of 1,048,575 keys, 8/2 heads of 64, in
+// 46 us; 200 of up to 900 keys in 49 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 108 us.
 #include "paged_row.cuh"
 
 #include <cuda_fp16.h>
-
-#ifndef Q4_TEAM
-#define Q4_TEAM 6
-#endif
-#ifndef Q4_TSMALL
-#define Q4_TSMALL 8
-#endif
-#ifndef Q4_TEAMS
-#define Q4_TEAMS 2
-#endif
-#ifndef Q4_COST
-#define Q4_COST 2
-#endif
 
 namespace mita {
 namespace {
@@ -50,17 +47,26 @@ namespace {
 // weight is then 2^11, so that a tile's eight of a lane stay below that.
 constexpr float kBoost = 11.f, kMostSum = 32768.f;
 
+// Shared memory and shape of one instantiation; RT: query rows of a segment.
+//
+// A CTA has two teams of warps, each with a share of its own.  (128 sequences of up to 8192 keys, 32/8 heads of
+// 128: one share for 12 warps 153 us, two teams of 6 132; 256 of up to 300 keys: 70 and 41.)  Registers
+// hold 12 warps' state for heads of 128, 16 for smaller ones (a million keys, heads of 64: teams of 6
+// 48 us, of 8 46), 8 where rows are 16 or a factor is two values (fp32, 64 sequences of up to 8192 keys,
+// heads of 128: teams of 4 109 us, of 5 117; heads of 64: teams of 4 72, of 8 62).
+// A warp takes 64 keys of a tile (32, and three stages instead of two: 147 us for 124), and ending a segment
+// is worth one tile (none: fp32 116 us for 109; two: 123 for 119).
 template <typename T, int D, int RT>
 struct Q4Shape {
   static constexpr bool kSplit = std::is_same<T, float>::value;
-  static constexpr int kTeams = Q4_TEAMS;
-  static constexpr int kTeamWarps = RT > 8 || kSplit ? 4 : D == 128 ? Q4_TEAM : Q4_TSMALL;
+  static constexpr int kTeams = 2;
+  static constexpr int kTeamWarps = D == 128 ? (RT > 8 || kSplit ? 4 : 6) : RT > 8 ? 6 : 8;
   static constexpr int kWarps = kTeams * kTeamWarps;
   static constexpr int kThreads = kWarps * 32, kTeamThreads = kTeamWarps * 32;
-  static constexpr int kKeys = 64;                        // of a warp
-  using Mask = unsigned long long;
+  static constexpr int kKeys = 64;
+  using Mask = unsigned long long;       // a bit a key
   static constexpr int kTile = kTeamWarps * kKeys;
-  static constexpr int kSegmentCost = Q4_COST;            // tiles that ending a segment is worth
+  static constexpr int kSegmentCost = 1;
   static constexpr int kChunks = D / kQ4Block;            // of a row: 16 bytes and one scale each
   static constexpr int kRowBytes = D / 2;
   static constexpr int kCodes = kKeys * kRowBytes, kScales = kKeys * kChunks;
@@ -158,6 +164,10 @@ template <bool kSigned>
 __device__ __forceinline__ uint32_t code_hi(uint32_t x) {
   x &= 0x00f000f0u;
   return kSigned ? fma_half(x, 0x68006800u, 0xa400a400u) : x;       // * 2^11 - 2^-6
+}
+// A pair of codes of each word, as a byte n1 n0: (16 (n1 - 8) + n0 - 8) * 2^-13
+__device__ __forceinline__ uint32_t code_pair(uint32_t x) {
+  return fma_half(x, 0x68006800u, 0xa440a440u);                     // * 2^11 - 136 * 2^-13
 }
 
 // The scale bytes of a row.
@@ -337,12 +347,13 @@ struct Q4State {
   __device__ __forceinline__ static unsigned decode_scales(uint32_t ks, uint32_t sk, uint32_t sv,
                                                            typename S::Mask mask) {
     const int lane = threadIdx.x & 31;
-    uint32_t wk[2], wv[2];
+    constexpr int kH = S::kKeys / 32;
+    uint32_t wk[kH], wv[kH];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kH; ++h) {
       wk[h] = scale_word<kC>(ks, lane + 32 * h);
       wv[h] = scale_word<kC>(ks + S::kScales, lane + 32 * h);
-      if (!((unsigned)(mask >> (32 * h)) >> lane & 1)) wv[h] = 0;
+      if (mask != ~0ull && !((unsigned)(mask >> (32 * h)) >> lane & 1)) wv[h] = 0;
     }
     __syncwarp();                    // they, and the last tile's scales, have been read
     auto put = [&](uint32_t at, uint32_t w) {          // as fp32, [key][chunk]
@@ -358,7 +369,7 @@ struct Q4State {
       }
     };
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kH; ++h) {
       put(sk + h * 128 * kC, wk[h]);
       if constexpr (kSplit) {
         put(sv + h * 128 * kC, wv[h]);
@@ -383,9 +394,9 @@ struct Q4State {
     }
     __syncwarp();
     unsigned most = 0;
-    if (__any_sync(0xffffffffu, (wv[0] | wv[1]) & 0x80808080u)) {
+    if (__any_sync(0xffffffffu, (wv[0] | wv[kH - 1]) & 0x80808080u)) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kH; ++h)
 #pragma unroll
         for (int c = 0; c < kC; ++c) most = max(most, (wv[h] >> (8 * c + 3)) & 31u);
       most = __reduce_max_sync(0xffffffffu, most);
@@ -624,11 +635,12 @@ struct Q4State {
               }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t x0 = x[u][k][i], x1 = x0 >> 8;
+              // codes 0 and 1, then 2 and 3 of each word: the lower one, and both as a byte
+              const uint32_t x0 = x[u][k][i] & 0x00ff00ffu, x1 = __byte_perm(x[u][k][i], 0, 0x4341);
               y[u][2 * i] = code_lo<true>(x0);
-              y[u][2 * i + 1] = code_hi<true>(x0);
+              y[u][2 * i + 1] = code_pair(x0);
               y[u][4 + 2 * i] = code_lo<true>(x1);
-              y[u][5 + 2 * i] = code_hi<true>(x1);
+              y[u][5 + 2 * i] = code_pair(x1);
             }
           }
 #pragma unroll
@@ -699,7 +711,8 @@ struct Q4State {
             f2unpack(o[c][k / 2][n][1], y[0], y[1]);
             float* to = dst + r * D + 32 * c + 4 * (lane / 4);
             to[k ^ spread(r)] = x[i] * f;
-            to[(k + 1) ^ spread(r)] = y[i] * f;
+            // of a pair (2^-13 of its number) what is left without its lower code
+            to[(k + 1) ^ spread(r)] = (16.f * y[i] - x[i]) * (f * 0.0625f);
           }
       }
   }
