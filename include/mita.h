@@ -541,7 +541,7 @@ uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page
  *                   and page*page_size + the row in its page; 0 and -1 for rows behind the last
  *                   sequence's and of sequences that were not granted.
  *   granted [S] int32       output: new_tokens, or 0 where the sequence got nothing.
- *   S               at most 2^14.
+ *   S, tokens       at most 2^14 and 2^30.
  * Pages of sequences that are done are pushed first, in the order of the sequences and of their
  * tables, and may be handed out again by the same call.  Then sequence s is granted its tokens if they
  * fit its row of the table and the step's rows and it needs no page, or the pages that the sequences up to
@@ -587,7 +587,7 @@ int mita_cache_plan(const mita_cache_plan_params* params, mita_stream_t stream);
  *                   over.  Of two tokens with one slot a mixture is left there.
  *   k_out, v_out [tokens,Hkv,d] or NULL   outputs: the values that the cache now holds for each token, in
  *                   the element type (exactly, in bf16 too), for attention of a prompt over what later tokens
- *                   will see.  Rows passed over stay as they are.
+ *                   will see; may be k, v themselves.  Rows passed over stay as they are.
  *   *_strides       elements between tokens and heads.
  */
 typedef struct mita_cache_append_q4_params {

@@ -1141,6 +1141,7 @@ int cache_plan_impl(const mita_cache_plan_params* p, cudaStream_t st) {
   if (p == nullptr) return fail(MITA_ERR_INVALID_ARG, "params is NULL");
   if (p->tokens < 0) return fail(MITA_ERR_INVALID_ARG, "need tokens >= 0 (got %d)", p->tokens);
   MITA_TRY(check_pages(p->S, 1, p->num_pages, p->page_size, p->table_width));
+  if (p->tokens > (1 << 30)) return fail(MITA_ERR_UNSUPPORTED, "tokens must be at most 2^30");
   if (p->S > kMaxPlanSequences)
     return fail(MITA_ERR_UNSUPPORTED, "S=%d: a plan takes at most %d sequences", p->S,
                 kMaxPlanSequences);

@@ -785,7 +785,7 @@ def mita_cache_append_q4(k, v, k_cache, v_cache, slots, k_out=None, v_out=None, 
 
     slots: int64 [T], each token's page*page_size + row, as mita_cache_plan gives them; -1: passed over.
     k_out, v_out [T,Hkv,d]: where given, the values that the cache now holds for each token (a row
-    passed over stays as it is).  All four may be strided views."""
+    passed over stays as it is); they may be k and v.  All four may be strided views."""
     dev = _device_of(k, "k")
     if stream is not None or dev != torch.cuda.current_device():
         with _on(stream, dev, k, v, k_cache, v_cache, slots, k_out, v_out):

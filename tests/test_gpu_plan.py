@@ -112,6 +112,29 @@ def test_bad_numbers_are_flagged_and_get_nothing():
     check([-1, -1], [40, 40], [[0, 1, 2], [3, 4, 5]], [7, 6, 9, 9], 2, 0, 16, error=1)
 
 
+def test_two_plans_at_once():
+    """Two pools' plans on two streams, many times over, next to each other: each is right."""
+    mita = M()
+    steps = [random_step(random.Random(i), 700 + 400 * i, 60, 16, 12, 4, padded=3) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        state = [(ints(new), ints(lengths), ints(table), ints(free), ints([count]), tokens, page)
+                 for new, lengths, table, free, count, tokens, page in steps]
+        torch.cuda.synchronize()
+        outs = [mita.mita_cache_plan(*args, stream=st) for args, st in zip(state, streams)]
+        torch.cuda.synchronize()
+        for step, args, got in zip(steps, state, outs):
+            want = Q.plan(*step)
+            assert got[2].tolist() == want["slots"] and args[1].tolist() == want["new_lengths"]
+            assert args[2].tolist() == want["table"] and args[4].tolist() == [want["count"]]
+
+
+def test_most_sequences():
+    """2^14 sequences, of which most get one token."""
+    rng = random.Random(3)
+    check(*random_step(rng, 1 << 14, 20, 16, 4, 0, prompts=0.01, padded=7))
+
+
 def test_given_outputs_and_another_stream():
     mita = M()
     args = random_step(random.Random(5), 50, 100, 16, 20, 4, padded=3)

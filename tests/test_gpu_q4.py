@@ -109,6 +109,22 @@ def test_append_takes_views_and_needs_no_outputs():
     assert torch.equal(a[0], c[0])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_append_rounds_in_place(dt):
+    """k_out and v_out may be k and v: a row's block is read before its values are written."""
+    mita = M()
+    T, Hkv, d, page = 300, 3, 128, 16
+    x = torch.randn(T, 2 * Hkv, d, generator=gen(2)).to(DT[dt]).cuda()
+    slots = torch.arange(T, device="cuda")
+    shape = mita.cache_q4_shape(T // page + 1, Hkv, page, d)
+    a, b = ([torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)] for _ in range(2))
+    out = [torch.empty(T, Hkv, d, dtype=x.dtype, device="cuda") for _ in range(2)]
+    mita.mita_cache_append_q4(*x.split(Hkv, 1), *a, slots, *out)
+    mita.mita_cache_append_q4(*x.split(Hkv, 1), *b, slots, *x.split(Hkv, 1))
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    assert torch.equal(x, torch.cat(out, 1))
+
+
 def test_append_nothing_and_bad_slots():
     mita = M()
     Hkv, d, page, pages = 1, 32, 16, 2

@@ -74,6 +74,7 @@ PLAN = dict(new=OK, n=OK, after=OK, table=OK, free=OK, count=OK, count2=OK, star
     (dict(S=-1), 1, "S, num_pages"), (dict(T=-1), 1, "tokens"), (dict(pages=-1), 1, "num_pages"),
     (dict(width=-1), 1, "table_width"), (dict(page=24), 2, "page_size"), (dict(page=0), 2, "page_size"),
     (dict(width=1 << 27), 2, "table_width"), (dict(S=(1 << 14) + 1), 2, "sequences"),
+    (dict(T=(1 << 30) + 1), 2, "tokens"), (dict(T=(1 << 31) - 1), 2, "tokens"),
     (dict(new=0), 1, "new_tokens"), (dict(n=ODD), 1, "lengths"), (dict(after=0), 1, "new_lengths"),
     (dict(table=0), 1, "page_table"), (dict(free=0), 1, "free_pages"), (dict(count=0), 1, "free_count"),
     (dict(count2=ODD), 1, "new_free_count"), (dict(start=0), 1, "seq_start"),
