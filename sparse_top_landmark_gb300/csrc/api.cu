@@ -1516,13 +1516,13 @@ int mita_paged_attn_q4_f32(const mita_paged_attn_params* params, mita_stream_t s
   return mita::guarded([&] { return mita::paged_attn_q4_impl<float>(params, stream); });
 }
 uint64_t mita_paged_attn_q4_workspace_bytes(int S, int Hq, int Hkv, int d, int page_size,
-                                         int table_width, int is_f32) {
+                                            int table_width, int is_f32) {
   if (mita::guarded([&] {
         return mita::check_paged_attn_q4(S, Hq, Hkv, d, 0, page_size, table_width);
       }) != MITA_OK)
     return 0;
   return mita::paged_attn_q4_ws_bytes(d, Hkv, Hq / Hkv, S, table_width, mita::log2_of(page_size),
-                                   is_f32, mita::current_sms());
+                                      is_f32, mita::current_sms());
 }
 
 int mita_cache_append_q4(const mita_cache_append_q4_params* params, mita_stream_t stream) {

