@@ -88,6 +88,21 @@ def test_first_come_first_served():
     assert want["granted"] == [20, 0, 0, 1, 5]
 
 
+@pytest.mark.parametrize("spare", [-60, 0, 5])
+def test_every_page_is_free_or_held_once(spare):
+    """Also where sequences that need no page go on behind one that is refused: what the refused ones would
+    have needed stays on the stack."""
+    for seed in range(7):
+        new, lengths, table, stack, count, tokens, page = random_step(random.Random(seed), 50, 60, 16, 9, spare)
+        state = ints(lengths), ints(table), ints(stack), ints([count])
+        granted = M().mita_cache_plan(ints(new), *state, tokens, page)[3].tolist()
+        n, rows, free, left = (x.tolist() for x in state)
+        if spare < 0:
+            assert any(x > 0 and g == 0 for x, g in zip(new, granted))
+        held = [p for s, row in enumerate(rows) for p in row[:-(-n[s] // page)]]
+        assert sorted(held + free[:left[0]]) == list(range(len(stack)))
+
+
 def test_pages_that_come_back_are_handed_out_again():
     want = check([-1, 30, -1], [20, 0, 1], [[3, 4], [-1, -1], [5, -1]], [0, -1, -1, -1, -1, -1], 1, 30, 16)
     assert want["table"][1] == [5, 4] and want["count"] == 2
