@@ -33,9 +33,9 @@
 // Bound by instructions: a tile of 32 keys of 128 takes a warp some 580 (128 masks and 48 shifts and
 // byte moves for 8192 codes, 64 to make values signed, 48 for the scales, 32 products), of which the four
 // schedulers issue 0.54 a cycle with 12 warps and with 16; with all pages in L2 it is 3 % faster, loads alone take
-// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 118 us, 4.7 TB/s
+// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 117 us, 4.8 TB/s
 // (paged_attn.cu takes 311 us for the same in bf16); one sequence of 1,048,575 keys, 8/2 heads of 64, in
-// 46 us; 200 of up to 900 keys in 49 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 108 us.
+// 46 us; 200 of up to 900 keys in 48 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 108 us.
 #include "paged_row.cuh"
 
 #include <cuda_fp16.h>
@@ -494,17 +494,22 @@ struct Q4State {
       float slope2[kN][2];
 #pragma unroll
       for (int n = 0; n < kN; ++n) pair_of(queries + S::kOffUnit + RT * 4, n, slope2[n]);
-      bool small = rule.cap > 0.f;
+      bool series = rule.cap > 0.f;
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            z[u][n][i] *= factor[n][i & 1];
-            small &= fabsf(z[u][n][i] * rule.rcap) < kSeries;
-          }
-      const bool series = __all_sync(0xffffffffu, small);
+          for (int i = 0; i < 4; ++i) z[u][n][i] *= factor[n][i & 1];
+      if (series) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) series &= fabsf(z[u][n][i] * rule.rcap) < kSeries;
+        series = __all_sync(0xffffffffu, series);
+      }
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -945,13 +950,13 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
     rule.plain = a.softcap == 0.f && a.slopes == nullptr && a.scale >= 0.f;
     int slot = 0, next = S::kStages - 1;     // stages: of this tile, of the next one to issue
     int from = at.t, which = 0;
-    bool begin = true;
+    bool begin = true, seen = false;         // seen: this warp has seen a key of the segment
     do {
       if (begin) {
         rule.last = at.span.len - 1;
         from = at.t;
         st.start();
-        begin = false;
+        begin = seen = false;
         // the next segment's queries are brought near
         Portion<S> then = p;
         if (then.skip(a.paged, a.window, HR, share.end)) {
@@ -970,18 +975,27 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
       ld.issue(a, coming, ring + next * S::kStageBytes, masks + next);
       coming = ld.look_up(a, HR);
       const Mask mask = masks[slot];
-      if (mask)
+      if (mask) {
+        seen = true;
         st.tile(rule, queries + which * S::kQueries, ring + slot * S::kStageBytes,
                 at.span.base + at.t * S::kTile + tw * S::kKeys, mask);
+      }
+      slot = slot + 1 == S::kStages ? 0 : slot + 1;
+      next = next + 1 == S::kStages ? 0 : next + 1;
 
-      if (p.left == 1) {
+      if (p.left > 1) {
+        ++p.at.t;
+        --p.left;
+      } else {
         // join the warps' parts
+        const int read = slot == 0 ? S::kStages - 1 : slot - 1;
         const bool ends = at.t + 1 == at.span.tiles;
         int head, rows;
         head_of(at, head, rows);
         st.put_ml(ml + tw * RT);
         Portion<S> then = p;
-        if (ends && then.skip(a.paged, a.window, HR, share.end)) put_queries(then.at, which ^ 1);
+        const bool more = ends && then.skip(a.paged, a.window, HR, share.end);
+        if (more) put_queries(then.at, which ^ 1);
         Team::sync();
         const bool whole = ends && from == 0;
         const int part = worker * 2 + (from == 0 ? 1 : 0);
@@ -993,8 +1007,8 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
         };
         // Every warp's sums go to the stage that it has just read: no copy goes there until its
         // next tile.
-        uint8_t* const sums = smem + team * kTeamWarps * S::kRing + slot * S::kStageBytes;
-        st.put_o(reinterpret_cast<float*>(sums + tw * S::kRing), rows, top);
+        uint8_t* const sums = smem + team * kTeamWarps * S::kRing + read * S::kStageBytes;
+        if (seen) st.put_o(reinterpret_cast<float*>(sums + tw * S::kRing), rows, top);
         Team::sync();
         for (int e = Team::thread(); e < rows * (D / 4); e += S::kTeamThreads) {
           const int r = e / (D / 4), c = e % (D / 4) * 4;
@@ -1003,12 +1017,13 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
           float sum = 0.f;
 #pragma unroll
           for (int w = 0; w < kTeamWarps; ++w) {
+            const float2 z = ml[w * RT + r];
+            if (z.y == 0.f) continue;          // it has seen nothing of the row, and left no sums
             const float4 y = *reinterpret_cast<const float4*>(sums + w * S::kRing + (r * D + c) * 4);
             x.x += y.x;
             x.y += y.y;
             x.z += y.z;
             x.w += y.w;
-            const float2 z = ml[w * RT + r];
             sum = fmaf(z.y, exp2_fast(z.x - tp), sum);
           }
           // columns c + k of a row stand at c + (k ^ spread)
@@ -1040,10 +1055,9 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
         }
         begin = true;
         which ^= 1;
+        p = then;
+        if (more) p.enter(share.end); else p.left = 0;
       }
-      slot = slot + 1 == S::kStages ? 0 : slot + 1;
-      next = next + 1 == S::kStages ? 0 : next + 1;
-      p.step(a.paged, a.window, HR, share.end);
     } while (p.left > 0);
     copy_wait<0>();
     Team::sync();
