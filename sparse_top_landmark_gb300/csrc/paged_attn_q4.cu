@@ -33,9 +33,9 @@
 // Bound by instructions: a tile of 32 keys of 128 takes a warp some 580 (128 masks and 48 shifts and
 // byte moves for 8192 codes, 64 to make values signed, 48 for the scales, 32 products), of which the four
 // schedulers issue 0.54 a cycle with 12 warps and with 16; with all pages in L2 it is 3 % faster, loads alone take
-// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 117 us, 4.8 TB/s
+// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 115 us, 4.9 TB/s
 // (paged_attn.cu takes 311 us for the same in bf16); one sequence of 1,048,575 keys, 8/2 heads of 64, in
-// 46 us; 200 of up to 900 keys in 48 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 108 us.
+// 46 us; 200 of up to 900 keys in 43 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 105 us.
 #include "paged_row.cuh"
 
 #include <cuda_fp16.h>
@@ -49,19 +49,21 @@ constexpr float kBoost = 11.f, kMostSum = 32768.f;
 
 // Shared memory and shape of one instantiation; RT: query rows of a segment.
 //
-// A CTA has two teams of warps, each with a share of its own.  (128 sequences of up to 8192 keys, 32/8 heads of
-// 128: one share for 12 warps 153 us, two teams of 6 132; 256 of up to 300 keys: 70 and 41.)  Registers
+// A CTA has several teams of warps, each with a share of its own: two, or four where there are many segments (128
+// sequences of up to 8192 keys, 32/8 heads of 128: one share for 12 warps 153 us, two teams of 6 then 132, now 117,
+// four of 3 115; 256 of up to 300 keys: one team 70, two 39, four 31; in fp32, 256 of up to 500: two 55, four 48;
+// 128/8 heads, of 16 rows then: two 195, four 209).  Registers
 // hold 12 warps' state for heads of 128, 16 for smaller ones (a million keys, heads of 64: teams of 6
 // 48 us, of 8 46), 8 where rows are 16 or a factor is two values (fp32, 64 sequences of up to 8192 keys,
 // heads of 128: teams of 4 109 us, of 5 117; heads of 64: teams of 4 72, of 8 62).
 // A warp takes 64 keys of a tile (32, and three stages instead of two: 147 us for 124), and ending a segment
-// is worth one tile (none: fp32 116 us for 109; two: 123 for 119).
-template <typename T, int D, int RT>
+// is worth one tile (none: fp32 116 us for 109, four teams 131 for 115; two: 123 for 119, four teams 115.4).
+template <typename T, int D, int RT, int TEAMS>
 struct Q4Shape {
   static constexpr bool kSplit = std::is_same<T, float>::value;
-  static constexpr int kTeams = 2;
-  static constexpr int kTeamWarps = D == 128 ? (RT > 8 || kSplit ? 4 : 6) : RT > 8 ? 6 : 8;
-  static constexpr int kWarps = kTeams * kTeamWarps;
+  static constexpr int kTeams = TEAMS;
+  static constexpr int kWarps = D == 128 ? (RT > 8 || kSplit ? 8 : 12) : RT > 8 ? 12 : 16;
+  static constexpr int kTeamWarps = kWarps / kTeams;
   static constexpr int kThreads = kWarps * 32, kTeamThreads = kTeamWarps * 32;
   static constexpr int kKeys = 64;
   using Mask = unsigned long long;       // a bit a key
@@ -76,27 +78,28 @@ struct Q4Shape {
   static constexpr int kDecodedK = kKeys * kChunks * 4, kDecodedV = kSplit ? kDecodedK : 0;
   static constexpr int kDecoded = kDecodedK + kDecodedV;
   // a team's queries as right operands, [part][heads / 8][chunk][lane] of 16 bytes, what a product
-  // starts from, [heads / 8][chunk][lane % 4] of 16 bytes, and [heads] units and slopes; twice
+  // starts from, [heads / 8][chunk][lane % 4] of 16 bytes, and [heads] units and slopes; twice where there
+  // is room for it
   static constexpr int kN = RT / 8, kParts = kSplit ? 2 : 1;
   static constexpr int kOffStart = kParts * kN * kChunks * 512;
   static constexpr int kOffUnit = kOffStart + (kSplit ? 0 : kN * kChunks * 64);
-  static constexpr int kQueries = kOffUnit + RT * 8;
+  static constexpr int kQueries = kOffUnit + RT * 8, kQuerySets = kTeams == 4 && D == 128 ? 1 : 2;
   static constexpr int kRest = kWarps * (kDecoded + RT * 8) +
-                               kTeams * (2 * kQueries + 2 * (int)sizeof(Join) + 16);
+                               kTeams * (kQuerySets * kQueries + 2 * (int)sizeof(Join) + 16);
   static constexpr int kFit = (232448 - 16 - kRest) / (kWarps * (kStageBytes + (int)sizeof(Mask)));
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kJoinBytes = kTeamWarps * kRing;                   // a team's
   static constexpr int kOffDecoded = kWarps * kRing;                      // [warps]
-  static constexpr int kOffQueries = kOffDecoded + kWarps * kDecoded;     // [teams][2]
-  static constexpr int kOffMl = kOffQueries + kTeams * 2 * kQueries;      // [teams][team's warps][RT][2]
+  static constexpr int kOffQueries = kOffDecoded + kWarps * kDecoded;     // [teams][sets]
+  static constexpr int kOffMl = kOffQueries + kTeams * kQuerySets * kQueries;      // [teams][team's warps][RT][2]
   static constexpr int kOffMask = kOffMl + kWarps * RT * 8;               // [warps][stages]
   static constexpr int kOffJoins = kOffMask + (kWarps * kStages * (int)sizeof(Mask) + 15) / 16 * 16;
   static constexpr int kOffBase = kOffJoins + kTeams * 2 * (int)sizeof(Join);
   static constexpr int kBytes = kOffBase + kTeams * 16;
   static_assert(kBytes <= 232448 && kStages >= 2 && kStageBytes % 16 == 0, "shared memory");
   static_assert(RT * D * 4 <= kStageBytes, "a warp's sums in one of its stages");
-  static_assert(kTeams <= 2, "two shares to a counter");
+  static_assert(kTeams == 2 || kTeams == 4, "a counter's fields");
   __device__ __forceinline__ static int warp() { return (threadIdx.x >> 5) % kTeamWarps; }
 };
 
@@ -225,9 +228,9 @@ __device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&x)[N]) {
 // (lane % 4) * 2, + 1 of each eight query heads; in the value tile the four value columns
 // 4 (lane / 4) .. + 3 of every chunk and the same heads.
 // ---------------------------------------------------------------------------
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, int TEAMS>
 struct Q4State {
-  using S = Q4Shape<T, D, RT>;
+  using S = Q4Shape<T, D, RT, TEAMS>;
   static constexpr bool kSplit = std::is_same<T, float>::value;
   static constexpr int kParts = kSplit ? 2 : 1;      // fp16 values that a factor is given as
   static constexpr int kN = RT / 8, kC = S::kChunks;
@@ -755,9 +758,9 @@ struct Portion {
 // ---------------------------------------------------------------------------
 // The warp's loader: rows and scales as they lie, 16 keys of a page at a time (a page holds as many).
 // ---------------------------------------------------------------------------
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, int TEAMS>
 struct Q4Loader {
-  using S = Q4Shape<T, D, RT>;
+  using S = Q4Shape<T, D, RT, TEAMS>;
   using Mask = typename S::Mask;
   static constexpr Mask kAll = (Mask)(~0ull >> (64 - S::kKeys));
   static constexpr int kEach = S::kKeys / 32;      // keys whose page a lane looks up
@@ -853,25 +856,32 @@ struct Q4Loader {
 };
 
 // Counts a part of the segment that share c0 begins, of n parts in all, as count_up does; returns those
-// counted before.  Two shares have one counter, c0 / 2, which is enough: where the even one's last
-// segment has more than two parts, the odd one begins none.  Two parts of the even one's are counted
-// by 1, all else by 4.
+// counted before.  A CTA's shares have one counter, which is enough: segments of at most TEAMS parts
+// that one of them but the last begins have a field each (a bit or two more than their parts need), and of
+// all others there is one at most, since shares inside of a segment begin none.
+template <int TEAMS>
 __device__ __forceinline__ int count_part(unsigned long long* counters, int c0, int n,
                                           unsigned long long base) {
-  const bool two = c0 % 2 == 0 && n == 2;
-  unsigned long long* const counter = counters + c0 / 2;
+  constexpr int kBits = TEAMS == 2 ? 2 : 3, kRest = (TEAMS - 1) * kBits;
+  static_assert(TEAMS < 1 << kBits, "a field holds its parts");
+  const int which = c0 % TEAMS, shift = which < TEAMS - 1 && n <= TEAMS ? which * kBits : kRest;
+  unsigned long long* const counter = counters + c0 / TEAMS;
   unsigned long long old;
   asm volatile("red.relaxed.gpu.global.max.u64 [%0], %1;" ::"l"(counter), "l"(base) : "memory");
   asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;"
                : "=l"(old)
-               : "l"(counter), "l"(two ? 1ull : 4ull)
+               : "l"(counter), "l"(1ull << shift)
                : "memory");
-  const int count = (int)(old - base);
-  return two ? count & 3 : count >> 2;
+  const int count = (int)(old - base) >> shift;
+  return shift < kRest ? count & ((1 << kBits) - 1) : count;
+}
+// The most parts that the rest of a counter's bits can count.
+constexpr int most_parts(int teams) {
+  return (1 << (kCountBits - (teams - 1) * (teams == 2 ? 2 : 3))) - 1;
 }
 
-// As paged_attn_kernel (paged_row.cuh), with two shares to a CTA, each a team of warps': ends of segments
-// are some thousand cycles of latency, during which the other team has the SM.  And each team has its
+// As paged_attn_kernel (paged_row.cuh), with several shares to a CTA, each a team of warps': ends of segments
+// are some thousand cycles of latency, during which other teams have the SM.  And each team has its
 // queries in shared memory, put there by a warp for each chunk while the segment before ends.
 template <typename K>
 __global__ void __launch_bounds__(K::S::kThreads, 1)
@@ -888,7 +898,8 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
   const int worker = blockIdx.x * S::kTeams + team, workers = gridDim.x * S::kTeams;
   const int HR = a.Hkv * a.row_blocks, Hq = a.Hkv * a.G;
   const uint32_t ring = smem_addr(smem) + warp * S::kRing;
-  const uint32_t queries = smem_addr(smem) + S::kOffQueries + team * 2 * S::kQueries;
+  constexpr int kSets = S::kQuerySets;
+  const uint32_t queries = smem_addr(smem) + S::kOffQueries + team * kSets * S::kQueries;
   float2* const ml = reinterpret_cast<float2*>(smem + S::kOffMl) + team * kTeamWarps * RT;
   Mask* const masks = reinterpret_cast<Mask*>(smem + S::kOffMask) + warp * S::kStages;
   // of the segment that another share begins, and of the one that another share ends
@@ -995,8 +1006,9 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
         st.put_ml(ml + tw * RT);
         Portion<S> then = p;
         const bool more = ends && then.skip(a.paged, a.window, HR, share.end);
-        if (more) put_queries(then.at, which ^ 1);
+        if (more && kSets == 2) put_queries(then.at, which ^ 1);
         Team::sync();
+        if (more && kSets == 1) put_queries(then.at, 0);
         const bool whole = ends && from == 0;
         const int part = worker * 2 + (from == 0 ? 1 : 0);
         auto top = [&](int r) {
@@ -1050,11 +1062,11 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
           // others go on meanwhile): the count is asked for now, and looked at then.
           const int c0 = from == 0 ? worker : share_of(at.segment, share.row, workers);
           const int n = share_of(at.segment + at.span.tiles - 1, share.row, workers) - c0 + 1;
-          const bool last = count_part(a.counters, c0, n, *base) == n - 1;
+          const bool last = count_part<S::kTeams>(a.counters, c0, n, *base) == n - 1;
           joins[from == 0] = {(long long)at.s * Hq + head, c0, last ? n : 0, rows, 0};
         }
         begin = true;
-        which ^= 1;
+        which = (which + 1) % kSets;
         p = then;
         if (more) p.enter(share.end); else p.left = 0;
       }
@@ -1081,34 +1093,47 @@ paged_attn_q4_kernel(const __grid_constant__ typename K::Args a) {
   }
 }
 
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, int TEAMS>
 struct Q4 {
   using Type = T;
   using Args = PagedAttnQ4Args<T>;
-  using S = Q4Shape<T, D, RT>;
-  using State = Q4State<T, D, RT>;
-  using Ld = Q4Loader<T, D, RT>;
+  using S = Q4Shape<T, D, RT, TEAMS>;
+  using State = Q4State<T, D, RT, TEAMS>;
+  using Ld = Q4Loader<T, D, RT, TEAMS>;
   using Team = Q4Team<S>;
   static constexpr int kD = D, kRT = RT;
   static auto kernel() { return paged_attn_q4_kernel<Q4>; }
 };
 
+// Four teams where there are that many segments, and the counters hold a segment's parts (tables of up to 24384
+// tokens, of 32512 for smaller heads); 16 rows are better off with two.
+template <typename T, int D, int RT, typename F>
+auto with_teams(int Hkv, int G, int S, int width, int page_log2, int sms, F f) {
+  if constexpr (RT == 8) {
+    using Four = Q4<T, D, RT, 4>;
+    const long long segments = (long long)S * Hkv * ((G + RT - 1) / RT);
+    const long long tiles = (((long long)width << page_log2) + Four::S::kTile - 1) / Four::S::kTile;
+    if (segments >= 3LL * sms && tiles <= most_parts(4)) return f(Run<Four>{});
+  }
+  return f(Run<Q4<T, D, RT, 2>>{});
+}
+
 // A CTA takes 8 query rows, in bf16 16 where the group has more (128 sequences of up to 8192 keys, 128/8 heads
 // of 128: 201 us, two segments of 8 rows 240; 64/4 heads of 32: 32 and 40); larger groups take several CTAs.
-template <typename T, int RT, typename F>
-auto with_dim(int d, F f) {
-  switch (d) {
-    case 32: return f(Run<Q4<T, 32, RT>>{});
-    case 64: return f(Run<Q4<T, 64, RT>>{});
-    default: return f(Run<Q4<T, 128, RT>>{});
-  }
-}
 template <typename T, typename F>
-auto with_shape(int d, int G, F f) {
+auto with_shape(int d, int Hkv, int G, int S, int width, int page_log2, int sms, F f) {
+  auto dim = [&](auto rt) {
+    constexpr int RT = decltype(rt)::value;
+    switch (d) {
+      case 32: return with_teams<T, 32, RT>(Hkv, G, S, width, page_log2, sms, f);
+      case 64: return with_teams<T, 64, RT>(Hkv, G, S, width, page_log2, sms, f);
+      default: return with_teams<T, 128, RT>(Hkv, G, S, width, page_log2, sms, f);
+    }
+  };
   if constexpr (std::is_same<T, bf16>::value) {
-    if (G > 8) return with_dim<T, 16>(d, f);
+    if (G > 8) return dim(std::integral_constant<int, 16>{});
   }
-  return with_dim<T, 8>(d, f);
+  return dim(std::integral_constant<int, 8>{});
 }
 
 }  // namespace
@@ -1116,12 +1141,14 @@ auto with_shape(int d, int G, F f) {
 size_t paged_attn_q4_ws_bytes(int d, int Hkv, int G, int S, int width, int page_log2, int is_f32,
                               int sms) {
   auto bytes = [&](auto run) { return run.bytes(Hkv, G, S, width, page_log2, sms); };
-  return is_f32 ? with_shape<float>(d, G, bytes) : with_shape<bf16>(d, G, bytes);
+  return is_f32 ? with_shape<float>(d, Hkv, G, S, width, page_log2, sms, bytes)
+                : with_shape<bf16>(d, Hkv, G, S, width, page_log2, sms, bytes);
 }
 
 template <typename T>
 cudaError_t launch_paged_attn_q4(PagedAttnQ4Args<T> a, int d, void* ws, int sms, cudaStream_t st) {
-  return with_shape<T>(d, a.G, [&](auto run) { return run.launch(a, ws, sms, st); });
+  return with_shape<T>(d, a.Hkv, a.G, a.paged.S, a.paged.width, a.paged.page_log2, sms,
+                       [&](auto run) { return run.launch(a, ws, sms, st); });
 }
 
 template cudaError_t launch_paged_attn_q4<float>(PagedAttnQ4Args<float>, int, void*, int,

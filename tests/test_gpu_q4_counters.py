@@ -1,5 +1,5 @@
 """The counters in the workspace of mita_paged_attn_q4: as in mita_paged_attn's (test_gpu_paged_counters.py),
-255 words under the number of the call that counted last, each for two shares of a CTA."""
+255 words under the number of the call that counted last, each for the two or four shares of a CTA."""
 import pytest
 import torch
 
@@ -43,7 +43,10 @@ def counters(mita):
 # one share's segments, segments of two shares and of many, cut at every place
 SHAPES = [((1,), 1, 1, 64), ((0, 0), 4, 2, 32), ((3000,), 8, 2, 128), ((200000, 5, 0, 7000), 4, 2, 64),
           ((90000,), 16, 1, 128), (tuple(200 + i * 29 % 900 for i in range(400)), 4, 1, 32),
-          (tuple(384 * (1 + i % 3) for i in range(211)), 4, 1, 128)]
+          (tuple(384 * (1 + i % 3) for i in range(211)), 4, 1, 128),
+          # as many segments as make four shares to a CTA, of one part, of two to six, of a hundred
+          (tuple(1 + i * 37 % 400 for i in range(330)), 4, 1, 128), ((20000,) + (1,) * 400, 8, 1, 128),
+          (tuple(200 * (1 + i % 7) for i in range(310)), 20, 2, 64), ((24000, 3, 24000) + (180,) * 304, 2, 1, 32)]
 
 
 def scale_of_values():
@@ -112,12 +115,13 @@ def test_calls_are_numbered_whatever_their_shapes(dt):
             assert int(after[-1]) - int(before[-1]) == STEP and int(after[-1]) % STEP == 0
             number = int(after[-1]) // STEP - 1
             assert int((after[:-1] >> BITS).max()) <= number
-            # 4 for each of at most 510 parts, and two parts of 1
-            assert int((after[:-1] & ((1 << BITS) - 1)).max()) <= 4 * 510 + 2
+            # two shares: two parts of 1, and 4 for each of at most 510; four: up to four parts of 1, 8 and 64,
+            # and 512 for each of at most 127
+            assert int((after[:-1] & ((1 << BITS) - 1)).max()) <= 512 * 127 + 4 * (64 + 8 + 1)
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("shape", SHAPES[2:5] + SHAPES[6:], ids=lambda s: f"{len(s[0])}x{max(s[0])}-{s[1:]}")
+@pytest.mark.parametrize("shape", SHAPES[2:5] + SHAPES[6:9], ids=lambda s: f"{len(s[0])}x{max(s[0])}-{s[1:]}")
 def test_what_a_disturbed_call_leaves_does_not_count(shape, dt):
     """Counts as a call would leave them whose lengths changed while it ran, under that call's number: the
     next call, and a call after a very great many, is right."""
