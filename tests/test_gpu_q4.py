@@ -150,6 +150,7 @@ def test_append_nothing_and_bad_slots():
 # attention
 # --------------------------------------------------------------------------------------------
 EDGES = (0, 1, 2, 15, 16, 17, 31, 32, 33, 65, 129, 255, 256, 257, 0, 513)
+MANY = tuple(430 if i % 19 == 7 else i * 53 % 60 for i in range(120))
 ATTN = [
     # lengths, Hq, Hkv, d, page, dtype, options
     ((1,), 1, 1, 64, 16, "bf16", {}),
@@ -188,6 +189,12 @@ ATTN = [
     # many short sequences: several segments to a CTA
     (tuple(1 + i * 37 % 100 for i in range(130)), 2, 2, 64, 16, "bf16", {}),
     (tuple(i * 29 % 40 for i in range(400)), 4, 1, 32, 16, "f32", {}),
+    # so many that a CTA has four shares
+    (MANY, 12, 4, 128, 16, "bf16", {"window": 333, "softcap": 5.0, "slopes": True}),
+    (MANY, 4, 4, 128, 16, "f32", {"window": 200}),
+    (MANY, 8, 4, 128, 16, "bf16", {}),
+    (MANY, 36, 4, 64, 32, "f32", {"slopes": True}),
+    (tuple(i * 29 % 90 for i in range(480)), 5, 1, 32, 16, "bf16", {"softcap": 2.0}),
 ]
 _caches = {}
 

@@ -45,8 +45,9 @@ SHAPES = [((1,), 1, 1, 64), ((0, 0), 4, 2, 32), ((3000,), 8, 2, 128), ((200000, 
           ((90000,), 16, 1, 128), (tuple(200 + i * 29 % 900 for i in range(400)), 4, 1, 32),
           (tuple(384 * (1 + i % 3) for i in range(211)), 4, 1, 128),
           # as many segments as make four shares to a CTA, of one part, of two to six, of a hundred
-          (tuple(1 + i * 37 % 400 for i in range(330)), 4, 1, 128), ((20000,) + (1,) * 400, 8, 1, 128),
-          (tuple(200 * (1 + i % 7) for i in range(310)), 20, 2, 64), ((24000, 3, 24000) + (180,) * 304, 2, 1, 32)]
+          (tuple(1 + i * 37 % 400 for i in range(470)), 4, 1, 128), ((20000,) + (1,) * 480, 8, 1, 128),
+          (tuple(200 * (1 + i % 7) for i in range(310)), 14, 2, 64), ((24000, 3, 24000) + (180,) * 454, 2, 1, 32),
+          ((33000,) + (1,) * 500, 3, 1, 64)]          # a table too wide for four
 
 
 def scale_of_values():
