@@ -35,7 +35,7 @@
 // schedulers issue 0.54 a cycle with 12 warps and with 16; with all pages in L2 it is 3 % faster, loads alone take
 // four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 115 us, 4.9 TB/s
 // (paged_attn.cu takes 311 us for the same in bf16); one sequence of 1,048,575 keys, 8/2 heads of 64, in
-// 46 us; 200 of up to 900 keys in 43 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 105 us.
+// 45 us; 200 of up to 900 keys in 43 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 105 us.
 #include "paged_row.cuh"
 
 #include <cuda_fp16.h>
@@ -604,8 +604,10 @@ struct Q4State {
           for (int i = 0; i < 2; ++i)
             pt[u][n][i] = turn8(pack_half(p[u][n][2 * i], p[u][n][2 * i + 1]));
     }
-    // two units' values at a time
-#pragma unroll 1
+    // two units' values at a time; in a loop where heads are large (128: 124 us so, 127 unrolled; a million
+    // keys of 64: 45.9 and 45.0)
+    constexpr int kUnroll = D <= 64 ? 2 : 1;
+#pragma unroll kUnroll
     for (int v0 = 0; v0 < kU; v0 += 2) {
 #pragma unroll
       for (int c0 = 0; c0 < kC; c0 += kP) {
