@@ -14,28 +14,39 @@
 // - keys (bf16): as the bits of an fp16 number a code n is the subnormal n * 2^-24 and n << 4 is 16 n * 2^-24;
 //   the 16 is taken out of the queries (an exact division), and the 8 out of the sum where it begins:
 //   z = sum over chunks c of s_c (-8 sum_i q_i + sum_i n_i q_i).
-// - values, and keys in fp32: one fp16 instruction more makes n - 8 of it.  (The tensor cores cut sums.
+// - values, and keys in fp32: one instruction more makes n - 8 of it.  (The tensor cores cut sums.
 //   Taken as n p from a sum of -8 p, a long context's values, which nearly cancel, lean by 2^-23 of
 //   eight times the sum of the weights for every product: 4.8e-6 of an fp32 result at 1000 keys, 1e-3 at a
 //   million.  With a sum of its own for 8 p they do not lean, for 2 % less time, but where a key of value zero has
 //   nearly all the weight, what is left of the others is off by 2^-21 of that key's scale: not kept.)  Of two
-//   codes of a word the lower one is taken alone and both as a byte, from whose sums the lower one's
-//   are taken at the end: an instruction less for four values.
+//   codes of a word the bf16 twin takes the lower one alone and both as a byte, from whose sums the lower
+//   one's are taken at the end: an instruction less for four values.
 //
-// Queries are scaled by a power of two, their row's largest to 2^14, so that fp16 holds what bf16 does,
-// down to 2^-38 of it; weights p are at most 2^15, so that fp16's subnormals begin at 2^-29 of a
-// weight's range.  Scales are at most 2 mostly, and p s then stays below fp16's end; where a tile holds
-// a larger one, its weights are made smaller by a power of two that is put back where the tile's sums are
-// added to the running ones (in fp32, outside the tensor cores: paged_attn.cu says why).  The bf16 twin
-// rounds a weight and its product with the scale to fp16's 11 bits; the fp32 twin gives every query and
-// every p s as a sum of two fp16 values, 22 bits.
+// Queries are scaled by a power of two, their row's largest to 2^14, so that fp16 holds what bf16 does, down
+// to 2^-34 of it; in fp32 they are sums of two fp16 values, 22 bits.
 //
-// Bound by instructions: a tile of 32 keys of 128 takes a warp some 580 (128 masks and 48 shifts and
-// byte moves for 8192 codes, 64 to make values signed, 48 for the scales, 32 products), of which the four
-// schedulers issue 0.54 a cycle with 12 warps and with 16; with all pages in L2 it is 3 % faster, loads alone take
-// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 115 us, 4.9 TB/s
+// Weights and scales meet in these ways, since most of the weight may be on keys whose values are small or
+// zero, and what the others add is then a small part of a weight's range, or of a scale's:
+//
+// - bf16: a weight p goes into fp16 times the power of two w of its key's largest scale, and the scale
+//   divided by it, 11 bits for the one and again for their product.  The running maximum is p w's, which
+//   is 2^10 to 2^14 where it is rounded, so that fp16's subnormals begin at 2^-24 of it; a key
+//   without values has w = 0.  Only a block 2^-21 times its own row's largest loses bits by itself.  (With p
+//   and the scale as they are: an output is off by 3 % where a key of value zero stands 15 above the others and
+//   their scales are 2^-13, in fp32 with two values for a product too.  With two bf16 values for a
+//   weight, as below, decode_batch's 120 us are 138: tensor cores.  With one w for a tile whose scales are near each
+//   other: 130, the two ways being a branch in the middle of a tile.)
+// - fp32: a weight is a sum of three bf16 values, which have fp32's exponents, and the scale is with the
+//   code: (n - 8) s has seven bits.
+//
+// A tile's sums are added to the running ones in fp32, outside the tensor cores: paged_attn.cu says why.
+//
+// Bound by instructions and their latency: three warps a scheduler issue 0.54 a cycle.  A tile of 32 keys of
+// 128 takes a warp some 600 (128 masks and 48 shifts and byte moves for 8192 codes, 64 to make values signed, 48 for
+// the scales, 32 products); with all pages in L2 it is 3 % faster, loads alone take
+// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 120 us, 4.7 TB/s
 // (paged_attn.cu takes 311 us for the same in bf16); one sequence of 1,048,575 keys, 8/2 heads of 64, in
-// 45 us; 200 of up to 900 keys in 43 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 105 us.
+// 47 us; 200 of up to 900 keys in 45 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 104 us.
 #include "paged_row.cuh"
 
 #include <cuda_fp16.h>
@@ -43,9 +54,10 @@
 namespace mita {
 namespace {
 
-// The running maximum is looked for again only where a lane's weights add up to more than 2^15; the largest
-// weight is then 2^11, so that a tile's eight of a lane stay below that.
-constexpr float kBoost = 11.f, kMostSum = 32768.f;
+// The running maximum is looked for again only where a lane's weights add up to more than 2^14; the largest
+// weight is then 2^10, so that a tile's eight of a lane stay below that.  (bf16: weights times their keys' powers of
+// two; weights alone may come to 2^100 where those differ, the largest then being 2^96.)
+constexpr float kBoost = 10.f, kMostSum = 16384.f, kRoom = 96.f, kMostWeight = 1.2676506e30f;
 
 // Shared memory and shape of one instantiation; RT: query rows of a segment.
 //
@@ -73,10 +85,9 @@ struct Q4Shape {
   static constexpr int kRowBytes = D / 2;
   static constexpr int kCodes = kKeys * kRowBytes, kScales = kKeys * kChunks;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);      // K's codes, V's, K's scales, V's
-  // a warp's decoded scales: K's in fp32, V's in fp32 or (where the scales' bytes stood in the stage) in
-  // fp16, of two keys side by side
-  static constexpr int kDecodedK = kKeys * kChunks * 4, kDecodedV = kSplit ? kDecodedK : 0;
-  static constexpr int kDecoded = kDecodedK + kDecodedV;
+  // a warp's decoded scales: K's in fp32, V's in 16 bits, two keys side by side (with a number more each, or in
+  // bf16 where the scales' bytes stood in the stage)
+  static constexpr int kDecodedK = kKeys * kChunks * 4, kDecoded = kDecodedK * (kSplit ? 2 : 1);
   // a team's queries as right operands, [part][heads / 8][chunk][lane] of 16 bytes, what a product
   // starts from, [heads / 8][chunk][lane % 4] of 16 bytes, and [heads] units and slopes; twice where there
   // is room for it
@@ -132,6 +143,19 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
                                         const uint32_t* b) {
   mma_f16(c, a0, a1, a2, a3, b, c[0], c[1], c[2], c[3]);
 }
+// the same with bf16 products
+__device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         const uint32_t* b, float c0, float c1, float c2, float c3) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         const uint32_t* b) {
+  mma_bf16(c, a0, a1, a2, a3, b, c[0], c[1], c[2], c[3]);
+}
 // An 8 x 8 matrix of 16-bit values, transposed (paged_row.cuh's, free to be moved among the products).
 __device__ __forceinline__ uint32_t turn8(uint32_t x) {
   uint32_t y;
@@ -156,6 +180,20 @@ __device__ __forceinline__ uint32_t mul_half(uint32_t a, uint32_t b) {
                             *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t fma_bf(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 // Codes 0 and 1 of the two 16-bit words of x (of x >> 8: 2 and 3), as fp16 numbers n * 2^-24 and
 // 16 n * 2^-24, or, kSigned, both as (n - 8) * 2^-9.
 template <bool kSigned>
@@ -171,6 +209,16 @@ __device__ __forceinline__ uint32_t code_hi(uint32_t x) {
 // A pair of codes of each word, as a byte n1 n0: (16 (n1 - 8) + n0 - 8) * 2^-13
 __device__ __forceinline__ uint32_t code_pair(uint32_t x) {
   return fma_half(x, 0x68006800u, 0xa440a440u);                     // * 2^11 - 136 * 2^-13
+}
+// Codes 0 and 1 of the two words of x as values in bf16: a code n is the subnormal n * 2^-133, m its scale times
+// 2^112 (bf16, a key each), so that these are (n - 8) s 2^-21 and 16 (n - 8) s 2^-21, seven bits and exact.
+// less: value_less(m).
+__device__ __forceinline__ uint32_t value_less(uint32_t m) { return mul_bf(m, 0x80088008u); }     // -8 * 2^-133 m
+__device__ __forceinline__ uint32_t value_lo(uint32_t x, uint32_t m, uint32_t less) {
+  return fma_bf(x & 0x000f000fu, m, less);
+}
+__device__ __forceinline__ uint32_t value_hi(uint32_t x, uint32_t m, uint32_t less) {
+  return fma_bf(x & 0x00f000f0u, m, mul_bf(less, 0x41804180u));     // 16 of them
 }
 
 // The scale bytes of a row.
@@ -188,6 +236,20 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t base, int key) {
 // The four (two, one) scales of a word as fp16 values: chunks 0 and 2, chunks 1 and 3.
 __device__ __forceinline__ uint32_t scales_02(uint32_t w) { return (w & 0x00ff00ffu) << 7; }
 __device__ __forceinline__ uint32_t scales_13(uint32_t w) { return w >> 1 & 0x7f807f80u; }
+// The largest scale byte of a row, infinities and NaN (248 and above) left out.
+template <int kChunks>
+__device__ __forceinline__ uint32_t largest_scale(uint32_t w) {
+  w &= ~((((w & 0x7f7f7f7fu) + 0x08080808u & w & 0x80808080u) >> 7) * 255u);
+  if constexpr (kChunks == 4) w = __vmaxu2(w & 0x00ff00ffu, w >> 8 & 0x00ff00ffu);
+  return kChunks == 4 ? max(w & 0xffu, w >> 16) : kChunks == 2 ? max(w & 0xffu, w >> 8) : w;
+}
+// The same times 2^112 in bf16, whose bits are a scale's 2^-112 times as large; a NaN's become an infinity,
+// which makes NaN of every code.
+__device__ __forceinline__ uint32_t factors(uint32_t bits) {
+  return mul_bf(mul_bf(bits, 0x77807780u), 0x77807780u);            // 2^112 twice
+}
+__device__ __forceinline__ uint32_t factors_02(uint32_t w) { return factors((w & 0x00ff00ffu) << 4); }
+__device__ __forceinline__ uint32_t factors_13(uint32_t w) { return factors(w >> 4 & 0x0ff00ff0u); }
 
 __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
   unsigned long long r;
@@ -232,7 +294,8 @@ template <typename T, int D, int RT, int TEAMS>
 struct Q4State {
   using S = Q4Shape<T, D, RT, TEAMS>;
   static constexpr bool kSplit = std::is_same<T, float>::value;
-  static constexpr int kParts = kSplit ? 2 : 1;      // fp16 values that a factor is given as
+  static constexpr int kParts = kSplit ? 2 : 1;      // fp16 values that a query is given as
+  static constexpr int kWeights = kSplit ? 3 : 1;    // values that a weight is given as
   static constexpr int kN = RT / 8, kC = S::kChunks;
   // 16 keys are a unit of work, kU of them are worked on together (as many as registers hold: 16 rows of 128
   // have 8 warps; 196 us for 201, and 28.5 for 26.2 with 16 rows of 64), and kP chunks
@@ -345,11 +408,12 @@ struct Q4State {
   }
 
   // Every lane decodes the scales of two keys (the lanes that use a key's are many: 4 its K's, 8 its V's):
-  // from `ks`, K's bytes and then V's, to `sk`, K's as fp32, and `sv`.  A value's scale of a key that is not
-  // seen is zero, whatever the row holds.  Returns the largest upper five bits of a value's scale, or
-  // less than 16.
-  __device__ __forceinline__ static unsigned decode_scales(uint32_t ks, uint32_t sk, uint32_t sv,
-                                                           typename S::Mask mask) {
+  // from `ks`, K's bytes and then V's, to `sk`, K's as fp32, and V's to `sv`: as value_lo takes them, or, in
+  // bf16, times the power of two that brings the row's largest to 2 to 4, whose inverse (zero for a row of
+  // zeros) is `unit`, of keys `lane` and `lane` + 32.  A value's scale of a key that is not seen is zero,
+  // whatever the row holds.
+  __device__ __forceinline__ static void decode_scales(uint32_t ks, uint32_t sk, uint32_t sv,
+                                                       typename S::Mask mask, float (&unit)[2]) {
     const int lane = threadIdx.x & 31;
     constexpr int kH = S::kKeys / 32;
     uint32_t wk[kH], wv[kH];
@@ -375,37 +439,46 @@ struct Q4State {
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       put(sk + h * 128 * kC, wk[h]);
+      // of two keys, [pair][chunk]: each of the two writes half
+      uint32_t even, odd = 0;
       if constexpr (kSplit) {
-        put(sv + h * 128 * kC, wv[h]);
-      } else {                       // as fp16 of two keys, [pair][chunk]: each of the two writes half
-        const uint32_t to = sv + h * 64 * kC;
-        const uint32_t even = scales_02(wv[h]), odd = scales_13(wv[h]);
-        const uint32_t even2 = __shfl_xor_sync(0xffffffffu, even, 1);
-        const bool second = lane & 1;
-        if constexpr (kC == 1) {
-          if (!second) store_shared(to + lane / 2 * 4, __byte_perm(even, even2, 0x5410));
+        even = factors_02(wv[h]);
+        if constexpr (kC > 1) odd = factors_13(wv[h]);
+      } else {
+        const uint32_t top = largest_scale<kC>(wv[h]), e = max(top >> 3, 1u);
+        const uint32_t by = ((31u - e) << 10) * 0x10001u;                // 2^(16 - e)
+        even = mul_half(scales_02(wv[h]), by);
+        if constexpr (kC > 1) odd = mul_half(scales_13(wv[h]), by);
+        unit[h] = __uint_as_float(top == 0 ? 0u : (e - 16 + 127) << 23);
+      }
+      const uint32_t even2 = __shfl_xor_sync(0xffffffffu, even, 1);
+      const bool second = lane & 1;
+      constexpr int kEach = kSplit ? 8 : 4;            // bytes of a pair's chunk
+      const uint32_t to = sv + (16 * h + lane / 2) * kC * kEach;
+      if constexpr (kC == 1) {
+        if (!second) put_factor(to, __byte_perm(even, even2, 0x5410));
+      } else {
+        const uint32_t odd2 = __shfl_xor_sync(0xffffffffu, odd, 1);
+        if constexpr (kC == 2) {
+          put_factor(to + (second ? kEach : 0), second ? __byte_perm(odd2, odd, 0x5410)
+                                                       : __byte_perm(even, even2, 0x5410));
         } else {
-          const uint32_t odd2 = __shfl_xor_sync(0xffffffffu, odd, 1);
-          if constexpr (kC == 2) {
-            store_shared(to + lane * 4, second ? __byte_perm(odd2, odd, 0x5410)
-                                               : __byte_perm(even, even2, 0x5410));
+          const uint32_t sel = second ? 0x3276u : 0x5410u;      // upper halves, or lower ones
+          const uint32_t m0 = __byte_perm(even, even2, sel), m1 = __byte_perm(odd, odd2, sel);
+          const uint32_t at = to + (second ? 2 * kEach : 0);
+          if constexpr (kSplit) {
+            const uint32_t x[4] = {m0, value_less(m0), m1, value_less(m1)};
+            store_shared(at, x);
           } else {
-            const uint32_t sel = second ? 0x3276u : 0x5410u;      // upper halves, or lower ones
-            store_shared(to + lane * 8, __byte_perm(even, even2, sel), __byte_perm(odd, odd2, sel));
+            store_shared(at, m0, m1);
           }
         }
       }
     }
     __syncwarp();
-    unsigned most = 0;
-    if (__any_sync(0xffffffffu, (wv[0] | wv[kH - 1]) & 0x80808080u)) {
-#pragma unroll
-      for (int h = 0; h < kH; ++h)
-#pragma unroll
-        for (int c = 0; c < kC; ++c) most = max(most, (wv[h] >> (8 * c + 3)) & 31u);
-      most = __reduce_max_sync(0xffffffffu, most);
-    }
-    return most;
+  }
+  __device__ __forceinline__ static void put_factor(uint32_t at, uint32_t m) {
+    if constexpr (kSplit) store_shared(at, m, value_less(m)); else store_shared(at, m);
   }
 
   // z += scale * (codes . q) of 16 keys, x their words of a chunk, q the chunk's queries, `from` what
@@ -441,17 +514,18 @@ struct Q4State {
     const uint32_t ks = stage + 2 * S::kCodes;
     const uint32_t sk = smem_addr(smem) + S::kOffDecoded + (threadIdx.x >> 5) * S::kDecoded;
     const uint32_t sv = kSplit ? sk + S::kDecodedK : ks;
-    const unsigned most = decode_scales(ks, sk, sv, mask);
+    float unit[2];
+    decode_scales(ks, sk, sv, mask, unit);
 #pragma unroll 1
     for (int u = 0; u < S::kKeys / 16; u += kU)
-      units(rule, queries, stage, sk, sv, u, key0 + 16 * u,
-            mask >> (16 * u) & (~0ull >> (64 - 16 * kU)), most);
+      work(rule, queries, stage, sk, sv, unit, u, key0 + 16 * u,
+            mask >> (16 * u) & (~0ull >> (64 - 16 * kU)));
   }
 
-  // units u0 .. u0 + kU - 1; mask: their seen keys; most: decode_scales'
-  __device__ __forceinline__ void units(const ScoreRule& rule, uint32_t queries, uint32_t stage,
-                                        uint32_t sk, uint32_t sv, int u0, int key0,
-                                        typename S::Mask mask, unsigned most) {
+  // units of 16 keys u0 .. u0 + kU - 1; mask: their seen keys; sk, sv, unit2: decode_scales'
+  __device__ __forceinline__ void work(const ScoreRule& rule, uint32_t queries, uint32_t stage,
+                                      uint32_t sk, uint32_t sv, const float (&unit2)[2], int u0, int key0,
+                                       typename S::Mask mask) {
     if (kU < S::kKeys / 16 && mask == 0) return;
     const int lane = threadIdx.x & 31;
     const uint32_t vt = stage + S::kCodes;
@@ -529,36 +603,49 @@ struct Q4State {
 #pragma unroll
       for (int n = 0; n < kN; ++n) factor[n][0] = factor[n][1] = 1.f;
     }
-    float drop = 0.f, up = 1.f;      // of the weights, so that their products with the scales stay finite
-    if (most >= 16) {
-      drop = (float)((int)most - 15);
-      up = __uint_as_float((most - 15 + 127) << 23);
+    float unit[kU][2];               // of keys lane / 4 and + 8
+    if constexpr (!kSplit) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          unit[u][i] = __shfl_sync(0xffffffffu, kU == 4 ? unit2[u / 2] : u0 ? unit2[1] : unit2[0],
+                                   lane / 4 + 8 * i + 16 * (u & 1));
     }
-    float p[kU][kN][4], sum_l[kN][2];
-    auto weigh = [&](float up) {
+    float p[kU][kN][4], sum_l[kN][2];            // p: what is multiplied with the values' scales
+    constexpr float kMost = kSplit ? kMostSum : kMostWeight;
+    bool above = false;
+    auto weigh = [&] {
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
         const unsigned long long f = f2pack(factor[n][0], factor[n][1]);
-        const unsigned long long less = f2pack(-m[n][0] - drop, -m[n][1] - drop);
-        unsigned long long sum = 0;
+        const unsigned long long less = f2pack(-m[n][0], -m[n][1]);
+        unsigned long long sum = 0, scaled = 0;
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float t0, t1;
             f2unpack(fma2(f2pack(z[u][n][2 * i], z[u][n][2 * i + 1]), f, less), t0, t1);
-            p[u][n][2 * i] = exp2_fast(t0);
-            p[u][n][2 * i + 1] = exp2_fast(t1);
-            const unsigned long long both = f2pack(p[u][n][2 * i], p[u][n][2 * i + 1]);
+            unsigned long long both = f2pack(exp2_fast(t0), exp2_fast(t1));
             sum = u + i == 0 ? both : add2(sum, both);
+            if constexpr (!kSplit) {
+              const float by = unit[u][i];
+              both = mul2(both, f2pack(by, by));
+              scaled = u + i == 0 ? both : add2(scaled, both);
+            }
+            f2unpack(both, p[u][n][2 * i], p[u][n][2 * i + 1]);
           }
-        f2unpack(mul2(sum, f2pack(up, up)), sum_l[n][0], sum_l[n][1]);
+        f2unpack(sum, sum_l[n][0], sum_l[n][1]);
+        above |= sum_l[n][0] > kMost || sum_l[n][1] > kMost;
+        if constexpr (!kSplit) {
+          float t0, t1;
+          f2unpack(scaled, t0, t1);
+          above |= t0 > kMostSum || t1 > kMostSum;
+        }
       }
     };
-    weigh(up);
-    bool above = false;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) above |= sum_l[n][0] > kMostSum || sum_l[n][1] > kMostSum;
+    weigh();
     if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
@@ -566,16 +653,23 @@ struct Q4State {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            top[0] = fmaxf(top[0], z[u][n][2 * i] * factor[n][0]);
-            top[1] = fmaxf(top[1], z[u][n][2 * i + 1] * factor[n][1]);
+          for (int i = 0; i < 4; ++i) {
+            const float t = z[u][n][i] * factor[n][i & 1];
+            float& to = top[i & 1];
+            if constexpr (kSplit) {
+              to = fmaxf(to, t - kBoost);
+            } else {
+              const float by = unit[u][i / 2];
+              const float log2 = (float)((int)(__float_as_uint(by) >> 23) - 127);
+              to = fmaxf(to, fmaxf(t - kRoom, by > 0.f ? t + log2 - kBoost : -INFINITY));
+            }
           }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
           for (int x = 4; x < 32; x *= 2)
             top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], x));
-          top[i] = fmaxf(m[n][i], top[i] - kBoost);
+          top[i] = fmaxf(m[n][i], top[i]);
           f[i] = exp2_fast(m[n][i] - top[i]);
           l[n][i] *= f[i];
           m[n][i] = top[i];
@@ -588,22 +682,32 @@ struct Q4State {
 #pragma unroll
             for (int i = 0; i < 2; ++i) o[c][t][n][i] = fma2(o[c][t][n][i], ff, none);
       }
-      weigh(up);
+      weigh();
     }
 #pragma unroll
     for (int n = 0; n < kN; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) l[n][i] += sum_l[n][i];
-    uint32_t pt[kU][kN][2];          // weights as right operand: keys in pairs, a column a head
-    if constexpr (!kSplit) {
+    uint32_t pt[kWeights][kU][kN][2];      // weights as right operand: keys in pairs, a column a head
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            pt[u][n][i] = turn8(pack_half(p[u][n][2 * i], p[u][n][2 * i + 1]));
-    }
+        for (int i = 0; i < 2; ++i) {
+          float lo = p[u][n][2 * i], hi = p[u][n][2 * i + 1];
+          if constexpr (!kSplit) {
+            pt[0][u][n][i] = turn8(pack_half(lo, hi));
+          } else {
+#pragma unroll
+            for (int part = 0; part < kWeights; ++part) {
+              const uint32_t h = pack_bf(lo, hi);
+              pt[part][u][n][i] = turn8(h);
+              lo -= __uint_as_float(h << 16);
+              hi -= __uint_as_float(h & 0xffff0000u);
+            }
+          }
+        }
     // two units' values at a time; in a loop where heads are large (128: 124 us so, 127 unrolled; a million
     // keys of 64: 45.9 and 45.0)
     constexpr int kUnroll = D <= 64 ? 2 : 1;
@@ -613,78 +717,85 @@ struct Q4State {
       for (int c0 = 0; c0 < kC; c0 += kP) {
         uint32_t x[2][kP][2];
         words<true>(vt, u0 + v0, c0, x);
-        // the values' scales: fp16 of keys (lane % 4) * 2, + 1 (i = 0), + 8, + 9 (1) of every 16, as the
-        // right operand has them; or, where weights are split, fp32 of keys lane / 4 and + 8
-        uint32_t w[2][2][kP];
+        // the values' scales, of keys (lane % 4) * 2, + 1 (i = 0), + 8, + 9 (1) of every 16, as the right
+        // operand has them
+        constexpr int kWords = kSplit ? 2 : 1;
+        uint32_t w[2][2][kP * kWords];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int unit = u0 + v0 + u;
-            load_shared(sv + ((kSplit ? 16 * unit + 8 * i + lane / 4 : 8 * unit + 4 * i + lane % 4) * kC +
-                              c0) * 4, w[u][i]);
-          }
+          for (int i = 0; i < 2; ++i)
+            load_shared(sv + ((8 * (u0 + v0 + u) + 4 * i + lane % 4) * kC + c0) * 4 * kWords, w[u][i]);
 #pragma unroll
         for (int k = 0; k < kP; ++k) {
-          uint32_t ps[kParts][2][kN][2], y[2][8];
+          uint32_t y[2][8];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int n = 0; n < kN; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if constexpr (kSplit) {
-                  const float f = __uint_as_float(w[u][i][k]);
-                  const float lo = p[u][n][2 * i] * f, hi = p[u][n][2 * i + 1] * f;
-                  const uint32_t h = pack_half(lo, hi);
-                  const float2 back = unpack_half(h);
-                  ps[0][u][n][i] = turn8(h);
-                  ps[kParts - 1][u][n][i] = turn8(pack_half(lo - back.x, hi - back.y));
-                } else {
-                  ps[0][u][n][i] = mul_half(pt[u][n][i], w[u][i][k]);
-                }
-              }
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              // codes 0 and 1, then 2 and 3 of each word: the lower one, and both as a byte
-              const uint32_t x0 = x[u][k][i] & 0x00ff00ffu, x1 = __byte_perm(x[u][k][i], 0, 0x4341);
-              y[u][2 * i] = code_lo<true>(x0);
-              y[u][2 * i + 1] = code_pair(x0);
-              y[u][4 + 2 * i] = code_lo<true>(x1);
-              y[u][5 + 2 * i] = code_pair(x1);
+              // codes 0 and 1, then 2 and 3 of each word: in bf16 the lower one, and both as a byte
+              if constexpr (kSplit) {
+                const uint32_t x0 = x[u][k][i], x1 = x0 >> 8;
+                const uint32_t f = w[u][i][k * kWords], less = w[u][i][k * kWords + kWords - 1];
+                y[u][2 * i] = value_lo(x0, f, less);
+                y[u][2 * i + 1] = value_hi(x0, f, less);
+                y[u][4 + 2 * i] = value_lo(x1, f, less);
+                y[u][5 + 2 * i] = value_hi(x1, f, less);
+              } else {
+                const uint32_t x0 = x[u][k][i] & 0x00ff00ffu, x1 = __byte_perm(x[u][k][i], 0, 0x4341);
+                y[u][2 * i] = code_lo<true>(x0);
+                y[u][2 * i + 1] = code_pair(x0);
+                y[u][4 + 2 * i] = code_lo<true>(x1);
+                y[u][5 + 2 * i] = code_pair(x1);
+              }
             }
-          }
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
             float sum[2][4];
+            // the smallest parts first: what a sum is cut by goes with its size
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int part = kWeights - 1; part >= 0; --part)
 #pragma unroll
-              for (int part = 0; part < kParts; ++part)
+              for (int u = 0; u < 2; ++u) {
+                uint32_t ps[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  ps[i] = pt[part][(kUnroll == 1 ? 0 : v0) + u][n][i];
+                  if constexpr (!kSplit) ps[i] = mul_half(ps[i], w[u][i][k]);
+                }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                   const uint32_t* v = y[u] + 4 * t;
-                  if (u == 0 && part == 0)
-                    mma_f16(sum[t], v[0], v[1], v[2], v[3], ps[0][0][n], 0.f, 0.f, 0.f, 0.f);
-                  else
-                    mma_f16(sum[t], v[0], v[1], v[2], v[3], ps[part][u][n]);
+                  if constexpr (kSplit) {
+                    if (u == 0 && part == kWeights - 1)
+                      mma_bf16(sum[t], v[0], v[1], v[2], v[3], ps, 0.f, 0.f, 0.f, 0.f);
+                    else
+                      mma_bf16(sum[t], v[0], v[1], v[2], v[3], ps);
+                  } else {
+                    if (u == 0)
+                      mma_f16(sum[t], v[0], v[1], v[2], v[3], ps, 0.f, 0.f, 0.f, 0.f);
+                    else
+                      mma_f16(sum[t], v[0], v[1], v[2], v[3], ps);
+                  }
                 }
-            const unsigned long long up2 = f2pack(up, up);
+              }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                o[c0 + k][t][n][i] = fma2(f2pack(sum[t][2 * i], sum[t][2 * i + 1]), up2, o[c0 + k][t][n][i]);
+                o[c0 + k][t][n][i] = add2(f2pack(sum[t][2 * i], sum[t][2 * i + 1]), o[c0 + k][t][n][i]);
           }
         }
       }
-      if constexpr (kU > 2 && !kSplit) {         // the next two units' weights
+      if constexpr (kU > 2 && kUnroll == 1) {    // the next two units' weights
 #pragma unroll
-        for (int u = 0; u + 2 < kU; ++u)
+        for (int part = 0; part < kWeights; ++part)
 #pragma unroll
-          for (int n = 0; n < kN; ++n)
+          for (int u = 0; u + 2 < kU; ++u)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) pt[u][n][i] = pt[u + 2][n][i];
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) pt[part][u][n][i] = pt[part][u + 2][n][i];
       }
     }
   }
@@ -698,7 +809,15 @@ struct Q4State {
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
-        if (lane < 4) ml[8 * n + lane * 2 + i] = make_float2(m[n][i], l[n][i]);
+        float base = m[n][i], sum = l[n][i];
+        if constexpr (!kSplit) {     // a sum of up to 2^127 is brought near one, for the sake of its logarithm
+          if (sum > kMostSum && sum < INFINITY) {
+            const int e = (int)(__float_as_uint(sum) >> 23) - 127;
+            base += (float)e;
+            sum *= __uint_as_float((unsigned)(127 - e) << 23);
+          }
+        }
+        if (lane < 4) ml[8 * n + lane * 2 + i] = make_float2(base, sum);
       }
   }
   // column c of a row of sums lies at c ^ spread(row): put_o's lanes write to different banks
@@ -712,7 +831,8 @@ struct Q4State {
       for (int i = 0; i < 2; ++i) {
         const int r = 8 * n + lane % 4 * 2 + i;
         if (r >= rows) continue;
-        const float f = exp2_fast(m[n][i] - top(r)) * 512.f;     // codes are 2^-9 of their numbers
+        // values are 2^-21 of theirs, or codes 2^-9
+        const float f = exp2_fast(m[n][i] - top(r)) * (kSplit ? 2097152.f : 512.f);
 #pragma unroll
         for (int c = 0; c < kC; ++c)
 #pragma unroll
@@ -722,8 +842,8 @@ struct Q4State {
             f2unpack(o[c][k / 2][n][1], y[0], y[1]);
             float* to = dst + r * D + 32 * c + 4 * (lane / 4);
             to[k ^ spread(r)] = x[i] * f;
-            // of a pair (2^-13 of its number) what is left without its lower code
-            to[(k + 1) ^ spread(r)] = (16.f * y[i] - x[i]) * (f * 0.0625f);
+            // 16 times the upper code's; or of a pair (2^-13 of its number), less its lower code
+            to[(k + 1) ^ spread(r)] = (kSplit ? y[i] : 16.f * y[i] - x[i]) * (f * 0.0625f);
           }
       }
   }
