@@ -530,8 +530,11 @@ def _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, axes, q_weight, k_weight
     dwq = dwk = ws = None
     nbytes = 0
     if qw or kw:
+        # for this call alone: it launches twice, and another thread's call on the same stream may
+        # come in between (one kept for each thread and stream took 1.5 us less of 42 and outlived its
+        # thread's and stream's use)
         nbytes = _norm_rope_backward_bytes(d, dev)
-        ws = _norm_rope_backward_workspace(nbytes, dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         dwq = torch.empty(d, dtype=torch.float32, device=q.device) if qw else None
         dwk = torch.empty(d, dtype=torch.float32, device=q.device) if kw else None
     grads = (dq.data_ptr(), dkp, dwq.data_ptr() if qw else 0, dwk.data_ptr() if kw else 0,
@@ -548,28 +551,6 @@ def _norm_rope_backward(q, k, dq_out, dk_out, inv_freq, axes, q_weight, k_weight
     if rc:
         _check(rc)
     return dq, dk, dwq, dwk
-
-
-_backward_workspaces = threading.local()
-
-
-def _norm_rope_backward_workspace(nbytes: int, device: int) -> torch.Tensor:
-    """The gradient's workspace: one for each thread and stream, since a call launches twice, and another
-    thread's call on the same stream may come in between.  A captured call has one of its graph's own."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-    held = _backward_workspaces.__dict__
-    key = device, _raw_stream(device), _released
-    ws = held.get(key)
-    if ws is None or ws.numel() < nbytes:
-        if ws is None:                 # those from before the last workspace_release()
-            for old in [k for k in held if k[2] != _released]:
-                del held[old]
-        ws = held[key] = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-    return ws
-
-
-_released = 0              # calls of workspace_release()
 
 
 @functools.lru_cache(maxsize=None)
@@ -1076,10 +1057,7 @@ def get_last_device_error(stream=None, device=None) -> int:
 
 def workspace_release() -> None:
     """Frees the cached workspaces, the library's and the binding's."""
-    global _released
-    _released += 1
     _paged_workspaces.clear()
-    _backward_workspaces.__dict__.clear()
     _check(load().mita_workspace_release())
 
 
