@@ -547,8 +547,8 @@ uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page
  * fit its row of the table and the step's rows and it needs no page, or the pages that the sequences up to
  * and with s need (those that fit) are no more than the free ones; the first of its pages is the one
  * under those that the sequences before it need, counted from the stack's top.  A sequence that is not
- * granted stays as it is: its rows have no places (mita_cache_append, which goes by lengths, must not be
- * given its rows).
+ * granted stays as it is: its rows have no places.  (mita_cache_append goes by lengths and would write them over
+ * the sequence's last tokens: it is given lengths that are 0 where granted is, by which it leaves them out.)
  * new_tokens below -1, lengths outside [0, table_width*page_size], a free_count outside [0, num_pages],
  * pushes beyond num_pages and page numbers outside [0, num_pages) under a row flag
  * MITA_ERR_DEVICE_CHECK; such sequences get nothing, such rows slot -1.  Every other entry of the

@@ -628,7 +628,7 @@ def _cache_of(k_cache, v_cache, page_table, lengths, dtype, device: int):
 
 def mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start=None, q=None,
                       inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
-                      interleaved: bool = False, q_out=None, stream=None):
+                      interleaved: bool = False, q_out=None, stream=None, granted=None):
     """New tokens into a paged cache: k [T,Hkv,d] normalised and rotated (as by
     mita_qk_norm_rope, at its position in its sequence) and v [T,Hkv,d] to their rows of
     k_cache, v_cache [num_pages,Hkv,page_size,d]; returns q [T,Hq,d] normalised and rotated (None
@@ -636,18 +636,25 @@ def mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start=Non
 
     page_table: int32 [S,width]; lengths: int32 [S], tokens of each sequence with the new
     ones (0: an idle slot, nothing is written for it); seq_start: int32 [S+1], the rows of each
-    sequence's new tokens (None: row s is sequence s's only one).  Rows that belong to no sequence
-    or to an idle slot leave q_out as it is."""
+    sequence's new tokens (None: row s is sequence s's only one); granted: int32 [S], as
+    mita_cache_plan gives it: a sequence with 0 is an idle slot, whatever its length (for a step some of
+    whose sequences got no page; a captured one too).  Rows that belong to no sequence or to an
+    idle slot leave q_out as it is."""
     dev = _device_of(k, "k")
     if stream is not None or dev != torch.cuda.current_device():
         with _on(stream, dev, k, v, k_cache, v_cache, page_table, lengths, seq_start, q, inv_freq,
-                 q_weight, k_weight, q_out):
+                 q_weight, k_weight, q_out, granted):
             return mita_cache_append(k, v, k_cache, v_cache, page_table, lengths, seq_start, q,
-                                     inv_freq, q_weight, k_weight, eps, interleaved, q_out)
+                                     inv_freq, q_weight, k_weight, eps, interleaved, q_out,
+                                     granted=granted)
     dt = k.dtype
     fn = _typed_fn("mita_cache_append", dt)
     (kc, vc, table, n), (S, pages, Hkv, page, d, width) = _cache_of(k_cache, v_cache, page_table,
                                                                     lengths, dt, dev)
+    if granted is not None:
+        _dense(granted, "granted", (S,), torch.int32, dev)
+        lengths = torch.where(granted > 0, lengths, 0)
+        n = lengths.data_ptr()
     T = k.shape[0]
     ks, vs = _rows(k, "k", (T, Hkv, d), dt, dev), _rows(v, "v", (T, Hkv, d), dt, dev)
     start = 0 if seq_start is None else _dense(seq_start, "seq_start", (S + 1,), torch.int32, dev)
@@ -689,8 +696,8 @@ def mita_cache_plan(new_tokens, lengths, page_table, free_pages, free_count, tok
     sequence.  slots: int64 [tokens], page*page_size + row in the page, -1 for rows that belong to nobody
     or to a sequence that was not granted.  granted: int32 [S], new_tokens, or 0 where its tokens fit
     neither the pool (first come, first served), the table nor the rows: such a sequence stays
-    as it is, and its rows must not be given to mita_cache_append, which goes by lengths
-    (mita_cache_append_q4 goes by slots and passes them over)."""
+    as it is.  mita_cache_append_q4 goes by slots and passes its rows over; mita_cache_append goes by
+    lengths and is given `granted`, or it would write them over the sequence's last tokens."""
     dev = _device_of(new_tokens, "new_tokens")
     if stream is not None or dev != torch.cuda.current_device():
         with _on(stream, dev, new_tokens, lengths, page_table, free_pages, free_count, new_lengths,
