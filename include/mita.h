@@ -550,9 +550,11 @@ uint64_t mita_paged_attn_workspace_bytes(int S, int Hq, int Hkv, int d, int page
  * granted stays as it is: its rows have no places.  (mita_cache_append goes by lengths and would write them over
  * the sequence's last tokens: it is given lengths that are 0 where granted is, by which it leaves them out.)
  * new_tokens below -1, lengths outside [0, table_width*page_size], a free_count outside [0, num_pages],
- * pushes beyond num_pages and page numbers outside [0, num_pages) under a row flag
- * MITA_ERR_DEVICE_CHECK; such sequences get nothing, such rows slot -1.  Every other entry of the
- * arrays stays as it is.  The arrays must not overlap, except as said.
+ * pushes beyond num_pages and page numbers outside [0, num_pages) that are pushed or lie under a row flag
+ * MITA_ERR_DEVICE_CHECK.  Such sequences get nothing, such rows slot -1; the length of one that is done, and the
+ * free_count, are cut to their range (its whole row of the table is pushed where its length is beyond it),
+ * and what is pushed is pushed as it is, so that after the flag the pool has to be made anew.  Every other
+ * entry of the arrays stays as it is.  The arrays must not overlap, except as said.
  */
 typedef struct mita_cache_plan_params {
   const int32_t *new_tokens, *lengths;

@@ -128,8 +128,10 @@ cache_plan_kernel(const __grid_constant__ CachePlanArgs a) {
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
             const int i = i0 + 32 * k;
-            if (i < n && to + i < a.num_pages) a.free_pages[to + i] = page[k];
-            else if (i < n) flag_error(a.status, kDevErrBadIndex);
+            if (i >= n) continue;
+            if (to + i < a.num_pages) a.free_pages[to + i] = page[k];
+            if (to + i >= a.num_pages || (unsigned)page[k] >= (unsigned)a.num_pages)
+              flag_error(a.status, kDevErrBadIndex);
           }
         }
       }
