@@ -278,18 +278,18 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return __float2bfloat16_rn(x); }
 
 // ---------------------------------------------------------------------------
-// What the warps' loaders share: page numbers one tile ahead of the copies, copies kStages - 1 tiles
-// ahead of the arithmetic.
+// A warp's place in the row, for at most a key a lane: page numbers one tile ahead of the copies, copies
+// kStages - 1 tiles ahead of the arithmetic.
 // ---------------------------------------------------------------------------
 template <typename S, typename Args>
 struct RowLoader {
   using Mask = typename S::Mask;         // a bit a key
-  static constexpr Mask kAll = (Mask)(~0ull >> (64 - S::kKeys));
-  static constexpr int kEach = S::kKeys > 32 ? S::kKeys / 32 : 1;    // keys whose page a lane looks up
+  static_assert(S::kKeys <= 32 && sizeof(Mask) == 4, "a lane's key");
+  static constexpr Mask kAll = ~0u >> (32 - S::kKeys);
   Cursor at;
   long long end;           // of the share
   struct Rows {            // a warp's keys of a tile
-    int page, key0, head;  // page: of this lane's first key
+    int page, key0, head;  // page: of this lane's key
     Mask mask;             // those to be seen
   };
 
@@ -304,7 +304,7 @@ struct RowLoader {
       mask = (kAll << lo) & (kAll >> (S::kKeys - hi));
       head = a.row_blocks == 1 ? at.hr : at.hr / a.row_blocks;
       // lanes whose key is not to be seen read the first one's page
-      const int mine = (threadIdx.x & 31) * kEach % S::kKeys;
+      const int mine = (threadIdx.x & 31) % S::kKeys;
       const int key = key0 + ((mask >> mine) & 1 ? mine : lo);
       page = a.paged.table[(long long)at.s * a.paged.width + (key >> a.paged.page_log2)];
     }
@@ -320,12 +320,7 @@ struct RowLoader {
       const unsigned wrong = __ballot_sync(0xffffffffu, bad);
       if (wrong) {
         if ((threadIdx.x & 31) == 0) flag_error(a.status, kDevErrBadIndex);
-        if constexpr (kEach == 1) {
-          mask &= ~wrong;
-        } else {
-          for (int i = 0; i < 32; ++i)
-            if ((wrong >> i) & 1) mask &= ~((Mask)((1u << kEach) - 1) << (kEach * i));
-        }
+        mask &= ~wrong;
       }
     }
     return mask;
