@@ -810,11 +810,13 @@ struct Q4State {
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
         float base = m[n][i], sum = l[n][i];
-        if constexpr (!kSplit) {     // a sum of up to 2^127 is brought near one, for the sake of its logarithm
-          if (sum > kMostSum && sum < INFINITY) {
-            const int e = (int)(__float_as_uint(sum) >> 23) - 127;
-            base += (float)e;
-            sum *= __uint_as_float((unsigned)(127 - e) << 23);
+        if constexpr (!kSplit) {
+          // a large sum is brought to 2^10, for the sake of its logarithm, by what the base can be raised by (of
+          // scores beyond 2^24 perhaps nothing)
+          if (sum > 16777216.f && sum < INFINITY) {
+            const float raised = base + (float)((int)(__float_as_uint(sum) >> 23) - 137);
+            sum *= exp2_fast(base - raised);
+            base = raised;
           }
         }
         if (lane < 4) ml[8 * n + lane * 2 + i] = make_float2(base, sum);

@@ -144,3 +144,35 @@ def test_values_of_every_size_side_by_side(dt, lengths, Hkv, G, d):
     q = q.to(DT[dt])
     want, bound = reference(q, cache, lengths, d ** -0.5)
     R.assert_close(run(q, cache, lengths, d ** -0.5), want, bound, "out")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [-1e30, -1e9, -1.5e7, -7e6, -1e6, -1e3, 1e6])
+def test_equal_scores_of_any_size(dt, size):
+    """Scores that are the same number for all keys, so that every weight is exactly 1 / n, over some keys and over
+    many; rows of zeros among the values, or not."""
+    mita = M()
+    d = 64
+    lengths = (3, 200, 2500)
+    for zeros in (False, True):
+        g = torch.Generator().manual_seed(5)
+        k = [torch.full((1, n, d), 7.0) for n in lengths]
+        v = [torch.randn(1, n, d, generator=g) for n in lengths]
+        if zeros:
+            for x in v:
+                x[:, ::3] = 0
+        cache = Q.Cache4(lengths, 1, 16, d, k=k, v=v)
+        q = torch.full((3, 5, d), 1 / 64.0).to(DT[dt])              # q k is 7, exactly
+        out, lse = mita.mita_paged_attn_q4(q.cuda(), cache.k8.cuda(), cache.v8.cuda(), cache.table.cuda(),
+                                           torch.tensor(lengths, dtype=torch.int32).cuda(), scale=size,
+                                           return_lse=True)
+        for s, n in enumerate(lengths):
+            value, scale = cache.kv[s][1]
+            want, size_of = value.mean(1), value.abs().mean(1)
+            # the weights are alike: what is left are a product's rounding (2^-11 twice in bf16), the sums, and what
+            # `reference` says of bytes and of weights far below the largest (rows are alike here, within 2^6)
+            rel = (2.0 ** -10 if dt == "bf16" else 2.0 ** -24) + 2 * n * U
+            bound = rel * size_of + R.half_step(DT[dt]) * want.abs() + 2.0 ** -20 * scale.mean(1)
+            R.assert_close(out[s], want.expand(5, d), bound.expand(5, d), f"{n} keys")
+            z = 7 * float(torch.tensor(size)) + float(torch.log(torch.tensor(float(n), dtype=torch.float64)))
+            assert float((lse[s].cpu().double() - z).abs().max()) <= 4 * 2 * U * abs(z) + 2 * n * U + 2.0 ** -20
