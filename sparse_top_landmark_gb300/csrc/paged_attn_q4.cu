@@ -58,6 +58,9 @@ namespace {
 // weight is then 2^10, so that a tile's eight of a lane stay below that.  (bf16: weights times their keys' powers of
 // two; weights alone may come to 2^100 where those differ, the largest then being 2^96.)
 constexpr float kBoost = 10.f, kMostSum = 16384.f, kRoom = 96.f, kMostWeight = 1.2676506e30f;
+// Where a maximum's own rounding may be as much as that of an exponent, scores are rounded before it is taken from
+// them: 2^20 and a sixteenth.
+constexpr float kFar = 1048576.f;
 
 // Shared memory and shape of one instantiation; RT: query rows of a segment.
 //
@@ -302,6 +305,7 @@ struct Q4State {
   static constexpr int kU = !kSplit && (kN == 1 || D == 128) ? 4 : 2, kP = kC == 1 ? 1 : 2;
   unsigned long long o[kC][2][kN][2];   // two heads of a value column each
   float m[kN][2], l[kN][2];          // m: the running maximum less kBoost; l: of this lane's keys
+  bool far;                          // a maximum is beyond kFar
 
   // Puts chunk c of a segment's queries to `to`, as every warp of the team will read them.
   __device__ __forceinline__ static void put_queries(const PagedAttnQ4Args<T>& a, int s, int head,
@@ -368,6 +372,7 @@ struct Q4State {
   }
 
   __device__ __forceinline__ void start() {
+    far = false;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
 #pragma unroll
@@ -603,6 +608,17 @@ struct Q4State {
 #pragma unroll
       for (int n = 0; n < kN; ++n) factor[n][0] = factor[n][1] = 1.f;
     }
+    auto round_scores = [&] {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[u][n][i] = __fmul_rn(z[u][n][i], factor[n][i & 1]);
+        factor[n][0] = factor[n][1] = 1.f;
+      }
+    };
+    if (far) round_scores();
     float unit[kU][2];               // of keys lane / 4 and + 8
     if constexpr (!kSplit) {
 #pragma unroll
@@ -654,7 +670,7 @@ struct Q4State {
         for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float t = z[u][n][i] * factor[n][i & 1];
+            const float t = __fmul_rn(z[u][n][i], factor[n][i & 1]);
             float& to = top[i & 1];
             if constexpr (kSplit) {
               to = fmaxf(to, t - kBoost);
@@ -673,6 +689,7 @@ struct Q4State {
           f[i] = exp2_fast(m[n][i] - top[i]);
           l[n][i] *= f[i];
           m[n][i] = top[i];
+          far |= fabsf(top[i]) > kFar && top[i] > kLowest;
         }
         const unsigned long long ff = f2pack(f[0], f[1]), none = 0;
 #pragma unroll
@@ -682,6 +699,7 @@ struct Q4State {
 #pragma unroll
             for (int i = 0; i < 2; ++i) o[c][t][n][i] = fma2(o[c][t][n][i], ff, none);
       }
+      if (far) round_scores();
       weigh();
     }
 #pragma unroll

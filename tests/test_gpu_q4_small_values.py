@@ -147,7 +147,7 @@ def test_values_of_every_size_side_by_side(dt, lengths, Hkv, G, d):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("size", [-1e30, -1e9, -1.5e7, -7e6, -1e6, -1e3, 1e6])
+@pytest.mark.parametrize("size", [-1e30, -1e9, -1.5e7, -7e6, -1e6, -1e3, 1e6, 3e6, 7e6, 1.5e7, 3e7, 1e9, 1e12, 1e30])
 def test_equal_scores_of_any_size(dt, size):
     """Scores that are the same number for all keys, so that every weight is exactly 1 / n, over some keys and over
     many; rows of zeros among the values, or not."""
