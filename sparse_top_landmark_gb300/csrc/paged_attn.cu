@@ -101,9 +101,12 @@ struct TensorState {
   float o[D / 16][kN][4];
   float m[kN][2], l[kN][2];          // l: of this lane's keys
   float slope2[kN][2];
+  bool plain;                        // the rule's, until a maximum is beyond kFar
 
-  __device__ __forceinline__ void start(const PagedAttnArgs<bf16>& a, int s, int head, int rows) {
+  __device__ __forceinline__ void start(const PagedAttnArgs<bf16>& a, int s, int head, int rows,
+                                        const ScoreRule& rule) {
     const int lane = threadIdx.x & 31;
+    plain = rule.plain;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       const int r = 8 * n + lane / 4;
@@ -150,7 +153,7 @@ struct TensorState {
     }
     // z becomes the scores, or stays the dot products where a factor is all that is missing
     float factor = rule.scale2;
-    if (!rule.plain || mask != (unsigned)((1ull << S::kKeys) - 1)) {
+    if (!plain || mask != (unsigned)((1ull << S::kKeys) - 1)) {
       factor = 1.f;
       bool small = rule.cap > 0.f;
 #pragma unroll
@@ -196,6 +199,7 @@ struct TensorState {
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
         float f[2];
+        bool far = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float top = fmaxf(z[0][n][i], z[0][n][i + 2]);
@@ -203,15 +207,26 @@ struct TensorState {
           for (int t = 1; t < kT; ++t) top = fmaxf(top, fmaxf(z[t][n][i], z[t][n][i + 2]));
 #pragma unroll
           for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          top = fmaxf(m[n][i], top * factor);
+          top = fmaxf(m[n][i], __fmul_rn(top, factor));
           f[i] = exp2_fast(m[n][i] - top);
           l[n][i] *= f[i];
           m[n][i] = top;
+          far |= fabsf(top) > kFar && top > kLowest;
         }
+        plain &= !__any_sync(0xffffffffu, far);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][n][i] *= f[i & 1];
+      }
+      if (!plain) {                  // (scores that are rounded already have a factor of one)
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[t][n][i] = __fmul_rn(z[t][n][i], factor);
+        factor = 1.f;
       }
     }
     // The weights go to the value product as a sum of two bf16 values, 16 bits in all: one alone
@@ -347,7 +362,8 @@ struct SplitState {
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 
-  __device__ __forceinline__ void start(const PagedAttnArgs<float>& a, int s, int head, int rows) {
+  __device__ __forceinline__ void start(const PagedAttnArgs<float>& a, int s, int head, int rows,
+                                        const ScoreRule&) {
     const int lane = threadIdx.x & 31, r = lane / 4;
     const float* p = a.q + s * a.q_s + (long long)(head + r) * a.q_h;
 #pragma unroll

@@ -58,9 +58,6 @@ namespace {
 // weight is then 2^10, so that a tile's eight of a lane stay below that.  (bf16: weights times their keys' powers of
 // two; weights alone may come to 2^100 where those differ, the largest then being 2^96.)
 constexpr float kBoost = 10.f, kMostSum = 16384.f, kRoom = 96.f, kMostWeight = 1.2676506e30f;
-// Where a maximum's own rounding may be as much as that of an exponent, scores are rounded before it is taken from
-// them: 2^20 and a sixteenth.
-constexpr float kFar = 1048576.f;
 
 // Shared memory and shape of one instantiation; RT: query rows of a segment.
 //

@@ -20,6 +20,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum before the first key: below every finite score, and finite, so that
 // differences with it need no special case (a score of -inf weighs nothing against it).
 constexpr float kLowest = -FLT_MAX;
+// Where scores are products, a maximum is taken from them in the same operation.  Where the maximum's own rounding
+// may be a sixteenth or more, scores are rounded before, as it was: equal ones have equal weights.
+constexpr float kFar = 1048576.f;
 constexpr int kMaxPagedCtas = 255;     // CTAs of a call, and counters in its workspace
 // Counters carry the number of the call that counts, above the count's kCountBits bits: whatever an
 // earlier call left in them is below this one's zero.  (Were a caller to change lengths while they are
@@ -521,7 +524,7 @@ paged_attn_kernel(const __grid_constant__ typename K::Args a) {
         rows = min(RT, a.G - rb * RT);
         rule.last = at.span.len - 1;
         from = at.t;
-        st.start(a, at.s, head, rows);
+        st.start(a, at.s, head, rows, rule);
         begin = false;
       }
       copy_wait<S::kStages - 2>();
