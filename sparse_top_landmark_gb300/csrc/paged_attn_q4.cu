@@ -302,7 +302,7 @@ struct Q4State {
   static constexpr int kU = !kSplit && (kN == 1 || D == 128) ? 4 : 2, kP = kC == 1 ? 1 : 2;
   unsigned long long o[kC][2][kN][2];   // two heads of a value column each
   float m[kN][2], l[kN][2];          // m: the running maximum less kBoost; l: of this lane's keys
-  bool far;                          // a maximum is beyond kFar
+  bool far;                          // a maximum of the warp's is beyond kFar
 
   // Puts chunk c of a segment's queries to `to`, as every warp of the team will read them.
   __device__ __forceinline__ static void put_queries(const PagedAttnQ4Args<T>& a, int s, int head,
@@ -564,7 +564,7 @@ struct Q4State {
     float factor[kN][2];
 #pragma unroll
     for (int n = 0; n < kN; ++n) pair_of(queries + S::kOffUnit, n, factor[n]);
-    if (rule.plain && full) {
+    if (rule.plain && full && !far) {
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -605,17 +605,6 @@ struct Q4State {
 #pragma unroll
       for (int n = 0; n < kN; ++n) factor[n][0] = factor[n][1] = 1.f;
     }
-    auto round_scores = [&] {
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[u][n][i] = __fmul_rn(z[u][n][i], factor[n][i & 1]);
-        factor[n][0] = factor[n][1] = 1.f;
-      }
-    };
-    if (far) round_scores();
     float unit[kU][2];               // of keys lane / 4 and + 8
     if constexpr (!kSplit) {
 #pragma unroll
@@ -696,7 +685,16 @@ struct Q4State {
 #pragma unroll
             for (int i = 0; i < 2; ++i) o[c][t][n][i] = fma2(o[c][t][n][i], ff, none);
       }
-      if (far) round_scores();
+      far = __any_sync(0xffffffffu, far);
+      // (here whatever the maximum: a branch more is 1 % of 200 contexts of up to 900 keys)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[u][n][i] = __fmul_rn(z[u][n][i], factor[n][i & 1]);
+        factor[n][0] = factor[n][1] = 1.f;
+      }
       weigh();
     }
 #pragma unroll
