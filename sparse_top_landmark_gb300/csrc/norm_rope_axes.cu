@@ -2,8 +2,9 @@
 //
 // A lane has four frequencies, so four positions a token instead of one, and no more arithmetic.  Measured (bf16):
 // 66,313 tokens of 16 + 4 heads of 128, three axes, in 111 us, 6.1 TB/s (one position:
-// 114); 16 x 1025 tokens of 12 + 12 heads of 64, two axes, in 22.3 us (20.4), their gradient in 34 us
-// (32), 4.4 TB/s, where it is the instructions that bound it.
+// 114; fp32 222, gradients 171 and 306, 6.0 and 6.7 TB/s); 16 x 1025 tokens of 12 + 12 heads of 64, two axes,
+// in 23 us (20.4; fp32 36), their gradient in 34.5 us (32; fp32 53), 4.4 TB/s, where neither HBM (45 %) nor the
+// schedulers (53 %) are full: latency, and 5 us of start, reduction and a second launch.
 #include "norm_rope_kernels.cuh"
 
 namespace mita {

@@ -31,22 +31,23 @@
 // - bf16: a weight p goes into fp16 times the power of two w of its key's largest scale, and the scale
 //   divided by it, 11 bits for the one and again for their product.  The running maximum is p w's, which
 //   is 2^10 to 2^14 where it is rounded, so that fp16's subnormals begin at 2^-24 of it; a key
-//   without values has w = 0.  Only a block 2^-21 times its own row's largest loses bits by itself.  (With p
+//   without values has w = 0.  A block 2^-21 times its own row's largest loses bits by itself, and the upper
+//   code of a byte has 2^-22 of what the block's scales add up to.  (With p
 //   and the scale as they are: an output is off by 3 % where a key of value zero stands 15 above the others and
 //   their scales are 2^-13, in fp32 with two values for a product too.  With two bf16 values for a
-//   weight, as below, decode_batch's 120 us are 138: tensor cores.  With one w for a tile whose scales are near each
-//   other: 130, the two ways being a branch in the middle of a tile.)
+//   weight, as below, the 128 sequences' 120 us are 138: tensor cores.  With one w for a tile whose scales are near
+//   each other: 130, the two ways being a branch in the middle of a tile.)
 // - fp32: a weight is a sum of three bf16 values, which have fp32's exponents, and the scale is with the
 //   code: (n - 8) s has seven bits.
 //
 // A tile's sums are added to the running ones in fp32, outside the tensor cores: paged_attn.cu says why.
 //
-// Bound by instructions and their latency: three warps a scheduler issue 0.54 a cycle.  A tile of 32 keys of
-// 128 takes a warp some 600 (128 masks and 48 shifts and byte moves for 8192 codes, 64 to make values signed, 48 for
-// the scales, 32 products); with all pages in L2 it is 3 % faster, loads alone take
-// four fifths of the time.  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 120 us, 4.7 TB/s
+// Bound by the latency of instructions: three warps a scheduler issue 0.58 a cycle, half-rate ones half of what their
+// pipe takes, the tensor cores 24 %, HBM 57 %.  A tile of 32 keys of 128 takes a warp some 620 instructions (128
+// masks and 48 shifts and byte moves for 8192 codes, 64 to make values signed, 48 for
+// the scales, 32 products).  Measured (bf16): 128 sequences of up to 8192 keys, 32/8 heads of 128, in 120 us, 4.7 TB/s
 // (paged_attn.cu takes 311 us for the same in bf16); one sequence of 1,048,575 keys, 8/2 heads of 64, in
-// 47 us; 200 of up to 900 keys in 45 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 104 us.
+// 47 us; 200 of up to 900 keys in 45 us; one of 333 in 8 us; fp32, 64 of up to 8192, 32/8 heads of 128, in 102 us.
 #include "paged_row.cuh"
 
 #include <cuda_fp16.h>
@@ -61,10 +62,11 @@ constexpr float kBoost = 10.f, kMostSum = 16384.f, kRoom = 96.f, kMostWeight = 1
 
 // Shared memory and shape of one instantiation; RT: query rows of a segment.
 //
-// A CTA has several teams of warps, each with a share of its own: two, or four where there are many segments (128
-// sequences of up to 8192 keys, 32/8 heads of 128: one share for 12 warps 153 us, two teams of 6 then 132, now 117,
-// four of 3 115; 256 of up to 300 keys: one team 70, two 39, four 31; in fp32, 256 of up to 500: two 55, four 48;
-// 128/8 heads, of 16 rows then: two 195, four 209).  Registers
+// A CTA has several teams of warps, each with a share of its own: two, or four where there are many segments (256
+// sequences of up to 300 keys, 32/8 heads of 128: two 42 us, four 32; 200 of up to 900: 51 and 45).  What follows was
+// measured on earlier forms of the kernel, up to 6 % faster or slower than this one: one team 70 us for those 256, two
+// 39, four 31; 128 sequences of up to 8192 keys one 153, two 132, later 117, four 115; in fp32, 256 of up to 500 two 55,
+// four 48; 128/8 heads, of 16 rows then, two 195, four 209.  Registers
 // hold 12 warps' state for heads of 128, 16 for smaller ones (a million keys, heads of 64: teams of 6
 // 48 us, of 8 46), 8 where rows are 16 or a factor is two values (fp32, 64 sequences of up to 8192 keys,
 // heads of 128: teams of 4 109 us, of 5 117; heads of 64: teams of 4 72, of 8 62).
@@ -1242,8 +1244,9 @@ struct Q4 {
   static auto kernel() { return paged_attn_q4_kernel<Q4>; }
 };
 
-// Four teams where there are that many segments, and the counters hold a segment's parts (tables of up to 24384
-// tokens, of 32512 for smaller heads); 16 rows are better off with two.
+// Four teams where there are that many segments, and the counters hold a segment's parts: tables of up to 127 tiles
+// (24384 tokens for heads of 128, 16256 of them in fp32, 32512 for smaller heads), whatever the lengths.  16 rows are
+// better off with two.
 template <typename T, int D, int RT, typename F>
 auto with_teams(int Hkv, int G, int S, int width, int page_log2, int sms, F f) {
   if constexpr (RT == 8) {
