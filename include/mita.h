@@ -611,8 +611,8 @@ int mita_cache_append_q4_f32(const mita_cache_append_q4_params* params, mita_str
  * with a scale, down to 2^-24 of the largest weight times its row's largest scale (below, 2^-35 of that is
  * lost a key), and to 2^-21 of a row's largest scale; of two values in a byte the upper one is good to 2^-22 of its
  * block's scales.  The _f32 twin keeps 22 bits of a query and 24 of a
- * weight, whatever the size of weights and scales.  A weight below 2^-100 of its row's largest may count as
- * nothing.  Query values beyond 2^100 may come out as NaN.
+ * weight, whatever the size of weights and scales.  A weight below 2^-70 of its sequence's largest may lose its
+ * bits.  Query values beyond 2^100 may come out as NaN.
  */
 int mita_paged_attn_q4(const mita_paged_attn_params* params, mita_stream_t stream);
 int mita_paged_attn_q4_f32(const mita_paged_attn_params* params, mita_stream_t stream);

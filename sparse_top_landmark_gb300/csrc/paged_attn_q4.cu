@@ -57,8 +57,9 @@ namespace {
 
 // The running maximum is looked for again only where a lane's weights add up to more than 2^14; the largest
 // weight is then 2^10, so that a tile's eight of a lane stay below that.  (bf16: weights times their keys' powers of
-// two; weights alone may come to 2^100 where those differ, the largest then being 2^96.)
-constexpr float kBoost = 10.f, kMostSum = 16384.f, kRoom = 96.f, kMostWeight = 1.2676506e30f;
+// two; weights alone may come to 2^64 where those differ, the largest then being 2^60, whose exponent is rounded
+// at 2^-19.)
+constexpr float kBoost = 10.f, kMostSum = 16384.f, kRoom = 60.f, kMostWeight = 18446744073709551616.f;
 
 // Shared memory and shape of one instantiation; RT: query rows of a segment.
 //
@@ -826,10 +827,10 @@ struct Q4State {
         for (int x = 4; x < 32; x *= 2) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
         float base = m[n][i], sum = l[n][i];
         if constexpr (!kSplit) {
-          // a large sum is brought to 2^10, for the sake of its logarithm, by what the base can be raised by (of
-          // scores beyond 2^24 perhaps nothing)
-          if (sum > 16777216.f && sum < INFINITY) {
-            const float raised = base + (float)((int)(__float_as_uint(sum) >> 23) - 137);
+          // A large sum is brought to 2^8, for the sake of its logarithm (whose error goes with its size, and values'
+          // powers of two go into it), by what the base can be raised by: of scores beyond 2^24 perhaps nothing.
+          if (sum > 4096.f && sum < INFINITY) {
+            const float raised = base + (float)((int)(__float_as_uint(sum) >> 23) - 135);
             sum *= exp2_fast(base - raised);
             base = raised;
           }

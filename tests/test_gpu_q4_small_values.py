@@ -176,3 +176,23 @@ def test_equal_scores_of_any_size(dt, size):
             R.assert_close(out[s], want.expand(5, d), bound.expand(5, d), f"{n} keys")
             z = 7 * float(torch.tensor(size)) + float(torch.log(torch.tensor(float(n), dtype=torch.float64)))
             assert float((lse[s].cpu().double() - z).abs().max()) <= 4 * 2 * U * abs(z) + 2 * n * U + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -15, 2.0 ** -6, 1.0, 2.0 ** 13])
+def test_the_logarithm_of_the_sum_does_not_depend_on_values(dt, size):
+    """Sums near one, of a few keys each: what is left of the logarithm is its own rounding."""
+    mita = M()
+    S, d = 600, 32
+    lengths = tuple(1 + i % 3 for i in range(S))
+    g = torch.Generator().manual_seed(9)
+    k = [torch.randn(1, n, d, generator=g) for n in lengths]
+    v = [torch.randn(1, n, d, generator=g) * size for n in lengths]
+    cache = Q.Cache4(lengths, 1, 16, d, k=k, v=v)
+    q = torch.zeros(S, 8, d, dtype=DT[dt])                # scores are the slopes'
+    slopes = torch.rand(8, generator=g) * 0.1
+    _, lse = mita.mita_paged_attn_q4(q.cuda(), cache.k8.cuda(), cache.v8.cuda(), cache.table.cuda(),
+                                     torch.tensor(lengths, dtype=torch.int32).cuda(), return_lse=True,
+                                     alibi_slopes=slopes.cuda())
+    _, _, want, bound = Q.paged_attn(q, cache, lengths, slopes=slopes)
+    R.assert_close(lse, want, bound, "lse")
